@@ -11,6 +11,11 @@
  *   moe_route_pull  moe_route_union, then (host waits) moe_slot_pull of its experts
  *   moe_expert_ffn  quantised SwiGLU experts read through the page table,
  *                   shared expert, weighted combine
+ * and the dense layers that stand between the routed ones:
+ *   moe_linear       product with 4-bit weights and group scales
+ *   moe_linear_gated gated feed-forward block with such weights (serving)
+ *   moe_gated        the same block with bf16 or fp32 weights, and
+ *   moe_gated_backward its backward pass (tuning)
  *
  * Conventions for every entry point:
  *  - Pointers named "device" are HIP device (or managed) memory; "host" is
@@ -433,6 +438,95 @@ moe_status moe_route_ffn(moe_ctx* ctx, int32_t layer, const void* x, int32_t x_d
                          const float* logits_in, int64_t T, int32_t* topk_ids, float* topk_w,
                          const moe_plan* plan, const void* shared_payload, int32_t prec, float* y,
                          moe_stream stream);
+
+/* ---- dense layers ------------------------------------------------------------
+ *
+ * Operators of a model's dense layers (projections, vocabulary, feed-forward
+ * blocks without routing).  They use a device context for its device and error
+ * text only: they read and write nothing of its slots, plan or workspace and do
+ * not wait for fills, so calls on different streams may overlap, also on one
+ * context.  They allocate nothing and may be captured into a graph; a captured
+ * call replays on the pointers and sizes it was given.  Every output element
+ * is written by one fixed order of sums: equal inputs give equal bits.
+ * Rows of activations may be strided ("ld", elements between rows, at least
+ * the row's length when there is more than one row); everything else is
+ * contiguous.  Pointers need the alignment of their elements.  Outputs must
+ * not overlap inputs or each other.  T = 0 is a call that writes nothing
+ * (weight gradients excepted, which become zero). */
+
+/* A matrix [rows, cols] of 4-bit codes q with one fp16 scale s and, if affine,
+ * one zero point z for every `group` consecutive columns of a row:
+ *   w[n, k] = s[n, k / group] * (q[n, k] - z[n, k / group]),
+ * z = 8 everywhere if not affine (with group 32 these are Q4_0's values).
+ * group 32, 64 or 128; cols a multiple of group; rows up to 2^30, cols up to
+ * 2^24.  data: device, 16-byte aligned, moe_linear_bytes() bytes, filled by
+ * moe_linear_pack. */
+typedef struct moe_qmat {
+    int64_t rows, cols;
+    int32_t group;
+    int32_t affine; /* 0 or 1 */
+    void* data;
+} moe_qmat;
+
+/* Bytes of a packed matrix (0 if the shape is not valid): tiles of 16 rows x
+ * 128 columns, each wave's load contiguous; rows and columns are padded to
+ * whole tiles. */
+size_t moe_linear_bytes(int64_t rows, int64_t cols, int32_t group, int32_t affine);
+
+/* Lay a matrix out for the products, once per matrix.  codes: device [rows,
+ * cols / 2], two codes a byte, the even column in the low half.  scales: device
+ * fp16 [rows, cols / group].  zeros: device uint8 [rows, cols / group], values
+ * 0..255, if m->affine (else ignored).  Writes m->data on `stream`. */
+moe_status moe_linear_pack(moe_ctx* ctx, const uint8_t* codes, const void* scales, const uint8_t* zeros,
+                           const moe_qmat* m, moe_stream stream);
+
+/* The values of a packed matrix in fp32, exactly: device out [rows, cols]. */
+moe_status moe_linear_dequant(moe_ctx* ctx, const moe_qmat* m, float* out, moe_stream stream);
+
+/* y[t, n] = sum_k x[t, k] w[n, k] for T >= 0 tokens.
+ * x: device [T, w->cols] (x_dtype), rows ldx apart; y: device [T, w->rows]
+ * (y_dtype: MOE_F32 or MOE_BF16), rows ldy apart.
+ * Sums, scales and zero points are fp32 and x is not rounded (fp32 x enters
+ * the matrix cores as three bf16 terms).  A token's row that holds an
+ * infinity or NaN gives a row that is not finite; other rows are not touched
+ * by it.  Finite x should stay below 2^120 (codes enter the sums as 16 + q). */
+moe_status moe_linear(moe_ctx* ctx, const void* x, int32_t x_dtype, int64_t ldx, int64_t T, const moe_qmat* w, void* y,
+                      int32_t y_dtype, int64_t ldy, moe_stream stream);
+
+/* h[t, f] = silu(g) * u with g = sum_k x[t, k] w_gate[f, k] and u the same of
+ * w_up, in one launch; silu(z) = z / (1 + exp(-z)).  Both matrices have the
+ * same rows, cols, group and affine.  Arguments and precision as moe_linear;
+ * g and u are not rounded before the product. */
+moe_status moe_linear_gated(moe_ctx* ctx, const void* x, int32_t x_dtype, int64_t ldx, int64_t T,
+                            const moe_qmat* w_gate, const moe_qmat* w_up, void* h, int32_t h_dtype, int64_t ldh,
+                            moe_stream stream);
+
+/* The gated block on weights in the activations' own type (dtype: MOE_F32 or
+ * MOE_BF16, of every array here): g = x w_gate^T, u = x w_up^T, h = silu(g) u.
+ * x: device [T, d], rows ldx apart; w_gate, w_up: device [F, d]; h: device
+ * [T, F].  gate, up: device [T, F] or NULL, g and u for moe_gated_backward
+ * (both or neither).  Sums are fp32; h comes from the unrounded g and u.
+ * Sizes: d and F from 1 to 2^20, T up to 2^24. */
+moe_status moe_gated(moe_ctx* ctx, const void* x, int32_t dtype, int64_t ldx, int64_t T, int32_t d, int32_t F,
+                     const void* w_gate, const void* w_up, void* h, void* gate, void* up, moe_stream stream);
+
+/* Bytes of moe_gated_backward's workspace for these sizes (0 if not valid). */
+size_t moe_gated_workspace(int64_t T, int32_t d, int32_t F, int32_t dtype);
+
+/* Gradients of the gated block from dh (device [T, F], rows lddh apart), the
+ * forward pass's x, weights and stored gate and up:
+ *   dg = dh u s(g) (1 + g (1 - s(g))),  du = dh g s(g),  s(g) = 1 / (1 + exp(-g))
+ *   dx = dg w_gate + du w_up            device [T, d], or NULL
+ *   dw_gate = dg^T x, dw_up = du^T x    device [F, d] each, or both NULL
+ * all in dtype.  Sums are fp32; dg and du are rounded to dtype before the
+ * products.  Gradients are written, not added to.
+ * workspace: device, 256-byte aligned, moe_gated_workspace() bytes or more,
+ * used until the call's work on `stream` is done; calls that may run at the
+ * same time (two streams, two captured graphs) need one each. */
+moe_status moe_gated_backward(moe_ctx* ctx, const void* dh, int64_t lddh, const void* x, int32_t dtype, int64_t ldx,
+                              int64_t T, int32_t d, int32_t F, const void* w_gate, const void* w_up, const void* gate,
+                              const void* up, void* dx, void* dw_gate, void* dw_up, void* workspace,
+                              size_t workspace_bytes, moe_stream stream);
 
 /* ---- inspection ------------------------------------------------------------- */
 

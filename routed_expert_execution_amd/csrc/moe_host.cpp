@@ -13,6 +13,7 @@
 #include <utility>
 #include <vector>
 
+#include "dense.h"
 #include "internal.h"
 
 using moe::Geom;
@@ -1349,6 +1350,168 @@ moe_status moe_dequant(moe_ctx* c, const void* payload, int32_t prec, float* out
     if (prec != MOE_PREC_F32 && prec != MOE_PREC_BF16) return fail(c, MOE_EINVAL, "moe_dequant: bad prec");
     DeviceGuard dg(c->cfg.device);
     HIP_TRY(c, moe::launch_dequant(c->g, (const uint8_t*)payload, prec, out, (hipStream_t)stream));
+    return MOE_OK;
+}
+
+// ---- dense layers ----
+// (arguments are judged before the context's device, so that a host-only context
+// names a bad argument too)
+
+static int elem_bytes(int32_t dtype) { return dtype == MOE_BF16 ? 2 : 4; }
+static bool dtype_valid(int32_t dtype) { return dtype == MOE_F32 || dtype == MOE_BF16; }
+static bool aligned_to(const void* p, size_t n) { return ((uintptr_t)p) % n == 0; }
+
+constexpr int64_t kDenseMaxT = 1 << 24;
+constexpr int32_t kDenseMaxWidth = 1 << 20;
+
+size_t moe_linear_bytes(int64_t rows, int64_t cols, int32_t group, int32_t affine) {
+    moe::QuantGeom g;
+    return g.init(rows, cols, group, affine) ? (size_t)g.bytes : 0;
+}
+
+static moe_status qmat_geom(moe_ctx* c, const char* fn, const moe_qmat* m, moe::QuantGeom* g) {
+    if (!m || !m->data) return fail(c, MOE_EINVAL, "%s: null matrix", fn);
+    if (!g->init(m->rows, m->cols, m->group, m->affine))
+        return fail(c, MOE_EINVAL, "%s: bad matrix: rows in [1, 2^30], group 32, 64 or 128, cols a multiple of it in "
+                    "[group, 2^24], affine 0 or 1", fn);
+    if (!aligned_to(m->data, 16)) return fail(c, MOE_EINVAL, "%s: matrix data must be 16-byte aligned", fn);
+    return MOE_OK;
+}
+
+moe_status moe_linear_pack(moe_ctx* c, const uint8_t* codes, const void* scales, const uint8_t* zeros,
+                           const moe_qmat* m, moe_stream stream) {
+    if (!c) return MOE_EINVAL;
+    moe::QuantGeom g;
+    if (moe_status st = qmat_geom(c, "moe_linear_pack", m, &g)) return st;
+    if (!codes || !scales || (g.affine && !zeros)) return fail(c, MOE_EINVAL, "moe_linear_pack: null argument");
+    if (!aligned_to(scales, 2)) return fail(c, MOE_EINVAL, "moe_linear_pack: misaligned scales");
+    if (moe_status st = need_device(c)) return st;
+    DeviceGuard dg(c->cfg.device);
+    HIP_TRY(c, moe::launch_linear_pack(g, codes, (const uint16_t*)scales, zeros, m->data, (hipStream_t)stream));
+    return MOE_OK;
+}
+
+moe_status moe_linear_dequant(moe_ctx* c, const moe_qmat* m, float* out, moe_stream stream) {
+    if (!c) return MOE_EINVAL;
+    moe::QuantGeom g;
+    if (moe_status st = qmat_geom(c, "moe_linear_dequant", m, &g)) return st;
+    if (!out || !aligned_to(out, 4)) return fail(c, MOE_EINVAL, "moe_linear_dequant: null or misaligned out");
+    if (moe_status st = need_device(c)) return st;
+    DeviceGuard dg(c->cfg.device);
+    HIP_TRY(c, moe::launch_linear_dequant(g, m->data, out, (hipStream_t)stream));
+    return MOE_OK;
+}
+
+// Activations [T, n] of one argument: type, stride and alignment.
+static moe_status rows_check(moe_ctx* c, const char* fn, const char* name, const void* p, int32_t dtype, int64_t T,
+                             int64_t n, int64_t ld) {
+    if (!dtype_valid(dtype)) return fail(c, MOE_EINVAL, "%s: bad type of %s", fn, name);
+    if (T > 0 && !p) return fail(c, MOE_EINVAL, "%s: null %s", fn, name);
+    if (!aligned_to(p, elem_bytes(dtype))) return fail(c, MOE_EINVAL, "%s: misaligned %s", fn, name);
+    if (T > 1 && (ld < n || ld > ((int64_t)1 << 40)))
+        return fail(c, MOE_EINVAL, "%s: rows of %s must be at least %lld elements apart", fn, name, (long long)n);
+    return MOE_OK;
+}
+
+static moe_status linear_call(moe_ctx* c, const char* fn, const void* x, int32_t x_dtype, int64_t ldx, int64_t T,
+                              const moe_qmat* w0, const moe_qmat* w1, void* y, int32_t y_dtype, int64_t ldy,
+                              moe_stream stream) {
+    if (!c) return MOE_EINVAL;
+    moe::QuantGeom g;
+    if (moe_status st = qmat_geom(c, fn, w0, &g)) return st;
+    if (w1) {
+        moe::QuantGeom g1;
+        if (moe_status st = qmat_geom(c, fn, w1, &g1)) return st;
+        if (g1.rows != g.rows || g1.cols != g.cols || g1.group != g.group || g1.affine != g.affine)
+            return fail(c, MOE_EINVAL, "%s: the two matrices differ in shape, group or kind", fn);
+    }
+    if (T < 0 || T > kDenseMaxT) return fail(c, MOE_EINVAL, "%s: T=%lld outside [0, 2^24]", fn, (long long)T);
+    if (moe_status st = rows_check(c, fn, "x", x, x_dtype, T, g.cols, ldx)) return st;
+    if (moe_status st = rows_check(c, fn, "the result", y, y_dtype, T, g.rows, ldy)) return st;
+    if (moe_status st = need_device(c)) return st;
+    if (T == 0) return MOE_OK;
+    DeviceGuard dg(c->cfg.device);
+    moe::LinearArgs a{};
+    a.w[0] = moe::quant_view(g, w0->data);
+    if (w1) a.w[1] = moe::quant_view(g, w1->data);
+    a.rows = (int)g.rows;
+    a.cols = (int)g.cols;
+    a.row_groups = (int)g.row_groups;
+    a.col_tiles = (int)g.col_tiles;
+    a.group = g.group;
+    a.x = x;
+    a.ldx = T > 1 ? ldx : g.cols;
+    a.x_bf16 = x_dtype == MOE_BF16;
+    a.T = T;
+    a.y = y;
+    a.ldy = T > 1 ? ldy : g.rows;
+    a.y_bf16 = y_dtype == MOE_BF16;
+    HIP_TRY(c, moe::launch_linear(a, w1 != nullptr, (hipStream_t)stream));
+    return MOE_OK;
+}
+
+moe_status moe_linear(moe_ctx* c, const void* x, int32_t x_dtype, int64_t ldx, int64_t T, const moe_qmat* w, void* y,
+                      int32_t y_dtype, int64_t ldy, moe_stream stream) {
+    return linear_call(c, "moe_linear", x, x_dtype, ldx, T, w, nullptr, y, y_dtype, ldy, stream);
+}
+
+moe_status moe_linear_gated(moe_ctx* c, const void* x, int32_t x_dtype, int64_t ldx, int64_t T,
+                            const moe_qmat* w_gate, const moe_qmat* w_up, void* h, int32_t h_dtype, int64_t ldh,
+                            moe_stream stream) {
+    if (!c) return MOE_EINVAL;
+    if (!w_up) return fail(c, MOE_EINVAL, "moe_linear_gated: null matrix");
+    return linear_call(c, "moe_linear_gated", x, x_dtype, ldx, T, w_gate, w_up, h, h_dtype, ldh, stream);
+}
+
+static bool gated_sizes(int64_t T, int32_t d, int32_t F) {
+    return T >= 0 && T <= kDenseMaxT && d >= 1 && d <= kDenseMaxWidth && F >= 1 && F <= kDenseMaxWidth;
+}
+
+moe_status moe_gated(moe_ctx* c, const void* x, int32_t dtype, int64_t ldx, int64_t T, int32_t d, int32_t F,
+                     const void* w_gate, const void* w_up, void* h, void* gate, void* up, moe_stream stream) {
+    if (!c) return MOE_EINVAL;
+    if (!gated_sizes(T, d, F)) return fail(c, MOE_EINVAL, "moe_gated: T outside [0, 2^24], or d or F outside [1, 2^20]");
+    if (moe_status st = rows_check(c, "moe_gated", "x", x, dtype, T, d, ldx)) return st;
+    if ((T > 0 && (!w_gate || !w_up || !h)) || !gate != !up) return fail(c, MOE_EINVAL, "moe_gated: null argument");
+    const size_t e = elem_bytes(dtype);
+    if (!aligned_to(w_gate, e) || !aligned_to(w_up, e) || !aligned_to(h, e) || !aligned_to(gate, e) || !aligned_to(up, e))
+        return fail(c, MOE_EINVAL, "moe_gated: misaligned argument");
+    if (moe_status st = need_device(c)) return st;
+    if (T == 0) return MOE_OK;
+    DeviceGuard dg(c->cfg.device);
+    moe::GatedArgs a{x, T > 1 ? ldx : d, T, d, F, dtype == MOE_BF16, w_gate, w_up, h, gate, up};
+    HIP_TRY(c, moe::launch_gated(a, (hipStream_t)stream));
+    return MOE_OK;
+}
+
+size_t moe_gated_workspace(int64_t T, int32_t d, int32_t F, int32_t dtype) {
+    if (!gated_sizes(T, d, F) || !dtype_valid(dtype)) return 0;
+    return std::max<size_t>(256, moe::gated_backward_bytes(T, d, F, dtype == MOE_BF16));
+}
+
+moe_status moe_gated_backward(moe_ctx* c, const void* dh, int64_t lddh, const void* x, int32_t dtype, int64_t ldx,
+                              int64_t T, int32_t d, int32_t F, const void* w_gate, const void* w_up, const void* gate,
+                              const void* up, void* dx, void* dw_gate, void* dw_up, void* workspace,
+                              size_t workspace_bytes, moe_stream stream) {
+    if (!c) return MOE_EINVAL;
+    if (!gated_sizes(T, d, F))
+        return fail(c, MOE_EINVAL, "moe_gated_backward: T outside [0, 2^24], or d or F outside [1, 2^20]");
+    if (moe_status st = rows_check(c, "moe_gated_backward", "x", x, dtype, T, d, ldx)) return st;
+    if (moe_status st = rows_check(c, "moe_gated_backward", "dh", dh, dtype, T, F, lddh)) return st;
+    if ((T > 0 && (!gate || !up || (dx && (!w_gate || !w_up)))) || !dw_gate != !dw_up || !workspace)
+        return fail(c, MOE_EINVAL, "moe_gated_backward: null argument");
+    const size_t e = elem_bytes(dtype);
+    for (const void* p : {w_gate, w_up, gate, up, (const void*)dx, (const void*)dw_gate, (const void*)dw_up})
+        if (!aligned_to(p, e)) return fail(c, MOE_EINVAL, "moe_gated_backward: misaligned argument");
+    if (!aligned_to(workspace, 256)) return fail(c, MOE_EINVAL, "moe_gated_backward: workspace must be 256-byte aligned");
+    const size_t need = moe_gated_workspace(T, d, F, dtype);
+    if (workspace_bytes < need)
+        return fail(c, MOE_EINVAL, "moe_gated_backward: workspace of %zu bytes, %zu needed", workspace_bytes, need);
+    if (moe_status st = need_device(c)) return st;
+    DeviceGuard dg(c->cfg.device);
+    moe::GatedBackwardArgs a{dh, T > 1 ? lddh : F, x, T > 1 ? ldx : d, T, d, F, dtype == MOE_BF16, w_gate, w_up, gate,
+                             up, dx, dw_gate, dw_up, workspace};
+    HIP_TRY(c, moe::launch_gated_backward(a, (hipStream_t)stream));
     return MOE_OK;
 }
 

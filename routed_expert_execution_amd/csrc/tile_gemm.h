@@ -1,0 +1,115 @@
+// Matrix products on the matrix cores, tiles of both operands in LDS:
+//   C[m, n] = sum_k A(m, k) B(n, k)
+// for operands stored along k (kAlongK: element (r, k) at p[r * ld + k]) or
+// across it (kAcrossK: at p[k * ld + r], so that a gradient's transposed
+// operand is read as it lies), bf16 or fp32, any sizes.
+#pragma once
+
+#include "device_util.h"
+
+namespace moe {
+namespace tile {
+
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef float f32x16 __attribute__((ext_vector_type(16)));
+typedef short s16x4 __attribute__((ext_vector_type(4)));
+typedef short s16x8 __attribute__((ext_vector_type(8)));
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+
+enum { kAlongK = 0, kAcrossK = 1 };
+
+template <bool BF16> struct Elem;
+template <> struct Elem<true> { typedef __bf16 type; typedef uint16_t raw; static constexpr int kChunk = 8; };
+template <> struct Elem<false> { typedef float type; typedef uint32_t raw; static constexpr int kChunk = 4; };
+
+struct __attribute__((packed, aligned(2))) Loose { u32x4 v; };
+
+// One operand: R rows, K columns.
+struct Operand {
+    const void* p;
+    int64_t ld;
+    int64_t R, K;
+};
+
+// 16 bytes of an operand in its storage order: elements `in` .. +chunk of line
+// `line` (along k: line is a row, in a column; across k the other way round),
+// zero where the line or the element is past the end.
+template <bool BF16>
+__device__ inline u32x4 load_chunk(const void* p, int64_t ld, int64_t line, int64_t in, int64_t lines, int64_t ins) {
+    typedef typename Elem<BF16>::raw raw;
+    constexpr int E = Elem<BF16>::kChunk;
+    u32x4 v = {0u, 0u, 0u, 0u};
+    if (line >= lines || in >= ins) return v;
+    const raw* q = (const raw*)p + line * ld + in;
+    if (in + E <= ins) return ((const Loose*)q)->v;
+    raw e[E];
+#pragma unroll
+    for (int i = 0; i < E; i++) e[i] = in + i < ins ? q[i] : (raw)0;
+    __builtin_memcpy(&v, e, 16);
+    return v;
+}
+
+// Tile of BR rows by BK columns (BK elements fill 128 bytes) in LDS.  Along k:
+// [BR][128 B], 16-byte chunk c of row r at c ^ (r / 2 % 8).  Across k: [BK][BR].
+// bf16 lines are read back through the transposing LDS load: there the four
+// lines of a 16-lane read are spread over the banks by xor of the chunk with
+// 4 (k % 4), fp32 lines are read a word a lane and need none.
+template <bool BF16, int BR, int LAY>
+struct TileOf {
+    static constexpr int E = Elem<BF16>::kChunk;
+    static constexpr int BK = 8 * E;
+    static constexpr int kBytes = BR * 128;
+    static constexpr int kLineChunks = LAY == kAlongK ? 8 : BR / E;  // 16-byte chunks a line
+    static constexpr int kChunks = kBytes / 16;
+
+    __device__ static int chunk_at(int line, int c) {  // LDS byte offset
+        if (LAY == kAlongK) return line * 128 + ((c ^ (line >> 1 & 7)) << 4);
+        if (BF16) return (line * kLineChunks + (c ^ (line & 3) * (kLineChunks >= 16 ? 4 : 2))) << 4;
+        return (line * kLineChunks + c) << 4;
+    }
+    // Operand of one 32-row block at row r0 for k step kk (16 bf16 / 8 fp32 columns).
+    __device__ static void frag(const char* lds, int r0, int kk, int lane, bf16x8& f) {
+        if (LAY == kAlongK) {
+            const int r = r0 + (lane & 31);
+            f = *(const bf16x8*)(lds + chunk_at(r, 2 * kk + (lane >> 5)));
+        } else {
+            const int k = 16 * kk + 8 * (lane >> 5) + (lane >> 2 & 3);
+            const int col = r0 + 16 * (lane >> 4 & 1) + 4 * (lane & 3);
+            s16x8 v;
+#pragma unroll
+            for (int h = 0; h < 2; h++) {
+                typedef __attribute__((address_space(3))) s16x4 lds4;
+                const s16x4 t = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+                    (lds4*)(lds + chunk_at(k + 4 * h, col >> 3) + ((col & 7) << 1)));
+#pragma unroll
+                for (int i = 0; i < 4; i++) v[4 * h + i] = t[i];
+            }
+            f = __builtin_bit_cast(bf16x8, v);
+        }
+    }
+    __device__ static void frag(const char* lds, int r0, int kk, int lane, f32x4& f) {
+        if (LAY == kAlongK) {
+            const int r = r0 + (lane & 31);
+            f = *(const f32x4*)(lds + chunk_at(r, 2 * kk + (lane >> 5)));
+        } else {
+#pragma unroll
+            for (int i = 0; i < 4; i++)
+                f[i] = *(const float*)(lds + ((8 * kk + 4 * (lane >> 5) + i) * BR + r0 + (lane & 31)) * 4);
+        }
+    }
+};
+
+__device__ inline void mma(f32x16& acc, const bf16x8& a, const bf16x8& b) {
+    acc = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, acc, 0, 0, 0);
+}
+__device__ inline void mma(f32x16& acc, const f32x4& a, const f32x4& b) {
+#pragma unroll
+    for (int i = 0; i < 4; i++) acc = __builtin_amdgcn_mfma_f32_32x32x2f32(a[i], b[i], acc, 0, 0, 0);
+}
+
+// Row of result register i of a 32 x 32 block (its column is lane % 32).
+__device__ inline int acc_row(int lane, int i) { return 8 * (i >> 2) + 4 * (lane >> 5) + (i & 3); }
+
+}  // namespace tile
+}  // namespace moe

@@ -43,6 +43,11 @@ class moe_plan(C.Structure):
                 ("entries", C.c_void_p)]
 
 
+class moe_qmat(C.Structure):
+    _fields_ = [("rows", C.c_int64), ("cols", C.c_int64), ("group", C.c_int32), ("affine", C.c_int32),
+                ("data", C.c_void_p)]
+
+
 def _load() -> C.CDLL:
     # torch ships its own HIP runtime.  Loading torch first makes libmoe's
     # libamdhip64.so.7 dependency resolve (by soname) to that same runtime;
@@ -54,6 +59,7 @@ def _load() -> C.CDLL:
     P, I32, I64, S = C.c_void_p, C.c_int32, C.c_int64, C.c_size_t
     cfgp = C.POINTER(moe_config)
     planp = C.POINTER(moe_plan)
+    qmatp = C.POINTER(moe_qmat)
     sig = {
         "moe_payload_bytes": (S, [cfgp]),
         "moe_plan_bytes": (C.c_int, [cfgp, I64, C.POINTER(S)]),
@@ -81,6 +87,14 @@ def _load() -> C.CDLL:
         "moe_expert_ffn_split": (C.c_int, [P, I32, P, I32, I64, planp, P, P, I32, P, I32, P, P, P]),
         "moe_route_ffn": (C.c_int, [P, I32, P, I32, P, P, I64, P, P, planp, P, I32, P, P]),
         "moe_dequant": (C.c_int, [P, P, I32, P, P]),
+        "moe_linear_bytes": (S, [I64, I64, I32, I32]),
+        "moe_linear_pack": (C.c_int, [P, P, P, P, qmatp, P]),
+        "moe_linear_dequant": (C.c_int, [P, qmatp, P, P]),
+        "moe_linear": (C.c_int, [P, P, I32, I64, I64, qmatp, P, I32, I64, P]),
+        "moe_linear_gated": (C.c_int, [P, P, I32, I64, I64, qmatp, qmatp, P, I32, I64, P]),
+        "moe_gated": (C.c_int, [P, P, I32, I64, I64, I32, I32, P, P, P, P, P, P]),
+        "moe_gated_workspace": (S, [I64, I32, I32, I32]),
+        "moe_gated_backward": (C.c_int, [P, P, I64, P, I32, I64, I64, I32, I32, P, P, P, P, P, P, P, P, S, P]),
         "moe_stats": (C.c_int, [P, C.POINTER(C.c_uint64)]),
         "moe_check": (C.c_int, [P, P]),
         "moe_page_table": (C.c_int, [P, C.POINTER(P)]),
@@ -103,7 +117,8 @@ EXPORTS = ("moe_payload_bytes", "moe_plan_bytes", "moe_pack_expert", "moe_unpack
            "moe_slot_map", "moe_slot_prefetch", "moe_prefetch_stats", "moe_prefetch_next", "moe_slot_fill", "moe_slot_stage", "moe_slot_pull", "moe_route_pull", "moe_slot_release",
            "moe_slot_bind", "moe_expert_ffn", "moe_expert_ffn_static", "moe_expert_ffn_split",
            "moe_route_ffn", "moe_dequant", "moe_stats", "moe_check", "moe_page_table", "moe_route_splits", "moe_hidden_rows", "moe_probe_read",
-           "moe_probe_mfma", "moe_probe_lds")
+           "moe_probe_mfma", "moe_probe_lds", "moe_linear_bytes", "moe_linear_pack", "moe_linear_dequant", "moe_linear",
+           "moe_linear_gated", "moe_gated", "moe_gated_workspace", "moe_gated_backward")
 
 
 def library() -> C.CDLL:
@@ -519,6 +534,134 @@ def moe_dequant(ctx: Context, payload, out, prec: int = MOE_PREC_F32, stream=Non
         raise ValueError("out must be float32 with 3 * d_ff * d_model elements")
     _check_dev(ctx, payload, out)
     _call(ctx, _lib.moe_dequant(ctx.handle, _ptr(payload), prec, _ptr(out), _stream(stream)))
+
+
+def _stream_on(ctx: Context, stream) -> int | None:
+    """As _stream, the default being the current stream of the context's device."""
+    if stream is None:
+        import torch
+        return torch.cuda.current_stream(ctx.device).cuda_stream
+    return _stream(stream)
+
+
+def _rows(t, shape, name: str) -> tuple:
+    """(address, elements between rows, type code) of a [rows, columns] tensor
+    whose rows are contiguous and may lie apart."""
+    if t.dim() != 2 or tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must be [{shape[0]}, {shape[1]}]")
+    if t.shape[1] > 1 and t.stride(1) != 1:
+        raise ValueError(f"the rows of {name} must be contiguous")
+    if t.shape[0] > 1 and t.stride(0) < t.shape[1]:
+        raise ValueError(f"the rows of {name} must not overlap")
+    return t.data_ptr(), (t.stride(0) if t.shape[0] > 1 else t.shape[1]), _x_dtype(t)
+
+
+class QuantMatrix:
+    """A packed 4-bit matrix [rows, cols] on the context's GPU (moe_linear_pack).
+
+    codes: uint8 [rows, cols / 2], two codes a byte, the even column in the low
+    half; scales: float16 [rows, cols / group]; zeros: uint8 of the scales'
+    shape, or None for a zero point of 8 everywhere.  The three may be dropped
+    afterwards."""
+
+    def __init__(self, ctx: Context, codes, scales, zeros=None, stream=None):
+        import torch
+        if codes.dtype != torch.uint8 or codes.dim() != 2 or scales.dtype != torch.float16 or scales.dim() != 2:
+            raise ValueError("codes must be uint8 [rows, cols / 2], scales float16 [rows, cols / group]")
+        rows, cols = codes.shape[0], 2 * codes.shape[1]
+        if scales.shape[0] != rows or scales.shape[1] < 1 or cols % scales.shape[1]:
+            raise ValueError("scales must be [rows, cols / group]")
+        if zeros is not None and (zeros.dtype != torch.uint8 or zeros.shape != scales.shape):
+            raise ValueError("zeros must be uint8 of the scales' shape")
+        _check_dev(ctx, codes, scales, zeros)
+        group = cols // scales.shape[1]
+        n = int(_lib.moe_linear_bytes(rows, cols, group, int(zeros is not None)))
+        if n == 0:
+            raise ValueError("unsupported matrix: group 32, 64 or 128, at least one row")
+        self.rows, self.cols, self.group, self.affine = rows, cols, group, zeros is not None
+        self.data = torch.empty(n, dtype=torch.uint8, device=codes.device)
+        self.c = moe_qmat(rows, cols, group, int(self.affine), _ptr(self.data))
+        _call(ctx, _lib.moe_linear_pack(ctx.handle, _ptr(codes), _ptr(scales), _ptr(zeros), C.byref(self.c),
+                                        _stream_on(ctx, stream)))
+
+
+def moe_linear_dequant(ctx: Context, w: QuantMatrix, out, stream=None) -> None:
+    import torch
+    if out.dtype != torch.float32 or tuple(out.shape) != (w.rows, w.cols):
+        raise ValueError("out must be float32 [rows, cols]")
+    _check_dev(ctx, w.data, out)
+    _call(ctx, _lib.moe_linear_dequant(ctx.handle, C.byref(w.c), _ptr(out), _stream_on(ctx, stream)))
+
+
+def moe_linear(ctx: Context, x, w: QuantMatrix, y, stream=None) -> None:
+    """y = x w^T.  x, y: float32 or bfloat16 [T, cols] / [T, rows], rows may lie apart."""
+    T = x.shape[0]
+    xp, ldx, xd = _rows(x, (T, w.cols), "x")
+    yp, ldy, yd = _rows(y, (T, w.rows), "y")
+    _check_dev(ctx, x, w.data, y)
+    _call(ctx, _lib.moe_linear(ctx.handle, xp, xd, ldx, T, C.byref(w.c), yp, yd, ldy, _stream_on(ctx, stream)))
+
+
+def moe_linear_gated(ctx: Context, x, w_gate: QuantMatrix, w_up: QuantMatrix, h, stream=None) -> None:
+    """h = silu(x w_gate^T) * (x w_up^T), x and h as in moe_linear."""
+    T = x.shape[0]
+    xp, ldx, xd = _rows(x, (T, w_gate.cols), "x")
+    hp, ldh, hd = _rows(h, (T, w_gate.rows), "h")
+    _check_dev(ctx, x, w_gate.data, w_up.data, h)
+    _call(ctx, _lib.moe_linear_gated(ctx.handle, xp, xd, ldx, T, C.byref(w_gate.c), C.byref(w_up.c), hp, hd, ldh,
+                                     _stream_on(ctx, stream)))
+
+
+def _same(name: str, t, shape, dtype) -> None:
+    if t is not None and (tuple(t.shape) != tuple(shape) or t.dtype != dtype):
+        raise ValueError(f"{name} must be {dtype} [{shape[0]}, {shape[1]}]")
+
+
+def moe_gated(ctx: Context, x, w_gate, w_up, h, gate_out=None, up_out=None, stream=None) -> None:
+    """h = silu(g) * u, g = x w_gate^T, u = x w_up^T, all of x's type (float32
+    or bfloat16); gate_out, up_out receive g and u for moe_gated_backward."""
+    if x.dim() != 2 or w_gate.dim() != 2:
+        raise ValueError("x must be [T, d], w_gate [F, d]")
+    T, d, F = x.shape[0], x.shape[1], w_gate.shape[0]
+    xp, ldx, xd = _rows(x, (T, d), "x")
+    _same("w_gate", w_gate, (F, d), x.dtype)
+    _same("w_up", w_up, (F, d), x.dtype)
+    for name, t in (("h", h), ("gate_out", gate_out), ("up_out", up_out)):
+        _same(name, t, (T, F), x.dtype)
+    _check_dev(ctx, x, w_gate, w_up, h, gate_out, up_out)
+    _call(ctx, _lib.moe_gated(ctx.handle, xp, xd, ldx, T, d, F, _ptr(w_gate), _ptr(w_up), _ptr(h), _ptr(gate_out),
+                              _ptr(up_out), _stream_on(ctx, stream)))
+
+
+def moe_gated_workspace(ctx: Context, T: int, d: int, F: int, dtype) -> int:
+    """Bytes of moe_gated_backward's workspace."""
+    import torch
+    n = int(_lib.moe_gated_workspace(T, d, F, {torch.float32: MOE_F32, torch.bfloat16: MOE_BF16}.get(dtype, -1)))
+    if n == 0:
+        raise ValueError("bad sizes or type (float32 or bfloat16)")
+    return n
+
+
+def moe_gated_backward(ctx: Context, dh, x, w_gate, w_up, gate, up, *, dx=None, dw_gate=None, dw_up=None, workspace,
+                       stream=None) -> None:
+    """Gradients of moe_gated from dh and the stored gate and up; dx, or dw_gate
+    and dw_up, may be left out.  workspace: uint8, moe_gated_workspace bytes."""
+    if x.dim() != 2 or w_gate.dim() != 2:
+        raise ValueError("x must be [T, d], w_gate [F, d]")
+    T, d, F = x.shape[0], x.shape[1], w_gate.shape[0]
+    xp, ldx, xd = _rows(x, (T, d), "x")
+    if dh.dtype != x.dtype:
+        raise ValueError("dh must have x's type")
+    dp, lddh, _ = _rows(dh, (T, F), "dh")
+    for name, t in (("w_gate", w_gate), ("w_up", w_up), ("dw_gate", dw_gate), ("dw_up", dw_up)):
+        _same(name, t, (F, d), x.dtype)
+    for name, t in (("gate", gate), ("up", up)):
+        _same(name, t, (T, F), x.dtype)
+    _same("dx", dx, (T, d), x.dtype)
+    _check_dev(ctx, dh, x, w_gate, w_up, gate, up, dx, dw_gate, dw_up, workspace)
+    _call(ctx, _lib.moe_gated_backward(ctx.handle, dp, lddh, xp, xd, ldx, T, d, F, _ptr(w_gate), _ptr(w_up),
+                                       _ptr(gate), _ptr(up), _ptr(dx), _ptr(dw_gate), _ptr(dw_up), _ptr(workspace),
+                                       workspace.numel() * workspace.element_size(), _stream_on(ctx, stream)))
 
 
 def moe_stats(ctx: Context) -> dict:
