@@ -30,7 +30,29 @@ struct Operand {
     const void* p;
     int64_t ld;
     int64_t R, K;
+    int padded;  // its lines are whole 16-byte chunks in memory, whatever R is
 };
+
+// 16 bytes a lane from base + offset straight into LDS at `lds` + 16 * lane
+// (a wave-uniform LDS address; no register in between).  The compiler does not
+// know of these loads: wait_loads() before the barrier that publishes them.
+__device__ inline void load_lds16(uint32_t lds, uint32_t offset, const void* base) {
+    asm volatile(
+        "s_mov_b32 m0, %0\n\t"
+        "s_nop 0\n\t"
+        "global_load_lds_dwordx4 %1, %2"
+        :
+        : "s"(lds), "v"(offset), "s"(base)
+        : "memory", "m0");
+}
+// This wave's loads into LDS have landed and its LDS reads are done, then the
+// workgroup meets: the tile is whole and the other buffer is free.
+__device__ inline void wait_loads_and_meet() {
+    asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+}
+__device__ inline uint32_t lds_address(const void* p) {
+    return (uint32_t)(uintptr_t)(__attribute__((address_space(3))) const char*)p;
+}
 
 // 16 bytes of an operand in its storage order: elements `in` .. +chunk of line
 // `line` (along k: line is a row, in a column; across k the other way round),
