@@ -16,7 +16,7 @@ OUT_DIR = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libmoe.so")
 
 SOURCES = ["moe_host.cpp", "route.hip", "plan.hip", "dequant.hip", "ffn_decode.hip", "ffn_prefill.hip", "probe.hip", "slots.hip", "scratch.hip",
-           "linear.hip", "linear_bf16.hip", "linear_f32.hip", "gated.hip"]
+           "linear.hip", "linear_bf16.hip", "linear_f32.hip", "linear_tiles.hip", "gated.hip"]
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 FLAGS = [

@@ -70,6 +70,7 @@ struct LinearArgs {
     int y_bf16;
 };
 hipError_t launch_linear(const LinearArgs& a, bool gated, hipStream_t s);
+hipError_t launch_linear_tiles(const LinearArgs& a, bool gated, hipStream_t s);
 
 struct GatedArgs {
     const void* x;  // [T, d], rows ldx elements apart

@@ -65,6 +65,7 @@ hipError_t launch_linear_dequant(const QuantGeom& g, const void* data, float* ou
 }
 
 hipError_t launch_linear(const LinearArgs& a, bool gated, hipStream_t s) {
+    if (a.T > 64 && a.x_bf16 && a.y_bf16) return launch_linear_tiles(a, gated, s);
     return a.x_bf16 ? launch_linear_rows_bf16(a, gated, s) : launch_linear_rows_f32(a, gated, s);
 }
 

@@ -1,0 +1,34 @@
+// Many tokens against 4-bit weights: bf16 in, bf16 out, tiles on the matrix cores.
+#include "tile_kernel.h"
+
+namespace moe {
+
+// Each weight s (q - z) is rounded to bf16 here, once, because scaling the sums
+// of exact codes group by group, as the row products do, costs the vector unit
+// more than the matrix cores take for a large tile (two fp32 operations an
+// element and group, in registers a 256 x 256 tile does not have).  The rounding
+// is independent from weight to weight and smaller than that of the result.
+hipError_t launch_linear_tiles(const LinearArgs& a, bool gated, hipStream_t s) {
+    using namespace tile;
+    TileArgs t{};
+    t.a[0] = Operand{a.x, a.ldx, a.T, a.cols, 0};
+    t.b[0] = t.b[1] = Operand{nullptr, 0, a.rows, a.cols, 0};
+    t.M = a.T;
+    t.N = a.rows;
+    t.out[0] = a.y;
+    t.ldo = a.ldy;
+    t.splits = 1;
+    t.q[0] = a.w[0];
+    t.q[1] = a.w[1];
+    t.per_tile = 128 / a.group;
+    t.row_groups = a.row_groups;
+    t.col_tiles = a.col_tiles;
+    if (gated) {
+        if (a.T > 512) return launch_tiles<true, 256, 256, 2, 4, kAlongK, kQuantised, kGatedForward>(t, s);
+        return launch_tiles<true, 128, 128, 2, 2, kAlongK, kQuantised, kGatedForward>(t, s);
+    }
+    if (a.T > 512) return launch_tiles<true, 256, 256, 2, 4, kAlongK, kQuantised, kOneResult>(t, s);
+    return launch_tiles<true, 128, 128, 2, 2, kAlongK, kQuantised, kOneResult>(t, s);
+}
+
+}  // namespace moe

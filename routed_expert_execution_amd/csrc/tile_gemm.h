@@ -17,7 +17,7 @@ typedef short s16x4 __attribute__((ext_vector_type(4)));
 typedef short s16x8 __attribute__((ext_vector_type(8)));
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 
-enum { kAlongK = 0, kAcrossK = 1 };
+enum { kAlongK = 0, kAcrossK = 1, kQuantised = 2 };
 
 template <bool BF16> struct Elem;
 template <> struct Elem<true> { typedef __bf16 type; typedef uint16_t raw; static constexpr int kChunk = 8; };
@@ -35,7 +35,8 @@ struct Operand {
 
 // 16 bytes a lane from base + offset straight into LDS at `lds` + 16 * lane
 // (a wave-uniform LDS address; no register in between).  The compiler does not
-// know of these loads: wait_loads() before the barrier that publishes them.
+// know of these loads: wait_loads_and_meet() before their first use.  (M0 is set
+// here alone: no other instruction of these kernels reads it.)
 __device__ inline void load_lds16(uint32_t lds, uint32_t offset, const void* base) {
     asm volatile(
         "s_mov_b32 m0, %0\n\t"
@@ -43,7 +44,7 @@ __device__ inline void load_lds16(uint32_t lds, uint32_t offset, const void* bas
         "global_load_lds_dwordx4 %1, %2"
         :
         : "s"(lds), "v"(offset), "s"(base)
-        : "memory", "m0");
+        : "memory");
 }
 // This wave's loads into LDS have landed and its LDS reads are done, then the
 // workgroup meets: the tile is whole and the other buffer is free.

@@ -1,0 +1,316 @@
+// The tile kernel behind the dense products with more than a few rows, and its
+// launch: see tile_gemm.h for the operands.
+#pragma once
+
+#include <type_traits>
+
+#include "dense.h"
+#include "tile_gemm.h"
+
+namespace moe {
+namespace tile {
+
+struct TileArgs {
+    Operand a[2], b[2];  // two products: summed over k, side by side in n, or one after the other in z
+    int64_t M, N;        // of one product's result
+    void* out[2];
+    int64_t ldo;
+    void* gate;
+    void* up;
+    float* part;         // [splits][products][M][N] partial sums
+    int splits;
+    int m_tiles, n_tiles;
+    int products;
+    // B in 4 bits (BLAY kQuantised; b holds its sizes): the matrices, scales a
+    // row has in a tile of 128 columns, and the tiles
+    QuantView q[2];
+    int per_tile, row_groups, col_tiles;
+};
+
+enum { kGatedForward, kSumOfTwo, kTwoResults, kOneResult };
+
+
+// Workgroup -> tile.  Workgroups go round the 8 XCDs by index; each XCD gets a
+// consecutive run of tiles, and a run walks kBand tiles of m for one of n after
+// the other, so that the tiles an XCD works on at a time share operand rows in
+// its L2.
+constexpr int kXcds = 8, kBand = 8;
+__device__ inline void tile_of(int id, int m_tiles, int n_tiles, int* m, int* n) {
+    const int total = m_tiles * n_tiles;
+    const int per = total / kXcds, rest = total % kXcds, x = id % kXcds, i = id / kXcds;
+    const int t = x * per + min(x, rest) + i;
+    const int band = t / (kBand * n_tiles), in = t % (kBand * n_tiles);
+    const int rows = min(kBand, m_tiles - band * kBand);
+    *m = band * kBand + in % rows;
+    *n = in / rows;
+}
+
+// WM x WN waves on a BM x BN tile.  kGatedForward: the tile's columns alternate
+// 32 of gate and 32 of up, so that a wave holds both of an element.
+// FAST: whole k steps are loaded straight into LDS, 16 bytes a lane (lines and
+// chunks past the end read the last one; what they make is not stored); the
+// last, partial step and everything else go through registers with zeros past
+// the end.
+// BLAY kQuantised: B is a packed 4-bit matrix.  Its words go to registers two
+// steps ahead and become bf16 in LDS one step ahead, each weight s (q - z)
+// rounded once; a word is 16 bytes of the tile, so 22 vector instructions make
+// 8 weights once for all rows of A in the tile.
+template <bool BF16, int BM, int BN, int WM, int WN, int ALAY, int BLAY, int MODE, bool FAST>
+__global__ __launch_bounds__(WM * WN * 64) void tile_kernel(TileArgs t) {
+    typedef TileOf<BF16, BM, ALAY> TA;
+    constexpr bool kQuant = BLAY == kQuantised;
+    typedef TileOf<BF16, BN, kQuant ? kAlongK : BLAY> TB;
+    constexpr int kThreads = WM * WN * 64;
+    constexpr int FM = BM / WM / 32, FN = BN / WN / 32;
+    constexpr int BK = TA::BK, E = TA::E;
+    constexpr int kStage = TA::kBytes + TB::kBytes;
+    __shared__ __attribute__((aligned(1024))) char lds[2 * kStage];
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int wm = wave / WN * (BM / WM), wn = wave % WN * (BN / WN);
+    int tm, tn;
+    tile_of(blockIdx.x, t.m_tiles, t.n_tiles, &tm, &tn);
+    const int64_t m0 = (int64_t)tm * BM;
+    const int64_t n0 = (int64_t)tn * (MODE == kGatedForward ? BN / 2 : BN);
+    const int which = MODE == kTwoResults ? blockIdx.y & 1 : 0;
+    const int split = MODE == kTwoResults ? blockIdx.y >> 1 : blockIdx.y;
+
+    const int64_t steps1 = (t.a[0].K + BK - 1) / BK;
+    const int64_t steps = MODE == kSumOfTwo ? 2 * steps1 : steps1;
+    const int64_t s0 = steps * split / t.splits, s1 = steps * (split + 1) / t.splits;
+
+    constexpr int CA = TA::kChunks / kThreads, CB = TB::kChunks / kThreads;
+    static_assert(TA::kChunks % kThreads == 0 && TB::kChunks % kThreads == 0, "whole chunks a thread");
+    // Through registers: any alignment, zeros past the end.
+    auto copy_step = [&](int p, int64_t k0, char* l) {
+        const Operand a = t.a[p];
+#pragma unroll
+        for (int i = 0; i < CA; i++) {
+            const int q = threadIdx.x + kThreads * i, line = q / TA::kLineChunks, c = q % TA::kLineChunks;
+            *(u32x4*)(l + TA::chunk_at(line, c)) =
+                ALAY == kAlongK ? load_chunk<BF16>(a.p, a.ld, m0 + line, k0 + c * E, a.R, a.K)
+                                : load_chunk<BF16>(a.p, a.ld, k0 + line, m0 + c * E, a.K, a.R);
+        }
+        if constexpr (!kQuant)
+#pragma unroll
+        for (int i = 0; i < CB; i++) {
+            const int q = threadIdx.x + kThreads * i, line = q / TB::kLineChunks, c = q % TB::kLineChunks;
+            u32x4 v;
+            if (MODE == kGatedForward) {
+                const Operand b = t.b[line >> 5 & 1];
+                v = load_chunk<BF16>(b.p, b.ld, n0 + (line >> 6) * 32 + (line & 31), k0 + c * E, b.R, b.K);
+            } else {
+                const Operand b = t.b[p];
+                v = BLAY == kAlongK ? load_chunk<BF16>(b.p, b.ld, n0 + line, k0 + c * E, b.R, b.K)
+                                    : load_chunk<BF16>(b.p, b.ld, k0 + line, n0 + c * E, b.K, b.R);
+            }
+            *(u32x4*)(l + TA::kBytes + TB::chunk_at(line, c)) = v;
+        }
+    };
+    // Straight into LDS: this thread's byte offsets from the tile's first
+    // element of a step.
+    constexpr int kBytes = 16 / E;
+    uint32_t oa[FAST ? CA : 1], ob[FAST ? CB : 1];
+    if constexpr (FAST) {
+        // the chunk of a line that lands in LDS position c
+        auto source = [&](auto tile, int line, int c) {
+            typedef decltype(tile) TT;
+            return ((TT::chunk_at(line, c) >> 4) - line * TT::kLineChunks);
+        };
+#pragma unroll
+        for (int i = 0; i < CA; i++) {
+            const int q = threadIdx.x + kThreads * i, line = q / TA::kLineChunks;
+            const int c = source(TA{}, line, q % TA::kLineChunks);
+            if (ALAY == kAlongK) oa[i] = (uint32_t)((min(m0 + line, t.M - 1) - m0) * t.a[0].ld + c * E) * kBytes;
+            else oa[i] = (uint32_t)(line * t.a[0].ld + (min(m0 + c * E, (t.M - 1) / E * E) - m0)) * kBytes;
+        }
+        if constexpr (!kQuant)
+#pragma unroll
+        for (int i = 0; i < CB; i++) {
+            const int q = threadIdx.x + kThreads * i, line = q / TB::kLineChunks;
+            const int c = source(TB{}, line, q % TB::kLineChunks);
+            const int row = MODE == kGatedForward ? (line >> 6) * 32 + (line & 31) : line;
+            if (BLAY == kAlongK) ob[i] = (uint32_t)((min(n0 + row, t.N - 1) - n0) * t.b[0].ld + c * E) * kBytes;
+            else ob[i] = (uint32_t)(line * t.b[0].ld + (min(n0 + c * E, (t.N - 1) / E * E) - n0)) * kBytes;
+        }
+    }
+    auto load_step = [&](int64_t s, char* l) {
+        const int p = MODE == kSumOfTwo ? s >= steps1 : which;
+        const int64_t k0 = (MODE == kSumOfTwo && s >= steps1 ? s - steps1 : s) * BK;
+        if (!FAST || k0 + BK > t.a[0].K) {
+            copy_step(p, k0, l);
+            return;
+        }
+        const uint32_t to = lds_address(l) + wave * 1024;
+        const char* a = (const char*)t.a[p].p + (ALAY == kAlongK ? m0 * t.a[0].ld + k0 : k0 * t.a[0].ld + m0) * kBytes;
+#pragma unroll
+        for (int i = 0; i < CA; i++) load_lds16(to + i * kThreads * 16, oa[i], a);
+        if constexpr (!kQuant)
+#pragma unroll
+        for (int i = 0; i < CB; i++) {
+            const int bp = MODE == kGatedForward ? ((wave * 64 + kThreads * i) / TB::kLineChunks) >> 5 & 1 : p;
+            const char* b = (const char*)t.b[bp].p + (BLAY == kAlongK ? n0 * t.b[0].ld + k0 : k0 * t.b[0].ld + n0) * kBytes;
+            load_lds16(to + TA::kBytes + i * kThreads * 16, ob[i], b);
+        }
+    };
+
+    // Packed words of a step: CQ places of (row group, lane), two words each.
+    constexpr int CQ = kQuant ? BN / 16 * 64 / kThreads : 1;
+    static_assert(!kQuant || (BF16 && CQ * kThreads == BN * 4), "whole places a thread");
+    struct Words {
+        uint2 code[CQ];
+        uint16_t scale[CQ][2];
+        uint8_t zero[CQ][2];
+    };
+    auto load_words = [&](int64_t s, Words& w) {
+        const int kt = (int)(s >> 1), half = (int)s & 1;
+#pragma unroll
+        for (int i = 0; i < CQ; i++) {
+            const int r = wave + WM * WN * i;  // row group of the tile
+            const int at = MODE == kGatedForward ? (r >> 2) * 2 + (r & 1) : r;
+            const QuantView v = t.q[MODE == kGatedForward ? r >> 1 & 1 : 0];
+            const int64_t p = (int64_t)min((int)(n0 >> 4) + at, t.row_groups - 1) * t.col_tiles + kt;
+            w.code[i] = ((const uint2*)v.codes)[(p * 64 + lane) * 2 + half];
+#pragma unroll
+            for (int j = 0; j < 2; j++) {
+                const int64_t g = (p * 16 + (lane & 15)) * t.per_tile + ((2 * half + j) * t.per_tile >> 2);
+                w.scale[i][j] = v.scales[g];
+                w.zero[i][j] = v.zeros ? v.zeros[g] : 8;
+            }
+        }
+    };
+    auto store_words = [&](const Words& w, char* l) {
+#pragma unroll
+        for (int i = 0; i < CQ; i++)
+#pragma unroll
+            for (int j = 0; j < 2; j++) {
+                const float sc = f16_bits_to_f32(w.scale[i][j]), off = -sc * (float)w.zero[i][j];
+                const uint32_t word = j ? w.code[i].y : w.code[i].x, lo = word & 0x0F0F0F0Fu, hi = word >> 4 & 0x0F0F0F0Fu;
+                bf16x8 v;
+#pragma unroll
+                for (int e = 0; e < 8; e++) {  // column e: pair e / 2, half e % 2 of the word
+                    const uint32_t b = (e / 2 % 2 ? hi : lo) >> (16 * (e % 2) + 8 * (e / 4));
+                    v[e] = (__bf16)fmaf(sc, (float)(uint8_t)b, off);
+                }
+                *(bf16x8*)(l + TA::kBytes + TB::chunk_at(16 * (wave + WM * WN * i) + (lane & 15), 4 * j + (lane >> 4))) = v;
+            }
+    };
+    Words words;
+
+    f32x16 acc[FM][FN];
+#pragma unroll
+    for (int i = 0; i < FM; i++)
+#pragma unroll
+        for (int j = 0; j < FN; j++)
+#pragma unroll
+            for (int e = 0; e < 16; e++) acc[i][j][e] = 0.f;
+
+    if (s0 < s1) {
+        load_step(s0, lds);
+        if constexpr (kQuant) {
+            load_words(s0, words);
+            store_words(words, lds);
+            if (s0 + 1 < s1) load_words(s0 + 1, words);
+        }
+    }
+    for (int64_t s = s0; s < s1; s++) {
+        const char* cur = lds + ((s - s0) & 1) * kStage;
+        wait_loads_and_meet();
+        char* next = lds + ((s - s0 + 1) & 1) * kStage;
+        if (s + 1 < s1) {
+            load_step(s + 1, next);
+            if constexpr (kQuant) {
+                store_words(words, next);
+                if (s + 2 < s1) load_words(s + 2, words);
+            }
+        }
+        typedef typename std::conditional<BF16, bf16x8, f32x4>::type Frag;
+#pragma unroll
+        for (int kk = 0; kk < 4; kk++) {
+            Frag fa[FM], fb[FN];
+#pragma unroll
+            for (int i = 0; i < FM; i++) TA::frag(cur, wm + 32 * i, kk, lane, fa[i]);
+#pragma unroll
+            for (int j = 0; j < FN; j++) TB::frag(cur + TA::kBytes, wn + 32 * j, kk, lane, fb[j]);
+#pragma unroll
+            for (int i = 0; i < FM; i++)
+#pragma unroll
+                for (int j = 0; j < FN; j++) mma(acc[i][j], fa[i], fb[j]);
+        }
+    }
+    wait_loads_and_meet();
+
+    // Results through a piece of LDS of the wave's own, 32 rows at a time, so
+    // that they leave in rows of 16 bytes a lane.
+    constexpr int kOut = MODE == kGatedForward ? FN * 16 : FN * 32;  // columns of a wave's rows
+    auto store_rows = [&](int i, void* out, int64_t ldo, auto value, auto elem) {
+        typedef decltype(elem) O;
+        constexpr int OE = 16 / sizeof(O), kPitch = kOut * sizeof(O) + 16;
+        char* w = lds + wave * (32 * kPitch);
+        static_assert(WM * WN * 32 * kPitch <= 2 * kStage, "the waves' pieces fit");
+#pragma unroll
+        for (int j = 0; j < kOut / 32; j++)
+#pragma unroll
+            for (int e = 0; e < 16; e++) *(O*)(w + acc_row(lane, e) * kPitch + (32 * j + (lane & 31)) * sizeof(O)) = (O)value(j, e);
+        constexpr int kPerRow = kOut / OE;
+#pragma unroll
+        for (int v = 0; v < 32 * kPerRow / 64; v++) {
+            const int r = (v * 64 + lane) / kPerRow, c = (v * 64 + lane) % kPerRow * OE;
+            const u32x4 d = *(const u32x4*)(w + r * kPitch + c * sizeof(O));
+            const int64_t m = m0 + wm + 32 * i + r, n = n0 + (MODE == kGatedForward ? wn / 2 : wn) + c;
+            if (m >= t.M || n >= t.N) continue;
+            O* o = (O*)out + m * ldo + n;
+            if (n + OE <= t.N) {
+                ((Loose*)o)->v = d;
+            } else {
+                O x[OE];
+                __builtin_memcpy(x, &d, 16);
+#pragma unroll
+                for (int q = 0; q < OE; q++)
+                    if (n + q < t.N) o[q] = x[q];
+            }
+        }
+    };
+    typedef typename Elem<BF16>::type T;
+#pragma unroll
+    for (int i = 0; i < FM; i++) {
+        if constexpr (MODE == kGatedForward) {
+            store_rows(i, t.out[0], t.ldo, [&](int j, int e) { return silu(acc[i][2 * j][e]) * acc[i][2 * j + 1][e]; }, T{});
+            if (t.gate) store_rows(i, t.gate, t.ldo, [&](int j, int e) { return acc[i][2 * j][e]; }, T{});
+            if (t.up) store_rows(i, t.up, t.ldo, [&](int j, int e) { return acc[i][2 * j + 1][e]; }, T{});
+        } else if (t.splits > 1) {
+            float* part = t.part + (int64_t)(split * t.products + which) * t.M * t.N;
+            store_rows(i, part, t.N, [&](int j, int e) { return acc[i][j][e]; }, float{});
+        } else {
+            store_rows(i, t.out[which], t.ldo, [&](int j, int e) { return acc[i][j][e]; }, T{});
+        }
+    }
+}
+
+// Whether whole steps may be loaded 16 bytes a lane: aligned lines, and offsets
+// within a tile's step that 32 bits hold.
+inline bool fast_operand(const Operand& o, int layout, int bf16) {
+    const int e = bf16 ? 8 : 4, bytes = bf16 ? 2 : 4;
+    if ((uintptr_t)o.p % 16 || o.ld % e) return false;
+    if (layout == kAcrossK && o.R % e && !o.padded) return false;
+    return o.ld <= ((int64_t)1 << 31) / 256 / bytes;
+}
+
+template <bool BF16, int BM, int BN, int WM, int WN, int ALAY, int BLAY, int MODE>
+hipError_t launch_tiles(TileArgs t, hipStream_t s) {
+    constexpr int cols = MODE == kGatedForward ? BN / 2 : BN;
+    t.m_tiles = (int)((t.M + BM - 1) / BM);
+    t.n_tiles = (int)((t.N + cols - 1) / cols);
+    t.products = MODE == kTwoResults ? 2 : 1;
+    bool fast = fast_operand(t.a[0], ALAY, BF16);
+    if (BLAY != kQuantised) {
+        fast = fast && fast_operand(t.b[0], BLAY, BF16);
+        if (MODE == kGatedForward || MODE == kSumOfTwo) fast = fast && fast_operand(t.b[1], BLAY, BF16);
+    }
+    const dim3 grid((unsigned)(t.m_tiles * t.n_tiles), t.products * t.splits), block(WM * WN * 64);
+    if (fast) hipLaunchKernelGGL((tile_kernel<BF16, BM, BN, WM, WN, ALAY, BLAY, MODE, true>), grid, block, 0, s, t);
+    else hipLaunchKernelGGL((tile_kernel<BF16, BM, BN, WM, WN, ALAY, BLAY, MODE, false>), grid, block, 0, s, t);
+    return hipGetLastError();
+}
+
+}  // namespace tile
+}  // namespace moe
