@@ -46,10 +46,25 @@ __device__ inline void load_lds16(uint32_t lds, uint32_t offset, const void* bas
         : "s"(lds), "v"(offset), "s"(base)
         : "memory");
 }
-// This wave's loads into LDS have landed and its LDS reads are done, then the
-// workgroup meets: the tile is whole and the other buffer is free.
+// This wave's loads into LDS have landed and its LDS reads are done (s_waitcnt
+// vmcnt(0) lgkmcnt(0)), then the workgroup meets: the tile is whole and the
+// other buffer is free.
 __device__ inline void wait_loads_and_meet() {
-    asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_s_waitcnt(0x0070);
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+}
+// Scheduling of one products step: READS LDS reads spread over its first PRODUCTS matrix instructions.
+template <int READS, int PRODUCTS, int I = 0>
+__device__ inline void spread_reads() {
+    if constexpr (I < PRODUCTS) {
+        constexpr int kPer = (READS + PRODUCTS - 1) / PRODUCTS;
+        constexpr int n = READS - I * kPer < kPer ? READS - I * kPer : kPer;
+        if constexpr (n > 0) __builtin_amdgcn_sched_group_barrier(0x100, n, 0);
+        __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+        spread_reads<READS, PRODUCTS, I + 1>();
+    }
 }
 __device__ inline uint32_t lds_address(const void* p) {
     return (uint32_t)(uintptr_t)(__attribute__((address_space(3))) const char*)p;
@@ -91,6 +106,7 @@ struct TileOf {
         if (BF16) return (line * kLineChunks + (c ^ (line & 3) * (kLineChunks >= 16 ? 4 : 2))) << 4;
         return (line * kLineChunks + c) << 4;
     }
+    static constexpr int kReads = LAY == kAlongK ? 1 : BF16 ? 2 : 4;  // LDS reads of one frag()
     // Operand of one 32-row block at row r0 for k step kk (16 bf16 / 8 fp32 columns).
     __device__ static void frag(const char* lds, int r0, int kk, int lane, bf16x8& f) {
         if (LAY == kAlongK) {
@@ -131,8 +147,16 @@ __device__ inline void mma(f32x16& acc, const f32x4& a, const f32x4& b) {
     for (int i = 0; i < 4; i++) acc = __builtin_amdgcn_mfma_f32_32x32x2f32(a[i], b[i], acc, 0, 0, 0);
 }
 
-// Row of result register i of a 32 x 32 block (its column is lane % 32).
-__device__ inline int acc_row(int lane, int i) { return 8 * (i >> 2) + 4 * (lane >> 5) + (i & 3); }
+// The products are taken with the operands exchanged, so that a lane's result
+// registers run along n: register i of a 32 x 32 block is row lane % 32 and
+// column acc_col(lane, i), four at a time side by side.
+__device__ inline int acc_col(int lane, int i) { return 8 * (i >> 2) + 4 * (lane >> 5) + (i & 3); }
+
+// silu for a result that is rounded to bf16: hardware exp2 and reciprocal, a few
+// fp32 steps of error (at g far below zero |g| of them, where the value vanishes).
+__device__ inline float silu_fast(float g) {
+    return g * __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(-1.44269504f * g));
+}
 
 }  // namespace tile
 }  // namespace moe

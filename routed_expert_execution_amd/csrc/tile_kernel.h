@@ -80,30 +80,49 @@ __global__ __launch_bounds__(WM * WN * 64) void tile_kernel(TileArgs t) {
 
     constexpr int CA = TA::kChunks / kThreads, CB = TB::kChunks / kThreads;
     static_assert(TA::kChunks % kThreads == 0 && TB::kChunks % kThreads == 0, "whole chunks a thread");
-    // Through registers: any alignment, zeros past the end.
-    auto copy_step = [&](int p, int64_t k0, char* l) {
+    // Through registers: any alignment, zeros past the end.  Where every step
+    // comes this way its chunks are loaded together, else (one step of many) one
+    // after the other, which keeps registers for the rest.
+    auto chunk_a = [&](int p, int64_t k0, int i) {
+        const int q = threadIdx.x + kThreads * i, line = q / TA::kLineChunks, c = q % TA::kLineChunks;
         const Operand a = t.a[p];
+        return ALAY == kAlongK ? load_chunk<BF16>(a.p, a.ld, m0 + line, k0 + c * E, a.R, a.K)
+                               : load_chunk<BF16>(a.p, a.ld, k0 + line, m0 + c * E, a.K, a.R);
+    };
+    auto chunk_b = [&](int p, int64_t k0, int i) {
+        const int q = threadIdx.x + kThreads * i, line = q / TB::kLineChunks, c = q % TB::kLineChunks;
+        const Operand b = t.b[MODE == kGatedForward ? line >> 5 & 1 : p];
+        const int row = MODE == kGatedForward ? (line >> 6) * 32 + (line & 31) : line;
+        return BLAY == kAlongK ? load_chunk<BF16>(b.p, b.ld, n0 + row, k0 + c * E, b.R, b.K)
+                               : load_chunk<BF16>(b.p, b.ld, k0 + line, n0 + c * E, b.K, b.R);
+    };
+    auto place_a = [&](char* l, int i, u32x4 v) {
+        const int q = threadIdx.x + kThreads * i;
+        *(u32x4*)(l + TA::chunk_at(q / TA::kLineChunks, q % TA::kLineChunks)) = v;
+    };
+    auto place_b = [&](char* l, int i, u32x4 v) {
+        const int q = threadIdx.x + kThreads * i;
+        *(u32x4*)(l + TA::kBytes + TB::chunk_at(q / TB::kLineChunks, q % TB::kLineChunks)) = v;
+    };
+    auto copy_step = [&](int p, int64_t k0, char* l) {
+        if constexpr (FAST) {
+#pragma unroll 1
+            for (int i = 0; i < CA; i++) place_a(l, i, chunk_a(p, k0, i));
+            if constexpr (!kQuant)
+#pragma unroll 1
+                for (int i = 0; i < CB; i++) place_b(l, i, chunk_b(p, k0, i));
+        } else {
+            u32x4 ra[CA], rb[kQuant ? 1 : CB];
 #pragma unroll
-        for (int i = 0; i < CA; i++) {
-            const int q = threadIdx.x + kThreads * i, line = q / TA::kLineChunks, c = q % TA::kLineChunks;
-            *(u32x4*)(l + TA::chunk_at(line, c)) =
-                ALAY == kAlongK ? load_chunk<BF16>(a.p, a.ld, m0 + line, k0 + c * E, a.R, a.K)
-                                : load_chunk<BF16>(a.p, a.ld, k0 + line, m0 + c * E, a.K, a.R);
-        }
-        if constexpr (!kQuant)
+            for (int i = 0; i < CA; i++) ra[i] = chunk_a(p, k0, i);
+            if constexpr (!kQuant)
 #pragma unroll
-        for (int i = 0; i < CB; i++) {
-            const int q = threadIdx.x + kThreads * i, line = q / TB::kLineChunks, c = q % TB::kLineChunks;
-            u32x4 v;
-            if (MODE == kGatedForward) {
-                const Operand b = t.b[line >> 5 & 1];
-                v = load_chunk<BF16>(b.p, b.ld, n0 + (line >> 6) * 32 + (line & 31), k0 + c * E, b.R, b.K);
-            } else {
-                const Operand b = t.b[p];
-                v = BLAY == kAlongK ? load_chunk<BF16>(b.p, b.ld, n0 + line, k0 + c * E, b.R, b.K)
-                                    : load_chunk<BF16>(b.p, b.ld, k0 + line, n0 + c * E, b.K, b.R);
-            }
-            *(u32x4*)(l + TA::kBytes + TB::chunk_at(line, c)) = v;
+                for (int i = 0; i < CB; i++) rb[i] = chunk_b(p, k0, i);
+#pragma unroll
+            for (int i = 0; i < CA; i++) place_a(l, i, ra[i]);
+            if constexpr (!kQuant)
+#pragma unroll
+                for (int i = 0; i < CB; i++) place_b(l, i, rb[i]);
         }
     };
     // Straight into LDS: this thread's byte offsets from the tile's first
@@ -133,22 +152,24 @@ __global__ __launch_bounds__(WM * WN * 64) void tile_kernel(TileArgs t) {
             else ob[i] = (uint32_t)(line * t.b[0].ld + (min(n0 + c * E, (t.N - 1) / E * E) - n0)) * kBytes;
         }
     }
+    const void *a0 = t.a[0].p, *a1 = t.a[1].p, *b0 = t.b[0].p, *b1 = t.b[1].p;
+    const int64_t lda = t.a[0].ld, ldb = t.b[0].ld, K = t.a[0].K;
     auto load_step = [&](int64_t s, char* l) {
         const int p = MODE == kSumOfTwo ? s >= steps1 : which;
         const int64_t k0 = (MODE == kSumOfTwo && s >= steps1 ? s - steps1 : s) * BK;
-        if (!FAST || k0 + BK > t.a[0].K) {
+        if (!FAST || k0 + BK > K) {
             copy_step(p, k0, l);
             return;
         }
         const uint32_t to = lds_address(l) + wave * 1024;
-        const char* a = (const char*)t.a[p].p + (ALAY == kAlongK ? m0 * t.a[0].ld + k0 : k0 * t.a[0].ld + m0) * kBytes;
+        const char* a = (const char*)(p ? a1 : a0) + (ALAY == kAlongK ? m0 * lda + k0 : k0 * lda + m0) * kBytes;
 #pragma unroll
         for (int i = 0; i < CA; i++) load_lds16(to + i * kThreads * 16, oa[i], a);
         if constexpr (!kQuant)
 #pragma unroll
         for (int i = 0; i < CB; i++) {
             const int bp = MODE == kGatedForward ? ((wave * 64 + kThreads * i) / TB::kLineChunks) >> 5 & 1 : p;
-            const char* b = (const char*)t.b[bp].p + (BLAY == kAlongK ? n0 * t.b[0].ld + k0 : k0 * t.b[0].ld + n0) * kBytes;
+            const char* b = (const char*)(bp ? b1 : b0) + (BLAY == kAlongK ? n0 * ldb + k0 : k0 * ldb + n0) * kBytes;
             load_lds16(to + TA::kBytes + i * kThreads * 16, ob[i], b);
         }
     };
@@ -204,6 +225,25 @@ __global__ __launch_bounds__(WM * WN * 64) void tile_kernel(TileArgs t) {
 #pragma unroll
             for (int e = 0; e < 16; e++) acc[i][j][e] = 0.f;
 
+    // Four products steps of 16 columns (bf16) a k step, operands read one ahead.
+    // The last of them comes after the barrier: by then every operand of the
+    // step is in registers and the next step has landed, so its first operands
+    // are read, and the loads of the step after it start, while these products run.
+    typedef typename std::conditional<BF16, bf16x8, f32x4>::type Frag;
+    Frag fa[2][FM], fb[2][FN];
+    auto read = [&](const char* l, int kk) {
+#pragma unroll
+        for (int j = 0; j < FN; j++) TB::frag(l + TA::kBytes, wn + 32 * j, kk, lane, fb[kk & 1][j]);
+#pragma unroll
+        for (int i = 0; i < FM; i++) TA::frag(l, wm + 32 * i, kk, lane, fa[kk & 1][i]);
+    };
+    auto multiply = [&](int kk) {
+#pragma unroll
+        for (int i = 0; i < FM; i++)
+#pragma unroll
+            for (int j = 0; j < FN; j++) mma(acc[i][j], fb[kk & 1][j], fa[kk & 1][i]);
+    };
+    constexpr int kReads = FM * TA::kReads + FN * TB::kReads, kProducts = FM * FN * (BF16 ? 1 : 4);
     if (s0 < s1) {
         load_step(s0, lds);
         if constexpr (kQuant) {
@@ -211,31 +251,30 @@ __global__ __launch_bounds__(WM * WN * 64) void tile_kernel(TileArgs t) {
             store_words(words, lds);
             if (s0 + 1 < s1) load_words(s0 + 1, words);
         }
+        wait_loads_and_meet();
+        if (s0 + 1 < s1) load_step(s0 + 1, lds + kStage);
+        read(lds, 0);
     }
     for (int64_t s = s0; s < s1; s++) {
-        const char* cur = lds + ((s - s0) & 1) * kStage;
-        wait_loads_and_meet();
+        char* cur = lds + ((s - s0) & 1) * kStage;
         char* next = lds + ((s - s0 + 1) & 1) * kStage;
-        if (s + 1 < s1) {
-            load_step(s + 1, next);
-            if constexpr (kQuant) {
+        if constexpr (kQuant) {
+            if (s + 1 < s1) {
                 store_words(words, next);
                 if (s + 2 < s1) load_words(s + 2, words);
             }
         }
-        typedef typename std::conditional<BF16, bf16x8, f32x4>::type Frag;
 #pragma unroll
-        for (int kk = 0; kk < 4; kk++) {
-            Frag fa[FM], fb[FN];
-#pragma unroll
-            for (int i = 0; i < FM; i++) TA::frag(cur, wm + 32 * i, kk, lane, fa[i]);
-#pragma unroll
-            for (int j = 0; j < FN; j++) TB::frag(cur + TA::kBytes, wn + 32 * j, kk, lane, fb[j]);
-#pragma unroll
-            for (int i = 0; i < FM; i++)
-#pragma unroll
-                for (int j = 0; j < FN; j++) mma(acc[i][j], fa[i], fb[j]);
+        for (int kk = 0; kk < 3; kk++) {
+            read(cur, kk + 1);
+            multiply(kk);
+            spread_reads<kReads, kProducts>();
         }
+        wait_loads_and_meet();
+        if (s + 2 < s1) load_step(s + 2, cur);
+        read(next, 0);  // (after the last step what lies there, not used)
+        multiply(3);
+        spread_reads<kReads, kProducts>();
     }
     wait_loads_and_meet();
 
@@ -250,7 +289,13 @@ __global__ __launch_bounds__(WM * WN * 64) void tile_kernel(TileArgs t) {
 #pragma unroll
         for (int j = 0; j < kOut / 32; j++)
 #pragma unroll
-            for (int e = 0; e < 16; e++) *(O*)(w + acc_row(lane, e) * kPitch + (32 * j + (lane & 31)) * sizeof(O)) = (O)value(j, e);
+            for (int e = 0; e < 16; e += 4) {
+                typedef O O4 __attribute__((ext_vector_type(4)));
+                O4 v;
+#pragma unroll
+                for (int q = 0; q < 4; q++) v[q] = (O)value(j, e + q);
+                *(O4*)(w + (lane & 31) * kPitch + (32 * j + acc_col(lane, e)) * sizeof(O)) = v;
+            }
         constexpr int kPerRow = kOut / OE;
 #pragma unroll
         for (int v = 0; v < 32 * kPerRow / 64; v++) {
@@ -274,7 +319,10 @@ __global__ __launch_bounds__(WM * WN * 64) void tile_kernel(TileArgs t) {
 #pragma unroll
     for (int i = 0; i < FM; i++) {
         if constexpr (MODE == kGatedForward) {
-            store_rows(i, t.out[0], t.ldo, [&](int j, int e) { return silu(acc[i][2 * j][e]) * acc[i][2 * j + 1][e]; }, T{});
+            store_rows(i, t.out[0], t.ldo, [&](int j, int e) {
+                const float g = acc[i][2 * j][e];
+                return (BF16 ? silu_fast(g) : silu(g)) * acc[i][2 * j + 1][e];
+            }, T{});
             if (t.gate) store_rows(i, t.gate, t.ldo, [&](int j, int e) { return acc[i][2 * j][e]; }, T{});
             if (t.up) store_rows(i, t.up, t.ldo, [&](int j, int e) { return acc[i][2 * j + 1][e]; }, T{});
         } else if (t.splits > 1) {
