@@ -13,10 +13,9 @@ namespace {
 
 using namespace tile;
 
-template <bool BF16> __device__ inline float load_elem(const void* p, int64_t i) {
-    if (BF16) return bf16_bits_to_f32(((const uint16_t*)p)[i]);
-    return ((const float*)p)[i];
-}
+// k steps of a tile
+int64_t steps_of(int64_t k, int bf16) { return (k + (bf16 ? 63 : 31)) / (bf16 ? 64 : 32); }
+
 template <bool BF16> __device__ inline void store_elem(void* p, int64_t i, float v) {
     if (BF16) ((__bf16*)p)[i] = (__bf16)v;
     else ((float*)p)[i] = v;
@@ -63,8 +62,134 @@ __global__ __launch_bounds__(256) void gate_backward_kernel(const void* __restri
     }
 }
 
+// ---- few tokens, forward ----------------------------------------------------
+
+// Up to 16 MT tokens: bound by the bytes of the weights, which go from memory
+// straight into the products' B operands, 16 rows of gate and of up a wave, the
+// waves of a workgroup taking every blockDim / 64-th tile of columns and adding
+// their sums in wave order through LDS.  A lane's 16 bytes of a row are columns
+// of one product (bf16) or one column each of four (fp32): the order of the
+// columns within a tile does not matter as long as x uses the same.  Four
+// tokens at most sit in rows 0, 4, 8, 12 of the products (TI = 1), so that one
+// result register holds them.
+template <bool BF16, int MT, int TI>
+__global__ __launch_bounds__(512) void gated_rows_kernel(GatedArgs a) {
+    constexpr int E = Elem<BF16>::kChunk, kCols = 16 * E;  // columns of a tile: 4 chunks for each of 4 lane rows
+    typedef float f32x4 __attribute__((ext_vector_type(4)));
+    extern __shared__ float red[];  // [2][waves][MT * TI][64]
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, waves = blockDim.x >> 6;
+    const int n = lane & 15, q = lane >> 4;
+    const int row0 = blockIdx.x * 16;
+    const int64_t t0 = (int64_t)blockIdx.y * (16 * MT);
+    const int tiles = (a.d + kCols - 1) / kCols;
+    const int64_t row = min(row0 + n, a.F - 1);
+
+    f32x4 acc[2][MT];
+#pragma unroll
+    for (int b = 0; b < 2; b++)
+#pragma unroll
+        for (int m = 0; m < MT; m++) acc[b][m] = f32x4{0.f, 0.f, 0.f, 0.f};
+
+    struct Chunks { u32x4 w[2][4]; };
+    const bool whole = a.d % E == 0;  // no chunk crosses the end of a row
+    auto chunk = [&](const void* p, int64_t ld, int64_t r, int64_t k) {
+        if (whole) {  // past the end: the row's last chunk, taken out below by x = 0 there
+            typedef typename Elem<BF16>::raw raw;
+            return ((const Loose*)((const raw*)p + r * ld + min(k, (int64_t)a.d - E)))->v;
+        }
+        return load_chunk<BF16>(p, ld, r, k, r + 1, a.d);
+    };
+    auto load = [&](int kt, Chunks& c) {
+#pragma unroll
+        for (int j = 0; j < 4; j++) {
+            const int64_t k = (int64_t)kt * kCols + (4 * j + q) * E;
+            c.w[0][j] = chunk(a.w_gate, a.d, row, k);
+            c.w[1][j] = chunk(a.w_up, a.d, row, k);
+        }
+    };
+    Chunks cur, nxt;
+    int kt = wave;
+    if (kt < tiles) load(kt, cur);
+    for (; kt < tiles; kt += waves) {
+        u32x4 x[MT][4];
+#pragma unroll
+        for (int m = 0; m < MT; m++) {
+            const int64_t t = t0 + (TI == 1 ? n / 4 : 16 * m + n);
+#pragma unroll
+            for (int j = 0; j < 4; j++)  // (rows past the last are computed and not stored)
+                x[m][j] = chunk(a.x, a.ldx, t < a.T ? t : a.T - 1, (int64_t)kt * kCols + (4 * j + q) * E);
+        }
+        if (kt + waves < tiles) load(kt + waves, nxt);
+#pragma unroll
+        for (int j = 0; j < 4; j++) {
+            const bool in = (int64_t)kt * kCols + (4 * j + q) * E < a.d;
+#pragma unroll
+            for (int b = 0; b < 2; b++) {
+                u32x4 w = cur.w[b][j];
+#pragma unroll
+                for (int e = 0; e < 4; e++) w[e] = in ? w[e] : 0u;
+#pragma unroll
+                for (int m = 0; m < MT; m++) {
+                    u32x4 v = x[m][j];
+#pragma unroll
+                    for (int e = 0; e < 4; e++) v[e] = in ? v[e] : 0u;
+                    if constexpr (BF16) {
+                        acc[b][m] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, v), __builtin_bit_cast(bf16x8, w),
+                                                                            acc[b][m], 0, 0, 0);
+                    } else {
+#pragma unroll
+                        for (int e = 0; e < 4; e++)
+                            acc[b][m] = __builtin_amdgcn_mfma_f32_16x16x4f32(__uint_as_float(v[e]), __uint_as_float(w[e]), acc[b][m], 0, 0, 0);
+                    }
+                }
+            }
+        }
+        cur = nxt;
+    }
+
+    constexpr int V = MT * TI;
+#pragma unroll
+    for (int b = 0; b < 2; b++)
+#pragma unroll
+        for (int m = 0; m < MT; m++)
+#pragma unroll
+            for (int i = 0; i < TI; i++) red[((b * waves + wave) * V + m * TI + i) * 64 + lane] = acc[b][m][i];
+    __syncthreads();
+    for (int v = threadIdx.x; v < V * 64; v += blockDim.x) {
+        float sum[2];
+#pragma unroll
+        for (int b = 0; b < 2; b++) {
+            sum[b] = red[b * waves * V * 64 + v];
+            for (int w = 1; w < waves; w++) sum[b] += red[(b * waves + w) * V * 64 + v];
+        }
+        const int l = v & 63, mi = v >> 6;
+        const int64_t t = t0 + (TI == 1 ? l >> 4 : 16 * (mi / TI) + 4 * (l >> 4) + mi % TI);
+        const int64_t f = row0 + (l & 15);
+        if (t < a.T && f < a.F) {
+            store_elem<BF16>(a.h, t * a.F + f, silu(sum[0]) * sum[1]);
+            if (a.gate) {
+                store_elem<BF16>(a.gate, t * a.F + f, sum[0]);
+                store_elem<BF16>(a.up, t * a.F + f, sum[1]);
+            }
+        }
+    }
+}
+
+template <bool BF16, int MT, int TI>
+hipError_t launch_gated_rows(const GatedArgs& a, hipStream_t s) {
+    const int tiles = (a.d + 16 * Elem<BF16>::kChunk - 1) / (16 * Elem<BF16>::kChunk);
+    int waves = 1;
+    while (waves < 8 && waves < tiles) waves *= 2;
+    const dim3 grid((a.F + 15) / 16, (unsigned)((a.T + 16 * MT - 1) / (16 * MT)));
+    hipLaunchKernelGGL((gated_rows_kernel<BF16, MT, TI>), grid, dim3(64 * waves), 2 * waves * MT * TI * 64 * sizeof(float), s, a);
+    return hipGetLastError();
+}
+
 template <bool BF16>
 hipError_t gated(const GatedArgs& a, hipStream_t s) {
+    if (a.T <= 4) return launch_gated_rows<BF16, 1, 1>(a, s);
+    if (a.T <= 16) return launch_gated_rows<BF16, 1, 4>(a, s);
+    if (a.T <= 64) return launch_gated_rows<BF16, 4, 4>(a, s);
     TileArgs t{};
     t.a[0] = Operand{a.x, a.ldx, a.T, a.d, 0};
     t.b[0] = Operand{a.w_gate, a.d, a.F, a.d, 0};
@@ -75,33 +200,23 @@ hipError_t gated(const GatedArgs& a, hipStream_t s) {
     t.ldo = a.F;
     t.gate = a.gate;
     t.up = a.up;
-    t.splits = 1;
-    if (a.T > 512) return launch_tiles<BF16, 256, 256, 2, 4, kAlongK, kAlongK, kGatedForward>(t, s);
-    return launch_tiles<BF16, 128, 128, 2, 2, kAlongK, kAlongK, kGatedForward>(t, s);
+    // (gate and up columns alternate: twice F of them)
+    return launch_tiles<BF16, kAlongK, kAlongK, kGatedForward>(t, plan_tiles(a.T, 2 * (int64_t)a.F, 1, steps_of(a.d, a.bf16), false, 1), s);
 }
 
 struct BackwardPlan {
     size_t dg, du, part, total;  // byte offsets in the workspace
     int64_t ld;                  // elements between rows of dg and du: F in whole 16-byte chunks
-    int dx_splits, dw_splits;
+    TilePlan dx, dw;
 };
-constexpr int kBM = 128, kBN = 128;
-int splits_for(int64_t tiles, int64_t steps) {
-    // enough workgroups for two on each of 256 CUs, each with at least 4 steps
-    int64_t n = 1;
-    while (n < 16 && tiles * n * 2 <= 512 && steps / (n * 2) >= 4) n *= 2;
-    return (int)n;
-}
 BackwardPlan backward_plan(int64_t T, int d, int F, int bf16) {
     const size_t e = bf16 ? 2 : 4;
     auto up = [](size_t v) { return (v + 255) / 256 * 256; };
-    auto tiles = [](int64_t m, int64_t n) { return (m + kBM - 1) / kBM * ((n + kBN - 1) / kBN); };
-    const int bk = bf16 ? 64 : 32;
     BackwardPlan p{};
-    p.dx_splits = splits_for(tiles(T, d), 2 * ((F + bk - 1) / bk));
-    p.dw_splits = splits_for(2 * tiles(F, d), (T + bk - 1) / bk);
-    const size_t dx_part = p.dx_splits > 1 ? (size_t)p.dx_splits * T * d * 4 : 0;
-    const size_t dw_part = p.dw_splits > 1 ? (size_t)p.dw_splits * 2 * F * d * 4 : 0;
+    p.dx = plan_tiles(T, d, 1, 2 * steps_of(F, bf16), false, 16);
+    p.dw = plan_tiles(F, d, 2, steps_of(T, bf16), false, 16);
+    const size_t dx_part = p.dx.splits > 1 ? (size_t)p.dx.splits * T * d * 4 : 0;
+    const size_t dw_part = p.dw.splits > 1 ? (size_t)p.dw.splits * 2 * F * d * 4 : 0;
     p.ld = (F + 16 / e - 1) / (16 / e) * (16 / e);
     p.dg = 0;
     p.du = up((size_t)T * p.ld * e);
@@ -133,12 +248,10 @@ hipError_t gated_backward(const GatedBackwardArgs& a, hipStream_t s) {
         t.out[0] = a.dx;
         t.ldo = a.d;
         t.part = part;
-        t.splits = p.dx_splits;
-        if (hipError_t e = a.T > 512 ? launch_tiles<BF16, 128, 256, 2, 4, kAlongK, kAcrossK, kSumOfTwo>(t, s)
-                                     : launch_tiles<BF16, 128, 128, 2, 2, kAlongK, kAcrossK, kSumOfTwo>(t, s)) return e;
-        if (t.splits > 1) {
+        if (hipError_t e = launch_tiles<BF16, kAlongK, kAcrossK, kSumOfTwo>(t, p.dx, s)) return e;
+        if (p.dx.splits > 1) {
             const int64_t n = t.M * t.N;
-            hipLaunchKernelGGL((reduce_kernel<BF16>), dim3((unsigned)((n + 255) / 256)), dim3(256), 0, s, part, t.splits,
+            hipLaunchKernelGGL((reduce_kernel<BF16>), dim3((unsigned)((n + 255) / 256)), dim3(256), 0, s, part, p.dx.splits,
                                (int64_t)1, n, a.dx, nullptr);
             if (hipError_t e = hipGetLastError()) return e;
         }
@@ -154,12 +267,10 @@ hipError_t gated_backward(const GatedBackwardArgs& a, hipStream_t s) {
         t.out[1] = a.dw_up;
         t.ldo = a.d;
         t.part = part;
-        t.splits = p.dw_splits;
-        if (hipError_t e = a.T > 512 ? launch_tiles<BF16, 256, 256, 2, 4, kAcrossK, kAcrossK, kTwoResults>(t, s)
-                                     : launch_tiles<BF16, 128, 128, 2, 2, kAcrossK, kAcrossK, kTwoResults>(t, s)) return e;
-        if (t.splits > 1) {
+        if (hipError_t e = launch_tiles<BF16, kAcrossK, kAcrossK, kTwoResults>(t, p.dw, s)) return e;
+        if (p.dw.splits > 1) {
             const int64_t n = t.M * t.N;
-            hipLaunchKernelGGL((reduce_kernel<BF16>), dim3((unsigned)((2 * n + 255) / 256)), dim3(256), 0, s, part, t.splits,
+            hipLaunchKernelGGL((reduce_kernel<BF16>), dim3((unsigned)((2 * n + 255) / 256)), dim3(256), 0, s, part, p.dw.splits,
                                (int64_t)2, n, a.dw_gate, a.dw_up);
             if (hipError_t e = hipGetLastError()) return e;
         }

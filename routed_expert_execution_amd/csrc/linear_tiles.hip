@@ -17,18 +17,14 @@ hipError_t launch_linear_tiles(const LinearArgs& a, bool gated, hipStream_t s) {
     t.N = a.rows;
     t.out[0] = a.y;
     t.ldo = a.ldy;
-    t.splits = 1;
     t.q[0] = a.w[0];
     t.q[1] = a.w[1];
     t.per_tile = 128 / a.group;
     t.row_groups = a.row_groups;
     t.col_tiles = a.col_tiles;
-    if (gated) {
-        if (a.T > 512) return launch_tiles<true, 256, 256, 2, 4, kAlongK, kQuantised, kGatedForward>(t, s);
-        return launch_tiles<true, 128, 128, 2, 2, kAlongK, kQuantised, kGatedForward>(t, s);
-    }
-    if (a.T > 512) return launch_tiles<true, 256, 256, 2, 4, kAlongK, kQuantised, kOneResult>(t, s);
-    return launch_tiles<true, 128, 128, 2, 2, kAlongK, kQuantised, kOneResult>(t, s);
+    const TilePlan p = plan_tiles(a.T, (int64_t)a.rows * (gated ? 2 : 1), 1, (a.cols + 63) / 64, true, 1);
+    return gated ? launch_tiles<true, kAlongK, kQuantised, kGatedForward>(t, p, s)
+                 : launch_tiles<true, kAlongK, kQuantised, kOneResult>(t, p, s);
 }
 
 }  // namespace moe
