@@ -77,7 +77,7 @@ __global__ __launch_bounds__(512) void gated_rows_kernel(GatedArgs a) {
     constexpr int E = Elem<BF16>::kChunk, kCols = 16 * E;  // columns of a tile: 4 chunks for each of 4 lane rows
     typedef float f32x4 __attribute__((ext_vector_type(4)));
     extern __shared__ float red[];  // [2][waves][MT * TI][64]
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, waves = blockDim.x >> 6;
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), waves = blockDim.x >> 6;
     const int n = lane & 15, q = lane >> 4;
     const int row0 = blockIdx.x * 16;
     const int64_t t0 = (int64_t)blockIdx.y * (16 * MT);

@@ -159,6 +159,14 @@ def _check_dev(ctx: "Context", *tensors):
             raise ValueError(f"tensor must be on cuda:{ctx.device}")
 
 
+import torch  # noqa: E402  (after _load, which orders the two libraries)
+
+_TYPE_CODES = {torch.float32: MOE_F32, torch.bfloat16: MOE_BF16}
+# the current stream's handle without the Stream object around it, where torch offers that
+_current_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
+    (lambda device: torch.cuda.current_stream(device).cuda_stream)
+
+
 def _x_dtype(x) -> int:
     import torch
     if x.dtype == torch.float32:
@@ -539,21 +547,30 @@ def moe_dequant(ctx: Context, payload, out, prec: int = MOE_PREC_F32, stream=Non
 def _stream_on(ctx: Context, stream) -> int | None:
     """As _stream, the default being the current stream of the context's device."""
     if stream is None:
-        import torch
-        return torch.cuda.current_stream(ctx.device).cuda_stream
+        return _current_stream(ctx.device)
     return _stream(stream)
 
 
-def _rows(t, shape, name: str) -> tuple:
-    """(address, elements between rows, type code) of a [rows, columns] tensor
-    whose rows are contiguous and may lie apart."""
-    if t.dim() != 2 or tuple(t.shape) != tuple(shape):
-        raise ValueError(f"{name} must be [{shape[0]}, {shape[1]}]")
-    if t.shape[1] > 1 and t.stride(1) != 1:
-        raise ValueError(f"the rows of {name} must be contiguous")
-    if t.shape[0] > 1 and t.stride(0) < t.shape[1]:
-        raise ValueError(f"the rows of {name} must not overlap")
-    return t.data_ptr(), (t.stride(0) if t.shape[0] > 1 else t.shape[1]), _x_dtype(t)
+def _dense(ctx: Context, t, rows: int, cols: int, name: str, dtype=None, strided: bool = False) -> tuple:
+    """(address, elements between rows, type code) of a float32 or bfloat16
+    [rows, cols] tensor on the context's GPU: contiguous or, if strided, with
+    contiguous rows that may lie apart.  (Few attribute calls: at one token the
+    checks cost as much as the kernel.)"""
+    shape = t.shape
+    if len(shape) != 2 or shape[0] != rows or shape[1] != cols:
+        raise ValueError(f"{name} must be [{rows}, {cols}]")
+    kind = t.dtype
+    code = _TYPE_CODES.get(kind)
+    if code is None or (dtype is not None and kind != dtype):
+        raise ValueError(f"{name} must be {dtype or 'float32 or bfloat16'}")
+    ld, step = t.stride()
+    if rows <= 1:
+        ld = cols
+    if (step != 1 and cols > 1) or (ld != cols if not strided else ld < cols):
+        raise ValueError(f"the rows of {name} must be contiguous" + (" and must not overlap" if strided else " and adjacent"))
+    if ctx.device < 0 or t.get_device() != ctx.device:
+        raise ValueError(f"{name} must be on cuda:{ctx.device}")
+    return t.data_ptr(), ld, code
 
 
 class QuantMatrix:
@@ -579,9 +596,11 @@ class QuantMatrix:
         if n == 0:
             raise ValueError("unsupported matrix: group 32, 64 or 128, at least one row")
         self.rows, self.cols, self.group, self.affine = rows, cols, group, zeros is not None
+        self.device = ctx.device
         self.data = torch.empty(n, dtype=torch.uint8, device=codes.device)
         self.c = moe_qmat(rows, cols, group, int(self.affine), _ptr(self.data))
-        _call(ctx, _lib.moe_linear_pack(ctx.handle, _ptr(codes), _ptr(scales), _ptr(zeros), C.byref(self.c),
+        self.ref = C.byref(self.c)
+        _call(ctx, _lib.moe_linear_pack(ctx.handle, _ptr(codes), _ptr(scales), _ptr(zeros), self.ref,
                                         _stream_on(ctx, stream)))
 
 
@@ -596,47 +615,46 @@ def moe_linear_dequant(ctx: Context, w: QuantMatrix, out, stream=None) -> None:
 def moe_linear(ctx: Context, x, w: QuantMatrix, y, stream=None) -> None:
     """y = x w^T.  x, y: float32 or bfloat16 [T, cols] / [T, rows], rows may lie apart."""
     T = x.shape[0]
-    xp, ldx, xd = _rows(x, (T, w.cols), "x")
-    yp, ldy, yd = _rows(y, (T, w.rows), "y")
-    _check_dev(ctx, x, w.data, y)
-    _call(ctx, _lib.moe_linear(ctx.handle, xp, xd, ldx, T, C.byref(w.c), yp, yd, ldy, _stream_on(ctx, stream)))
+    xp, ldx, xd = _dense(ctx, x, T, w.cols, "x", strided=True)
+    yp, ldy, yd = _dense(ctx, y, T, w.rows, "y", strided=True)
+    _on_device(ctx, w)
+    _call(ctx, _lib.moe_linear(ctx.handle, xp, xd, ldx, T, w.ref, yp, yd, ldy, _stream_on(ctx, stream)))
 
 
 def moe_linear_gated(ctx: Context, x, w_gate: QuantMatrix, w_up: QuantMatrix, h, stream=None) -> None:
     """h = silu(x w_gate^T) * (x w_up^T), x and h as in moe_linear."""
     T = x.shape[0]
-    xp, ldx, xd = _rows(x, (T, w_gate.cols), "x")
-    hp, ldh, hd = _rows(h, (T, w_gate.rows), "h")
-    _check_dev(ctx, x, w_gate.data, w_up.data, h)
-    _call(ctx, _lib.moe_linear_gated(ctx.handle, xp, xd, ldx, T, C.byref(w_gate.c), C.byref(w_up.c), hp, hd, ldh,
+    xp, ldx, xd = _dense(ctx, x, T, w_gate.cols, "x", strided=True)
+    hp, ldh, hd = _dense(ctx, h, T, w_gate.rows, "h", strided=True)
+    _on_device(ctx, w_gate)
+    _on_device(ctx, w_up)
+    _call(ctx, _lib.moe_linear_gated(ctx.handle, xp, xd, ldx, T, w_gate.ref, w_up.ref, hp, hd, ldh,
                                      _stream_on(ctx, stream)))
 
 
-def _same(name: str, t, shape, dtype) -> None:
-    if t is not None and (tuple(t.shape) != tuple(shape) or t.dtype != dtype):
-        raise ValueError(f"{name} must be {dtype} [{shape[0]}, {shape[1]}]")
+def _on_device(ctx: Context, w: QuantMatrix) -> None:
+    if w.device != ctx.device:
+        raise ValueError(f"the matrix must be on cuda:{ctx.device}")
 
 
 def moe_gated(ctx: Context, x, w_gate, w_up, h, gate_out=None, up_out=None, stream=None) -> None:
     """h = silu(g) * u, g = x w_gate^T, u = x w_up^T, all of x's type (float32
-    or bfloat16); gate_out, up_out receive g and u for moe_gated_backward."""
-    if x.dim() != 2 or w_gate.dim() != 2:
-        raise ValueError("x must be [T, d], w_gate [F, d]")
-    T, d, F = x.shape[0], x.shape[1], w_gate.shape[0]
-    xp, ldx, xd = _rows(x, (T, d), "x")
-    _same("w_gate", w_gate, (F, d), x.dtype)
-    _same("w_up", w_up, (F, d), x.dtype)
-    for name, t in (("h", h), ("gate_out", gate_out), ("up_out", up_out)):
-        _same(name, t, (T, F), x.dtype)
-    _check_dev(ctx, x, w_gate, w_up, h, gate_out, up_out)
-    _call(ctx, _lib.moe_gated(ctx.handle, xp, xd, ldx, T, d, F, _ptr(w_gate), _ptr(w_up), _ptr(h), _ptr(gate_out),
-                              _ptr(up_out), _stream_on(ctx, stream)))
+    or bfloat16); gate_out, up_out receive g and u for moe_gated_backward.  The
+    rows of x may lie apart."""
+    T, d = x.shape
+    F, kind = w_gate.shape[0], x.dtype
+    xp, ldx, xd = _dense(ctx, x, T, d, "x", strided=True)
+    wg = _dense(ctx, w_gate, F, d, "w_gate", kind)[0]
+    wu = _dense(ctx, w_up, F, d, "w_up", kind)[0]
+    hp = _dense(ctx, h, T, F, "h", kind)[0]
+    gp = None if gate_out is None else _dense(ctx, gate_out, T, F, "gate_out", kind)[0]
+    up = None if up_out is None else _dense(ctx, up_out, T, F, "up_out", kind)[0]
+    _call(ctx, _lib.moe_gated(ctx.handle, xp, xd, ldx, T, d, F, wg, wu, hp, gp, up, _stream_on(ctx, stream)))
 
 
 def moe_gated_workspace(ctx: Context, T: int, d: int, F: int, dtype) -> int:
     """Bytes of moe_gated_backward's workspace."""
-    import torch
-    n = int(_lib.moe_gated_workspace(T, d, F, {torch.float32: MOE_F32, torch.bfloat16: MOE_BF16}.get(dtype, -1)))
+    n = int(_lib.moe_gated_workspace(T, d, F, _TYPE_CODES.get(dtype, -1)))
     if n == 0:
         raise ValueError("bad sizes or type (float32 or bfloat16)")
     return n
@@ -644,24 +662,24 @@ def moe_gated_workspace(ctx: Context, T: int, d: int, F: int, dtype) -> int:
 
 def moe_gated_backward(ctx: Context, dh, x, w_gate, w_up, gate, up, *, dx=None, dw_gate=None, dw_up=None, workspace,
                        stream=None) -> None:
-    """Gradients of moe_gated from dh and the stored gate and up; dx, or dw_gate
-    and dw_up, may be left out.  workspace: uint8, moe_gated_workspace bytes."""
-    if x.dim() != 2 or w_gate.dim() != 2:
-        raise ValueError("x must be [T, d], w_gate [F, d]")
-    T, d, F = x.shape[0], x.shape[1], w_gate.shape[0]
-    xp, ldx, xd = _rows(x, (T, d), "x")
-    if dh.dtype != x.dtype:
-        raise ValueError("dh must have x's type")
-    dp, lddh, _ = _rows(dh, (T, F), "dh")
-    for name, t in (("w_gate", w_gate), ("w_up", w_up), ("dw_gate", dw_gate), ("dw_up", dw_up)):
-        _same(name, t, (F, d), x.dtype)
-    for name, t in (("gate", gate), ("up", up)):
-        _same(name, t, (T, F), x.dtype)
-    _same("dx", dx, (T, d), x.dtype)
-    _check_dev(ctx, dh, x, w_gate, w_up, gate, up, dx, dw_gate, dw_up, workspace)
-    _call(ctx, _lib.moe_gated_backward(ctx.handle, dp, lddh, xp, xd, ldx, T, d, F, _ptr(w_gate), _ptr(w_up),
-                                       _ptr(gate), _ptr(up), _ptr(dx), _ptr(dw_gate), _ptr(dw_up), _ptr(workspace),
-                                       workspace.numel() * workspace.element_size(), _stream_on(ctx, stream)))
+    """Gradients of moe_gated from dh and the stored gate and up, all of x's
+    type; dx, or dw_gate and dw_up, may be left out.  The rows of x and dh may
+    lie apart.  workspace: uint8, moe_gated_workspace bytes."""
+    T, d = x.shape
+    F, kind = w_gate.shape[0], x.dtype
+    xp, ldx, xd = _dense(ctx, x, T, d, "x", strided=True)
+    dp, lddh, _ = _dense(ctx, dh, T, F, "dh", kind, strided=True)
+    wg = _dense(ctx, w_gate, F, d, "w_gate", kind)[0]
+    wu = _dense(ctx, w_up, F, d, "w_up", kind)[0]
+    gp = _dense(ctx, gate, T, F, "gate", kind)[0]
+    up_ = _dense(ctx, up, T, F, "up", kind)[0]
+    dxp = None if dx is None else _dense(ctx, dx, T, d, "dx", kind)[0]
+    dwg = None if dw_gate is None else _dense(ctx, dw_gate, F, d, "dw_gate", kind)[0]
+    dwu = None if dw_up is None else _dense(ctx, dw_up, F, d, "dw_up", kind)[0]
+    _check_dev(ctx, workspace)
+    _call(ctx, _lib.moe_gated_backward(ctx.handle, dp, lddh, xp, xd, ldx, T, d, F, wg, wu, gp, up_, dxp, dwg, dwu,
+                                       _ptr(workspace), workspace.numel() * workspace.element_size(),
+                                       _stream_on(ctx, stream)))
 
 
 def moe_stats(ctx: Context) -> dict:
