@@ -38,12 +38,16 @@ struct Operand {
 // know of these loads: wait_loads_and_meet() before their first use.  (M0 is set
 // here alone: no other instruction of these kernels reads it.)
 __device__ inline void load_lds16(uint32_t lds, uint32_t offset, const void* base) {
+    const uint64_t b = (uint64_t)base;  // (wave-uniform, which the compiler does not always see)
+    const uint64_t scalar = (uint64_t)__builtin_amdgcn_readfirstlane((uint32_t)(b >> 32)) << 32 |
+                            (uint32_t)__builtin_amdgcn_readfirstlane((uint32_t)b);
+    lds = __builtin_amdgcn_readfirstlane(lds);
     asm volatile(
         "s_mov_b32 m0, %0\n\t"
         "s_nop 0\n\t"
         "global_load_lds_dwordx4 %1, %2"
         :
-        : "s"(lds), "v"(offset), "s"(base)
+        : "s"(lds), "v"(offset), "s"(scalar)
         : "memory");
 }
 // This wave's loads into LDS have landed and its LDS reads are done (s_waitcnt
@@ -88,11 +92,48 @@ __device__ inline u32x4 load_chunk(const void* p, int64_t ld, int64_t line, int6
     return v;
 }
 
+// Operands of one product of 16 columns for 32 rows: lane l holds row l % 32,
+// columns 8 (l / 32) + 0..7, as they come from LDS (Raw) and as the matrix cores
+// take them.  bf16 is taken as it is.  fp32 is taken as three bf16 terms,
+// x = a + b + c to 24 bits, and a product as the six products of terms that are
+// above 2^-25 of it: the bf16 cores do that 2.7 times as fast as the fp32 ones
+// do the product (32x32x16 at 1/32 a clock six times, 32x32x2 at 1/64 eight).
+template <bool BF16> struct Fragment;
+template <> struct Fragment<true> {
+    bf16x8 raw;
+    __device__ void split() {}
+};
+template <> struct Fragment<false> {
+    float raw[8];
+    bf16x8 t[3];
+    __device__ void split() {
+#pragma unroll
+        for (int i = 0; i < 8; i++) {
+            t[0][i] = (__bf16)raw[i];
+            const float r = raw[i] - (float)t[0][i];
+            t[1][i] = (__bf16)r;
+            t[2][i] = (__bf16)(r - (float)t[1][i]);
+        }
+    }
+};
+__device__ inline void mma(f32x16& acc, const Fragment<true>& a, const Fragment<true>& b) {
+    acc = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a.raw, b.raw, acc, 0, 0, 0);
+}
+__device__ inline void mma(f32x16& acc, const Fragment<false>& a, const Fragment<false>& b) {
+    acc = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a.t[2], b.t[0], acc, 0, 0, 0);
+    acc = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a.t[0], b.t[2], acc, 0, 0, 0);
+    acc = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a.t[1], b.t[1], acc, 0, 0, 0);
+    acc = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a.t[1], b.t[0], acc, 0, 0, 0);
+    acc = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a.t[0], b.t[1], acc, 0, 0, 0);
+    acc = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a.t[0], b.t[0], acc, 0, 0, 0);
+}
+
 // Tile of BR rows by BK columns (BK elements fill 128 bytes) in LDS.  Along k:
 // [BR][128 B], 16-byte chunk c of row r at c ^ (r / 2 % 8).  Across k: [BK][BR].
 // bf16 lines are read back through the transposing LDS load: there the four
 // lines of a 16-lane read are spread over the banks by xor of the chunk with
-// 4 (k % 4), fp32 lines are read a word a lane and need none.
+// 4 (k % 4).  fp32 lines are read a word a lane; the two halves of a wave read
+// lines 8 apart, spread by xor with 8 (k / 8 % 2).
 template <bool BF16, int BR, int LAY>
 struct TileOf {
     static constexpr int E = Elem<BF16>::kChunk;
@@ -100,18 +141,18 @@ struct TileOf {
     static constexpr int kBytes = BR * 128;
     static constexpr int kLineChunks = LAY == kAlongK ? 8 : BR / E;  // 16-byte chunks a line
     static constexpr int kChunks = kBytes / 16;
+    static constexpr int kSteps = BK / 16;  // products steps of a tile
+    static constexpr int kReads = (BF16 ? 1 : 2) * (LAY == kAlongK ? 1 : BF16 ? 2 : 4);  // LDS reads of one frag()
 
     __device__ static int chunk_at(int line, int c) {  // LDS byte offset
         if (LAY == kAlongK) return line * 128 + ((c ^ (line >> 1 & 7)) << 4);
         if (BF16) return (line * kLineChunks + (c ^ (line & 3) * (kLineChunks >= 16 ? 4 : 2))) << 4;
-        return (line * kLineChunks + c) << 4;
+        return (line * kLineChunks + (c ^ (line >> 3 & 1) << 3)) << 4;
     }
-    static constexpr int kReads = LAY == kAlongK ? 1 : BF16 ? 2 : 4;  // LDS reads of one frag()
-    // Operand of one 32-row block at row r0 for k step kk (16 bf16 / 8 fp32 columns).
-    __device__ static void frag(const char* lds, int r0, int kk, int lane, bf16x8& f) {
+    // Operand of the 32 rows at r0 for products step kk.
+    __device__ static void frag(const char* lds, int r0, int kk, int lane, Fragment<true>& f) {
         if (LAY == kAlongK) {
-            const int r = r0 + (lane & 31);
-            f = *(const bf16x8*)(lds + chunk_at(r, 2 * kk + (lane >> 5)));
+            f.raw = *(const bf16x8*)(lds + chunk_at(r0 + (lane & 31), 2 * kk + (lane >> 5)));
         } else {
             const int k = 16 * kk + 8 * (lane >> 5) + (lane >> 2 & 3);
             const int col = r0 + 16 * (lane >> 4 & 1) + 4 * (lane & 3);
@@ -124,28 +165,25 @@ struct TileOf {
 #pragma unroll
                 for (int i = 0; i < 4; i++) v[4 * h + i] = t[i];
             }
-            f = __builtin_bit_cast(bf16x8, v);
+            f.raw = __builtin_bit_cast(bf16x8, v);
         }
     }
-    __device__ static void frag(const char* lds, int r0, int kk, int lane, f32x4& f) {
+    __device__ static void frag(const char* lds, int r0, int kk, int lane, Fragment<false>& f) {
+        const int r = r0 + (lane & 31);
         if (LAY == kAlongK) {
-            const int r = r0 + (lane & 31);
-            f = *(const f32x4*)(lds + chunk_at(r, 2 * kk + (lane >> 5)));
+#pragma unroll
+            for (int h = 0; h < 2; h++) {
+                const f32x4 v = *(const f32x4*)(lds + chunk_at(r, 4 * kk + 2 * (lane >> 5) + h));
+#pragma unroll
+                for (int i = 0; i < 4; i++) f.raw[4 * h + i] = v[i];
+            }
         } else {
 #pragma unroll
-            for (int i = 0; i < 4; i++)
-                f[i] = *(const float*)(lds + ((8 * kk + 4 * (lane >> 5) + i) * BR + r0 + (lane & 31)) * 4);
+            for (int i = 0; i < 8; i++)
+                f.raw[i] = *(const float*)(lds + chunk_at(16 * kk + 8 * (lane >> 5) + i, r >> 2) + ((r & 3) << 2));
         }
     }
 };
-
-__device__ inline void mma(f32x16& acc, const bf16x8& a, const bf16x8& b) {
-    acc = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, acc, 0, 0, 0);
-}
-__device__ inline void mma(f32x16& acc, const f32x4& a, const f32x4& b) {
-#pragma unroll
-    for (int i = 0; i < 4; i++) acc = __builtin_amdgcn_mfma_f32_32x32x2f32(a[i], b[i], acc, 0, 0, 0);
-}
 
 // The products are taken with the operands exchanged, so that a lane's result
 // registers run along n: register i of a 32 x 32 block is row lane % 32 and

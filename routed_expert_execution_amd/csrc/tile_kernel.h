@@ -55,8 +55,9 @@ __device__ inline void tile_of(int id, int m_tiles, int n_tiles, int* m, int* n)
 // steps ahead and become bf16 in LDS one step ahead, each weight s (q - z)
 // rounded once; a word is 16 bytes of the tile, so 22 vector instructions make
 // 8 weights once for all rows of A in the tile.
+template <int BM, int BN> constexpr int tile_lds() { return 2 * (BM + BN) * 128; }
 template <bool BF16, int BM, int BN, int WM, int WN, int ALAY, int BLAY, int MODE, bool FAST>
-__global__ __launch_bounds__(WM * WN * 64) void tile_kernel(TileArgs t) {
+__device__ void tile_body(const TileArgs& t, int tile, int part, char* lds) {
     typedef TileOf<BF16, BM, ALAY> TA;
     constexpr bool kQuant = BLAY == kQuantised;
     typedef TileOf<BF16, BN, kQuant ? kAlongK : BLAY> TB;
@@ -64,15 +65,14 @@ __global__ __launch_bounds__(WM * WN * 64) void tile_kernel(TileArgs t) {
     constexpr int FM = BM / WM / 32, FN = BN / WN / 32;
     constexpr int BK = TA::BK, E = TA::E;
     constexpr int kStage = TA::kBytes + TB::kBytes;
-    __shared__ __attribute__((aligned(1024))) char lds[2 * kStage];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int wm = wave / WN * (BM / WM), wn = wave % WN * (BN / WN);
     int tm, tn;
-    tile_of(blockIdx.x, t.m_tiles, t.n_tiles, &tm, &tn);
+    tile_of(tile, t.m_tiles, t.n_tiles, &tm, &tn);
     const int64_t m0 = (int64_t)tm * BM;
     const int64_t n0 = (int64_t)tn * (MODE == kGatedForward ? BN / 2 : BN);
-    const int which = MODE == kTwoResults ? blockIdx.y & 1 : 0;
-    const int split = MODE == kTwoResults ? blockIdx.y >> 1 : blockIdx.y;
+    const int which = MODE == kTwoResults ? part & 1 : 0;
+    const int split = MODE == kTwoResults ? part >> 1 : part;
 
     const int64_t steps1 = (t.a[0].K + BK - 1) / BK;
     const int64_t steps = MODE == kSumOfTwo ? 2 * steps1 : steps1;
@@ -225,25 +225,30 @@ __global__ __launch_bounds__(WM * WN * 64) void tile_kernel(TileArgs t) {
 #pragma unroll
             for (int e = 0; e < 16; e++) acc[i][j][e] = 0.f;
 
-    // Four products steps of 16 columns (bf16) a k step, operands read one ahead.
-    // The last of them comes after the barrier: by then every operand of the
-    // step is in registers and the next step has landed, so its first operands
-    // are read, and the loads of the step after it start, while these products run.
-    typedef typename std::conditional<BF16, bf16x8, f32x4>::type Frag;
-    Frag fa[2][FM], fb[2][FN];
+    // Products steps of 16 columns, operands read one ahead.  The last of a k step
+    // comes after the barrier: by then every operand of the step is in registers
+    // and the next step has landed, so its first operands are read, and the loads
+    // of the step after it start, while these products run.
+    constexpr int kSteps = TA::kSteps;
+    Fragment<BF16> fa[2][FM], fb[2][FN];
     auto read = [&](const char* l, int kk) {
 #pragma unroll
         for (int j = 0; j < FN; j++) TB::frag(l + TA::kBytes, wn + 32 * j, kk, lane, fb[kk & 1][j]);
 #pragma unroll
         for (int i = 0; i < FM; i++) TA::frag(l, wm + 32 * i, kk, lane, fa[kk & 1][i]);
     };
+    constexpr int kReads = FM * TA::kReads + FN * TB::kReads, kProducts = FM * FN * (BF16 ? 1 : 6);
     auto multiply = [&](int kk) {
+#pragma unroll
+        for (int j = 0; j < FN; j++) fb[kk & 1][j].split();
+#pragma unroll
+        for (int i = 0; i < FM; i++) fa[kk & 1][i].split();
 #pragma unroll
         for (int i = 0; i < FM; i++)
 #pragma unroll
             for (int j = 0; j < FN; j++) mma(acc[i][j], fb[kk & 1][j], fa[kk & 1][i]);
+        if constexpr (BF16) spread_reads<kReads, kProducts>();
     };
-    constexpr int kReads = FM * TA::kReads + FN * TB::kReads, kProducts = FM * FN * (BF16 ? 1 : 4);
     if (s0 < s1) {
         load_step(s0, lds);
         if constexpr (kQuant) {
@@ -265,16 +270,14 @@ __global__ __launch_bounds__(WM * WN * 64) void tile_kernel(TileArgs t) {
             }
         }
 #pragma unroll
-        for (int kk = 0; kk < 3; kk++) {
+        for (int kk = 0; kk < kSteps - 1; kk++) {
             read(cur, kk + 1);
             multiply(kk);
-            spread_reads<kReads, kProducts>();
         }
         wait_loads_and_meet();
         if (s + 2 < s1) load_step(s + 2, cur);
         read(next, 0);  // (after the last step what lies there, not used)
-        multiply(3);
-        spread_reads<kReads, kProducts>();
+        multiply(kSteps - 1);
     }
     wait_loads_and_meet();
 
@@ -332,6 +335,12 @@ __global__ __launch_bounds__(WM * WN * 64) void tile_kernel(TileArgs t) {
             store_rows(i, t.out[which], t.ldo, [&](int j, int e) { return acc[i][j][e]; }, T{});
         }
     }
+}
+
+template <bool BF16, int BM, int BN, int WM, int WN, int ALAY, int BLAY, int MODE, bool FAST>
+__global__ __launch_bounds__(WM * WN * 64) void tile_kernel(TileArgs t) {
+    __shared__ __attribute__((aligned(1024))) char lds[tile_lds<BM, BN>()];
+    tile_body<BF16, BM, BN, WM, WN, ALAY, BLAY, MODE, FAST>(t, blockIdx.x, blockIdx.y, lds);
 }
 
 // Whether whole steps may be loaded 16 bytes a lane: aligned lines, and offsets

@@ -10,7 +10,9 @@ documents, element by element, with u = 2^-24 (fp32) and half a step of bf16,
     on the matrix cores, then 2 roundings for scale and zero point, then the
     groups of a wave and the waves: D <= 3 * 128 + cols / 32 + 16.  Their terms
     are (16 + q) x and (16 + z) x, times the scale.
-    The bf16 and fp32 products add all of k in some order: D <= k + 16.
+    The bf16 products add all of k in some order: D <= k + 16.  The fp32 ones are
+    six products of bf16 terms (24 bits of each factor in three terms, what is
+    left out below 2^-25 of the product), all added to one sum: D <= 6 k + 32.
   - h = silu(g) u: |silu'| <= 1.1, and 8 u for the logistic function itself
   - dg and du are rounded to the type before the products: the reference rounds
     its 64-bit values in the same way, and where one lies within 32 u of the
@@ -72,6 +74,10 @@ def _values(q, group):
     z = torch.full_like(scales, 8.0, dtype=torch.float64) if zeros is None else zeros.double()
     z, s = z.repeat_interleave(group, 1), scales.double().repeat_interleave(group, 1)
     return s * (c - z), s.abs() * (32 + c + z)
+
+
+def _chain(k, dtype):
+    return (k + 16 if dtype == torch.bfloat16 else 6 * k + 32) * U
 
 
 def _half_step(ref, dtype):
@@ -256,7 +262,7 @@ def test_gated(ctx, T, d, F, dtype):
         moe.moe_gated(ctx, x, wg, wu, h, gate_out=g_out, up_out=u_out)
         X, G, W = x.double(), wg.double(), wu.double()
         g, u = X @ G.t(), X @ W.t()
-        D = (d + 16) * U
+        D = _chain(d, dt)
         tg, tu = D * (X.abs() @ G.abs().t()), D * (X.abs() @ W.abs().t())
         ref = _silu(g) * u
         _close(h, ref, _gated_tol(g, u, tg, tu, ref, dt), "h")
@@ -287,11 +293,11 @@ def _backward_ref(dh, x, wg, wu, gate, up, dt):
     slack_g = slack_g + (0 if dt == torch.bfloat16 else 32 * U * (dh * u * s).abs() * (1 + g.abs()))
     T, F = dh.shape
     dx = dg @ G + du @ W
-    tx = (2 * F + 16) * U * (dg.abs() @ G.abs() + du.abs() @ W.abs()) + slack_g @ G.abs() + slack_u @ W.abs() + _half_step(dx, dt)
+    tx = _chain(2 * F, dt) * (dg.abs() @ G.abs() + du.abs() @ W.abs()) + slack_g @ G.abs() + slack_u @ W.abs() + _half_step(dx, dt)
     out = [(dx, tx)]
     for v, sl in ((dg, slack_g), (du, slack_u)):
         dw = v.t() @ X
-        out.append((dw, (T + 16) * U * (v.abs().t() @ X.abs()) + sl.t() @ X.abs() + _half_step(dw, dt)))
+        out.append((dw, _chain(T, dt) * (v.abs().t() @ X.abs()) + sl.t() @ X.abs() + _half_step(dw, dt)))
     return [(a, b + 1e-30) for a, b in out]
 
 
