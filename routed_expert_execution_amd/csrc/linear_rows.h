@@ -15,13 +15,14 @@
 // (16 + q against q - z).
 #pragma once
 
+#include "bf16_terms.h"
 #include "dense.h"
 #include "device_util.h"
 
 namespace moe {
 namespace linear {
 
-typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef bf16x8_t bf16x8;
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 
@@ -60,14 +61,10 @@ struct XOperand<false> {
         raw[1] = ((const Loose16f*)(p + 4))->v;
     }
     __device__ void terms(bf16x8 (&t)[3]) const {
+        float v[8];
 #pragma unroll
-        for (int i = 0; i < 8; i++) {
-            const float v = raw[i / 4][i % 4];
-            t[0][i] = (__bf16)v;
-            const float r = v - (float)t[0][i];
-            t[1][i] = (__bf16)r;
-            t[2][i] = (__bf16)(r - (float)t[1][i]);
-        }
+        for (int i = 0; i < 8; i++) v[i] = raw[i / 4][i % 4];
+        bf16_terms(v, t);
     }
 };
 

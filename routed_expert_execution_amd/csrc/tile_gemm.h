@@ -5,12 +5,13 @@
 // operand is read as it lies), bf16 or fp32, any sizes.
 #pragma once
 
+#include "bf16_terms.h"
 #include "device_util.h"
 
 namespace moe {
 namespace tile {
 
-typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef bf16x8_t bf16x8;
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef float f32x16 __attribute__((ext_vector_type(16)));
 typedef short s16x4 __attribute__((ext_vector_type(4)));
@@ -106,15 +107,7 @@ template <> struct Fragment<true> {
 template <> struct Fragment<false> {
     float raw[8];
     bf16x8 t[3];
-    __device__ void split() {
-#pragma unroll
-        for (int i = 0; i < 8; i++) {
-            t[0][i] = (__bf16)raw[i];
-            const float r = raw[i] - (float)t[0][i];
-            t[1][i] = (__bf16)r;
-            t[2][i] = (__bf16)(r - (float)t[1][i]);
-        }
-    }
+    __device__ void split() { bf16_terms(raw, t); }
 };
 __device__ inline void mma(f32x16& acc, const Fragment<true>& a, const Fragment<true>& b) {
     acc = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a.raw, b.raw, acc, 0, 0, 0);
