@@ -201,7 +201,7 @@ hipError_t gated(const GatedArgs& a, hipStream_t s) {
     t.gate = a.gate;
     t.up = a.up;
     // (gate and up columns alternate: twice F of them)
-    return launch_tiles<BF16, kAlongK, kAlongK, kGatedForward>(t, plan_tiles(a.T, 2 * (int64_t)a.F, 1, steps_of(a.d, a.bf16), false, 1), s);
+    return launch_tiles<BF16, kAlongK, kAlongK, kGatedForward>(t, plan_tiles(a.bf16 ? kBf16 : kFp32, a.T, 2 * (int64_t)a.F, 1, steps_of(a.d, a.bf16), 1), s);
 }
 
 struct BackwardPlan {
@@ -213,8 +213,9 @@ BackwardPlan backward_plan(int64_t T, int d, int F, int bf16) {
     const size_t e = bf16 ? 2 : 4;
     auto up = [](size_t v) { return (v + 255) / 256 * 256; };
     BackwardPlan p{};
-    p.dx = plan_tiles(T, d, 1, 2 * steps_of(F, bf16), false, 16);
-    p.dw = plan_tiles(F, d, 2, steps_of(T, bf16), false, 16);
+    const int kind = bf16 ? kBf16 : kFp32;
+    p.dx = plan_tiles(kind, T, d, 1, 2 * steps_of(F, bf16), 16);
+    p.dw = plan_tiles(kind, F, d, 2, steps_of(T, bf16), 16);
     const size_t dx_part = p.dx.splits > 1 ? (size_t)p.dx.splits * T * d * 4 : 0;
     const size_t dw_part = p.dw.splits > 1 ? (size_t)p.dw.splits * 2 * F * d * 4 : 0;
     p.ld = (F + 16 / e - 1) / (16 / e) * (16 / e);

@@ -22,7 +22,7 @@ hipError_t launch_linear_tiles(const LinearArgs& a, bool gated, hipStream_t s) {
     t.per_tile = 128 / a.group;
     t.row_groups = a.row_groups;
     t.col_tiles = a.col_tiles;
-    const TilePlan p = plan_tiles(a.T, (int64_t)a.rows * (gated ? 2 : 1), 1, (a.cols + 63) / 64, true, 1);
+    const TilePlan p = plan_tiles(kQuant4, a.T, (int64_t)a.rows * (gated ? 2 : 1), 1, (a.cols + 63) / 64, 1);
     return gated ? launch_tiles<true, kAlongK, kQuantised, kGatedForward>(t, p, s)
                  : launch_tiles<true, kAlongK, kQuantised, kOneResult>(t, p, s);
 }

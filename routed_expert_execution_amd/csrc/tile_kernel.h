@@ -371,29 +371,34 @@ hipError_t launch_shape(TileArgs t, hipStream_t s) {
 // Tile shape and number of parts of k for a product of M x N with `steps` k
 // steps, by estimated time: rounds of workgroups over the CUs, times the steps
 // of a part, times the measured time of a step (us, all CUs busy):
-//                 bf16    4-bit B
-//   256 x 256     1.7     1.95    one workgroup a CU
-//   256 x 128     1.2     1.32    one
-//   128 x 128     1.2     1.6     for the two a CU holds; 0.65, 1.06 where there is one
-// Parts write and read partial sums in fp32 (4 MB a us) and cost a launch more (4 us).
+//                 bf16    4-bit B    fp32
+//   256 x 256     1.7     1.95       -      one workgroup a CU (fp32: spills, 5.1)
+//   256 x 128     1.2     1.32       3.3    one
+//   128 x 128     1.2     1.6        3.2    for the two a CU holds; 0.65, 1.06, 1.5
+//                                           where there is one
+// Parts write and read partial sums in fp32 (4 MB a us) and cost a launch more
+// (4 us).
 struct TilePlan { int shape, splits; };
 enum { kShape256, kShape256x128, kShape128 };
-inline TilePlan plan_tiles(int64_t M, int64_t N, int products, int64_t steps, bool quantised, int64_t most_splits) {
-    static const struct { int bm, bn, per_cu; float one, full; } shapes[2][3] = {
+enum { kBf16, kQuant4, kFp32 };
+inline TilePlan plan_tiles(int kind, int64_t M, int64_t N, int products, int64_t steps, int64_t most_splits) {
+    static const struct { int bm, bn, per_cu; float one, full; } shapes[3][3] = {
         {{256, 256, 1, 1.7f, 1.7f}, {256, 128, 1, 1.2f, 1.2f}, {128, 128, 2, 0.65f, 1.2f}},
-        {{256, 256, 1, 1.95f, 1.95f}, {256, 128, 1, 1.32f, 1.32f}, {128, 128, 2, 1.06f, 1.6f}}};
+        {{256, 256, 1, 1.95f, 1.95f}, {256, 128, 1, 1.32f, 1.32f}, {128, 128, 2, 1.06f, 1.6f}},
+        {{256, 256, 0, 0.f, 0.f}, {256, 128, 1, 3.3f, 3.3f}, {128, 128, 2, 1.5f, 3.2f}}};
     constexpr int kCus = 256;
     TilePlan best{kShape128, 1};
-    float best_us = 0.f;
+    float best_us = 1e30f;
     for (int h = 0; h < 3; h++) {
-        const auto& c = shapes[quantised][h];
+        const auto& c = shapes[kind][h];
+        if (!c.per_cu) continue;
         const int64_t tiles = (M + c.bm - 1) / c.bm * ((N + c.bn - 1) / c.bn) * products;
         for (int64_t n = 1; n <= most_splits && (n == 1 || steps / n >= 2); n *= 2) {
             const int64_t wgs = tiles * n, part = (steps + n - 1) / n;
             const int64_t rounds = (wgs + kCus * c.per_cu - 1) / (kCus * c.per_cu);
             float us = (float)part * (wgs <= kCus ? c.one : (float)rounds * c.full);
             if (n > 1) us += 4.f + (float)M * (float)N * products * (float)(8 * n + 4) / 4e6f;
-            if ((h == 0 && n == 1) || us < best_us) {
+            if (us < best_us) {
                 best = TilePlan{h, (int)n};
                 best_us = us;
             }
@@ -407,7 +412,9 @@ hipError_t launch_tiles(TileArgs t, const TilePlan& p, hipStream_t s) {
     t.products = MODE == kTwoResults ? 2 : 1;
     t.splits = p.splits;
     switch (p.shape) {
-        case kShape256: return launch_shape<BF16, 256, 256, 2, 4, ALAY, BLAY, MODE>(t, s);
+        case kShape256:
+            if constexpr (BF16) return launch_shape<BF16, 256, 256, 2, 4, ALAY, BLAY, MODE>(t, s);
+            else return hipErrorInvalidValue;
         case kShape256x128: return launch_shape<BF16, 256, 128, 4, 2, ALAY, BLAY, MODE>(t, s);
         default: return launch_shape<BF16, 128, 128, 2, 2, ALAY, BLAY, MODE>(t, s);
     }
