@@ -21,16 +21,42 @@ template <bool BF16> __device__ inline void store_elem(void* p, int64_t i, float
     else ((float*)p)[i] = v;
 }
 
-// Partial sums added in split order.
+// Both products of the backward pass in one launch: the workgroups of dx first
+// (a whole number of rounds over the XCDs of them, as tile_of counts from zero),
+// then those of dWg and dWu, which fill the CUs that dx leaves.
+struct BackwardCounts { int dx_groups, dx_tiles, dw_tiles; };  // dx's workgroups, rounded up; tiles of one part of each
+template <bool BF16, int BM, int BN, int WM, int WN, bool FAST>
+__global__ __launch_bounds__(WM * WN * 64) void backward_tiles_kernel(TileArgs dx, TileArgs dw, BackwardCounts b) {
+    __shared__ __attribute__((aligned(1024))) char lds[tile_lds<BM, BN>()];
+    const int id = blockIdx.x;
+    if (id < b.dx_groups) {
+        if (id < b.dx_tiles * dx.splits)
+            tile_body<BF16, BM, BN, WM, WN, kAlongK, kAcrossK, kSumOfTwo, FAST>(dx, id % b.dx_tiles, id / b.dx_tiles, lds);
+    } else {
+        const int i = id - b.dx_groups;
+        tile_body<BF16, BM, BN, WM, WN, kAcrossK, kAcrossK, kTwoResults, FAST>(dw, i % b.dw_tiles, i / b.dw_tiles, lds);
+    }
+}
+
+// Partial sums added in split order: of dx, then of dWg and dWu.
+struct ReduceArgs {
+    const float* part[2];
+    int splits[2];
+    int64_t each[2];    // elements of one part: T d, 2 F d; 0 where nothing is to be added
+    void* out[3];       // dx, dWg, dWu
+};
 template <bool BF16>
-__global__ __launch_bounds__(256) void reduce_kernel(const float* __restrict__ part, int splits, int64_t products,
-                                                     int64_t n, void* out0, void* out1) {
-    const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
-    if (i >= products * n) return;
-    float s = part[i];
-    for (int k = 1; k < splits; k++) s += part[(int64_t)k * products * n + i];
-    if (i < n) store_elem<BF16>(out0, i, s);
-    else store_elem<BF16>(out1, i - n, s);
+__global__ __launch_bounds__(256) void reduce_kernel(ReduceArgs r) {
+    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < r.each[0] + r.each[1]; i += (int64_t)gridDim.x * 256) {
+        const int w = i >= r.each[0];
+        const int64_t k = w ? i - r.each[0] : i;
+        const float* p = r.part[w] + k;
+        float s = *p;
+        for (int n = 1; n < r.splits[w]; n++) s += p[n * r.each[w]];
+        if (!w) store_elem<BF16>(r.out[0], k, s);
+        else if (k < r.each[1] / 2) store_elem<BF16>(r.out[1], k, s);
+        else store_elem<BF16>(r.out[2], k - r.each[1] / 2, s);
+    }
 }
 
 // dg and du into rows of whole 16-byte chunks (ld >= F), a chunk a thread.  In
@@ -191,39 +217,82 @@ hipError_t gated(const GatedArgs& a, hipStream_t s) {
     if (a.T <= 16) return launch_gated_rows<BF16, 1, 4>(a, s);
     if (a.T <= 64) return launch_gated_rows<BF16, 4, 4>(a, s);
     TileArgs t{};
-    t.a[0] = Operand{a.x, a.ldx, a.T, a.d, 0};
-    t.b[0] = Operand{a.w_gate, a.d, a.F, a.d, 0};
-    t.b[1] = Operand{a.w_up, a.d, a.F, a.d, 0};
+    t.a = Operand{{a.x, nullptr}, a.ldx, 0};
+    t.b = Operand{{a.w_gate, a.w_up}, a.d, 0};
     t.M = a.T;
     t.N = a.F;
+    t.K = a.d;
     t.out[0] = a.h;
     t.ldo = a.F;
     t.gate = a.gate;
     t.up = a.up;
     // (gate and up columns alternate: twice F of them)
-    return launch_tiles<BF16, kAlongK, kAlongK, kGatedForward>(t, plan_tiles(a.bf16 ? kBf16 : kFp32, a.T, 2 * (int64_t)a.F, 1, steps_of(a.d, a.bf16), 1), s);
+    return launch_tiles<BF16, kAlongK, kAlongK, kGatedForward>(t, plan_tiles(a.bf16 ? kBf16 : kFp32, a.T, 2 * (int64_t)a.F, steps_of(a.d, a.bf16)), s);
 }
 
 struct BackwardPlan {
-    size_t dg, du, part, total;  // byte offsets in the workspace
-    int64_t ld;                  // elements between rows of dg and du: F in whole 16-byte chunks
-    TilePlan dx, dw;
+    size_t dg, du, dx_part, dw_part, total;  // byte offsets in the workspace
+    int64_t ld;                              // elements between rows of dg and du: F in whole 16-byte chunks
+    int shape, dx_splits, dw_splits;
 };
+// One tile shape for both products (one launch) and a number of parts for each,
+// by the estimate of plan_tiles; here the CUs share the steps of both, and no
+// part may outlast them.
 BackwardPlan backward_plan(int64_t T, int d, int F, int bf16) {
+    BackwardPlan p{};
+    const int64_t dx_steps = 2 * steps_of(F, bf16), dw_steps = steps_of(T, bf16);
+    float best = 1e30f;
+    for (int h = 0; h < 3; h++) {
+        const TileShape& c = kTileShapes[bf16 ? kBf16 : kFp32][h];
+        if (!c.per_cu) continue;
+        auto tiles = [&](int64_t m, int64_t n) { return (m + c.bm - 1) / c.bm * ((n + c.bn - 1) / c.bn); };
+        const int64_t dx_tiles = tiles(T, d), dw_tiles = 2 * tiles(F, d);
+        for (int64_t n = 1; n <= 16 && (n == 1 || dx_steps / n >= 2); n *= 2)
+            for (int64_t m = 1; m <= 16 && (m == 1 || dw_steps / m >= 2); m *= 2) {
+                const int64_t a = (dx_steps + n - 1) / n, b = (dw_steps + m - 1) / m, most = std::max(a, b);
+                const int64_t groups = dx_tiles * n + dw_tiles * m, cap = kTileCus * c.per_cu;
+                float us;
+                if (groups <= kTileCus) us = (float)most * c.one;
+                else us = std::max((float)(dx_tiles * n * a + dw_tiles * m * b) / cap + 0.25f * std::min(a, b), (float)most) * c.full;
+                if (n > 1 || m > 1) us += 4.f;
+                if (n > 1) us += (float)T * d * (float)(8 * n + 4) / 4e6f;
+                if (m > 1) us += 2.f * F * d * (float)(8 * m + 4) / 4e6f;
+                if (us < best) {
+                    best = us;
+                    p.shape = h;
+                    p.dx_splits = (int)n;
+                    p.dw_splits = (int)m;
+                }
+            }
+    }
     const size_t e = bf16 ? 2 : 4;
     auto up = [](size_t v) { return (v + 255) / 256 * 256; };
-    BackwardPlan p{};
-    const int kind = bf16 ? kBf16 : kFp32;
-    p.dx = plan_tiles(kind, T, d, 1, 2 * steps_of(F, bf16), 16);
-    p.dw = plan_tiles(kind, F, d, 2, steps_of(T, bf16), 16);
-    const size_t dx_part = p.dx.splits > 1 ? (size_t)p.dx.splits * T * d * 4 : 0;
-    const size_t dw_part = p.dw.splits > 1 ? (size_t)p.dw.splits * 2 * F * d * 4 : 0;
     p.ld = (F + 16 / e - 1) / (16 / e) * (16 / e);
     p.dg = 0;
     p.du = up((size_t)T * p.ld * e);
-    p.part = 2 * p.du;
-    p.total = p.part + up(std::max(dx_part, dw_part));
+    p.dx_part = 2 * p.du;
+    p.dw_part = p.dx_part + (p.dx_splits > 1 ? up((size_t)p.dx_splits * T * d * 4) : 0);
+    p.total = p.dw_part + (p.dw_splits > 1 ? up((size_t)p.dw_splits * 2 * F * d * 4) : 0);
     return p;
+}
+
+template <bool BF16, int BM, int BN, int WM, int WN>
+hipError_t launch_backward_tiles(TileArgs x, TileArgs w, bool dx, bool dw, hipStream_t s) {
+    auto tiles = [](TileArgs& t) {
+        t.m_tiles = (int)((t.M + BM - 1) / BM);
+        t.n_tiles = (int)((t.N + BN - 1) / BN);
+        return t.m_tiles * t.n_tiles;
+    };
+    BackwardCounts b{0, tiles(x), tiles(w)};
+    x.products = 1;
+    w.products = 2;
+    if (dx) b.dx_groups = (b.dx_tiles * x.splits + kXcds - 1) / kXcds * kXcds;
+    const bool fast = (!dx || (fast_operand(x.a, kAlongK, x.M, true, BF16) && fast_operand(x.b, kAcrossK, x.N, true, BF16))) &&
+                      (!dw || (fast_operand(w.a, kAcrossK, w.M, true, BF16) && fast_operand(w.b, kAcrossK, w.N, false, BF16)));
+    const dim3 grid((unsigned)(b.dx_groups + (dw ? 2 * b.dw_tiles * w.splits : 0))), block(WM * WN * 64);
+    if (fast) hipLaunchKernelGGL((backward_tiles_kernel<BF16, BM, BN, WM, WN, true>), grid, block, 0, s, x, w, b);
+    else hipLaunchKernelGGL((backward_tiles_kernel<BF16, BM, BN, WM, WN, false>), grid, block, 0, s, x, w, b);
+    return hipGetLastError();
 }
 
 template <bool BF16>
@@ -231,50 +300,45 @@ hipError_t gated_backward(const GatedBackwardArgs& a, hipStream_t s) {
     const BackwardPlan p = backward_plan(a.T, a.d, a.F, a.bf16);
     char* ws = (char*)a.workspace;
     void *dg = ws + p.dg, *du = ws + p.du;
-    float* part = (float*)(ws + p.part);
+    const bool dx = a.dx && a.T > 0, dw = a.dw_gate != nullptr;
+    if (!dx && !dw) return hipSuccess;
     if (a.T > 0) {
         const int64_t chunks = a.T * (p.ld / Elem<BF16>::kChunk);
         hipLaunchKernelGGL((gate_backward_kernel<BF16>), dim3((unsigned)std::min<int64_t>((chunks + 255) / 256, 1 << 20)),
                            dim3(256), 0, s, a.dh, a.lddh, a.gate, a.up, a.T, a.F, p.ld, dg, du);
         if (hipError_t e = hipGetLastError()) return e;
     }
-    if (a.dx && a.T > 0) {
-        TileArgs t{};
-        t.a[0] = Operand{dg, p.ld, a.T, a.F, 1};
-        t.a[1] = Operand{du, p.ld, a.T, a.F, 1};
-        t.b[0] = Operand{a.w_gate, a.d, a.d, a.F, 0};
-        t.b[1] = Operand{a.w_up, a.d, a.d, a.F, 0};
-        t.M = a.T;
-        t.N = a.d;
-        t.out[0] = a.dx;
-        t.ldo = a.d;
-        t.part = part;
-        if (hipError_t e = launch_tiles<BF16, kAlongK, kAcrossK, kSumOfTwo>(t, p.dx, s)) return e;
-        if (p.dx.splits > 1) {
-            const int64_t n = t.M * t.N;
-            hipLaunchKernelGGL((reduce_kernel<BF16>), dim3((unsigned)((n + 255) / 256)), dim3(256), 0, s, part, p.dx.splits,
-                               (int64_t)1, n, a.dx, nullptr);
-            if (hipError_t e = hipGetLastError()) return e;
-        }
-    }
-    if (a.dw_gate) {
-        TileArgs t{};
-        t.a[0] = Operand{dg, p.ld, a.F, a.T, 1};
-        t.a[1] = Operand{du, p.ld, a.F, a.T, 1};
-        t.b[0] = t.b[1] = Operand{a.x, a.ldx, a.d, a.T, 0};
-        t.M = a.F;
-        t.N = a.d;
-        t.out[0] = a.dw_gate;
-        t.out[1] = a.dw_up;
-        t.ldo = a.d;
-        t.part = part;
-        if (hipError_t e = launch_tiles<BF16, kAcrossK, kAcrossK, kTwoResults>(t, p.dw, s)) return e;
-        if (p.dw.splits > 1) {
-            const int64_t n = t.M * t.N;
-            hipLaunchKernelGGL((reduce_kernel<BF16>), dim3((unsigned)((2 * n + 255) / 256)), dim3(256), 0, s, part, p.dw.splits,
-                               (int64_t)2, n, a.dw_gate, a.dw_up);
-            if (hipError_t e = hipGetLastError()) return e;
-        }
+    TileArgs x{}, w{};
+    x.a = Operand{{dg, du}, p.ld, 1};
+    x.b = Operand{{a.w_gate, a.w_up}, a.d, 0};
+    x.M = a.T;
+    x.N = a.d;
+    x.K = a.F;
+    x.out[0] = a.dx;
+    x.ldo = a.d;
+    x.part = (float*)(ws + p.dx_part);
+    x.splits = p.dx_splits;
+    w.a = Operand{{dg, du}, p.ld, 1};
+    w.b = Operand{{a.x, a.x}, a.ldx, 0};
+    w.M = a.F;
+    w.N = a.d;
+    w.K = a.T;
+    w.out[0] = a.dw_gate;
+    w.out[1] = a.dw_up;
+    w.ldo = a.d;
+    w.part = (float*)(ws + p.dw_part);
+    w.splits = p.dw_splits;
+    hipError_t e = hipErrorInvalidValue;
+    if (p.shape == kShape256x128) e = launch_backward_tiles<BF16, 256, 128, 4, 2>(x, w, dx, dw, s);
+    else if (p.shape == kShape128) e = launch_backward_tiles<BF16, 128, 128, 2, 2>(x, w, dx, dw, s);
+    else if constexpr (BF16) e = launch_backward_tiles<BF16, 256, 256, 2, 4>(x, w, dx, dw, s);
+    if (e) return e;
+    ReduceArgs r{{x.part, w.part}, {p.dx_splits, p.dw_splits},
+                 {dx && p.dx_splits > 1 ? a.T * a.d : 0, dw && p.dw_splits > 1 ? (int64_t)2 * a.F * a.d : 0},
+                 {a.dx, a.dw_gate, a.dw_up}};
+    if (const int64_t n = r.each[0] + r.each[1]) {
+        hipLaunchKernelGGL((reduce_kernel<BF16>), dim3((unsigned)std::min<int64_t>((n + 255) / 256, 1 << 20)), dim3(256), 0, s, r);
+        return hipGetLastError();
     }
     return hipSuccess;
 }

@@ -11,10 +11,10 @@ namespace moe {
 hipError_t launch_linear_tiles(const LinearArgs& a, bool gated, hipStream_t s) {
     using namespace tile;
     TileArgs t{};
-    t.a[0] = Operand{a.x, a.ldx, a.T, a.cols, 0};
-    t.b[0] = t.b[1] = Operand{nullptr, 0, a.rows, a.cols, 0};
+    t.a = Operand{{a.x, nullptr}, a.ldx, 0};
     t.M = a.T;
     t.N = a.rows;
+    t.K = a.cols;
     t.out[0] = a.y;
     t.ldo = a.ldy;
     t.q[0] = a.w[0];
@@ -22,9 +22,9 @@ hipError_t launch_linear_tiles(const LinearArgs& a, bool gated, hipStream_t s) {
     t.per_tile = 128 / a.group;
     t.row_groups = a.row_groups;
     t.col_tiles = a.col_tiles;
-    const TilePlan p = plan_tiles(kQuant4, a.T, (int64_t)a.rows * (gated ? 2 : 1), 1, (a.cols + 63) / 64, 1);
-    return gated ? launch_tiles<true, kAlongK, kQuantised, kGatedForward>(t, p, s)
-                 : launch_tiles<true, kAlongK, kQuantised, kOneResult>(t, p, s);
+    const int shape = plan_tiles(kQuant4, a.T, (int64_t)a.rows * (gated ? 2 : 1), (a.cols + 63) / 64);
+    return gated ? launch_tiles<true, kAlongK, kQuantised, kGatedForward>(t, shape, s)
+                 : launch_tiles<true, kAlongK, kQuantised, kOneResult>(t, shape, s);
 }
 
 }  // namespace moe

@@ -26,29 +26,32 @@ template <> struct Elem<false> { typedef float type; typedef uint32_t raw; stati
 
 struct __attribute__((packed, aligned(2))) Loose { u32x4 v; };
 
-// One operand: R rows, K columns.
+// An operand of one or two products.
 struct Operand {
-    const void* p;
+    const void* p[2];
     int64_t ld;
-    int64_t R, K;
-    int padded;  // its lines are whole 16-byte chunks in memory, whatever R is
+    int padded;  // its lines are whole 16-byte chunks in memory, whatever their length
 };
 
-// 16 bytes a lane from base + offset straight into LDS at `lds` + 16 * lane
-// (a wave-uniform LDS address; no register in between).  The compiler does not
-// know of these loads: wait_loads_and_meet() before their first use.  (M0 is set
-// here alone: no other instruction of these kernels reads it.)
+// A wave-uniform pointer in scalar registers, where the compiler does not see
+// that it is one.
+__device__ inline const void* uniform(const void* p) {
+    const uint64_t b = (uint64_t)p;
+    return (const void*)((uint64_t)__builtin_amdgcn_readfirstlane((uint32_t)(b >> 32)) << 32 |
+                         (uint32_t)__builtin_amdgcn_readfirstlane((uint32_t)b));
+}
+
+// 16 bytes a lane from base + offset straight into LDS at `lds` + 16 * lane (lds
+// and base wave-uniform; no register in between).  The compiler does not know of
+// these loads: wait_loads_and_meet() before their first use.  (M0 is set here
+// alone: no other instruction of these kernels reads it.)
 __device__ inline void load_lds16(uint32_t lds, uint32_t offset, const void* base) {
-    const uint64_t b = (uint64_t)base;  // (wave-uniform, which the compiler does not always see)
-    const uint64_t scalar = (uint64_t)__builtin_amdgcn_readfirstlane((uint32_t)(b >> 32)) << 32 |
-                            (uint32_t)__builtin_amdgcn_readfirstlane((uint32_t)b);
-    lds = __builtin_amdgcn_readfirstlane(lds);
     asm volatile(
         "s_mov_b32 m0, %0\n\t"
         "s_nop 0\n\t"
         "global_load_lds_dwordx4 %1, %2"
         :
-        : "s"(lds), "v"(offset), "s"(scalar)
+        : "s"(__builtin_amdgcn_readfirstlane(lds)), "v"(offset), "s"(uniform(base))
         : "memory");
 }
 // This wave's loads into LDS have landed and its LDS reads are done (s_waitcnt

@@ -11,8 +11,9 @@ namespace moe {
 namespace tile {
 
 struct TileArgs {
-    Operand a[2], b[2];  // two products: summed over k, side by side in n, or one after the other in z
-    int64_t M, N;        // of one product's result
+    // two products: summed over k, side by side in n (b alone has two), or two results
+    Operand a, b;
+    int64_t M, N, K;     // of one product
     void* out[2];
     int64_t ldo;
     void* gate;
@@ -21,7 +22,7 @@ struct TileArgs {
     int splits;
     int m_tiles, n_tiles;
     int products;
-    // B in 4 bits (BLAY kQuantised; b holds its sizes): the matrices, scales a
+    // B in 4 bits (BLAY kQuantised): the matrices, scales a
     // row has in a tile of 128 columns, and the tiles
     QuantView q[2];
     int per_tile, row_groups, col_tiles;
@@ -45,6 +46,9 @@ __device__ inline void tile_of(int id, int m_tiles, int n_tiles, int* m, int* n)
     *n = in / rows;
 }
 
+// (A lambda left as a call would need the arguments it refers to in memory.)
+#define TILE_INLINE __attribute__((always_inline))
+
 // WM x WN waves on a BM x BN tile.  kGatedForward: the tile's columns alternate
 // 32 of gate and 32 of up, so that a wave holds both of an element.
 // FAST: whole k steps are loaded straight into LDS, 16 bytes a lane (lines and
@@ -57,7 +61,7 @@ __device__ inline void tile_of(int id, int m_tiles, int n_tiles, int* m, int* n)
 // 8 weights once for all rows of A in the tile.
 template <int BM, int BN> constexpr int tile_lds() { return 2 * (BM + BN) * 128; }
 template <bool BF16, int BM, int BN, int WM, int WN, int ALAY, int BLAY, int MODE, bool FAST>
-__device__ void tile_body(const TileArgs& t, int tile, int part, char* lds) {
+__device__ TILE_INLINE void tile_body(const TileArgs& t, int tile, int part, char* lds) {
     typedef TileOf<BF16, BM, ALAY> TA;
     constexpr bool kQuant = BLAY == kQuantised;
     typedef TileOf<BF16, BN, kQuant ? kAlongK : BLAY> TB;
@@ -74,7 +78,12 @@ __device__ void tile_body(const TileArgs& t, int tile, int part, char* lds) {
     const int which = MODE == kTwoResults ? part & 1 : 0;
     const int split = MODE == kTwoResults ? part >> 1 : part;
 
-    const int64_t steps1 = (t.a[0].K + BK - 1) / BK;
+    // (the second matrix as a distance: a choice between two of the arguments would
+    // be made in memory, on a copy of them all)
+    const char *a0 = (const char*)uniform(t.a.p[0]), *b0 = (const char*)uniform(t.b.p[0]);
+    const int64_t a_next = (const char*)uniform(t.a.p[1]) - a0, b_next = (const char*)uniform(t.b.p[1]) - b0;
+    const int64_t lda = t.a.ld, ldb = t.b.ld;
+    const int64_t steps1 = (t.K + BK - 1) / BK;
     const int64_t steps = MODE == kSumOfTwo ? 2 * steps1 : steps1;
     const int64_t s0 = steps * split / t.splits, s1 = steps * (split + 1) / t.splits;
 
@@ -83,28 +92,28 @@ __device__ void tile_body(const TileArgs& t, int tile, int part, char* lds) {
     // Through registers: any alignment, zeros past the end.  Where every step
     // comes this way its chunks are loaded together, else (one step of many) one
     // after the other, which keeps registers for the rest.
-    auto chunk_a = [&](int p, int64_t k0, int i) {
+    auto chunk_a = [&](int p, int64_t k0, int i) TILE_INLINE {
         const int q = threadIdx.x + kThreads * i, line = q / TA::kLineChunks, c = q % TA::kLineChunks;
-        const Operand a = t.a[p];
-        return ALAY == kAlongK ? load_chunk<BF16>(a.p, a.ld, m0 + line, k0 + c * E, a.R, a.K)
-                               : load_chunk<BF16>(a.p, a.ld, k0 + line, m0 + c * E, a.K, a.R);
+        const void* a = a0 + (p ? a_next : 0);
+        return ALAY == kAlongK ? load_chunk<BF16>(a, lda, m0 + line, k0 + c * E, t.M, t.K)
+                               : load_chunk<BF16>(a, lda, k0 + line, m0 + c * E, t.K, t.M);
     };
-    auto chunk_b = [&](int p, int64_t k0, int i) {
+    auto chunk_b = [&](int p, int64_t k0, int i) TILE_INLINE {
         const int q = threadIdx.x + kThreads * i, line = q / TB::kLineChunks, c = q % TB::kLineChunks;
-        const Operand b = t.b[MODE == kGatedForward ? line >> 5 & 1 : p];
+        const void* b = b0 + ((MODE == kGatedForward ? line >> 5 & 1 : p) ? b_next : 0);
         const int row = MODE == kGatedForward ? (line >> 6) * 32 + (line & 31) : line;
-        return BLAY == kAlongK ? load_chunk<BF16>(b.p, b.ld, n0 + row, k0 + c * E, b.R, b.K)
-                               : load_chunk<BF16>(b.p, b.ld, k0 + line, n0 + c * E, b.K, b.R);
+        return BLAY == kAlongK ? load_chunk<BF16>(b, ldb, n0 + row, k0 + c * E, t.N, t.K)
+                               : load_chunk<BF16>(b, ldb, k0 + line, n0 + c * E, t.K, t.N);
     };
-    auto place_a = [&](char* l, int i, u32x4 v) {
+    auto place_a = [&](char* l, int i, u32x4 v) TILE_INLINE {
         const int q = threadIdx.x + kThreads * i;
         *(u32x4*)(l + TA::chunk_at(q / TA::kLineChunks, q % TA::kLineChunks)) = v;
     };
-    auto place_b = [&](char* l, int i, u32x4 v) {
+    auto place_b = [&](char* l, int i, u32x4 v) TILE_INLINE {
         const int q = threadIdx.x + kThreads * i;
         *(u32x4*)(l + TA::kBytes + TB::chunk_at(q / TB::kLineChunks, q % TB::kLineChunks)) = v;
     };
-    auto copy_step = [&](int p, int64_t k0, char* l) {
+    auto copy_step = [&](int p, int64_t k0, char* l) TILE_INLINE {
         if constexpr (FAST) {
 #pragma unroll 1
             for (int i = 0; i < CA; i++) place_a(l, i, chunk_a(p, k0, i));
@@ -131,7 +140,7 @@ __device__ void tile_body(const TileArgs& t, int tile, int part, char* lds) {
     uint32_t oa[FAST ? CA : 1], ob[FAST ? CB : 1];
     if constexpr (FAST) {
         // the chunk of a line that lands in LDS position c
-        auto source = [&](auto tile, int line, int c) {
+        auto source = [&](auto tile, int line, int c) TILE_INLINE {
             typedef decltype(tile) TT;
             return ((TT::chunk_at(line, c) >> 4) - line * TT::kLineChunks);
         };
@@ -139,8 +148,8 @@ __device__ void tile_body(const TileArgs& t, int tile, int part, char* lds) {
         for (int i = 0; i < CA; i++) {
             const int q = threadIdx.x + kThreads * i, line = q / TA::kLineChunks;
             const int c = source(TA{}, line, q % TA::kLineChunks);
-            if (ALAY == kAlongK) oa[i] = (uint32_t)((min(m0 + line, t.M - 1) - m0) * t.a[0].ld + c * E) * kBytes;
-            else oa[i] = (uint32_t)(line * t.a[0].ld + (min(m0 + c * E, (t.M - 1) / E * E) - m0)) * kBytes;
+            if (ALAY == kAlongK) oa[i] = (uint32_t)((min(m0 + line, t.M - 1) - m0) * lda + c * E) * kBytes;
+            else oa[i] = (uint32_t)(line * lda + (min(m0 + c * E, (t.M - 1) / E * E) - m0)) * kBytes;
         }
         if constexpr (!kQuant)
 #pragma unroll
@@ -148,28 +157,26 @@ __device__ void tile_body(const TileArgs& t, int tile, int part, char* lds) {
             const int q = threadIdx.x + kThreads * i, line = q / TB::kLineChunks;
             const int c = source(TB{}, line, q % TB::kLineChunks);
             const int row = MODE == kGatedForward ? (line >> 6) * 32 + (line & 31) : line;
-            if (BLAY == kAlongK) ob[i] = (uint32_t)((min(n0 + row, t.N - 1) - n0) * t.b[0].ld + c * E) * kBytes;
-            else ob[i] = (uint32_t)(line * t.b[0].ld + (min(n0 + c * E, (t.N - 1) / E * E) - n0)) * kBytes;
+            if (BLAY == kAlongK) ob[i] = (uint32_t)((min(n0 + row, t.N - 1) - n0) * ldb + c * E) * kBytes;
+            else ob[i] = (uint32_t)(line * ldb + (min(n0 + c * E, (t.N - 1) / E * E) - n0)) * kBytes;
         }
     }
-    const void *a0 = t.a[0].p, *a1 = t.a[1].p, *b0 = t.b[0].p, *b1 = t.b[1].p;
-    const int64_t lda = t.a[0].ld, ldb = t.b[0].ld, K = t.a[0].K;
-    auto load_step = [&](int64_t s, char* l) {
+    auto load_step = [&](int64_t s, char* l) TILE_INLINE {
         const int p = MODE == kSumOfTwo ? s >= steps1 : which;
         const int64_t k0 = (MODE == kSumOfTwo && s >= steps1 ? s - steps1 : s) * BK;
-        if (!FAST || k0 + BK > K) {
+        if (!FAST || k0 + BK > t.K) {
             copy_step(p, k0, l);
             return;
         }
         const uint32_t to = lds_address(l) + wave * 1024;
-        const char* a = (const char*)(p ? a1 : a0) + (ALAY == kAlongK ? m0 * lda + k0 : k0 * lda + m0) * kBytes;
+        const char* a = a0 + (p ? a_next : 0) + (ALAY == kAlongK ? m0 * lda + k0 : k0 * lda + m0) * kBytes;
 #pragma unroll
         for (int i = 0; i < CA; i++) load_lds16(to + i * kThreads * 16, oa[i], a);
         if constexpr (!kQuant)
 #pragma unroll
         for (int i = 0; i < CB; i++) {
             const int bp = MODE == kGatedForward ? ((wave * 64 + kThreads * i) / TB::kLineChunks) >> 5 & 1 : p;
-            const char* b = (const char*)(bp ? b1 : b0) + (BLAY == kAlongK ? n0 * ldb + k0 : k0 * ldb + n0) * kBytes;
+            const char* b = b0 + (bp ? b_next : 0) + (BLAY == kAlongK ? n0 * ldb + k0 : k0 * ldb + n0) * kBytes;
             load_lds16(to + TA::kBytes + i * kThreads * 16, ob[i], b);
         }
     };
@@ -182,7 +189,7 @@ __device__ void tile_body(const TileArgs& t, int tile, int part, char* lds) {
         uint16_t scale[CQ][2];
         uint8_t zero[CQ][2];
     };
-    auto load_words = [&](int64_t s, Words& w) {
+    auto load_words = [&](int64_t s, Words& w) TILE_INLINE {
         const int kt = (int)(s >> 1), half = (int)s & 1;
 #pragma unroll
         for (int i = 0; i < CQ; i++) {
@@ -199,7 +206,7 @@ __device__ void tile_body(const TileArgs& t, int tile, int part, char* lds) {
             }
         }
     };
-    auto store_words = [&](const Words& w, char* l) {
+    auto store_words = [&](const Words& w, char* l) TILE_INLINE {
 #pragma unroll
         for (int i = 0; i < CQ; i++)
 #pragma unroll
@@ -231,14 +238,14 @@ __device__ void tile_body(const TileArgs& t, int tile, int part, char* lds) {
     // of the step after it start, while these products run.
     constexpr int kSteps = TA::kSteps;
     Fragment<BF16> fa[2][FM], fb[2][FN];
-    auto read = [&](const char* l, int kk) {
+    auto read = [&](const char* l, int kk) TILE_INLINE {
 #pragma unroll
         for (int j = 0; j < FN; j++) TB::frag(l + TA::kBytes, wn + 32 * j, kk, lane, fb[kk & 1][j]);
 #pragma unroll
         for (int i = 0; i < FM; i++) TA::frag(l, wm + 32 * i, kk, lane, fa[kk & 1][i]);
     };
     constexpr int kReads = FM * TA::kReads + FN * TB::kReads, kProducts = FM * FN * (BF16 ? 1 : 6);
-    auto multiply = [&](int kk) {
+    auto multiply = [&](int kk) TILE_INLINE {
 #pragma unroll
         for (int j = 0; j < FN; j++) fb[kk & 1][j].split();
 #pragma unroll
@@ -284,7 +291,7 @@ __device__ void tile_body(const TileArgs& t, int tile, int part, char* lds) {
     // Results through a piece of LDS of the wave's own, 32 rows at a time, so
     // that they leave in rows of 16 bytes a lane.
     constexpr int kOut = MODE == kGatedForward ? FN * 16 : FN * 32;  // columns of a wave's rows
-    auto store_rows = [&](int i, void* out, int64_t ldo, auto value, auto elem) {
+    auto store_rows = [&](int i, void* out, int64_t ldo, auto value, auto elem) TILE_INLINE {
         typedef decltype(elem) O;
         constexpr int OE = 16 / sizeof(O), kPitch = kOut * sizeof(O) + 16;
         char* w = lds + wave * (32 * kPitch);
@@ -319,6 +326,8 @@ __device__ void tile_body(const TileArgs& t, int tile, int part, char* lds) {
         }
     };
     typedef typename Elem<BF16>::type T;
+    char* out = (char*)uniform(t.out[0]);
+    if (which) out += (char*)uniform(t.out[1]) - out;
 #pragma unroll
     for (int i = 0; i < FM; i++) {
         if constexpr (MODE == kGatedForward) {
@@ -332,7 +341,7 @@ __device__ void tile_body(const TileArgs& t, int tile, int part, char* lds) {
             float* part = t.part + (int64_t)(split * t.products + which) * t.M * t.N;
             store_rows(i, part, t.N, [&](int j, int e) { return acc[i][j][e]; }, float{});
         } else {
-            store_rows(i, t.out[which], t.ldo, [&](int j, int e) { return acc[i][j][e]; }, T{});
+            store_rows(i, out, t.ldo, [&](int j, int e) { return acc[i][j][e]; }, T{});
         }
     }
 }
@@ -340,15 +349,16 @@ __device__ void tile_body(const TileArgs& t, int tile, int part, char* lds) {
 template <bool BF16, int BM, int BN, int WM, int WN, int ALAY, int BLAY, int MODE, bool FAST>
 __global__ __launch_bounds__(WM * WN * 64) void tile_kernel(TileArgs t) {
     __shared__ __attribute__((aligned(1024))) char lds[tile_lds<BM, BN>()];
-    tile_body<BF16, BM, BN, WM, WN, ALAY, BLAY, MODE, FAST>(t, blockIdx.x, blockIdx.y, lds);
+    tile_body<BF16, BM, BN, WM, WN, ALAY, BLAY, MODE, FAST>(t, blockIdx.x, 0, lds);
 }
 
 // Whether whole steps may be loaded 16 bytes a lane: aligned lines, and offsets
 // within a tile's step that 32 bits hold.
-inline bool fast_operand(const Operand& o, int layout, int bf16) {
+// `length`: of its lines across k (kAcrossK).
+inline bool fast_operand(const Operand& o, int layout, int64_t length, bool two, int bf16) {
     const int e = bf16 ? 8 : 4, bytes = bf16 ? 2 : 4;
-    if ((uintptr_t)o.p % 16 || o.ld % e) return false;
-    if (layout == kAcrossK && o.R % e && !o.padded) return false;
+    if ((uintptr_t)o.p[0] % 16 || (two && (uintptr_t)o.p[1] % 16) || o.ld % e) return false;
+    if (layout == kAcrossK && length % e && !o.padded) return false;
     return o.ld <= ((int64_t)1 << 31) / 256 / bytes;
 }
 
@@ -357,61 +367,53 @@ hipError_t launch_shape(TileArgs t, hipStream_t s) {
     constexpr int cols = MODE == kGatedForward ? BN / 2 : BN;
     t.m_tiles = (int)((t.M + BM - 1) / BM);
     t.n_tiles = (int)((t.N + cols - 1) / cols);
-    bool fast = fast_operand(t.a[0], ALAY, BF16);
-    if (BLAY != kQuantised) {
-        fast = fast && fast_operand(t.b[0], BLAY, BF16);
-        if (MODE == kGatedForward || MODE == kSumOfTwo) fast = fast && fast_operand(t.b[1], BLAY, BF16);
-    }
-    const dim3 grid((unsigned)(t.m_tiles * t.n_tiles), t.products * t.splits), block(WM * WN * 64);
+    const bool fast = fast_operand(t.a, ALAY, t.M, false, BF16) &&
+                      (BLAY == kQuantised || fast_operand(t.b, BLAY, t.N, MODE == kGatedForward, BF16));
+    const dim3 grid((unsigned)(t.m_tiles * t.n_tiles)), block(WM * WN * 64);
     if (fast) hipLaunchKernelGGL((tile_kernel<BF16, BM, BN, WM, WN, ALAY, BLAY, MODE, true>), grid, block, 0, s, t);
     else hipLaunchKernelGGL((tile_kernel<BF16, BM, BN, WM, WN, ALAY, BLAY, MODE, false>), grid, block, 0, s, t);
     return hipGetLastError();
 }
 
-// Tile shape and number of parts of k for a product of M x N with `steps` k
-// steps, by estimated time: rounds of workgroups over the CUs, times the steps
-// of a part, times the measured time of a step (us, all CUs busy):
+// Tile shape for a product of M x N with `steps` k steps, by estimated time:
+// rounds of workgroups over the CUs, times the steps, times the measured time of
+// a step (us, all CUs busy):
 //                 bf16    4-bit B    fp32
 //   256 x 256     1.7     1.95       -      one workgroup a CU (fp32: spills, 5.1)
 //   256 x 128     1.2     1.32       3.3    one
 //   128 x 128     1.2     1.6        3.2    for the two a CU holds; 0.65, 1.06, 1.5
 //                                           where there is one
-// Parts write and read partial sums in fp32 (4 MB a us) and cost a launch more
-// (4 us).
-struct TilePlan { int shape, splits; };
+// (The backward pass also splits k into parts: they write and read partial sums
+// in fp32, 4 MB a us, and cost a launch more, 4 us.)
 enum { kShape256, kShape256x128, kShape128 };
 enum { kBf16, kQuant4, kFp32 };
-inline TilePlan plan_tiles(int kind, int64_t M, int64_t N, int products, int64_t steps, int64_t most_splits) {
-    static const struct { int bm, bn, per_cu; float one, full; } shapes[3][3] = {
-        {{256, 256, 1, 1.7f, 1.7f}, {256, 128, 1, 1.2f, 1.2f}, {128, 128, 2, 0.65f, 1.2f}},
-        {{256, 256, 1, 1.95f, 1.95f}, {256, 128, 1, 1.32f, 1.32f}, {128, 128, 2, 1.06f, 1.6f}},
-        {{256, 256, 0, 0.f, 0.f}, {256, 128, 1, 3.3f, 3.3f}, {128, 128, 2, 1.5f, 3.2f}}};
-    constexpr int kCus = 256;
-    TilePlan best{kShape128, 1};
+struct TileShape { int bm, bn, per_cu; float one, full; };
+constexpr int kTileCus = 256;
+static const TileShape kTileShapes[3][3] = {
+    {{256, 256, 1, 1.7f, 1.7f}, {256, 128, 1, 1.2f, 1.2f}, {128, 128, 2, 0.65f, 1.2f}},
+    {{256, 256, 1, 1.95f, 1.95f}, {256, 128, 1, 1.32f, 1.32f}, {128, 128, 2, 1.06f, 1.6f}},
+    {{256, 256, 0, 0.f, 0.f}, {256, 128, 1, 3.3f, 3.3f}, {128, 128, 2, 1.5f, 3.2f}}};
+inline int plan_tiles(int kind, int64_t M, int64_t N, int64_t steps) {
+    int best = kShape128;
     float best_us = 1e30f;
     for (int h = 0; h < 3; h++) {
-        const auto& c = shapes[kind][h];
+        const TileShape& c = kTileShapes[kind][h];
         if (!c.per_cu) continue;
-        const int64_t tiles = (M + c.bm - 1) / c.bm * ((N + c.bn - 1) / c.bn) * products;
-        for (int64_t n = 1; n <= most_splits && (n == 1 || steps / n >= 2); n *= 2) {
-            const int64_t wgs = tiles * n, part = (steps + n - 1) / n;
-            const int64_t rounds = (wgs + kCus * c.per_cu - 1) / (kCus * c.per_cu);
-            float us = (float)part * (wgs <= kCus ? c.one : (float)rounds * c.full);
-            if (n > 1) us += 4.f + (float)M * (float)N * products * (float)(8 * n + 4) / 4e6f;
-            if (us < best_us) {
-                best = TilePlan{h, (int)n};
-                best_us = us;
-            }
+        const int64_t groups = (M + c.bm - 1) / c.bm * ((N + c.bn - 1) / c.bn);
+        const int64_t rounds = (groups + kTileCus * c.per_cu - 1) / (kTileCus * c.per_cu);
+        const float us = (float)steps * (groups <= kTileCus ? c.one : (float)rounds * c.full);
+        if (us < best_us) {
+            best = h;
+            best_us = us;
         }
     }
     return best;
 }
 
 template <bool BF16, int ALAY, int BLAY, int MODE>
-hipError_t launch_tiles(TileArgs t, const TilePlan& p, hipStream_t s) {
-    t.products = MODE == kTwoResults ? 2 : 1;
-    t.splits = p.splits;
-    switch (p.shape) {
+hipError_t launch_tiles(TileArgs t, int shape, hipStream_t s) {
+    t.products = t.splits = 1;
+    switch (shape) {
         case kShape256:
             if constexpr (BF16) return launch_shape<BF16, 256, 256, 2, 4, ALAY, BLAY, MODE>(t, s);
             else return hipErrorInvalidValue;
