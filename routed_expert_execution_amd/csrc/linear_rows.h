@@ -2,17 +2,18 @@
 //
 //   y[t, n] = sum_g s[n, g] * sum_{k in g} (q[n, k] - z[n, g]) x[t, k]
 //
-// Bound by the bytes of the weights, so a weight has to cost few instructions:
-// its code goes into the top mantissa bits of a bf16 whose exponent is that of
-// 16, which makes the pair of codes in a word two bf16 16 + q in a shift and
+// Bound by the bytes of the weights, so a weight has to cost few instructions.
+// bf16 x: a code goes into the top mantissa bits of a bf16 whose exponent is that
+// of 16, which makes the pair of codes in a word two bf16 16 + q in a shift and
 // one and-or, and the matrix cores sum (16 + q) x over a group exactly as they
 // would sum the weights.  The group's sum of x alone, one more product with a
 // matrix of ones shared by every row, turns that into the sum of (q - z) x in
-// fp32:   s * (sum (16 + q) x - (16 + z) sum x).   Nothing is rounded to bf16:
-// codes and bf16 x are exact in the products, fp32 x enters as three bf16 terms
-// (x = a + b + c to 24 bits) with a product each, and scales, zero points and
-// sums stay in fp32.  The subtraction costs about two bits of the sum's 24
-// (16 + q against q - z).
+// fp32:   s * (sum (16 + q) x - (16 + z) sum x).
+// fp32 x enters as three bf16 terms (x = a + b + c to 24 bits) with a product
+// each, and there the sums of 16 + q would cost two of the 24 bits: the codes are
+// made q - z, exact in bf16, at three times the instructions, which the terms
+// outweigh.  Nothing is rounded to bf16: codes and terms are exact in the
+// products, and scales and sums stay in fp32.
 #pragma once
 
 #include "bf16_terms.h"
@@ -39,6 +40,16 @@ __device__ inline bf16x8 codes_bf16(uint32_t w) {
     r[2] = ((w >> 5) & mask) | one;
     r[3] = ((w >> 9) & mask) | one;
     return __builtin_bit_cast(bf16x8, r);
+}
+
+// A word's 8 codes as bf16 q - z (integers of 8 bits at most), columns in order.
+__device__ inline bf16x8 codes_less_zero(uint32_t w, float z) {
+    const uint32_t lo = w & 0x0F0F0F0Fu, hi = w >> 4 & 0x0F0F0F0Fu;
+    bf16x8 v;
+#pragma unroll
+    for (int e = 0; e < 8; e++)  // column e: pair e / 2, half e % 2 of the word
+        v[e] = (__bf16)((float)(uint8_t)((e / 2 % 2 ? hi : lo) >> (16 * (e % 2) + 8 * (e / 4))) - z);
+    return v;
 }
 
 // The A operands of one 32-column step: 8 columns of this lane's token.
@@ -124,12 +135,13 @@ __global__ __launch_bounds__(512) void rows_kernel(LinearArgs a) {
             }
             bf16x8 xt[kTerms];
             cur.x[j].terms(xt);
-#pragma unroll
-            for (int c = kTerms - 1; c >= 0; c--) xs = __builtin_amdgcn_mfma_f32_16x16x32_bf16(xt[c], ones, xs, 0, 0, 0);
+            if constexpr (XBF16) xs = __builtin_amdgcn_mfma_f32_16x16x32_bf16(xt[0], ones, xs, 0, 0, 0);
 #pragma unroll
             for (int r = 0; r < RB; r++) {
                 const uint4 c4 = cur.code[r];
-                const bf16x8 w = codes_bf16(j == 0 ? c4.x : j == 1 ? c4.y : j == 2 ? c4.z : c4.w);
+                const uint32_t word = j == 0 ? c4.x : j == 1 ? c4.y : j == 2 ? c4.z : c4.w;
+                const float z = a.w[r / R].zeros ? (float)cur.zero[r][j / (4 / S)] : 8.f;
+                const bf16x8 w = XBF16 ? codes_bf16(word) : codes_less_zero(word, z);
 #pragma unroll
                 for (int c = kTerms - 1; c >= 0; c--) acc[r] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(xt[c], w, acc[r], 0, 0, 0);
             }
@@ -139,7 +151,7 @@ __global__ __launch_bounds__(512) void rows_kernel(LinearArgs a) {
                     const float s = f16_bits_to_f32(cur.scale[r][j / (4 / S)]);
                     const float z = a.w[r / R].zeros ? 16.f + (float)cur.zero[r][j / (4 / S)] : 24.f;
 #pragma unroll
-                    for (int i = 0; i < TI; i++) out[r][i] = fmaf(s, fmaf(-z, xs[i], acc[r][i]), out[r][i]);
+                    for (int i = 0; i < TI; i++) out[r][i] = fmaf(s, XBF16 ? fmaf(-z, xs[i], acc[r][i]) : acc[r][i], out[r][i]);
                 }
             }
         }
@@ -282,14 +294,16 @@ __global__ __launch_bounds__(64 * RW * KW) void shared_rows_kernel(LinearArgs a)
 #pragma unroll
             for (int b = 0; b < NB; b++) {
                 const uint4 c = cur.code[b];
-                w[b] = codes_bf16(j == 0 ? c.x : j == 1 ? c.y : j == 2 ? c.z : c.w);
+                const uint32_t word = j == 0 ? c.x : j == 1 ? c.y : j == 2 ? c.z : c.w;
+                const float z = a.w[b].zeros ? (float)cur.zero[b][j / (4 / S)] : 8.f;
+                w[b] = XBF16 ? codes_bf16(word) : codes_less_zero(word, z);
             }
 #pragma unroll
             for (int c = kTerms - 1; c >= 0; c--)
 #pragma unroll
                 for (int m = 0; m < MT; m++) {
                     const bf16x8 xt = *(const bf16x8*)(mine + c * kPlane + (16 * m + n) * 256 + (((4 * j + q) ^ n) << 4));
-                    xs[m] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(xt, ones, xs[m], 0, 0, 0);
+                    if constexpr (XBF16) xs[m] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(xt, ones, xs[m], 0, 0, 0);
 #pragma unroll
                     for (int b = 0; b < NB; b++)
                         acc[b][m] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(xt, w[b], acc[b][m], 0, 0, 0);
@@ -302,7 +316,8 @@ __global__ __launch_bounds__(64 * RW * KW) void shared_rows_kernel(LinearArgs a)
 #pragma unroll
                     for (int m = 0; m < MT; m++)
 #pragma unroll
-                        for (int i = 0; i < 4; i++) out[b][m][i] = fmaf(s, fmaf(-z, xs[m][i], acc[b][m][i]), out[b][m][i]);
+                        for (int i = 0; i < 4; i++)
+                            out[b][m][i] = fmaf(s, XBF16 ? fmaf(-z, xs[m][i], acc[b][m][i]) : acc[b][m][i], out[b][m][i]);
                 }
             }
         }
