@@ -70,7 +70,10 @@ struct LinearArgs {
     int y_bf16;
 };
 hipError_t launch_linear(const LinearArgs& a, bool gated, hipStream_t s);
+// Many tokens, x and y bf16: on tiles, with each weight rounded to bf16; and the
+// time that is estimated to take.
 hipError_t launch_linear_tiles(const LinearArgs& a, bool gated, hipStream_t s);
+float linear_tiles_us(const LinearArgs& a, bool gated);
 
 struct GatedArgs {
     const void* x;  // [T, d], rows ldx elements apart

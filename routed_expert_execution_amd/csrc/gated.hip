@@ -117,20 +117,17 @@ __global__ __launch_bounds__(512) void gated_rows_kernel(GatedArgs a) {
         for (int m = 0; m < MT; m++) acc[b][m] = f32x4{0.f, 0.f, 0.f, 0.f};
 
     struct Chunks { u32x4 w[2][4]; };
-    const bool whole = a.d % E == 0;  // no chunk crosses the end of a row
-    auto chunk = [&](const void* p, int64_t ld, int64_t r, int64_t k) {
-        if (whole) {  // past the end: the row's last chunk, taken out below by x = 0 there
-            typedef typename Elem<BF16>::raw raw;
-            return ((const Loose*)((const raw*)p + r * ld + min(k, (int64_t)a.d - E)))->v;
-        }
+    // (inside: wave-uniform, whether the whole tile lies before the rows' end)
+    auto chunk = [&](const void* p, int64_t ld, int64_t r, int64_t k, bool inside) {
+        if (inside) return ((const Loose*)((const typename Elem<BF16>::raw*)p + r * ld + k))->v;
         return load_chunk<BF16>(p, ld, r, k, r + 1, a.d);
     };
     auto load = [&](int kt, Chunks& c) {
 #pragma unroll
         for (int j = 0; j < 4; j++) {
             const int64_t k = (int64_t)kt * kCols + (4 * j + q) * E;
-            c.w[0][j] = chunk(a.w_gate, a.d, row, k);
-            c.w[1][j] = chunk(a.w_up, a.d, row, k);
+            c.w[0][j] = chunk(a.w_gate, a.d, row, k, (kt + 1) * kCols <= a.d);
+            c.w[1][j] = chunk(a.w_up, a.d, row, k, (kt + 1) * kCols <= a.d);
         }
     };
     Chunks cur, nxt;
@@ -143,22 +140,17 @@ __global__ __launch_bounds__(512) void gated_rows_kernel(GatedArgs a) {
             const int64_t t = t0 + (TI == 1 ? n / 4 : 16 * m + n);
 #pragma unroll
             for (int j = 0; j < 4; j++)  // (rows past the last are computed and not stored)
-                x[m][j] = chunk(a.x, a.ldx, t < a.T ? t : a.T - 1, (int64_t)kt * kCols + (4 * j + q) * E);
+                x[m][j] = chunk(a.x, a.ldx, t < a.T ? t : a.T - 1, (int64_t)kt * kCols + (4 * j + q) * E, (kt + 1) * kCols <= a.d);
         }
         if (kt + waves < tiles) load(kt + waves, nxt);
 #pragma unroll
         for (int j = 0; j < 4; j++) {
-            const bool in = (int64_t)kt * kCols + (4 * j + q) * E < a.d;
 #pragma unroll
             for (int b = 0; b < 2; b++) {
-                u32x4 w = cur.w[b][j];
-#pragma unroll
-                for (int e = 0; e < 4; e++) w[e] = in ? w[e] : 0u;
+                const u32x4 w = cur.w[b][j];
 #pragma unroll
                 for (int m = 0; m < MT; m++) {
-                    u32x4 v = x[m][j];
-#pragma unroll
-                    for (int e = 0; e < 4; e++) v[e] = in ? v[e] : 0u;
+                    const u32x4 v = x[m][j];
                     if constexpr (BF16) {
                         acc[b][m] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, v), __builtin_bit_cast(bf16x8, w),
                                                                             acc[b][m], 0, 0, 0);
@@ -242,7 +234,7 @@ BackwardPlan backward_plan(int64_t T, int d, int F, int bf16) {
     BackwardPlan p{};
     const int64_t dx_steps = 2 * steps_of(F, bf16), dw_steps = steps_of(T, bf16);
     float best = 1e30f;
-    for (int h = 0; h < 3; h++) {
+    for (int h = 0; h < kShapes; h++) {
         const TileShape& c = kTileShapes[bf16 ? kBf16 : kFp32][h];
         if (!c.per_cu) continue;
         auto tiles = [&](int64_t m, int64_t n) { return (m + c.bm - 1) / c.bm * ((n + c.bn - 1) / c.bn); };
@@ -331,6 +323,7 @@ hipError_t gated_backward(const GatedBackwardArgs& a, hipStream_t s) {
     hipError_t e = hipErrorInvalidValue;
     if (p.shape == kShape256x128) e = launch_backward_tiles<BF16, 256, 128, 4, 2>(x, w, dx, dw, s);
     else if (p.shape == kShape128) e = launch_backward_tiles<BF16, 128, 128, 2, 2>(x, w, dx, dw, s);
+    else if (p.shape == kShapeSmall) e = launch_backward_tiles<BF16, 64, 64, 2, 2>(x, w, dx, dw, s);
     else if constexpr (BF16) e = launch_backward_tiles<BF16, 256, 256, 2, 4>(x, w, dx, dw, s);
     if (e) return e;
     ReduceArgs r{{x.part, w.part}, {p.dx_splits, p.dw_splits},

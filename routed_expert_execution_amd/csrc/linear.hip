@@ -64,8 +64,20 @@ hipError_t launch_linear_dequant(const QuantGeom& g, const void* data, float* ou
     return hipGetLastError();
 }
 
+// Tiles or shared rows for many bf16 tokens, by estimated time.  A workgroup of
+// the shared rows (64 tokens, 4 row groups) takes 1.5 us for two column tiles
+// where one is on a CU, gated 3.1, and more workgroups as much longer.  Measured,
+// us, rows against tiles: 384 tokens, 4096 x 4096 36 / 64; 128 tokens, gated
+// 8192 x 2048 28 / 36, 256 tokens 48 / 38; 384 tokens, 512 x 4096 15 / 37; 2048
+// tokens, 4096 x 4096 190 / 81.
+static bool tiles_faster(const LinearArgs& a, bool gated) {
+    const float groups = (float)((a.row_groups + 3) / 4) * (float)((a.T + 63) / 64);
+    const float rows_us = (float)((a.col_tiles + 1) / 2) * (groups > 256.f ? groups / 256.f : 1.f) * (gated ? 3.1f : 1.5f);
+    return linear_tiles_us(a, gated) < rows_us;
+}
+
 hipError_t launch_linear(const LinearArgs& a, bool gated, hipStream_t s) {
-    if (a.T > 64 && a.x_bf16 && a.y_bf16) return launch_linear_tiles(a, gated, s);
+    if (a.T > 64 && a.x_bf16 && a.y_bf16 && tiles_faster(a, gated)) return launch_linear_tiles(a, gated, s);
     return a.x_bf16 ? launch_linear_rows_bf16(a, gated, s) : launch_linear_rows_f32(a, gated, s);
 }
 

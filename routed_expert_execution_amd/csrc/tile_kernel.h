@@ -383,20 +383,21 @@ hipError_t launch_shape(TileArgs t, hipStream_t s) {
 //   256 x 128     1.2     1.32       3.3    one
 //   128 x 128     1.2     1.6        3.2    for the two a CU holds; 0.65, 1.06, 1.5
 //                                           where there is one
+//   64 x 64       1.4     1.9        3.6    for four; 0.4, 0.62, 0.95 for one
 // (The backward pass also splits k into parts: they write and read partial sums
 // in fp32, 4 MB a us, and cost a launch more, 4 us.)
-enum { kShape256, kShape256x128, kShape128 };
+enum { kShape256, kShape256x128, kShape128, kShapeSmall, kShapes };
 enum { kBf16, kQuant4, kFp32 };
 struct TileShape { int bm, bn, per_cu; float one, full; };
 constexpr int kTileCus = 256;
-static const TileShape kTileShapes[3][3] = {
-    {{256, 256, 1, 1.7f, 1.7f}, {256, 128, 1, 1.2f, 1.2f}, {128, 128, 2, 0.65f, 1.2f}},
-    {{256, 256, 1, 1.95f, 1.95f}, {256, 128, 1, 1.32f, 1.32f}, {128, 128, 2, 1.06f, 1.6f}},
-    {{256, 256, 0, 0.f, 0.f}, {256, 128, 1, 3.3f, 3.3f}, {128, 128, 2, 1.5f, 3.2f}}};
-inline int plan_tiles(int kind, int64_t M, int64_t N, int64_t steps) {
+static const TileShape kTileShapes[3][kShapes] = {
+    {{256, 256, 1, 1.7f, 1.7f}, {256, 128, 1, 1.2f, 1.2f}, {128, 128, 2, 0.65f, 1.2f}, {64, 64, 4, 0.4f, 1.4f}},
+    {{256, 256, 1, 1.95f, 1.95f}, {256, 128, 1, 1.32f, 1.32f}, {128, 128, 2, 1.06f, 1.6f}, {64, 64, 4, 0.62f, 1.9f}},
+    {{256, 256, 0, 0.f, 0.f}, {256, 128, 1, 3.3f, 3.3f}, {128, 128, 2, 1.5f, 3.2f}, {64, 64, 4, 0.95f, 3.6f}}};
+inline int plan_tiles(int kind, int64_t M, int64_t N, int64_t steps, float* estimate = nullptr) {
     int best = kShape128;
     float best_us = 1e30f;
-    for (int h = 0; h < 3; h++) {
+    for (int h = 0; h < kShapes; h++) {
         const TileShape& c = kTileShapes[kind][h];
         if (!c.per_cu) continue;
         const int64_t groups = (M + c.bm - 1) / c.bm * ((N + c.bn - 1) / c.bn);
@@ -407,6 +408,7 @@ inline int plan_tiles(int kind, int64_t M, int64_t N, int64_t steps) {
             best_us = us;
         }
     }
+    if (estimate) *estimate = best_us;
     return best;
 }
 
@@ -418,6 +420,9 @@ hipError_t launch_tiles(TileArgs t, int shape, hipStream_t s) {
             if constexpr (BF16) return launch_shape<BF16, 256, 256, 2, 4, ALAY, BLAY, MODE>(t, s);
             else return hipErrorInvalidValue;
         case kShape256x128: return launch_shape<BF16, 256, 128, 4, 2, ALAY, BLAY, MODE>(t, s);
+        case kShapeSmall:  // (gate and up of an element in one wave)
+            if constexpr (MODE == kGatedForward) return launch_shape<BF16, 64, 64, 2, 1, ALAY, BLAY, MODE>(t, s);
+            else return launch_shape<BF16, 64, 64, 2, 2, ALAY, BLAY, MODE>(t, s);
         default: return launch_shape<BF16, 128, 128, 2, 2, ALAY, BLAY, MODE>(t, s);
     }
 }

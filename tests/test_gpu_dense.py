@@ -130,7 +130,10 @@ LINEAR = [  # T, K, N, group, affine, x, y, pad
     (64, 512, 129, 32, True, "f32", "f32", 0), (65, 288, 65, 32, False, "bf16", "f32", 1), (100, 1280, 200, 128, True, "f32", "f32", 4),
     (129, 256, 257, 64, True, "bf16", "bf16", 8), (200, 1344, 384, 64, True, "bf16", "bf16", 1), (513, 1024, 640, 128, True, "bf16", "bf16", 0),
     (700, 416, 530, 32, True, "bf16", "bf16", 8), (1024, 2048, 1024, 128, False, "bf16", "bf16", 0), (600, 768, 700, 64, False, "bf16", "f32", 0),
-    (530, 512, 300, 128, True, "f32", "bf16", 0), (2, 128, 70001, 128, False, "bf16", "f32", 0)]
+    (530, 512, 300, 128, True, "f32", "bf16", 0), (2, 128, 70001, 128, False, "bf16", "f32", 0),
+    # every tile shape, rows of x that can and cannot be loaded 16 bytes a lane, a last step of half the columns
+    (2000, 544, 4100, 32, True, "bf16", "bf16", 0), (2000, 544, 4100, 32, False, "bf16", "bf16", 5), (1500, 1088, 2050, 64, True, "bf16", "bf16", 0),
+    (1500, 320, 2050, 64, True, "bf16", "bf16", 3), (3000, 416, 147, 32, False, "bf16", "bf16", 0), (70, 4096, 30000, 128, True, "bf16", "bf16", 0)]
 
 
 def _weights_rounded(T, x_dtype, y_dtype):
@@ -242,7 +245,9 @@ def test_linear_of_zeros_and_of_no_tokens(ctx):
 GATED = [  # T, d, F
     (1, 1, 1), (1, 128, 512), (1, 2048, 512), (2, 65, 33), (4, 2048, 512), (5, 96, 130), (16, 200, 48), (17, 256, 264), (33, 1000, 65),
     (64, 512, 192), (65, 127, 129), (100, 72, 300), (128, 256, 256), (130, 264, 520), (300, 1024, 640), (257, 333, 1411), (600, 2048, 512),
-    (513, 8, 8), (1030, 320, 1100)]
+    (513, 8, 8), (1030, 320, 1100),
+    # the largest tiles: whole and partial last steps, aligned and not
+    (2048, 520, 4100), (2050, 513, 4096), (1030, 2048, 1026), (4100, 256, 264)]
 
 
 def _block(gen, T, d, F, dtype, pad=0):
@@ -493,6 +498,30 @@ def test_captured_step(ctx, dtype):
         torch.cuda.synchronize()
         for a, b in zip(got, (h, dx, dwg, dwu, yq)):
             assert torch.equal(a, b)
+
+
+def test_given_streams(ctx):
+    """stream= as a torch stream and as its handle: the work is on that stream."""
+    gen = _gen(4)
+    w = moe.QuantMatrix(ctx, *_quantised(gen, 64, 256, 32, False))
+    x, wg, wu, dh, h, g, u = _step_buffers(gen, 9, 256, 72, torch.bfloat16)
+    want = torch.empty(9, 64, dtype=torch.bfloat16, device="cuda")
+    moe.moe_linear(ctx, x, w, want)
+    moe.moe_gated(ctx, x, wg, wu, h, gate_out=g, up_out=u)
+    grads = _backward(ctx, dh, x, wg, wu, g, u)
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    for given in (s, s.cuda_stream):
+        with torch.cuda.stream(s):
+            torch.cuda._sleep(10_000_000)  # the buffers are filled late on that stream
+            y, h2 = torch.zeros_like(want), torch.zeros_like(h)
+            out = [torch.zeros_like(t) for t in grads]
+            ws = torch.zeros(moe.moe_gated_workspace(ctx, 9, 256, 72, torch.bfloat16), dtype=torch.uint8, device="cuda")
+        moe.moe_linear(ctx, x, w, y, stream=given)
+        moe.moe_gated(ctx, x, wg, wu, h2, stream=given)
+        moe.moe_gated_backward(ctx, dh, x, wg, wu, g, u, dx=out[0], dw_gate=out[1], dw_up=out[2], workspace=ws, stream=given)
+        s.synchronize()
+        assert torch.equal(y, want) and torch.equal(h2, h) and all(torch.equal(a, b) for a, b in zip(out, grads))
 
 
 def test_two_streams_at_once(ctx):
