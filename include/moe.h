@@ -458,7 +458,7 @@ moe_status moe_route_ffn(moe_ctx* ctx, int32_t layer, const void* x, int32_t x_d
  * one zero point z for every `group` consecutive columns of a row:
  *   w[n, k] = s[n, k / group] * (q[n, k] - z[n, k / group]),
  * z = 8 everywhere if not affine (with group 32 these are Q4_0's values).
- * group 32, 64 or 128; cols a multiple of group; rows up to 2^30, cols up to
+ * group 32, 64 or 128; cols a multiple of group; rows and cols up to
  * 2^24.  data: device, 16-byte aligned, moe_linear_bytes() bytes, filled by
  * moe_linear_pack. */
 typedef struct moe_qmat {
@@ -483,7 +483,7 @@ moe_status moe_linear_pack(moe_ctx* ctx, const uint8_t* codes, const void* scale
 /* The values of a packed matrix in fp32, exactly: device out [rows, cols]. */
 moe_status moe_linear_dequant(moe_ctx* ctx, const moe_qmat* m, float* out, moe_stream stream);
 
-/* y[t, n] = sum_k x[t, k] w[n, k] for T >= 0 tokens.
+/* y[t, n] = sum_k x[t, k] w[n, k] for T from 0 to 2^20 tokens.
  * x: device [T, w->cols] (x_dtype), rows ldx apart; y: device [T, w->rows]
  * (y_dtype: MOE_F32 or MOE_BF16), rows ldy apart.
  * Sums, scales and zero points are fp32 and x is not rounded (fp32 x enters
@@ -512,7 +512,7 @@ moe_status moe_linear_gated(moe_ctx* ctx, const void* x, int32_t x_dtype, int64_
  * factors enter the matrix cores as three bf16 terms of 24 bits together (in
  * calls of more than 64 tokens and in the backward pass): an infinity there
  * gives NaN, as does a value above 3.38e38.
- * Sizes: d and F from 1 to 2^20, T up to 2^24. */
+ * Sizes: d and F from 1 to 2^20, T up to 2^20. */
 moe_status moe_gated(moe_ctx* ctx, const void* x, int32_t dtype, int64_t ldx, int64_t T, int32_t d, int32_t F,
                      const void* w_gate, const void* w_up, void* h, void* gate, void* up, moe_stream stream);
 

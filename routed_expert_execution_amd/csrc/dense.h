@@ -30,7 +30,7 @@ struct QuantGeom {
         rows = rows_; cols = cols_; group = group_; affine = affine_;
         if (group != 32 && group != 64 && group != 128) return false;
         if (affine != 0 && affine != 1) return false;
-        if (rows < 1 || cols < 1 || rows > (1 << 30) || cols > (1 << 24) || cols % group) return false;
+        if (rows < 1 || cols < 1 || rows > (1 << 24) || cols > (1 << 24) || cols % group) return false;
         row_groups = (rows + 15) / 16;
         col_tiles = (cols + 127) / 128;
         per_tile = 128 / group;

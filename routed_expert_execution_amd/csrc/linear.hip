@@ -12,55 +12,58 @@ namespace {
 __global__ __launch_bounds__(256) void pack_kernel(QuantGeom g, const uint8_t* __restrict__ codes,
                                                    const uint16_t* __restrict__ scales, const uint8_t* __restrict__ zeros,
                                                    uint8_t* __restrict__ data) {
-    const int64_t tile = blockIdx.x;
-    const int64_t rg = tile / g.col_tiles, kt = tile % g.col_tiles;
-    const int lane = threadIdx.x >> 2, j = threadIdx.x & 3;
-    const int64_t row = rg * 16 + (lane & 15), col = kt * 128 + 32 * j + 8 * (lane >> 4);
-    uint32_t word = 0;
-    if (row < g.rows && col < g.cols) {  // (columns come in whole 32s)
-        const uint8_t* src = codes + row * (g.cols / 2) + col / 2;
-        for (int p = 0; p < 4; p++) word |= (uint32_t)(src[p] & 15) << (4 * p) | (uint32_t)(src[p] >> 4) << (16 + 4 * p);
-    }
-    ((uint32_t*)data)[tile * 256 + lane * 4 + j] = word;
-    const int S = g.per_tile;
-    if ((int)threadIdx.x < 16 * S) {
-        const int64_t r = rg * 16 + threadIdx.x / S, c = kt * S + threadIdx.x % S, per_row = g.cols / g.group;
-        const bool in = r < g.rows && c < per_row;
-        ((uint16_t*)(data + g.scales_at))[tile * 16 * S + threadIdx.x] = in ? scales[r * per_row + c] : 0;
-        if (g.affine) (data + g.zeros_at)[tile * 16 * S + threadIdx.x] = in ? zeros[r * per_row + c] : 0;
+    const int lane = threadIdx.x >> 2, j = threadIdx.x & 3, S = g.per_tile;
+    for (int64_t tile = blockIdx.x; tile < g.row_groups * g.col_tiles; tile += gridDim.x) {
+        const int64_t rg = tile / g.col_tiles, kt = tile % g.col_tiles;
+        const int64_t row = rg * 16 + (lane & 15), col = kt * 128 + 32 * j + 8 * (lane >> 4);
+        uint32_t word = 0;
+        if (row < g.rows && col < g.cols) {  // (columns come in whole 32s)
+            const uint8_t* src = codes + row * (g.cols / 2) + col / 2;
+            for (int p = 0; p < 4; p++) word |= (uint32_t)(src[p] & 15) << (4 * p) | (uint32_t)(src[p] >> 4) << (16 + 4 * p);
+        }
+        ((uint32_t*)data)[tile * 256 + lane * 4 + j] = word;
+        if ((int)threadIdx.x < 16 * S) {
+            const int64_t r = rg * 16 + threadIdx.x / S, c = kt * S + threadIdx.x % S, per_row = g.cols / g.group;
+            const bool in = r < g.rows && c < per_row;
+            ((uint16_t*)(data + g.scales_at))[tile * 16 * S + threadIdx.x] = in ? scales[r * per_row + c] : 0;
+            if (g.affine) (data + g.zeros_at)[tile * 16 * S + threadIdx.x] = in ? zeros[r * per_row + c] : 0;
+        }
     }
 }
 
 // fp32 value s (q - z) of every element, row-major: exact, as 11 bits of scale
 // times at most 8 of code fit in 24.
 __global__ __launch_bounds__(256) void dequant_kernel(QuantGeom g, const uint8_t* __restrict__ data, float* __restrict__ out) {
-    const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x, words = g.cols / 8;
-    if (i >= g.rows * words) return;
-    const int64_t row = i / words, col = i % words * 8;
-    const int64_t tile = row / 16 * g.col_tiles + col / 128;
-    const int lane = (int)(row % 16) + 16 * (int)(col % 32 / 8), j = (int)(col % 128 / 32);
-    const uint32_t word = ((const uint32_t*)data)[tile * 256 + lane * 4 + j];
-    const int64_t at = (tile * 16 + row % 16) * g.per_tile + col % 128 / g.group;
-    const float s = f16_bits_to_f32(((const uint16_t*)(data + g.scales_at))[at]);
-    const float z = g.affine ? (float)(data + g.zeros_at)[at] : 8.f;
-    for (int e = 0; e < 8; e++) {
-        const uint32_t q = word >> (e % 2 * 16 + e / 2 * 4) & 15;
-        out[row * g.cols + col + e] = s * ((float)q - z);
+    const int64_t words = g.cols / 8;
+    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < g.rows * words; i += (int64_t)gridDim.x * 256) {
+        const int64_t row = i / words, col = i % words * 8;
+        const int64_t tile = row / 16 * g.col_tiles + col / 128;
+        const int lane = (int)(row % 16) + 16 * (int)(col % 32 / 8), j = (int)(col % 128 / 32);
+        const uint32_t word = ((const uint32_t*)data)[tile * 256 + lane * 4 + j];
+        const int64_t at = (tile * 16 + row % 16) * g.per_tile + col % 128 / g.group;
+        const float s = f16_bits_to_f32(((const uint16_t*)(data + g.scales_at))[at]);
+        const float z = g.affine ? (float)(data + g.zeros_at)[at] : 8.f;
+        for (int e = 0; e < 8; e++) {
+            const uint32_t q = word >> (e % 2 * 16 + e / 2 * 4) & 15;
+            out[row * g.cols + col + e] = s * ((float)q - z);
+        }
     }
 }
+
+// workgroups of a pass that goes round (2^32 threads are the most of a launch)
+dim3 workgroups(int64_t n) { return dim3((unsigned)(n < (1 << 20) ? n : 1 << 20)); }
 
 }  // namespace
 
 hipError_t launch_linear_pack(const QuantGeom& g, const uint8_t* codes, const uint16_t* scales, const uint8_t* zeros,
                               void* data, hipStream_t s) {
-    hipLaunchKernelGGL(pack_kernel, dim3((unsigned)(g.row_groups * g.col_tiles)), dim3(256), 0, s, g, codes, scales, zeros,
-                       (uint8_t*)data);
+    hipLaunchKernelGGL(pack_kernel, workgroups(g.row_groups * g.col_tiles), dim3(256), 0, s, g, codes, scales, zeros, (uint8_t*)data);
     return hipGetLastError();
 }
 
 hipError_t launch_linear_dequant(const QuantGeom& g, const void* data, float* out, hipStream_t s) {
     const int64_t words = g.rows * (g.cols / 8);
-    hipLaunchKernelGGL(dequant_kernel, dim3((unsigned)((words + 255) / 256)), dim3(256), 0, s, g, (const uint8_t*)data, out);
+    hipLaunchKernelGGL(dequant_kernel, workgroups((words + 255) / 256), dim3(256), 0, s, g, (const uint8_t*)data, out);
     return hipGetLastError();
 }
 

@@ -1361,7 +1361,9 @@ static int elem_bytes(int32_t dtype) { return dtype == MOE_BF16 ? 2 : 4; }
 static bool dtype_valid(int32_t dtype) { return dtype == MOE_F32 || dtype == MOE_BF16; }
 static bool aligned_to(const void* p, size_t n) { return ((uintptr_t)p) % n == 0; }
 
-constexpr int64_t kDenseMaxT = 1 << 24;
+// (T, rows and widths such that no launch passes 65535 workgroups in y or 2^32
+// threads: tiles of more rows or columns than memory holds are not reached)
+constexpr int64_t kDenseMaxT = 1 << 20;
 constexpr int32_t kDenseMaxWidth = 1 << 20;
 
 size_t moe_linear_bytes(int64_t rows, int64_t cols, int32_t group, int32_t affine) {
@@ -1372,7 +1374,7 @@ size_t moe_linear_bytes(int64_t rows, int64_t cols, int32_t group, int32_t affin
 static moe_status qmat_geom(moe_ctx* c, const char* fn, const moe_qmat* m, moe::QuantGeom* g) {
     if (!m || !m->data) return fail(c, MOE_EINVAL, "%s: null matrix", fn);
     if (!g->init(m->rows, m->cols, m->group, m->affine))
-        return fail(c, MOE_EINVAL, "%s: bad matrix: rows in [1, 2^30], group 32, 64 or 128, cols a multiple of it in "
+        return fail(c, MOE_EINVAL, "%s: bad matrix: rows in [1, 2^24], group 32, 64 or 128, cols a multiple of it in "
                     "[group, 2^24], affine 0 or 1", fn);
     if (!aligned_to(m->data, 16)) return fail(c, MOE_EINVAL, "%s: matrix data must be 16-byte aligned", fn);
     return MOE_OK;
@@ -1425,7 +1427,7 @@ static moe_status linear_call(moe_ctx* c, const char* fn, const void* x, int32_t
         if (g1.rows != g.rows || g1.cols != g.cols || g1.group != g.group || g1.affine != g.affine)
             return fail(c, MOE_EINVAL, "%s: the two matrices differ in shape, group or kind", fn);
     }
-    if (T < 0 || T > kDenseMaxT) return fail(c, MOE_EINVAL, "%s: T=%lld outside [0, 2^24]", fn, (long long)T);
+    if (T < 0 || T > kDenseMaxT) return fail(c, MOE_EINVAL, "%s: T=%lld outside [0, 2^20]", fn, (long long)T);
     if (moe_status st = rows_check(c, fn, "x", x, x_dtype, T, g.cols, ldx)) return st;
     if (moe_status st = rows_check(c, fn, "the result", y, y_dtype, T, g.rows, ldy)) return st;
     if (moe_status st = need_device(c)) return st;
@@ -1470,7 +1472,7 @@ static bool gated_sizes(int64_t T, int32_t d, int32_t F) {
 moe_status moe_gated(moe_ctx* c, const void* x, int32_t dtype, int64_t ldx, int64_t T, int32_t d, int32_t F,
                      const void* w_gate, const void* w_up, void* h, void* gate, void* up, moe_stream stream) {
     if (!c) return MOE_EINVAL;
-    if (!gated_sizes(T, d, F)) return fail(c, MOE_EINVAL, "moe_gated: T outside [0, 2^24], or d or F outside [1, 2^20]");
+    if (!gated_sizes(T, d, F)) return fail(c, MOE_EINVAL, "moe_gated: T outside [0, 2^20], or d or F outside [1, 2^20]");
     if (moe_status st = rows_check(c, "moe_gated", "x", x, dtype, T, d, ldx)) return st;
     if ((T > 0 && (!w_gate || !w_up || !h)) || !gate != !up) return fail(c, MOE_EINVAL, "moe_gated: null argument");
     const size_t e = elem_bytes(dtype);
@@ -1495,7 +1497,7 @@ moe_status moe_gated_backward(moe_ctx* c, const void* dh, int64_t lddh, const vo
                               size_t workspace_bytes, moe_stream stream) {
     if (!c) return MOE_EINVAL;
     if (!gated_sizes(T, d, F))
-        return fail(c, MOE_EINVAL, "moe_gated_backward: T outside [0, 2^24], or d or F outside [1, 2^20]");
+        return fail(c, MOE_EINVAL, "moe_gated_backward: T outside [0, 2^20], or d or F outside [1, 2^20]");
     if (moe_status st = rows_check(c, "moe_gated_backward", "x", x, dtype, T, d, ldx)) return st;
     if (moe_status st = rows_check(c, "moe_gated_backward", "dh", dh, dtype, T, F, lddh)) return st;
     if ((T > 0 && (!gate || !up || (dx && (!w_gate || !w_up)))) || !dw_gate != !dw_up || !workspace)

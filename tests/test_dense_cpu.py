@@ -42,7 +42,7 @@ def test_linear_bytes():
     assert f(16, 128, 32, 1) == 1024 + 4 * 48
     assert f(17, 160, 32, 1) == 4 * (1024 + 4 * 48)
     for bad in ((0, 128, 32, 0), (16, 0, 32, 0), (16, 100, 32, 0), (16, 96, 64, 0), (16, 128, 16, 0), (16, 256, 256, 0),
-                (16, 128, 32, 2), (-1, 128, 32, 0), ((1 << 30) + 1, 128, 32, 0), (16, (1 << 24) + 128, 128, 0)):
+                (16, 128, 32, 2), (-1, 128, 32, 0), ((1 << 24) + 1, 128, 32, 0), (16, (1 << 24) + 128, 128, 0)):
         assert f(*bad) == 0, bad
 
 
@@ -58,7 +58,7 @@ def test_linear_good_arguments_reach_the_device_check(ctx):
     (dict(x=None), "null x"), (dict(y=None), "null the result"), (dict(xd=2), "type of x"), (dict(yd=-1), "type of the result"),
     (dict(x=BASE + 2), "misaligned x"), (dict(xd=1, x=BASE + 1), "misaligned x"), (dict(y=BASE + 1), "misaligned the result"),
     (dict(ldx=127), "rows of x"), (dict(ldy=31), "rows of the result"), (dict(ldx=-128), "rows of x"),
-    (dict(ldx=(1 << 40) + 1), "rows of x"), (dict(T=-1), "outside"), (dict(T=(1 << 24) + 1), "outside")])
+    (dict(ldx=(1 << 40) + 1), "rows of x"), (dict(T=-1), "outside"), (dict(T=(1 << 20) + 1), "outside")])
 def test_linear_refuses(ctx, kw, text):
     _refused(ctx, _linear(ctx, **kw), text)
 
@@ -119,7 +119,7 @@ def test_gated_refuses(ctx, kw, text):
 @pytest.mark.parametrize("kw,text", [
     ({}, "host-only"), (dict(dx=None), "host-only"), (dict(dwg=None, dwu=None), "host-only"),
     (dict(T=0, dh=None, x=None, gate=None, up=None, wg=None, wu=None), "host-only"),
-    (dict(d=0), "outside"), (dict(T=(1 << 24) + 1), "outside"), (dict(dtype=2), "type of x"), (dict(ldx=63), "rows of x"),
+    (dict(d=0), "outside"), (dict(T=(1 << 20) + 1), "outside"), (dict(dtype=2), "type of x"), (dict(ldx=63), "rows of x"),
     (dict(lddh=95), "rows of dh"), (dict(dh=None), "null dh"), (dict(x=None), "null x"), (dict(gate=None), "null"),
     (dict(up=None), "null"), (dict(wg=None), "null"), (dict(wu=None), "null"), (dict(dwg=None), "null"),
     (dict(dwu=None), "null"), (dict(ws=None), "null"), (dict(ws=BASE + 128), "256-byte"), (dict(n=255), "needed"),

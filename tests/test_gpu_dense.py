@@ -454,6 +454,57 @@ def test_far_rows(ctx):
         assert torch.equal(p, q)
 
 
+def test_a_matrix_of_more_tiles_than_a_launch_has_workgroups(ctx):
+    """The passes over a matrix go round where it has more than 2^20 tiles."""
+    N, K, group = (1 << 20) + 5, 2080, 32
+    gen = _gen(10)
+    codes, scales, zeros = _quantised(gen, N, K, group, True)
+    w = moe.QuantMatrix(ctx, codes, scales, zeros)
+    out = torch.full((N, K), float("nan"), device="cuda")
+    moe.moe_linear_dequant(ctx, w, out)
+    x = _normal(gen, 1, K, torch.bfloat16)
+    y = torch.empty(1, N, device="cuda")
+    moe.moe_linear(ctx, x, w, y)
+    for n in range(0, N, 1 << 15):
+        e = slice(n, min(n + (1 << 15), N))
+        ref, mag = _values((codes[e], scales[e], zeros[e]), group)
+        assert torch.equal(out[e].double(), ref), n
+        dot = x.double() @ ref.t()
+        _close(y[:, e], dot, _linear_tol(x, mag, dot, torch.float32), n)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_most_tokens(ctx, dtype):
+    T, d, F, dt = 1 << 20, 32, 24, DT[dtype]
+    gen = _gen(11)
+    x, wg, wu = _block(gen, T, d, F, dt)
+    X = x.double()
+    q, r = _quantised(gen, F, d, 32, True), _quantised(gen, F, d, 32, True)
+    p, s = moe.QuantMatrix(ctx, *q), moe.QuantMatrix(ctx, *r)
+    (w, mag), (v, mag_v) = _values(q, 32), _values(r, 32)
+    a, b = X @ w.t(), X @ v.t()
+    D = (3 * 128 + d / 32 + 16) * U
+    for yd in DT.values():
+        extra = 2.0 ** -8 if _weights_rounded(T, dt, yd) else 0.0
+        y = torch.empty(T, F, dtype=yd, device="cuda")
+        moe.moe_linear(ctx, x, p, y)
+        _close(y, a, _linear_tol(x, mag, a, yd) + extra * (X.abs() @ w.abs().t()))
+        moe.moe_linear_gated(ctx, x, p, s, y)
+        ta, tb = (D * (X.abs() @ m.t()) + extra * (X.abs() @ k.abs().t()) for m, k in ((mag, w), (mag_v, v)))
+        h = _silu(a) * b
+        _close(y, h, _gated_tol(a, b, ta, tb, h, yd))
+    h, gate, up = (torch.empty(T, F, dtype=dt, device="cuda") for _ in range(3))
+    moe.moe_gated(ctx, x, wg, wu, h, gate_out=gate, up_out=up)
+    g, u = X @ wg.double().t(), X @ wu.double().t()
+    tg, tu = (_chain(d, dt) * (X.abs() @ m.double().abs().t()) for m in (wg, wu))
+    ref = _silu(g) * u
+    _close(h, ref, _gated_tol(g, u, tg, tu, ref, dt))
+    gate, dh = _cancels(gate), _normal(gen, T, F, dt)
+    for name, y, (ref, tol) in zip(("dx", "dw_gate", "dw_up"), _backward(ctx, dh, x, wg, wu, gate, up),
+                                   _backward_ref(dh, x, wg, wu, gate, up, dt)):
+        _close(y, ref, tol, name)
+
+
 def _step_buffers(gen, T, d, F, dt):
     x, wg, wu = _block(gen, T, d, F, dt)
     dh = _normal(gen, T, F, dt)
