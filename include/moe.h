@@ -510,7 +510,7 @@ moe_status moe_linear_gated(moe_ctx* ctx, const void* x, int32_t x_dtype, int64_
  * [T, F].  gate, up: device [T, F] or NULL, g and u for moe_gated_backward
  * (both or neither).  Sums are fp32; h comes from the unrounded g and u.  fp32
  * factors enter the matrix cores as three bf16 terms of 24 bits together (in
- * calls of more than 64 tokens and in the backward pass): an infinity there
+ * calls of more than 16 tokens and in the backward pass): an infinity there
  * gives NaN, as does a value above 3.38e38.
  * Sizes: d and F from 1 to 2^20, T up to 2^20. */
 moe_status moe_gated(moe_ctx* ctx, const void* x, int32_t dtype, int64_t ldx, int64_t T, int32_t d, int32_t F,

@@ -203,11 +203,40 @@ hipError_t launch_gated_rows(const GatedArgs& a, hipStream_t s) {
     return hipGetLastError();
 }
 
+// Tokens a workgroup of the rows kernel takes (16 of them: 1, 2 or 4), by
+// estimated time: the tiles of columns a wave takes one after the other, times
+// what one costs.  In fp32 that is the products, 2 us for each 16 tokens (and
+// more precise than the terms of the tiles); in bf16 mostly the wait for loads,
+// 2.4 us and 1 for each 16.  Measured, us, 1 or 2, 4, and the tiles: fp32 100
+// tokens 4096 x 512 41, 67, 59, 463 tokens 2005 x 350 43, 38, 51; bf16 100
+// tokens 4096 x 512 17, 25, 15, 135 tokens 288 x 224 4.4, 6.1, 6.2.
+int plan_rows(const GatedArgs& a, float* us) {
+    const int cols = a.bf16 ? 128 : 64, tiles = (a.d + cols - 1) / cols;
+    int best = 4;
+    *us = 1e30f;
+    for (int mt = 1; mt <= 4; mt *= 2) {
+        const int64_t groups = (int64_t)((a.F + 15) / 16) * ((a.T + 16 * mt - 1) / (16 * mt));
+        const float t = (float)((tiles + 7) / 8) * (float)((groups + kTileCus - 1) / kTileCus) * (a.bf16 ? 2.4f + mt : 0.4f + 2.f * mt);
+        if (t < *us) {
+            best = mt;
+            *us = t;
+        }
+    }
+    return best;
+}
+
 template <bool BF16>
 hipError_t gated(const GatedArgs& a, hipStream_t s) {
     if (a.T <= 4) return launch_gated_rows<BF16, 1, 1>(a, s);
     if (a.T <= 16) return launch_gated_rows<BF16, 1, 4>(a, s);
-    if (a.T <= 64) return launch_gated_rows<BF16, 4, 4>(a, s);
+    // (gate and up columns alternate: twice F of them)
+    float tiles_us, rows_us;
+    const int shape = plan_tiles(BF16 ? kBf16 : kFp32, a.T, 2 * (int64_t)a.F, steps_of(a.d, BF16), &tiles_us);
+    const int mt = plan_rows(a, &rows_us);
+    if (rows_us < tiles_us + 1.5f) {
+        if (mt == 1) return launch_gated_rows<BF16, 1, 4>(a, s);
+        return mt == 2 ? launch_gated_rows<BF16, 2, 4>(a, s) : launch_gated_rows<BF16, 4, 4>(a, s);
+    }
     TileArgs t{};
     t.a = Operand{{a.x, nullptr}, a.ldx, 0};
     t.b = Operand{{a.w_gate, a.w_up}, a.d, 0};
@@ -218,8 +247,7 @@ hipError_t gated(const GatedArgs& a, hipStream_t s) {
     t.ldo = a.F;
     t.gate = a.gate;
     t.up = a.up;
-    // (gate and up columns alternate: twice F of them)
-    return launch_tiles<BF16, kAlongK, kAlongK, kGatedForward>(t, plan_tiles(a.bf16 ? kBf16 : kFp32, a.T, 2 * (int64_t)a.F, steps_of(a.d, a.bf16)), s);
+    return launch_tiles<BF16, kAlongK, kAlongK, kGatedForward>(t, shape, s);
 }
 
 struct BackwardPlan {
@@ -236,7 +264,7 @@ BackwardPlan backward_plan(int64_t T, int d, int F, int bf16) {
     float best = 1e30f;
     for (int h = 0; h < kShapes; h++) {
         const TileShape& c = kTileShapes[bf16 ? kBf16 : kFp32][h];
-        if (!c.per_cu) continue;
+        if (!c.per_cu || c.parts > 1) continue;
         auto tiles = [&](int64_t m, int64_t n) { return (m + c.bm - 1) / c.bm * ((n + c.bn - 1) / c.bn); };
         const int64_t dx_tiles = tiles(T, d), dw_tiles = 2 * tiles(F, d);
         for (int64_t n = 1; n <= 16 && (n == 1 || dx_steps / n >= 2); n *= 2)

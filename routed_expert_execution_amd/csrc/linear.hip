@@ -68,15 +68,17 @@ hipError_t launch_linear_dequant(const QuantGeom& g, const void* data, float* ou
 }
 
 // Tiles or shared rows for many bf16 tokens, by estimated time.  A workgroup of
-// the shared rows (64 tokens, 4 row groups) takes 1.5 us for two column tiles
-// where one is on a CU, gated 3.1, and more workgroups as much longer.  Measured,
-// us, rows against tiles: 384 tokens, 4096 x 4096 36 / 64; 128 tokens, gated
-// 8192 x 2048 28 / 36, 256 tokens 48 / 38; 384 tokens, 512 x 4096 15 / 37; 2048
-// tokens, 4096 x 4096 190 / 81.
+// the shared rows (64 tokens, 4 row groups) takes 0.9 us for two column tiles
+// where few are at work and 1.5 where one is on every CU, gated 1.5 and 3.1, and
+// more workgroups as much longer; the tiles need 1.5 us more around their steps.
+// Measured, us, rows against tiles: 384 tokens, 4096 x 512 17 / 23; 128 tokens,
+// 8192 x 1024 33 / 41; 106 tokens, gated 3360 x 2226 25 / 22; 128 tokens, gated
+// 8192 x 2048 28 / 36, 256 tokens 48 / 38; 2048 tokens, 4096 x 4096 190 / 81.
 static bool tiles_faster(const LinearArgs& a, bool gated) {
-    const float groups = (float)((a.row_groups + 3) / 4) * (float)((a.T + 63) / 64);
-    const float rows_us = (float)((a.col_tiles + 1) / 2) * (groups > 256.f ? groups / 256.f : 1.f) * (gated ? 3.1f : 1.5f);
-    return linear_tiles_us(a, gated) < rows_us;
+    const float on_cu = (float)((a.row_groups + 3) / 4) * (float)((a.T + 63) / 64) / 256.f;
+    const float few = gated ? 1.5f : 0.9f, full = gated ? 3.1f : 1.5f;
+    const float rows_us = (float)((a.col_tiles + 1) / 2) * (on_cu < 1.f ? few + (full - few) * on_cu : full * on_cu);
+    return linear_tiles_us(a, gated) + 1.5f < rows_us;
 }
 
 hipError_t launch_linear(const LinearArgs& a, bool gated, hipStream_t s) {

@@ -59,8 +59,10 @@ __device__ inline void tile_of(int id, int m_tiles, int n_tiles, int* m, int* n)
 // steps ahead and become bf16 in LDS one step ahead, each weight s (q - z)
 // rounded once; a word is 16 bytes of the tile, so 22 vector instructions make
 // 8 weights once for all rows of A in the tile.
-template <int BM, int BN> constexpr int tile_lds() { return 2 * (BM + BN) * 128; }
-template <bool BF16, int BM, int BN, int WM, int WN, int ALAY, int BLAY, int MODE, bool FAST>
+// KW > 1: that many groups of WM x WN waves each take a run of the k steps, in
+// LDS of their own, and their sums are added in the groups' order at the end.
+template <int BM, int BN, int KW = 1> constexpr int tile_lds() { return 2 * (BM + BN) * 128 * KW; }
+template <bool BF16, int BM, int BN, int WM, int WN, int ALAY, int BLAY, int MODE, bool FAST, int KW = 1>
 __device__ TILE_INLINE void tile_body(const TileArgs& t, int tile, int part, char* lds) {
     typedef TileOf<BF16, BM, ALAY> TA;
     constexpr bool kQuant = BLAY == kQuantised;
@@ -69,7 +71,10 @@ __device__ TILE_INLINE void tile_body(const TileArgs& t, int tile, int part, cha
     constexpr int FM = BM / WM / 32, FN = BN / WN / 32;
     constexpr int BK = TA::BK, E = TA::E;
     constexpr int kStage = TA::kBytes + TB::kBytes;
-    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int tid = KW == 1 ? threadIdx.x : threadIdx.x % kThreads;
+    const int group = KW == 1 ? 0 : __builtin_amdgcn_readfirstlane(threadIdx.x / kThreads);
+    lds += group * 2 * kStage;
+    const int lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int wm = wave / WN * (BM / WM), wn = wave % WN * (BN / WN);
     int tm, tn;
     tile_of(tile, t.m_tiles, t.n_tiles, &tm, &tn);
@@ -85,7 +90,9 @@ __device__ TILE_INLINE void tile_body(const TileArgs& t, int tile, int part, cha
     const int64_t lda = t.a.ld, ldb = t.b.ld;
     const int64_t steps1 = (t.K + BK - 1) / BK;
     const int64_t steps = MODE == kSumOfTwo ? 2 * steps1 : steps1;
-    const int64_t s0 = steps * split / t.splits, s1 = steps * (split + 1) / t.splits;
+    const int64_t part0 = steps * split / t.splits, part1 = steps * (split + 1) / t.splits;
+    const int64_t rounds = (part1 - part0 + KW - 1) / KW;  // (the groups meet as often, also one with fewer steps)
+    const int64_t s0 = min(part0 + rounds * group, part1), s1 = min(s0 + rounds, part1);
 
     constexpr int CA = TA::kChunks / kThreads, CB = TB::kChunks / kThreads;
     static_assert(TA::kChunks % kThreads == 0 && TB::kChunks % kThreads == 0, "whole chunks a thread");
@@ -93,24 +100,24 @@ __device__ TILE_INLINE void tile_body(const TileArgs& t, int tile, int part, cha
     // comes this way its chunks are loaded together, else (one step of many) one
     // after the other, which keeps registers for the rest.
     auto chunk_a = [&](int p, int64_t k0, int i) TILE_INLINE {
-        const int q = threadIdx.x + kThreads * i, line = q / TA::kLineChunks, c = q % TA::kLineChunks;
+        const int q = tid + kThreads * i, line = q / TA::kLineChunks, c = q % TA::kLineChunks;
         const void* a = a0 + (p ? a_next : 0);
         return ALAY == kAlongK ? load_chunk<BF16>(a, lda, m0 + line, k0 + c * E, t.M, t.K)
                                : load_chunk<BF16>(a, lda, k0 + line, m0 + c * E, t.K, t.M);
     };
     auto chunk_b = [&](int p, int64_t k0, int i) TILE_INLINE {
-        const int q = threadIdx.x + kThreads * i, line = q / TB::kLineChunks, c = q % TB::kLineChunks;
+        const int q = tid + kThreads * i, line = q / TB::kLineChunks, c = q % TB::kLineChunks;
         const void* b = b0 + ((MODE == kGatedForward ? line >> 5 & 1 : p) ? b_next : 0);
         const int row = MODE == kGatedForward ? (line >> 6) * 32 + (line & 31) : line;
         return BLAY == kAlongK ? load_chunk<BF16>(b, ldb, n0 + row, k0 + c * E, t.N, t.K)
                                : load_chunk<BF16>(b, ldb, k0 + line, n0 + c * E, t.K, t.N);
     };
     auto place_a = [&](char* l, int i, u32x4 v) TILE_INLINE {
-        const int q = threadIdx.x + kThreads * i;
+        const int q = tid + kThreads * i;
         *(u32x4*)(l + TA::chunk_at(q / TA::kLineChunks, q % TA::kLineChunks)) = v;
     };
     auto place_b = [&](char* l, int i, u32x4 v) TILE_INLINE {
-        const int q = threadIdx.x + kThreads * i;
+        const int q = tid + kThreads * i;
         *(u32x4*)(l + TA::kBytes + TB::chunk_at(q / TB::kLineChunks, q % TB::kLineChunks)) = v;
     };
     auto copy_step = [&](int p, int64_t k0, char* l) TILE_INLINE {
@@ -146,7 +153,7 @@ __device__ TILE_INLINE void tile_body(const TileArgs& t, int tile, int part, cha
         };
 #pragma unroll
         for (int i = 0; i < CA; i++) {
-            const int q = threadIdx.x + kThreads * i, line = q / TA::kLineChunks;
+            const int q = tid + kThreads * i, line = q / TA::kLineChunks;
             const int c = source(TA{}, line, q % TA::kLineChunks);
             if (ALAY == kAlongK) oa[i] = (uint32_t)((min(m0 + line, t.M - 1) - m0) * lda + c * E) * kBytes;
             else oa[i] = (uint32_t)(line * lda + (min(m0 + c * E, (t.M - 1) / E * E) - m0)) * kBytes;
@@ -154,7 +161,7 @@ __device__ TILE_INLINE void tile_body(const TileArgs& t, int tile, int part, cha
         if constexpr (!kQuant)
 #pragma unroll
         for (int i = 0; i < CB; i++) {
-            const int q = threadIdx.x + kThreads * i, line = q / TB::kLineChunks;
+            const int q = tid + kThreads * i, line = q / TB::kLineChunks;
             const int c = source(TB{}, line, q % TB::kLineChunks);
             const int row = MODE == kGatedForward ? (line >> 6) * 32 + (line & 31) : line;
             if (BLAY == kAlongK) ob[i] = (uint32_t)((min(n0 + row, t.N - 1) - n0) * ldb + c * E) * kBytes;
@@ -256,37 +263,59 @@ __device__ TILE_INLINE void tile_body(const TileArgs& t, int tile, int part, cha
             for (int j = 0; j < FN; j++) mma(acc[i][j], fb[kk & 1][j], fa[kk & 1][i]);
         if constexpr (BF16) spread_reads<kReads, kProducts>();
     };
-    if (s0 < s1) {
-        load_step(s0, lds);
-        if constexpr (kQuant) {
-            load_words(s0, words);
-            store_words(words, lds);
-            if (s0 + 1 < s1) load_words(s0 + 1, words);
-        }
+    if (rounds > 0) {
+        const bool any = KW == 1 || s0 < s1;
+        if (any) load_step(s0, lds);
+        if constexpr (kQuant)
+            if (any) {
+                load_words(s0, words);
+                store_words(words, lds);
+                if (s0 + 1 < s1) load_words(s0 + 1, words);
+            }
         wait_loads_and_meet();
         if (s0 + 1 < s1) load_step(s0 + 1, lds + kStage);
-        read(lds, 0);
+        if (any) read(lds, 0);
     }
-    for (int64_t s = s0; s < s1; s++) {
+    for (int64_t s = s0; s < s0 + rounds; s++) {
         char* cur = lds + ((s - s0) & 1) * kStage;
         char* next = lds + ((s - s0 + 1) & 1) * kStage;
-        if constexpr (kQuant) {
-            if (s + 1 < s1) {
-                store_words(words, next);
-                if (s + 2 < s1) load_words(s + 2, words);
+        const bool any = KW == 1 || s < s1;
+        if (any) {
+            if constexpr (kQuant) {
+                if (s + 1 < s1) {
+                    store_words(words, next);
+                    if (s + 2 < s1) load_words(s + 2, words);
+                }
             }
-        }
 #pragma unroll
-        for (int kk = 0; kk < kSteps - 1; kk++) {
-            read(cur, kk + 1);
-            multiply(kk);
+            for (int kk = 0; kk < kSteps - 1; kk++) {
+                read(cur, kk + 1);
+                multiply(kk);
+            }
         }
         wait_loads_and_meet();
         if (s + 2 < s1) load_step(s + 2, cur);
-        read(next, 0);  // (after the last step what lies there, not used)
-        multiply(kSteps - 1);
+        if (any) {
+            read(next, 0);  // (after the last step what lies there, not used)
+            multiply(kSteps - 1);
+        }
     }
     wait_loads_and_meet();
+    if constexpr (KW > 1) {
+        static_assert(BM * BN * 4 <= 2 * kStage, "a group's sums fit");
+        constexpr int kGroupSums = 2 * kStage / 4;
+        float* sums = (float*)lds + wave * (FM * FN * 16 * 64) + lane;
+        if (group) {
+#pragma unroll
+            for (int i = 0; i < FM * FN * 16; i++) sums[i * 64] = acc[i / 16 / FN][i / 16 % FN][i % 16];
+        }
+        __syncthreads();
+        if (group) return;
+#pragma unroll
+        for (int g = 1; g < KW; g++)
+#pragma unroll
+            for (int i = 0; i < FM * FN * 16; i++) acc[i / 16 / FN][i / 16 % FN][i % 16] += sums[g * kGroupSums + i * 64];
+    }
 
     // Results through a piece of LDS of the wave's own, 32 rows at a time, so
     // that they leave in rows of 16 bytes a lane.
@@ -346,10 +375,10 @@ __device__ TILE_INLINE void tile_body(const TileArgs& t, int tile, int part, cha
     }
 }
 
-template <bool BF16, int BM, int BN, int WM, int WN, int ALAY, int BLAY, int MODE, bool FAST>
-__global__ __launch_bounds__(WM * WN * 64) void tile_kernel(TileArgs t) {
-    __shared__ __attribute__((aligned(1024))) char lds[tile_lds<BM, BN>()];
-    tile_body<BF16, BM, BN, WM, WN, ALAY, BLAY, MODE, FAST>(t, blockIdx.x, 0, lds);
+template <bool BF16, int BM, int BN, int WM, int WN, int ALAY, int BLAY, int MODE, bool FAST, int KW>
+__global__ __launch_bounds__(WM * WN * KW * 64) void tile_kernel(TileArgs t) {
+    __shared__ __attribute__((aligned(1024))) char lds[tile_lds<BM, BN, KW>()];
+    tile_body<BF16, BM, BN, WM, WN, ALAY, BLAY, MODE, FAST, KW>(t, blockIdx.x, 0, lds);
 }
 
 // Whether whole steps may be loaded 16 bytes a lane: aligned lines, and offsets
@@ -362,38 +391,43 @@ inline bool fast_operand(const Operand& o, int layout, int64_t length, bool two,
     return o.ld <= ((int64_t)1 << 31) / 256 / bytes;
 }
 
-template <bool BF16, int BM, int BN, int WM, int WN, int ALAY, int BLAY, int MODE>
+template <bool BF16, int BM, int BN, int WM, int WN, int ALAY, int BLAY, int MODE, int KW = 1>
 hipError_t launch_shape(TileArgs t, hipStream_t s) {
     constexpr int cols = MODE == kGatedForward ? BN / 2 : BN;
     t.m_tiles = (int)((t.M + BM - 1) / BM);
     t.n_tiles = (int)((t.N + cols - 1) / cols);
     const bool fast = fast_operand(t.a, ALAY, t.M, false, BF16) &&
                       (BLAY == kQuantised || fast_operand(t.b, BLAY, t.N, MODE == kGatedForward, BF16));
-    const dim3 grid((unsigned)(t.m_tiles * t.n_tiles)), block(WM * WN * 64);
-    if (fast) hipLaunchKernelGGL((tile_kernel<BF16, BM, BN, WM, WN, ALAY, BLAY, MODE, true>), grid, block, 0, s, t);
-    else hipLaunchKernelGGL((tile_kernel<BF16, BM, BN, WM, WN, ALAY, BLAY, MODE, false>), grid, block, 0, s, t);
+    const dim3 grid((unsigned)(t.m_tiles * t.n_tiles)), block(WM * WN * KW * 64);
+    if (fast) hipLaunchKernelGGL((tile_kernel<BF16, BM, BN, WM, WN, ALAY, BLAY, MODE, true, KW>), grid, block, 0, s, t);
+    else hipLaunchKernelGGL((tile_kernel<BF16, BM, BN, WM, WN, ALAY, BLAY, MODE, false, KW>), grid, block, 0, s, t);
     return hipGetLastError();
 }
 
 // Tile shape for a product of M x N with `steps` k steps, by estimated time:
 // rounds of workgroups over the CUs, times the steps, times the measured time of
-// a step (us, all CUs busy):
-//                 bf16    4-bit B    fp32
-//   256 x 256     1.7     1.95       -      one workgroup a CU (fp32: spills, 5.1)
-//   256 x 128     1.2     1.32       3.3    one
-//   128 x 128     1.2     1.6        3.2    for the two a CU holds; 0.65, 1.06, 1.5
-//                                           where there is one
-//   64 x 64       1.4     1.9        3.6    for four; 0.4, 0.62, 0.95 for one
-// (The backward pass also splits k into parts: they write and read partial sums
-// in fp32, 4 MB a us, and cost a launch more, 4 us.)
-enum { kShape256, kShape256x128, kShape128, kShapeSmall, kShapes };
+// a step (us, with one workgroup on every CU, and with as many as a CU holds;
+// in between by the number there):
+//                   bf16         4-bit B      fp32
+//   256 x 256       1.7          1.95         -           one a CU (fp32: spills, 5.1)
+//   256 x 128       1.2          1.32         3.3         one
+//   128 x 128       0.65 - 1.2   1.06 - 1.6   1.5 - 3.2   two
+//   64 x 64         0.4 - 1.4    0.62 - 1.9   0.95 - 3.6  four
+//   64 x 64 x 4     0.9          1.25         2.0         one; four steps at a time, and
+//                                                         2 us to add the four sums
+// The last is for few tiles of many steps, which wait for loads one step after
+// the other: fp32 100 tokens 4096 x 512 59 us (64 x 64 107), 4-bit gated 106
+// tokens 3360 x 2226 22 (51); but bf16 1000 tokens 1024 x 1024 15 (11.5).
+// (The backward pass also splits k into parts over workgroups: they write and
+// read partial sums in fp32, 4 MB a us, and cost a launch more, 4 us.)
+enum { kShape256, kShape256x128, kShape128, kShapeSmall, kShapeParts, kShapes };
 enum { kBf16, kQuant4, kFp32 };
-struct TileShape { int bm, bn, per_cu; float one, full; };
+struct TileShape { int bm, bn, per_cu, parts; float one, full; };
 constexpr int kTileCus = 256;
 static const TileShape kTileShapes[3][kShapes] = {
-    {{256, 256, 1, 1.7f, 1.7f}, {256, 128, 1, 1.2f, 1.2f}, {128, 128, 2, 0.65f, 1.2f}, {64, 64, 4, 0.4f, 1.4f}},
-    {{256, 256, 1, 1.95f, 1.95f}, {256, 128, 1, 1.32f, 1.32f}, {128, 128, 2, 1.06f, 1.6f}, {64, 64, 4, 0.62f, 1.9f}},
-    {{256, 256, 0, 0.f, 0.f}, {256, 128, 1, 3.3f, 3.3f}, {128, 128, 2, 1.5f, 3.2f}, {64, 64, 4, 0.95f, 3.6f}}};
+    {{256, 256, 1, 1, 1.7f, 1.7f}, {256, 128, 1, 1, 1.2f, 1.2f}, {128, 128, 2, 1, 0.65f, 1.2f}, {64, 64, 4, 1, 0.4f, 1.4f}, {64, 64, 1, 4, 0.9f, 0.9f}},
+    {{256, 256, 1, 1, 1.95f, 1.95f}, {256, 128, 1, 1, 1.32f, 1.32f}, {128, 128, 2, 1, 1.06f, 1.6f}, {64, 64, 4, 1, 0.62f, 1.9f}, {64, 64, 1, 4, 1.25f, 1.25f}},
+    {{256, 256, 0, 1, 0.f, 0.f}, {256, 128, 1, 1, 3.3f, 3.3f}, {128, 128, 2, 1, 1.5f, 3.2f}, {64, 64, 4, 1, 0.95f, 3.6f}, {64, 64, 1, 4, 2.0f, 2.0f}}};
 inline int plan_tiles(int kind, int64_t M, int64_t N, int64_t steps, float* estimate = nullptr) {
     int best = kShape128;
     float best_us = 1e30f;
@@ -401,8 +435,9 @@ inline int plan_tiles(int kind, int64_t M, int64_t N, int64_t steps, float* esti
         const TileShape& c = kTileShapes[kind][h];
         if (!c.per_cu) continue;
         const int64_t groups = (M + c.bm - 1) / c.bm * ((N + c.bn - 1) / c.bn);
-        const int64_t rounds = (groups + kTileCus * c.per_cu - 1) / (kTileCus * c.per_cu);
-        const float us = (float)steps * (groups <= kTileCus ? c.one : (float)rounds * c.full);
+        const int64_t on_cu = (groups + kTileCus - 1) / kTileCus, rounds = (on_cu + c.per_cu - 1) / c.per_cu;
+        const float step = rounds > 1 || c.per_cu == 1 ? c.full : c.one + (c.full - c.one) * (float)(on_cu - 1) / (float)(c.per_cu - 1);
+        const float us = (float)rounds * ((float)((steps + c.parts - 1) / c.parts) * step + (c.parts > 1 ? 2.f : 0.f));
         if (us < best_us) {
             best = h;
             best_us = us;
@@ -423,6 +458,7 @@ hipError_t launch_tiles(TileArgs t, int shape, hipStream_t s) {
         case kShapeSmall:  // (gate and up of an element in one wave)
             if constexpr (MODE == kGatedForward) return launch_shape<BF16, 64, 64, 2, 1, ALAY, BLAY, MODE>(t, s);
             else return launch_shape<BF16, 64, 64, 2, 2, ALAY, BLAY, MODE>(t, s);
+        case kShapeParts: return launch_shape<BF16, 64, 64, 2, 1, ALAY, BLAY, MODE, 4>(t, s);
         default: return launch_shape<BF16, 128, 128, 2, 2, ALAY, BLAY, MODE>(t, s);
     }
 }
