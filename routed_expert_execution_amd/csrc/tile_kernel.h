@@ -97,8 +97,8 @@ __device__ TILE_INLINE void tile_body(const TileArgs& t, int tile, int part, cha
     constexpr int CA = TA::kChunks / kThreads, CB = TB::kChunks / kThreads;
     static_assert(TA::kChunks % kThreads == 0 && TB::kChunks % kThreads == 0, "whole chunks a thread");
     // Through registers: any alignment, zeros past the end.  Where every step
-    // comes this way its chunks are loaded together, else (one step of many) one
-    // after the other, which keeps registers for the rest.
+    // comes this way its chunks are loaded together (fetch_step), else (one step of
+    // many, copy_step) one after the other, which keeps registers for the rest.
     auto chunk_a = [&](int p, int64_t k0, int i) TILE_INLINE {
         const int q = tid + kThreads * i, line = q / TA::kLineChunks, c = q % TA::kLineChunks;
         const void* a = a0 + (p ? a_next : 0);
@@ -121,25 +121,33 @@ __device__ TILE_INLINE void tile_body(const TileArgs& t, int tile, int part, cha
         *(u32x4*)(l + TA::kBytes + TB::chunk_at(q / TB::kLineChunks, q % TB::kLineChunks)) = v;
     };
     auto copy_step = [&](int p, int64_t k0, char* l) TILE_INLINE {
-        if constexpr (FAST) {
 #pragma unroll 1
-            for (int i = 0; i < CA; i++) place_a(l, i, chunk_a(p, k0, i));
-            if constexpr (!kQuant)
+        for (int i = 0; i < CA; i++) place_a(l, i, chunk_a(p, k0, i));
+        if constexpr (!kQuant)
 #pragma unroll 1
-                for (int i = 0; i < CB; i++) place_b(l, i, chunk_b(p, k0, i));
-        } else {
-            u32x4 ra[CA], rb[kQuant ? 1 : CB];
+            for (int i = 0; i < CB; i++) place_b(l, i, chunk_b(p, k0, i));
+    };
+    // Forward, a step is fetched one ahead of being placed, so that the loads run
+    // beside the products (us, fp32 2896 tokens 1926 x 489 124, without 139; bf16
+    // 4096 tokens 1999 x 4001 167 and 176).  The backward pass, whose operands
+    // across k take more registers, has none left for it (702 and 568).
+    constexpr bool kAhead = !FAST && (MODE == kGatedForward || MODE == kOneResult);
+    u32x4 ra[FAST ? 1 : CA], rb[FAST || kQuant ? 1 : CB];
+    auto fetch_step = [&](int64_t s) TILE_INLINE {
+        const int p = MODE == kSumOfTwo ? s >= steps1 : which;
+        const int64_t k0 = (MODE == kSumOfTwo && s >= steps1 ? s - steps1 : s) * BK;
 #pragma unroll
-            for (int i = 0; i < CA; i++) ra[i] = chunk_a(p, k0, i);
-            if constexpr (!kQuant)
+        for (int i = 0; i < CA; i++) ra[i] = chunk_a(p, k0, i);
+        if constexpr (!kQuant)
 #pragma unroll
-                for (int i = 0; i < CB; i++) rb[i] = chunk_b(p, k0, i);
+            for (int i = 0; i < CB; i++) rb[i] = chunk_b(p, k0, i);
+    };
+    auto place_step = [&](char* l) TILE_INLINE {
 #pragma unroll
-            for (int i = 0; i < CA; i++) place_a(l, i, ra[i]);
-            if constexpr (!kQuant)
+        for (int i = 0; i < CA; i++) place_a(l, i, ra[i]);
+        if constexpr (!kQuant)
 #pragma unroll
-                for (int i = 0; i < CB; i++) place_b(l, i, rb[i]);
-        }
+            for (int i = 0; i < CB; i++) place_b(l, i, rb[i]);
     };
     // Straight into LDS: this thread's byte offsets from the tile's first
     // element of a step.
@@ -171,7 +179,7 @@ __device__ TILE_INLINE void tile_body(const TileArgs& t, int tile, int part, cha
     auto load_step = [&](int64_t s, char* l) TILE_INLINE {
         const int p = MODE == kSumOfTwo ? s >= steps1 : which;
         const int64_t k0 = (MODE == kSumOfTwo && s >= steps1 ? s - steps1 : s) * BK;
-        if (!FAST || k0 + BK > t.K) {
+        if (k0 + BK > t.K) {
             copy_step(p, k0, l);
             return;
         }
@@ -265,7 +273,13 @@ __device__ TILE_INLINE void tile_body(const TileArgs& t, int tile, int part, cha
     };
     if (rounds > 0) {
         const bool any = KW == 1 || s0 < s1;
-        if (any) load_step(s0, lds);
+        if (any) {
+            if constexpr (FAST) load_step(s0, lds);
+            else {
+                fetch_step(s0);
+                place_step(lds);
+            }
+        }
         if constexpr (kQuant)
             if (any) {
                 load_words(s0, words);
@@ -273,7 +287,11 @@ __device__ TILE_INLINE void tile_body(const TileArgs& t, int tile, int part, cha
                 if (s0 + 1 < s1) load_words(s0 + 1, words);
             }
         wait_loads_and_meet();
-        if (s0 + 1 < s1) load_step(s0 + 1, lds + kStage);
+        if (s0 + 1 < s1) {
+            if constexpr (FAST) load_step(s0 + 1, lds + kStage);
+            else fetch_step(s0 + 1);
+            if constexpr (!FAST && !kAhead) place_step(lds + kStage);
+        }
         if (any) read(lds, 0);
     }
     for (int64_t s = s0; s < s0 + rounds; s++) {
@@ -293,8 +311,14 @@ __device__ TILE_INLINE void tile_body(const TileArgs& t, int tile, int part, cha
                 multiply(kk);
             }
         }
+        if constexpr (kAhead)
+            if (s + 1 < s1) place_step(next);
         wait_loads_and_meet();
-        if (s + 2 < s1) load_step(s + 2, cur);
+        if (s + 2 < s1) {
+            if constexpr (FAST) load_step(s + 2, cur);
+            else fetch_step(s + 2);
+            if constexpr (!FAST && !kAhead) place_step(cur);
+        }
         if (any) {
             read(next, 0);  // (after the last step what lies there, not used)
             multiply(kSteps - 1);
