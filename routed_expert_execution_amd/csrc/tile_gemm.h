@@ -54,7 +54,7 @@ __device__ inline void load_lds16(uint32_t lds, uint32_t offset, const void* bas
         "global_load_lds_dwordx4 %1, %2"
         :
         : "s"(__builtin_amdgcn_readfirstlane(lds)), "v"(offset), "s"(uniform(base))
-        : "memory");
+        : "m0", "memory");
 }
 // This wave's loads into LDS have landed and its LDS reads are done (s_waitcnt
 // vmcnt(0) lgkmcnt(0)), then the workgroup meets: the tile is whole and the

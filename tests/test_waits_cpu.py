@@ -75,3 +75,30 @@ def test_loads_wait_for_scalars_that_vector_instructions_write(tmp_path):
         bad += [(f, *b) for b in short_waits(lines)]
     assert objects and loads, "no device code read"
     assert not bad, (len(bad), bad[:8])
+
+
+M0_KERNEL = r"""
+#include "tile_gemm.h"
+extern "C" __global__ void k(const char* p, char* q) {
+    __shared__ __attribute__((aligned(16))) char lds[4096];
+    typedef __attribute__((address_space(1))) const void G;
+    typedef __attribute__((address_space(3))) void L;
+    __builtin_amdgcn_global_load_lds((G*)(p + threadIdx.x * 16), (L*)lds, 16, 0, 0);
+    moe::tile::load_lds16(moe::tile::lds_address(lds + 1024), threadIdx.x * 16, p + 4096);
+    __builtin_amdgcn_global_load_lds((G*)(p + 8192 + threadIdx.x * 16), (L*)lds, 16, 0, 0);
+    moe::tile::wait_loads_and_meet();
+    q[threadIdx.x] = lds[threadIdx.x];
+}
+"""
+
+
+def test_the_compiler_knows_that_a_load_into_lds_sets_m0(tmp_path):
+    """Its own loads to one LDS address on both sides of the block: M0, their
+    destination, is set for each of the three."""
+    if not os.path.exists(build.HIPCC):
+        pytest.skip("no hipcc")
+    (tmp_path / "m0.hip").write_text(M0_KERNEL)
+    asm = subprocess.run([build.HIPCC, "-x", "hip", *build.FLAGS, "-I", build.CSRC, "--cuda-device-only", "-S", str(tmp_path / "m0.hip"),
+                          "-o", "-"], check=True, capture_output=True, text=True).stdout
+    steps = re.findall(r"s_mov_b32 m0|global_load_lds_dwordx4", asm)
+    assert steps == ["s_mov_b32 m0", "global_load_lds_dwordx4"] * 3, steps
