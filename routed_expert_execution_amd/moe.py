@@ -551,6 +551,20 @@ def _stream_on(ctx: Context, stream) -> int | None:
     return _stream(stream)
 
 
+def _lend(ctx: Context, stream: int, *tensors) -> None:
+    """Make tensors safe to use on another stream than the current one, given by
+    its handle: it waits for what the current stream has queued, which may still
+    use their memory, and their memory is not handed out again before it is done."""
+    if stream == _current_stream(ctx.device):
+        return
+    # (a handle of 0 is the default stream, which ExternalStream does not take)
+    other = torch.cuda.ExternalStream(stream, device=ctx.device) if stream else torch.cuda.default_stream(ctx.device)
+    other.wait_stream(torch.cuda.current_stream(ctx.device))
+    for t in tensors:
+        if t is not None:
+            t.record_stream(other)
+
+
 def _dense(ctx: Context, t, rows: int, cols: int, name: str, dtype=None, strided: bool = False) -> tuple:
     """(address, elements between rows, type code) of a float32 or bfloat16
     [rows, cols] tensor on the context's GPU: contiguous or, if strided, with
@@ -579,7 +593,8 @@ class QuantMatrix:
     codes: uint8 [rows, cols / 2], two codes a byte, the even column in the low
     half; scales: float16 [rows, cols / group]; zeros: uint8 of the scales'
     shape, or None for a zero point of 8 everywhere.  The three may be dropped
-    afterwards."""
+    afterwards.  stream: where the packing runs, after what the current stream has
+    queued; calls on other streams have to wait for it."""
 
     def __init__(self, ctx: Context, codes, scales, zeros=None, stream=None):
         import torch
@@ -600,8 +615,9 @@ class QuantMatrix:
         self.data = torch.empty(n, dtype=torch.uint8, device=codes.device)
         self.c = moe_qmat(rows, cols, group, int(self.affine), _ptr(self.data))
         self.ref = C.byref(self.c)
-        _call(ctx, _lib.moe_linear_pack(ctx.handle, _ptr(codes), _ptr(scales), _ptr(zeros), self.ref,
-                                        _stream_on(ctx, stream)))
+        on = _stream_on(ctx, stream)
+        _lend(ctx, on, codes, scales, zeros, self.data)
+        _call(ctx, _lib.moe_linear_pack(ctx.handle, _ptr(codes), _ptr(scales), _ptr(zeros), self.ref, on))
 
 
 def moe_linear_dequant(ctx: Context, w: QuantMatrix, out, stream=None) -> None:
