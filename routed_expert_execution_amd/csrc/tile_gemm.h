@@ -44,17 +44,17 @@ __device__ inline const void* uniform(const void* p) {
 // 16 bytes a lane from base + offset straight into LDS at `lds` + 16 * lane (lds
 // and base wave-uniform; no register in between).  The compiler does not know of
 // these loads: wait_loads_and_meet() before their first use.  Nor does it count
-// wait states inside the block: the load needs one after M0 is set, and five
-// after a vector instruction (the v_readfirstlane of `base`, which may come right
-// before the block) has written the scalar registers of its address.
+// wait states inside the block: the load needs one after M0, which takes its LDS
+// address, is set, and five after a vector instruction (the v_readfirstlane of
+// `base`, which may come right before the block) has written the scalar registers
+// of its address.
 __device__ inline void load_lds16(uint32_t lds, uint32_t offset, const void* base) {
     asm volatile(
-        "s_mov_b32 m0, %0\n\t"
         "s_nop 4\n\t"
-        "global_load_lds_dwordx4 %1, %2"
+        "global_load_lds_dwordx4 %0, %1"
         :
-        : "s"(__builtin_amdgcn_readfirstlane(lds)), "v"(offset), "s"(uniform(base))
-        : "m0", "memory");
+        : "v"(offset), "s"(uniform(base)), "{m0}"(__builtin_amdgcn_readfirstlane(lds))
+        : "memory");
 }
 // This wave's loads into LDS have landed and its LDS reads are done (s_waitcnt
 // vmcnt(0) lgkmcnt(0)), then the workgroup meets: the tile is whole and the
