@@ -100,5 +100,5 @@ def test_the_compiler_knows_that_a_load_into_lds_sets_m0(tmp_path):
     (tmp_path / "m0.hip").write_text(M0_KERNEL)
     asm = subprocess.run([build.HIPCC, "-x", "hip", *build.FLAGS, "-I", build.CSRC, "--cuda-device-only", "-S", str(tmp_path / "m0.hip"),
                           "-o", "-"], check=True, capture_output=True, text=True).stdout
-    steps = re.findall(r"s_mov_b32 m0|global_load_lds_dwordx4", asm)
-    assert steps == ["s_mov_b32 m0", "global_load_lds_dwordx4"] * 3, steps
+    steps = re.findall(r"s_\w+ (m0),|(global_load_lds)_dwordx4", asm)
+    assert steps == [("m0", ""), ("", "global_load_lds")] * 3, asm
