@@ -486,13 +486,11 @@ moe_status moe_linear_dequant(moe_ctx* ctx, const moe_qmat* m, float* out, moe_s
 /* y[t, n] = sum_k x[t, k] w[n, k] for T from 0 to 2^20 tokens.
  * x: device [T, w->cols] (x_dtype), rows ldx apart; y: device [T, w->rows]
  * (y_dtype: MOE_F32 or MOE_BF16), rows ldy apart.
- * Sums, scales and zero points are fp32 and x is not rounded (fp32 x enters
- * the matrix cores as three bf16 terms).  Weights are not rounded either, but
- * calls of more than 64 tokens with x and y both bf16 may round each weight
- * s (q - z) to bf16 once, which the sizes alone decide.  A token's row that
- * holds an infinity or NaN gives a row that is not finite; other rows are not
- * touched by it.  Finite x should stay below 2^120 (codes enter the sums of
- * bf16 x as 16 + q). */
+ * Sums, scales and zero points are fp32 and neither x (fp32 x enters the matrix
+ * cores as three bf16 terms) nor a weight is rounded, whatever the number of
+ * tokens.  A token's row that holds an infinity or NaN gives a row that is not
+ * finite; other rows are not touched by it.  Finite x should stay below 2^120
+ * (codes enter the sums of bf16 x as 16 + q). */
 moe_status moe_linear(moe_ctx* ctx, const void* x, int32_t x_dtype, int64_t ldx, int64_t T, const moe_qmat* w, void* y,
                       int32_t y_dtype, int64_t ldy, moe_stream stream);
 

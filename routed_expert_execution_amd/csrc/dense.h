@@ -70,8 +70,7 @@ struct LinearArgs {
     int y_bf16;
 };
 hipError_t launch_linear(const LinearArgs& a, bool gated, hipStream_t s);
-// Many tokens, x and y bf16: on tiles, with each weight rounded to bf16; and the
-// time that is estimated to take.
+// Many tokens, x and y bf16: on tiles; and the time that is estimated to take.
 hipError_t launch_linear_tiles(const LinearArgs& a, bool gated, hipStream_t s);
 float linear_tiles_us(const LinearArgs& a, bool gated);
 

@@ -71,9 +71,11 @@ hipError_t launch_linear_dequant(const QuantGeom& g, const void* data, float* ou
 // the shared rows (64 tokens, 4 row groups) takes 0.9 us for two column tiles
 // where few are at work and 1.5 where one is on every CU, gated 1.5 and 3.1, and
 // more workgroups as much longer; the tiles need 1.5 us more around their steps.
-// Measured, us, rows against tiles: 384 tokens, 4096 x 512 17 / 23; 128 tokens,
-// 8192 x 1024 33 / 41; 106 tokens, gated 3360 x 2226 25 / 22; 128 tokens, gated
-// 8192 x 2048 28 / 36, 256 tokens 48 / 38; 2048 tokens, 4096 x 4096 190 / 81.
+// Measured, us, rows against tiles (4-bit matrices of groups of 64 unless said):
+// 384 tokens, 4096 x 512, groups of 128 8.2 / 11.9; 128 tokens, 8192 x 1024 9.5 /
+// 9.9; 106 tokens, gated 3360 x 2208, groups of 32 19.2 / 18.4; 128 tokens, gated
+// 8192 x 2048 22 / 27, 256 tokens 44 / 37; 512 tokens, 4096 x 4096, groups of 32 50
+// / 58; 2048 tokens, 4096 x 4096 190 / 88.
 static bool tiles_faster(const LinearArgs& a, bool gated) {
     const float on_cu = (float)((a.row_groups + 3) / 4) * (float)((a.T + 63) / 64) / 256.f;
     const float few = gated ? 1.5f : 0.9f, full = gated ? 3.1f : 1.5f;

@@ -19,6 +19,7 @@
 #include "bf16_terms.h"
 #include "dense.h"
 #include "device_util.h"
+#include "quant_codes.h"
 
 namespace moe {
 namespace linear {
@@ -40,16 +41,6 @@ __device__ inline bf16x8 codes_bf16(uint32_t w) {
     r[2] = ((w >> 5) & mask) | one;
     r[3] = ((w >> 9) & mask) | one;
     return __builtin_bit_cast(bf16x8, r);
-}
-
-// A word's 8 codes as bf16 q - z (integers of 8 bits at most), columns in order.
-__device__ inline bf16x8 codes_less_zero(uint32_t w, float z) {
-    const uint32_t lo = w & 0x0F0F0F0Fu, hi = w >> 4 & 0x0F0F0F0Fu;
-    bf16x8 v;
-#pragma unroll
-    for (int e = 0; e < 8; e++)  // column e: pair e / 2, half e % 2 of the word
-        v[e] = (__bf16)((float)(uint8_t)((e / 2 % 2 ? hi : lo) >> (16 * (e % 2) + 8 * (e / 4))) - z);
-    return v;
 }
 
 // The A operands of one 32-column step: 8 columns of this lane's token.

@@ -18,7 +18,7 @@ typedef short s16x4 __attribute__((ext_vector_type(4)));
 typedef short s16x8 __attribute__((ext_vector_type(8)));
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 
-enum { kAlongK = 0, kAcrossK = 1, kQuantised = 2 };
+enum { kAlongK = 0, kAcrossK = 1 };
 
 template <bool BF16> struct Elem;
 template <> struct Elem<true> { typedef __bf16 type; typedef uint16_t raw; static constexpr int kChunk = 8; };

@@ -22,13 +22,9 @@ struct TileArgs {
     int splits;
     int m_tiles, n_tiles;
     int products;
-    // B in 4 bits (BLAY kQuantised): the matrices, scales a
-    // row has in a tile of 128 columns, and the tiles
-    QuantView q[2];
-    int per_tile, row_groups, col_tiles;
 };
 
-enum { kGatedForward, kSumOfTwo, kTwoResults, kOneResult };
+enum { kGatedForward, kSumOfTwo, kTwoResults };
 
 
 // Workgroup -> tile.  Workgroups go round the 8 XCDs by index; each XCD gets a
@@ -55,18 +51,13 @@ __device__ inline void tile_of(int id, int m_tiles, int n_tiles, int* m, int* n)
 // chunks past the end read the last one; what they make is not stored); the
 // last, partial step and everything else go through registers with zeros past
 // the end.
-// BLAY kQuantised: B is a packed 4-bit matrix.  Its words go to registers two
-// steps ahead and become bf16 in LDS one step ahead, each weight s (q - z)
-// rounded once; a word is 16 bytes of the tile, so 22 vector instructions make
-// 8 weights once for all rows of A in the tile.
 // KW > 1: that many groups of WM x WN waves each take a run of the k steps, in
 // LDS of their own, and their sums are added in the groups' order at the end.
 template <int BM, int BN, int KW = 1> constexpr int tile_lds() { return 2 * (BM + BN) * 128 * KW; }
 template <bool BF16, int BM, int BN, int WM, int WN, int ALAY, int BLAY, int MODE, bool FAST, int KW = 1>
 __device__ TILE_INLINE void tile_body(const TileArgs& t, int tile, int part, char* lds) {
     typedef TileOf<BF16, BM, ALAY> TA;
-    constexpr bool kQuant = BLAY == kQuantised;
-    typedef TileOf<BF16, BN, kQuant ? kAlongK : BLAY> TB;
+    typedef TileOf<BF16, BN, BLAY> TB;
     constexpr int kThreads = WM * WN * 64;
     constexpr int FM = BM / WM / 32, FN = BN / WN / 32;
     constexpr int BK = TA::BK, E = TA::E;
@@ -123,7 +114,6 @@ __device__ TILE_INLINE void tile_body(const TileArgs& t, int tile, int part, cha
     auto copy_step = [&](int p, int64_t k0, char* l) TILE_INLINE {
 #pragma unroll 1
         for (int i = 0; i < CA; i++) place_a(l, i, chunk_a(p, k0, i));
-        if constexpr (!kQuant)
 #pragma unroll 1
             for (int i = 0; i < CB; i++) place_b(l, i, chunk_b(p, k0, i));
     };
@@ -131,21 +121,19 @@ __device__ TILE_INLINE void tile_body(const TileArgs& t, int tile, int part, cha
     // beside the products (us, fp32 2896 tokens 1926 x 489 124, without 139; bf16
     // 4096 tokens 1999 x 4001 167 and 176).  The backward pass, whose operands
     // across k take more registers, has none left for it (702 and 568).
-    constexpr bool kAhead = !FAST && (MODE == kGatedForward || MODE == kOneResult);
-    u32x4 ra[FAST ? 1 : CA], rb[FAST || kQuant ? 1 : CB];
+    constexpr bool kAhead = !FAST && MODE == kGatedForward;
+    u32x4 ra[FAST ? 1 : CA], rb[FAST ? 1 : CB];
     auto fetch_step = [&](int64_t s) TILE_INLINE {
         const int p = MODE == kSumOfTwo ? s >= steps1 : which;
         const int64_t k0 = (MODE == kSumOfTwo && s >= steps1 ? s - steps1 : s) * BK;
 #pragma unroll
         for (int i = 0; i < CA; i++) ra[i] = chunk_a(p, k0, i);
-        if constexpr (!kQuant)
 #pragma unroll
             for (int i = 0; i < CB; i++) rb[i] = chunk_b(p, k0, i);
     };
     auto place_step = [&](char* l) TILE_INLINE {
 #pragma unroll
         for (int i = 0; i < CA; i++) place_a(l, i, ra[i]);
-        if constexpr (!kQuant)
 #pragma unroll
             for (int i = 0; i < CB; i++) place_b(l, i, rb[i]);
     };
@@ -166,7 +154,6 @@ __device__ TILE_INLINE void tile_body(const TileArgs& t, int tile, int part, cha
             if (ALAY == kAlongK) oa[i] = (uint32_t)((min(m0 + line, t.M - 1) - m0) * lda + c * E) * kBytes;
             else oa[i] = (uint32_t)(line * lda + (min(m0 + c * E, (t.M - 1) / E * E) - m0)) * kBytes;
         }
-        if constexpr (!kQuant)
 #pragma unroll
         for (int i = 0; i < CB; i++) {
             const int q = tid + kThreads * i, line = q / TB::kLineChunks;
@@ -187,7 +174,6 @@ __device__ TILE_INLINE void tile_body(const TileArgs& t, int tile, int part, cha
         const char* a = a0 + (p ? a_next : 0) + (ALAY == kAlongK ? m0 * lda + k0 : k0 * lda + m0) * kBytes;
 #pragma unroll
         for (int i = 0; i < CA; i++) load_lds16(to + i * kThreads * 16, oa[i], a);
-        if constexpr (!kQuant)
 #pragma unroll
         for (int i = 0; i < CB; i++) {
             const int bp = MODE == kGatedForward ? ((wave * 64 + kThreads * i) / TB::kLineChunks) >> 5 & 1 : p;
@@ -195,49 +181,6 @@ __device__ TILE_INLINE void tile_body(const TileArgs& t, int tile, int part, cha
             load_lds16(to + TA::kBytes + i * kThreads * 16, ob[i], b);
         }
     };
-
-    // Packed words of a step: CQ places of (row group, lane), two words each.
-    constexpr int CQ = kQuant ? BN / 16 * 64 / kThreads : 1;
-    static_assert(!kQuant || (BF16 && CQ * kThreads == BN * 4), "whole places a thread");
-    struct Words {
-        uint2 code[CQ];
-        uint16_t scale[CQ][2];
-        uint8_t zero[CQ][2];
-    };
-    auto load_words = [&](int64_t s, Words& w) TILE_INLINE {
-        const int kt = (int)(s >> 1), half = (int)s & 1;
-#pragma unroll
-        for (int i = 0; i < CQ; i++) {
-            const int r = wave + WM * WN * i;  // row group of the tile
-            const int at = MODE == kGatedForward ? (r >> 2) * 2 + (r & 1) : r;
-            const QuantView v = t.q[MODE == kGatedForward ? r >> 1 & 1 : 0];
-            const int64_t p = (int64_t)min((int)(n0 >> 4) + at, t.row_groups - 1) * t.col_tiles + kt;
-            w.code[i] = ((const uint2*)v.codes)[(p * 64 + lane) * 2 + half];
-#pragma unroll
-            for (int j = 0; j < 2; j++) {
-                const int64_t g = (p * 16 + (lane & 15)) * t.per_tile + ((2 * half + j) * t.per_tile >> 2);
-                w.scale[i][j] = v.scales[g];
-                w.zero[i][j] = v.zeros ? v.zeros[g] : 8;
-            }
-        }
-    };
-    auto store_words = [&](const Words& w, char* l) TILE_INLINE {
-#pragma unroll
-        for (int i = 0; i < CQ; i++)
-#pragma unroll
-            for (int j = 0; j < 2; j++) {
-                const float sc = f16_bits_to_f32(w.scale[i][j]), off = -sc * (float)w.zero[i][j];
-                const uint32_t word = j ? w.code[i].y : w.code[i].x, lo = word & 0x0F0F0F0Fu, hi = word >> 4 & 0x0F0F0F0Fu;
-                bf16x8 v;
-#pragma unroll
-                for (int e = 0; e < 8; e++) {  // column e: pair e / 2, half e % 2 of the word
-                    const uint32_t b = (e / 2 % 2 ? hi : lo) >> (16 * (e % 2) + 8 * (e / 4));
-                    v[e] = (__bf16)fmaf(sc, (float)(uint8_t)b, off);
-                }
-                *(bf16x8*)(l + TA::kBytes + TB::chunk_at(16 * (wave + WM * WN * i) + (lane & 15), 4 * j + (lane >> 4))) = v;
-            }
-    };
-    Words words;
 
     f32x16 acc[FM][FN];
 #pragma unroll
@@ -280,12 +223,6 @@ __device__ TILE_INLINE void tile_body(const TileArgs& t, int tile, int part, cha
                 place_step(lds);
             }
         }
-        if constexpr (kQuant)
-            if (any) {
-                load_words(s0, words);
-                store_words(words, lds);
-                if (s0 + 1 < s1) load_words(s0 + 1, words);
-            }
         wait_loads_and_meet();
         if (s0 + 1 < s1) {
             if constexpr (FAST) load_step(s0 + 1, lds + kStage);
@@ -299,12 +236,6 @@ __device__ TILE_INLINE void tile_body(const TileArgs& t, int tile, int part, cha
         char* next = lds + ((s - s0 + 1) & 1) * kStage;
         const bool any = KW == 1 || s < s1;
         if (any) {
-            if constexpr (kQuant) {
-                if (s + 1 < s1) {
-                    store_words(words, next);
-                    if (s + 2 < s1) load_words(s + 2, words);
-                }
-            }
 #pragma unroll
             for (int kk = 0; kk < kSteps - 1; kk++) {
                 read(cur, kk + 1);
@@ -421,7 +352,7 @@ hipError_t launch_shape(TileArgs t, hipStream_t s) {
     t.m_tiles = (int)((t.M + BM - 1) / BM);
     t.n_tiles = (int)((t.N + cols - 1) / cols);
     const bool fast = fast_operand(t.a, ALAY, t.M, false, BF16) &&
-                      (BLAY == kQuantised || fast_operand(t.b, BLAY, t.N, MODE == kGatedForward, BF16));
+                      fast_operand(t.b, BLAY, t.N, MODE == kGatedForward, BF16);
     const dim3 grid((unsigned)(t.m_tiles * t.n_tiles)), block(WM * WN * KW * 64);
     if (fast) hipLaunchKernelGGL((tile_kernel<BF16, BM, BN, WM, WN, ALAY, BLAY, MODE, true, KW>), grid, block, 0, s, t);
     else hipLaunchKernelGGL((tile_kernel<BF16, BM, BN, WM, WN, ALAY, BLAY, MODE, false, KW>), grid, block, 0, s, t);
@@ -433,15 +364,15 @@ hipError_t launch_shape(TileArgs t, hipStream_t s) {
 // a step (us, with one workgroup on every CU, and with as many as a CU holds;
 // in between by the number there):
 //                   bf16         4-bit B      fp32
-//   256 x 256       1.7          1.95         -           one a CU (fp32: spills, 5.1)
-//   256 x 128       1.2          1.32         3.3         one
-//   128 x 128       0.65 - 1.2   1.06 - 1.6   1.5 - 3.2   two
-//   64 x 64         0.4 - 1.4    0.62 - 1.9   0.95 - 3.6  four
-//   64 x 64 x 4     0.9          1.25         2.0         one; four steps at a time, and
+//   256 x 256       1.7          2.2          -           one a CU (fp32: spills, 5.1)
+//   256 x 128       1.2          1.35         3.3         one
+//   128 x 128       0.65 - 1.2   1.06 - 1.5   1.5 - 3.2   two
+//   64 x 64         0.4 - 1.4    -            0.95 - 3.6  four (4-bit: never the fastest)
+//   64 x 64 x 4     0.9          1.3          2.0         one; four steps at a time, and
 //                                                         2 us to add the four sums
 // The last is for few tiles of many steps, which wait for loads one step after
 // the other: fp32 100 tokens 4096 x 512 59 us (64 x 64 107), 4-bit gated 106
-// tokens 3360 x 2226 22 (51); but bf16 1000 tokens 1024 x 1024 15 (11.5).
+// tokens 3360 x 2208 18 (128 x 128 49); but bf16 1000 tokens 1024 x 1024 15 (11.5).
 // (The backward pass also splits k into parts over workgroups: they write and
 // read partial sums in fp32, 4 MB a us, and cost a launch more, 4 us.)
 enum { kShape256, kShape256x128, kShape128, kShapeSmall, kShapeParts, kShapes };
@@ -450,7 +381,7 @@ struct TileShape { int bm, bn, per_cu, parts; float one, full; };
 constexpr int kTileCus = 256;
 static const TileShape kTileShapes[3][kShapes] = {
     {{256, 256, 1, 1, 1.7f, 1.7f}, {256, 128, 1, 1, 1.2f, 1.2f}, {128, 128, 2, 1, 0.65f, 1.2f}, {64, 64, 4, 1, 0.4f, 1.4f}, {64, 64, 1, 4, 0.9f, 0.9f}},
-    {{256, 256, 1, 1, 1.95f, 1.95f}, {256, 128, 1, 1, 1.32f, 1.32f}, {128, 128, 2, 1, 1.06f, 1.6f}, {64, 64, 4, 1, 0.62f, 1.9f}, {64, 64, 1, 4, 1.25f, 1.25f}},
+    {{256, 256, 1, 1, 2.2f, 2.2f}, {256, 128, 1, 1, 1.35f, 1.35f}, {128, 128, 2, 1, 1.06f, 1.5f}, {64, 64, 0, 1, 0.f, 0.f}, {64, 64, 1, 4, 1.3f, 1.3f}},
     {{256, 256, 0, 1, 0.f, 0.f}, {256, 128, 1, 1, 3.3f, 3.3f}, {128, 128, 2, 1, 1.5f, 3.2f}, {64, 64, 4, 1, 0.95f, 3.6f}, {64, 64, 1, 4, 2.0f, 2.0f}}};
 inline int plan_tiles(int kind, int64_t M, int64_t N, int64_t steps, float* estimate = nullptr) {
     int best = kShape128;
