@@ -532,6 +532,20 @@ moe_status moe_gated_backward(moe_ctx* ctx, const void* dh, int64_t lddh, const 
                               const void* up, void* dx, void* dw_gate, void* dw_up, void* workspace,
                               size_t workspace_bytes, moe_stream stream);
 
+/* Which kernel a call of a dense operator runs at these sizes, on the host; it is
+ * chosen by sizes and types alone (how operands are loaded depends on their
+ * alignment too).  plan (host): [0] MOE_PLAN_*, [1] tokens and [2] rows of each
+ * matrix that a workgroup takes, [3] parts of the columns that it sums, and for the
+ * backward pass, where [1] x [2] is the tile of its products, the parts over
+ * workgroups of [4] dx and [5] dw_gate and dw_up (else 1).  MOE_EINVAL for what
+ * the call itself refuses and for T = 0, where forward nothing runs. */
+#define MOE_PLAN_ROWS 0        /* each wave reads x for itself */
+#define MOE_PLAN_SHARED_ROWS 1 /* x staged once for several waves */
+#define MOE_PLAN_TILES 2       /* tiles of x and the weights */
+moe_status moe_linear_plan(int64_t T, int64_t rows, int64_t cols, int32_t group, int32_t x_dtype, int32_t y_dtype,
+                           int32_t gated, int32_t plan[6]);
+moe_status moe_gated_plan(int64_t T, int32_t d, int32_t F, int32_t dtype, int32_t backward, int32_t plan[6]);
+
 /* ---- inspection ------------------------------------------------------------- */
 
 /* Dequantise one device payload into device out [3 * d_ff * d_model] fp32 in

@@ -56,6 +56,15 @@ hipError_t launch_linear_pack(const QuantGeom& g, const uint8_t* codes, const ui
                               void* data, hipStream_t s);
 hipError_t launch_linear_dequant(const QuantGeom& g, const void* data, float* out, hipStream_t s);
 
+// The kernel of a call, chosen by sizes and types alone.
+struct DensePlan {
+    int kind;          // MOE_PLAN_*
+    int tokens, rows;  // of a workgroup; rows of each matrix (backward: the tile of both products)
+    int parts;         // of the columns (k), summed inside a workgroup
+    int dx_parts, dw_parts;  // backward: of k over workgroups
+    int shape;         // tiles: row of the table of shapes
+};
+
 struct LinearArgs {
     QuantView w[2];  // the matrix; or gate and up
     int rows, cols;  // of each
@@ -69,10 +78,11 @@ struct LinearArgs {
     int64_t ldy;
     int y_bf16;
 };
+DensePlan linear_plan(const LinearArgs& a, bool gated);
 hipError_t launch_linear(const LinearArgs& a, bool gated, hipStream_t s);
 // Many tokens, x and y bf16: on tiles; and the time that is estimated to take.
-hipError_t launch_linear_tiles(const LinearArgs& a, bool gated, hipStream_t s);
-float linear_tiles_us(const LinearArgs& a, bool gated);
+hipError_t launch_linear_tiles(const LinearArgs& a, bool gated, int shape, hipStream_t s);
+DensePlan linear_tiles_plan(const LinearArgs& a, bool gated, float* us);
 
 struct GatedArgs {
     const void* x;  // [T, d], rows ldx elements apart
@@ -84,6 +94,7 @@ struct GatedArgs {
     void* h;                    // [T, F]
     void *gate, *up;            // [T, F] or null
 };
+DensePlan gated_plan(int64_t T, int d, int F, int bf16);
 hipError_t launch_gated(const GatedArgs& a, hipStream_t s);
 
 struct GatedBackwardArgs {
@@ -100,6 +111,7 @@ struct GatedBackwardArgs {
     void *dw_gate, *dw_up;      // [F, d] or null
     void* workspace;
 };
+DensePlan gated_backward_plan(int64_t T, int d, int F, int bf16);
 size_t gated_backward_bytes(int64_t T, int d, int F, int bf16);
 hipError_t launch_gated_backward(const GatedBackwardArgs& a, hipStream_t s);
 

@@ -194,10 +194,7 @@ __global__ __launch_bounds__(512) void gated_rows_kernel(GatedArgs a) {
 }
 
 template <bool BF16, int MT, int TI>
-hipError_t launch_gated_rows(const GatedArgs& a, hipStream_t s) {
-    const int tiles = (a.d + 16 * Elem<BF16>::kChunk - 1) / (16 * Elem<BF16>::kChunk);
-    int waves = 1;
-    while (waves < 8 && waves < tiles) waves *= 2;
+hipError_t launch_gated_rows(const GatedArgs& a, int waves, hipStream_t s) {
     const dim3 grid((a.F + 15) / 16, (unsigned)((a.T + 16 * MT - 1) / (16 * MT)));
     hipLaunchKernelGGL((gated_rows_kernel<BF16, MT, TI>), grid, dim3(64 * waves), 2 * waves * MT * TI * 64 * sizeof(float), s, a);
     return hipGetLastError();
@@ -210,13 +207,13 @@ hipError_t launch_gated_rows(const GatedArgs& a, hipStream_t s) {
 // 2.4 us and 1 for each 16.  Measured, us, 1 or 2, 4, and the tiles: fp32 100
 // tokens 4096 x 512 41, 67, 59, 463 tokens 2005 x 350 43, 38, 51; bf16 100
 // tokens 4096 x 512 17, 25, 15, 135 tokens 288 x 224 4.4, 6.1, 6.2.
-int plan_rows(const GatedArgs& a, float* us) {
-    const int cols = a.bf16 ? 128 : 64, tiles = (a.d + cols - 1) / cols;
+int plan_rows(int64_t T, int d, int F, int bf16, float* us) {
+    const int cols = bf16 ? 128 : 64, tiles = (d + cols - 1) / cols;
     int best = 4;
     *us = 1e30f;
     for (int mt = 1; mt <= 4; mt *= 2) {
-        const int64_t groups = (int64_t)((a.F + 15) / 16) * ((a.T + 16 * mt - 1) / (16 * mt));
-        const float t = (float)((tiles + 7) / 8) * (float)((groups + kTileCus - 1) / kTileCus) * (a.bf16 ? 2.4f + mt : 0.4f + 2.f * mt);
+        const int64_t groups = (int64_t)((F + 15) / 16) * ((T + 16 * mt - 1) / (16 * mt));
+        const float t = (float)((tiles + 7) / 8) * (float)((groups + kTileCus - 1) / kTileCus) * (bf16 ? 2.4f + mt : 0.4f + 2.f * mt);
         if (t < *us) {
             best = mt;
             *us = t;
@@ -227,15 +224,11 @@ int plan_rows(const GatedArgs& a, float* us) {
 
 template <bool BF16>
 hipError_t gated(const GatedArgs& a, hipStream_t s) {
-    if (a.T <= 4) return launch_gated_rows<BF16, 1, 1>(a, s);
-    if (a.T <= 16) return launch_gated_rows<BF16, 1, 4>(a, s);
-    // (gate and up columns alternate: twice F of them)
-    float tiles_us, rows_us;
-    const int shape = plan_tiles(BF16 ? kBf16 : kFp32, a.T, 2 * (int64_t)a.F, steps_of(a.d, BF16), &tiles_us);
-    const int mt = plan_rows(a, &rows_us);
-    if (rows_us < tiles_us + 1.5f) {
-        if (mt == 1) return launch_gated_rows<BF16, 1, 4>(a, s);
-        return mt == 2 ? launch_gated_rows<BF16, 2, 4>(a, s) : launch_gated_rows<BF16, 4, 4>(a, s);
+    const DensePlan p = gated_plan(a.T, a.d, a.F, BF16);
+    if (p.kind == MOE_PLAN_ROWS) {
+        if (p.tokens == 4) return launch_gated_rows<BF16, 1, 1>(a, p.parts, s);
+        if (p.tokens == 16) return launch_gated_rows<BF16, 1, 4>(a, p.parts, s);
+        return p.tokens == 32 ? launch_gated_rows<BF16, 2, 4>(a, p.parts, s) : launch_gated_rows<BF16, 4, 4>(a, p.parts, s);
     }
     TileArgs t{};
     t.a = Operand{{a.x, nullptr}, a.ldx, 0};
@@ -247,7 +240,7 @@ hipError_t gated(const GatedArgs& a, hipStream_t s) {
     t.ldo = a.F;
     t.gate = a.gate;
     t.up = a.up;
-    return launch_tiles<BF16, kAlongK, kAlongK, kGatedForward>(t, shape, s);
+    return launch_tiles<BF16, kAlongK, kAlongK, kGatedForward>(t, p.shape, s);
 }
 
 struct BackwardPlan {
@@ -365,6 +358,27 @@ hipError_t gated_backward(const GatedBackwardArgs& a, hipStream_t s) {
 }
 
 }  // namespace
+
+DensePlan gated_plan(int64_t T, int d, int F, int bf16) {
+    int waves = 1;
+    while (waves < 8 && waves < (d + (bf16 ? 127 : 63)) / (bf16 ? 128 : 64)) waves *= 2;
+    if (T <= 4) return {MOE_PLAN_ROWS, 4, 16, waves, 1, 1, 0};
+    if (T <= 16) return {MOE_PLAN_ROWS, 16, 16, waves, 1, 1, 0};
+    // (gate and up columns alternate: twice F of them)
+    float tiles_us, rows_us;
+    const int kind = bf16 ? kBf16 : kFp32, shape = plan_tiles(kind, T, 2 * (int64_t)F, steps_of(d, bf16), &tiles_us);
+    const int mt = plan_rows(T, d, F, bf16, &rows_us);
+    if (rows_us < tiles_us + 1.5f) return {MOE_PLAN_ROWS, 16 * mt, 16, waves, 1, 1, 0};
+    return tiles_plan(kind, shape, true);
+}
+
+DensePlan gated_backward_plan(int64_t T, int d, int F, int bf16) {
+    const BackwardPlan p = backward_plan(T, d, F, bf16);
+    DensePlan plan = tiles_plan(bf16 ? kBf16 : kFp32, p.shape, false);
+    plan.dx_parts = p.dx_splits;
+    plan.dw_parts = p.dw_splits;
+    return plan;
+}
 
 hipError_t launch_gated(const GatedArgs& a, hipStream_t s) { return a.bf16 ? gated<true>(a, s) : gated<false>(a, s); }
 

@@ -76,16 +76,22 @@ hipError_t launch_linear_dequant(const QuantGeom& g, const void* data, float* ou
 // 9.9; 106 tokens, gated 3360 x 2208, groups of 32 19.2 / 18.4; 128 tokens, gated
 // 8192 x 2048 22 / 27, 256 tokens 44 / 37; 512 tokens, 4096 x 4096, groups of 32 50
 // / 58; 2048 tokens, 4096 x 4096 190 / 88.
-static bool tiles_faster(const LinearArgs& a, bool gated) {
-    const float on_cu = (float)((a.row_groups + 3) / 4) * (float)((a.T + 63) / 64) / 256.f;
-    const float few = gated ? 1.5f : 0.9f, full = gated ? 3.1f : 1.5f;
-    const float rows_us = (float)((a.col_tiles + 1) / 2) * (on_cu < 1.f ? few + (full - few) * on_cu : full * on_cu);
-    return linear_tiles_us(a, gated) + 1.5f < rows_us;
+DensePlan linear_plan(const LinearArgs& a, bool gated) {
+    if (a.T > 64 && a.x_bf16 && a.y_bf16) {
+        const float on_cu = (float)((a.row_groups + 3) / 4) * (float)((a.T + 63) / 64) / 256.f;
+        const float few = gated ? 1.5f : 0.9f, full = gated ? 3.1f : 1.5f;
+        const float rows_us = (float)((a.col_tiles + 1) / 2) * (on_cu < 1.f ? few + (full - few) * on_cu : full * on_cu);
+        float tiles_us;
+        const DensePlan tiles = linear_tiles_plan(a, gated, &tiles_us);
+        if (tiles_us + 1.5f < rows_us) return tiles;
+    }
+    return linear::rows_plan(a);
 }
 
 hipError_t launch_linear(const LinearArgs& a, bool gated, hipStream_t s) {
-    if (a.T > 64 && a.x_bf16 && a.y_bf16 && tiles_faster(a, gated)) return launch_linear_tiles(a, gated, s);
-    return a.x_bf16 ? launch_linear_rows_bf16(a, gated, s) : launch_linear_rows_f32(a, gated, s);
+    const DensePlan p = linear_plan(a, gated);
+    if (p.kind == MOE_PLAN_TILES) return launch_linear_tiles(a, gated, p.shape, s);
+    return a.x_bf16 ? launch_linear_rows_bf16(a, gated, p, s) : launch_linear_rows_f32(a, gated, p, s);
 }
 
 }  // namespace moe

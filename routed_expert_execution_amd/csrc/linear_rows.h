@@ -355,9 +355,7 @@ hipError_t launch_shared(const LinearArgs& a, hipStream_t s) {
 }
 
 template <bool XBF16, int TI, int R, bool GATED>
-hipError_t launch_rows(const LinearArgs& a, int most_waves, hipStream_t s) {
-    int waves = 1;
-    while (waves < most_waves && waves < a.col_tiles) waves *= 2;
+hipError_t launch_rows(const LinearArgs& a, int waves, hipStream_t s) {
     const dim3 grid((a.row_groups + R - 1) / R), block(64 * waves);
     const size_t lds = (size_t)(GATED ? 2 : 1) * waves * TI * 64 * sizeof(float);
     if (a.group == 32) hipLaunchKernelGGL((rows_kernel<XBF16, TI, R, 4, GATED>), grid, block, lds, s, a);
@@ -377,18 +375,31 @@ hipError_t launch_rows(const LinearArgs& a, int most_waves, hipStream_t s) {
 //   64 tokens, 4096 x 4096: 2 row groups and 4 parts 15, 4 and 2 23; 37 tokens,
 //     gated 10240 x 4096: 50 and 41: fewer parts once the workgroups fill half
 //     the CUs.
+inline DensePlan rows_plan(const LinearArgs& a) {
+    if (a.T <= 16) {
+        const bool two = a.x_bf16 ? a.T <= 4 && a.row_groups >= 4096 : a.T > 4 && a.row_groups >= 256;
+        const int most = a.x_bf16 && two ? 4 : 8;
+        int waves = 1;
+        while (waves < most && waves < a.col_tiles) waves *= 2;
+        return {MOE_PLAN_ROWS, a.T <= 4 ? 4 : 16, two ? 32 : 16, waves, 1, 1, 0};
+    }
+    if (!a.x_bf16) return {MOE_PLAN_SHARED_ROWS, 32, 64, 2, 1, 1, 0};
+    if (a.T <= 32) return {MOE_PLAN_SHARED_ROWS, 32, 64, 4, 1, 1, 0};
+    const bool few = (a.row_groups + 3) / 4 * ((a.T + 63) / 64) <= 128;
+    return {MOE_PLAN_SHARED_ROWS, a.T <= 48 ? 48 : 64, few ? 32 : 64, few ? 4 : 2, 1, 1, 0};
+}
+
 template <bool XBF16, bool GATED>
-hipError_t launch_rows_t(const LinearArgs& a, hipStream_t s) {
+hipError_t launch_rows_t(const LinearArgs& a, const DensePlan& p, hipStream_t s) {
     if constexpr (XBF16) {
-        if (a.T <= 4) return a.row_groups >= 4096 ? launch_rows<true, 1, 2, GATED>(a, 4, s) : launch_rows<true, 1, 1, GATED>(a, 8, s);
-        if (a.T <= 16) return launch_rows<true, 4, 1, GATED>(a, 8, s);
-        if (a.T <= 32) return launch_shared<true, 2, 4, 4, GATED>(a, s);
-        const bool few = (a.row_groups + 3) / 4 * ((a.T + 63) / 64) <= 128;
-        if (a.T <= 48) return few ? launch_shared<true, 3, 2, 4, GATED>(a, s) : launch_shared<true, 3, 4, 2, GATED>(a, s);
-        return few ? launch_shared<true, 4, 2, 4, GATED>(a, s) : launch_shared<true, 4, 4, 2, GATED>(a, s);
+        if (p.tokens == 4) return p.rows == 32 ? launch_rows<true, 1, 2, GATED>(a, p.parts, s) : launch_rows<true, 1, 1, GATED>(a, p.parts, s);
+        if (p.tokens == 16) return launch_rows<true, 4, 1, GATED>(a, p.parts, s);
+        if (p.tokens == 32) return launch_shared<true, 2, 4, 4, GATED>(a, s);
+        if (p.tokens == 48) return p.rows == 32 ? launch_shared<true, 3, 2, 4, GATED>(a, s) : launch_shared<true, 3, 4, 2, GATED>(a, s);
+        return p.rows == 32 ? launch_shared<true, 4, 2, 4, GATED>(a, s) : launch_shared<true, 4, 4, 2, GATED>(a, s);
     } else {
-        if (a.T <= 4) return launch_rows<false, 1, 1, GATED>(a, 8, s);
-        if (a.T <= 16) return a.row_groups >= 256 ? launch_rows<false, 4, 2, GATED>(a, 8, s) : launch_rows<false, 4, 1, GATED>(a, 8, s);
+        if (p.tokens == 4) return launch_rows<false, 1, 1, GATED>(a, p.parts, s);
+        if (p.tokens == 16) return p.rows == 32 ? launch_rows<false, 4, 2, GATED>(a, p.parts, s) : launch_rows<false, 4, 1, GATED>(a, p.parts, s);
         return launch_shared<false, 2, 4, 2, GATED>(a, s);
     }
 }
@@ -396,7 +407,7 @@ hipError_t launch_rows_t(const LinearArgs& a, hipStream_t s) {
 }  // namespace linear
 
 // One translation unit each (linear_bf16.hip, linear_f32.hip).
-hipError_t launch_linear_rows_bf16(const LinearArgs& a, bool gated, hipStream_t s);
-hipError_t launch_linear_rows_f32(const LinearArgs& a, bool gated, hipStream_t s);
+hipError_t launch_linear_rows_bf16(const LinearArgs& a, bool gated, const DensePlan& p, hipStream_t s);
+hipError_t launch_linear_rows_f32(const LinearArgs& a, bool gated, const DensePlan& p, hipStream_t s);
 
 }  // namespace moe

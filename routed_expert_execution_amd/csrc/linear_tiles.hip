@@ -349,22 +349,16 @@ hipError_t launch_shape4(const QuantTileArgs& t, int shape, hipStream_t s) {
     }
 }
 
-int plan(const LinearArgs& a, bool gated, float* us = nullptr) {
-    const int shape = plan_tiles(kQuant4, a.T, (int64_t)a.rows * (gated ? 2 : 1), (a.cols + 63) / 64, us);
-    if (us && a.group == 32) *us *= 1.25f;  // (two additions a step: 1.2 to 1.28 in every shape)
-    return shape;
-}
-
 }  // namespace
 }  // namespace tile
 
-float linear_tiles_us(const LinearArgs& a, bool gated) {
-    float us;
-    tile::plan(a, gated, &us);
-    return us;
+DensePlan linear_tiles_plan(const LinearArgs& a, bool gated, float* us) {
+    const int shape = tile::plan_tiles(tile::kQuant4, a.T, (int64_t)a.rows * (gated ? 2 : 1), (a.cols + 63) / 64, us);
+    if (a.group == 32) *us *= 1.25f;  // (two additions a step: 1.2 to 1.28 in every shape)
+    return tile::tiles_plan(tile::kQuant4, shape, gated);
 }
 
-hipError_t launch_linear_tiles(const LinearArgs& a, bool gated, hipStream_t s) {
+hipError_t launch_linear_tiles(const LinearArgs& a, bool gated, int shape, hipStream_t s) {
     tile::QuantTileArgs t{};
     t.x = tile::Operand{{a.x, nullptr}, a.ldx, 0};
     t.M = a.T;
@@ -377,7 +371,6 @@ hipError_t launch_linear_tiles(const LinearArgs& a, bool gated, hipStream_t s) {
     t.per_tile = 128 / a.group;
     t.row_groups = a.row_groups;
     t.col_tiles = a.col_tiles;
-    const int shape = tile::plan(a, gated);
     return gated ? tile::launch_shape4<true>(t, shape, s) : tile::launch_shape4<false>(t, shape, s);
 }
 

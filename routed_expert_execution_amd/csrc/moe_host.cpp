@@ -1517,6 +1517,35 @@ moe_status moe_gated_backward(moe_ctx* c, const void* dh, int64_t lddh, const vo
     return MOE_OK;
 }
 
+static void plan_out(const moe::DensePlan& p, int32_t out[6]) {
+    const int v[6] = {p.kind, p.tokens, p.rows, p.parts, p.dx_parts, p.dw_parts};
+    std::copy(v, v + 6, out);
+}
+
+moe_status moe_linear_plan(int64_t T, int64_t rows, int64_t cols, int32_t group, int32_t x_dtype, int32_t y_dtype,
+                           int32_t gated, int32_t plan[6]) {
+    moe::QuantGeom g;
+    if (!plan || !g.init(rows, cols, group, 0) || T < 1 || T > kDenseMaxT || !dtype_valid(x_dtype) || !dtype_valid(y_dtype))
+        return MOE_EINVAL;
+    moe::LinearArgs a{};
+    a.rows = (int)g.rows;
+    a.cols = (int)g.cols;
+    a.row_groups = (int)g.row_groups;
+    a.col_tiles = (int)g.col_tiles;
+    a.group = g.group;
+    a.T = T;
+    a.x_bf16 = x_dtype == MOE_BF16;
+    a.y_bf16 = y_dtype == MOE_BF16;
+    plan_out(moe::linear_plan(a, gated != 0), plan);
+    return MOE_OK;
+}
+
+moe_status moe_gated_plan(int64_t T, int32_t d, int32_t F, int32_t dtype, int32_t backward, int32_t plan[6]) {
+    if (!plan || T < 1 || !gated_sizes(T, d, F) || !dtype_valid(dtype)) return MOE_EINVAL;
+    plan_out(backward ? moe::gated_backward_plan(T, d, F, dtype == MOE_BF16) : moe::gated_plan(T, d, F, dtype == MOE_BF16), plan);
+    return MOE_OK;
+}
+
 moe_status moe_stats(const moe_ctx* c, uint64_t out[5]) {
     if (!c || !out) return MOE_EINVAL;
     for (int i = 0; i < 5; i++) out[i] = c->stats[i];

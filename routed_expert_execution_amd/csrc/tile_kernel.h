@@ -402,6 +402,11 @@ inline int plan_tiles(int kind, int64_t M, int64_t N, int64_t steps, float* esti
     return best;
 }
 
+inline DensePlan tiles_plan(int kind, int shape, bool gated) {
+    const TileShape& c = kTileShapes[kind][shape];
+    return {MOE_PLAN_TILES, c.bm, gated ? c.bn / 2 : c.bn, c.parts, 1, 1, shape};
+}
+
 template <bool BF16, int ALAY, int BLAY, int MODE>
 hipError_t launch_tiles(TileArgs t, int shape, hipStream_t s) {
     t.products = t.splits = 1;

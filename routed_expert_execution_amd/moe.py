@@ -22,6 +22,7 @@ MOE_Q8_0, MOE_Q4_0 = 0, 1
 MOE_F32, MOE_BF16 = 0, 1
 MOE_PREC_F32, MOE_PREC_BF16 = 0, 1
 MOE_MAX_STAGE_STREAMS = 8
+MOE_PLAN_ROWS, MOE_PLAN_SHARED_ROWS, MOE_PLAN_TILES = 0, 1, 2
 
 
 class MoeError(RuntimeError):
@@ -95,6 +96,8 @@ def _load() -> C.CDLL:
         "moe_gated": (C.c_int, [P, P, I32, I64, I64, I32, I32, P, P, P, P, P, P]),
         "moe_gated_workspace": (S, [I64, I32, I32, I32]),
         "moe_gated_backward": (C.c_int, [P, P, I64, P, I32, I64, I64, I32, I32, P, P, P, P, P, P, P, P, S, P]),
+        "moe_linear_plan": (C.c_int, [I64, I64, I64, I32, I32, I32, I32, C.POINTER(I32)]),
+        "moe_gated_plan": (C.c_int, [I64, I32, I32, I32, I32, C.POINTER(I32)]),
         "moe_stats": (C.c_int, [P, C.POINTER(C.c_uint64)]),
         "moe_check": (C.c_int, [P, P]),
         "moe_page_table": (C.c_int, [P, C.POINTER(P)]),
@@ -118,7 +121,8 @@ EXPORTS = ("moe_payload_bytes", "moe_plan_bytes", "moe_pack_expert", "moe_unpack
            "moe_slot_bind", "moe_expert_ffn", "moe_expert_ffn_static", "moe_expert_ffn_split",
            "moe_route_ffn", "moe_dequant", "moe_stats", "moe_check", "moe_page_table", "moe_route_splits", "moe_hidden_rows", "moe_probe_read",
            "moe_probe_mfma", "moe_probe_lds", "moe_linear_bytes", "moe_linear_pack", "moe_linear_dequant", "moe_linear",
-           "moe_linear_gated", "moe_gated", "moe_gated_workspace", "moe_gated_backward")
+           "moe_linear_gated", "moe_gated", "moe_gated_workspace", "moe_gated_backward", "moe_linear_plan",
+           "moe_gated_plan")
 
 
 def library() -> C.CDLL:
@@ -696,6 +700,22 @@ def moe_gated_backward(ctx: Context, dh, x, w_gate, w_up, gate, up, *, dx=None, 
     _call(ctx, _lib.moe_gated_backward(ctx.handle, dp, lddh, xp, xd, ldx, T, d, F, wg, wu, gp, up_, dxp, dwg, dwu,
                                        _ptr(workspace), workspace.numel() * workspace.element_size(),
                                        _stream_on(ctx, stream)))
+
+
+def moe_linear_plan(T: int, rows: int, cols: int, group: int, x_dtype, y_dtype, gated: bool = False) -> tuple:
+    """(kind, tokens, rows, parts, 1, 1) of the kernel that moe_linear or, gated,
+    moe_linear_gated runs at these sizes; kind MOE_PLAN_*."""
+    out = (C.c_int32 * 6)()
+    _call(None, _lib.moe_linear_plan(T, rows, cols, group, _TYPE_CODES.get(x_dtype, -1), _TYPE_CODES.get(y_dtype, -1), int(gated), out))
+    return tuple(out)
+
+
+def moe_gated_plan(T: int, d: int, F: int, dtype, backward: bool = False) -> tuple:
+    """(kind, tokens, rows, parts, parts of dx, of the weights' gradients) of the
+    kernel that moe_gated or moe_gated_backward runs at these sizes."""
+    out = (C.c_int32 * 6)()
+    _call(None, _lib.moe_gated_plan(T, d, F, _TYPE_CODES.get(dtype, -1), int(backward), out))
+    return tuple(out)
 
 
 def moe_stats(ctx: Context) -> dict:
