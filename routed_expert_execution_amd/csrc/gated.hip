@@ -366,7 +366,7 @@ DensePlan gated_plan(int64_t T, int d, int F, int bf16) {
     if (T <= 16) return {MOE_PLAN_ROWS, 16, 16, waves, 1, 1, 0};
     // (gate and up columns alternate: twice F of them)
     float tiles_us, rows_us;
-    const int kind = bf16 ? kBf16 : kFp32, shape = plan_tiles(kind, T, 2 * (int64_t)F, steps_of(d, bf16), &tiles_us);
+    const int kind = bf16 ? kBf16 : kFp32, shape = plan_tiles(kind, T, 2 * (int64_t)F, steps_of(d, bf16), bf16 ? kShapes : kShape256x128, &tiles_us);
     const int mt = plan_rows(T, d, F, bf16, &rows_us);
     if (rows_us < tiles_us + 1.5f) return {MOE_PLAN_ROWS, 16 * mt, 16, waves, 1, 1, 0};
     return tiles_plan(kind, shape, true);

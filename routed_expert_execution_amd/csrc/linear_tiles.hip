@@ -330,7 +330,8 @@ hipError_t launch_quant(QuantTileArgs t, hipStream_t s) {
     const bool fast = fast_operand(t.x, kAlongK, t.M, false, true);
     const dim3 grid((unsigned)(t.m_tiles * t.n_tiles)), block(WM * WN * KW * 64);
     if (t.per_tile == 4) {
-        if (fast) hipLaunchKernelGGL((quant_tile_kernel<BM, BN, WM, WN, GATED, true, true, KW>), grid, block, 0, s, t);
+        if constexpr (!GATED && KW > 1) return hipErrorInvalidValue;
+        else if (fast) hipLaunchKernelGGL((quant_tile_kernel<BM, BN, WM, WN, GATED, true, true, KW>), grid, block, 0, s, t);
         else hipLaunchKernelGGL((quant_tile_kernel<BM, BN, WM, WN, GATED, true, false, KW>), grid, block, 0, s, t);
     } else {
         if (fast) hipLaunchKernelGGL((quant_tile_kernel<BM, BN, WM, WN, GATED, false, true, KW>), grid, block, 0, s, t);
@@ -353,7 +354,10 @@ hipError_t launch_shape4(const QuantTileArgs& t, int shape, hipStream_t s) {
 }  // namespace tile
 
 DensePlan linear_tiles_plan(const LinearArgs& a, bool gated, float* us) {
-    const int shape = tile::plan_tiles(tile::kQuant4, a.T, (int64_t)a.rows * (gated ? 2 : 1), (a.cols + 63) / 64, us);
+    // (64 x 64 in four parts is the shape of the shared rows' workgroups: with groups
+    // of 32, not gated, they are faster at every size)
+    const int but = a.group == 32 && !gated ? tile::kShapeParts : tile::kShapes;
+    const int shape = tile::plan_tiles(tile::kQuant4, a.T, (int64_t)a.rows * (gated ? 2 : 1), (a.cols + 63) / 64, but, us);
     if (a.group == 32) *us *= 1.25f;  // (two additions a step: 1.2 to 1.28 in every shape)
     return tile::tiles_plan(tile::kQuant4, shape, gated);
 }

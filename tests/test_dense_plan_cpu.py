@@ -3,10 +3,13 @@ the GPU tests run hold every kernel that any size takes, and no other."""
 import ctypes as C
 import math
 import random
+import re
+import shutil
+import subprocess
 
 import pytest
 
-from routed_expert_execution_amd import moe
+from routed_expert_execution_amd import build, moe
 from tests import dense_cases as D
 
 torch = pytest.importorskip("torch")
@@ -87,3 +90,30 @@ def test_plans_refuse():
         moe.moe_linear_plan(1, 32, 128, 32, torch.float16, F32)
     with pytest.raises(moe.MoeError):
         moe.moe_gated_plan(1, 8, 8, torch.float16)
+
+
+def test_no_kernel_is_compiled_that_no_size_takes():
+    """The kernels in the library's symbols against those of the cases."""
+    nm = shutil.which("nm")
+    if nm is None:
+        pytest.skip("no nm")
+    text = subprocess.run([nm, "-C", build.LIB], check=True, capture_output=True, text=True).stdout
+    built = {}
+    for name, args in re.findall(r"(?<!__device_stub__)\b(\w+_kernel)<([^>]*)>", text):
+        built.setdefault(name, set()).add(tuple({"true": True, "false": False}.get(a, a if not a.isdigit() else int(a)) for a in args.split(", ")))
+    rows, shared, tiles = set(), set(), set()
+    for gated, bf16, (kind, tokens, n, parts), half, whole in D.LINEAR:
+        for s in (4, 2, 1):
+            if kind == D.ROWS:
+                rows.add((bf16, 1 if tokens == 4 else 4, n // 16, s, gated))
+            elif kind == D.SHARED:
+                shared.add((bf16, tokens // 16, n // 16, parts, s, gated))
+            elif s < 4 or half:
+                tiles |= {(tokens, n * (2 if gated else 1), gated, s == 4, fast, parts) for fast in (False, True)}
+    assert built["rows_kernel"] == rows and built["shared_rows_kernel"] == shared
+    assert {t[:2] + t[4:] for t in built["quant_tile_kernel"]} == tiles
+    forward = {(b, p[1], 2 * p[2], fast, p[3]) for b, p, *_ in D.GATED if p[0] == D.TILES for fast in (False, True)}
+    assert {t[:3] + t[8:] for t in built["tile_kernel"]} == forward
+    few = {(b, max(1, p[1] // 16), 1 if p[1] == 4 else 4) for b, p, *_ in D.GATED if p[0] == D.ROWS}
+    assert built["gated_rows_kernel"] == few
+    assert {t[:3] + t[5:] for t in built["backward_tiles_kernel"]} == {(b, *tile, fast) for b, tile, *_ in D.BACKWARD for fast in (False, True)}
