@@ -487,8 +487,8 @@ moe_status moe_linear_dequant(moe_ctx* ctx, const moe_qmat* m, float* out, moe_s
  * x: device [T, w->cols] (x_dtype), rows ldx apart; y: device [T, w->rows]
  * (y_dtype: MOE_F32 or MOE_BF16), rows ldy apart.
  * Sums, scales and zero points are fp32 and neither x (fp32 x enters the matrix
- * cores as three bf16 terms) nor a weight is rounded, whatever the number of
- * tokens.  A token's row that holds an infinity or NaN gives a row that is not
+ * cores as three bf16 terms, exact from 2^-110 up and to 2^-134 below that) nor a
+ * weight is rounded, whatever the number of tokens.  A token's row that holds an infinity or NaN gives a row that is not
  * finite; other rows are not touched by it.  Finite x should stay below 2^120
  * (codes enter the sums of bf16 x as 16 + q). */
 moe_status moe_linear(moe_ctx* ctx, const void* x, int32_t x_dtype, int64_t ldx, int64_t T, const moe_qmat* w, void* y,
@@ -507,9 +507,9 @@ moe_status moe_linear_gated(moe_ctx* ctx, const void* x, int32_t x_dtype, int64_
  * x: device [T, d], rows ldx apart; w_gate, w_up: device [F, d]; h: device
  * [T, F].  gate, up: device [T, F] or NULL, g and u for moe_gated_backward
  * (both or neither).  Sums are fp32; h comes from the unrounded g and u.  fp32
- * factors enter the matrix cores as three bf16 terms of 24 bits together (in
- * calls of more than 16 tokens and in the backward pass): an infinity there
- * gives NaN, as does a value above 3.38e38.
+ * factors enter the matrix cores as three bf16 terms (in calls of more than 16
+ * tokens and in the backward pass): 24 bits together from 2^-110 up, to 2^-134
+ * below that; an infinity there gives NaN, as does a value above 3.38e38.
  * Sizes: d and F from 1 to 2^20, T up to 2^20. */
 moe_status moe_gated(moe_ctx* ctx, const void* x, int32_t dtype, int64_t ldx, int64_t T, int32_t d, int32_t F,
                      const void* w_gate, const void* w_up, void* h, void* gate, void* up, moe_stream stream);

@@ -10,8 +10,9 @@ typedef __bf16 bf16x8_t __attribute__((ext_vector_type(8)));
 typedef __bf16 bf16x2_t __attribute__((ext_vector_type(2)));
 
 // v = t[0] + t[1] + t[2], each term the rounding of what the ones before leave:
-// 24 bits, all of a normal fp32 value (past 3.39e38, the largest bf16, the first
-// term is an infinity).  What a term leaves is exact, so it may be taken as a
+// 24 bits, all of an fp32 value from 2^-110 up.  Of a smaller one what lies below
+// bf16's least value, 2^-133, is rounded off: at most 2^-134.  (Past 3.39e38, the
+// largest bf16, the first term is an infinity.)  What a term leaves is exact, so it may be taken as a
 // dot product with (-1, 0) or (0, -1): one instruction in place of a shift and
 // a subtraction, 3.5 a value in all.  The two constants pass through a register
 // because the instruction reads an inline -1.0 as fp32's bits, the other half.

@@ -89,3 +89,106 @@ def test_many_tokens_round_no_weight(ctx, T, K, N, pad, group, affine):
     h = g * torch.sigmoid(g) * u
     _within(y[:, :N], h, 1.1 * tg * (u.abs() + tu) + (g * torch.sigmoid(g)).abs() * tu + (8 + 2 * g.abs()) * U * h.abs())
     assert (y[:, N:] == 777.0).all()
+
+
+# ---- fp32 factors as three bf16 terms ----
+#
+# Against the identity a product is its other factor, so that the terms' sum shows:
+# all 24 bits of a value from 2^-110 up (two terms would leave 2^-17 of it), and at
+# most 2^-134, half of bf16's least value, off below that.
+
+def _whole(gen, rows, cols, e):
+    """fp32 values of 24 bits and both signs in [2^e, 2^(e + 1))."""
+    m = 1 + torch.rand(rows, cols, generator=gen, device="cuda", dtype=torch.float64)
+    return (m * torch.where(torch.rand(rows, cols, generator=gen, device="cuda") < 0.5, -1.0, 1.0) * 2.0 ** e).float()
+
+
+def _same(y, x, e, what):
+    if e >= -110:
+        assert torch.equal(y, x), (what, e, (y - x).abs().max())
+    else:
+        assert ((y.double() - x.double()).abs() <= 2.0 ** -134).all(), (what, e)
+
+
+EXPONENTS = [-130, -120, -111, -110, -60, -1, 0, 40, 110]
+
+
+@pytest.mark.parametrize("T,N", [(1, 128), (9, 128), (9, 4224), (40, 128)])
+def test_fp32_x_is_whole_in_4_bit_products(ctx, T, N):
+    """Codes of 9 on the diagonal and of 8, the zero point, elsewhere."""
+    K = 128
+    c = torch.full((N, K), 8, dtype=torch.uint8, device="cuda")
+    c[:K].fill_diagonal_(9)
+    w = moe.QuantMatrix(ctx, (c[:, 0::2] | c[:, 1::2] << 4).contiguous(), torch.ones(N, 1, dtype=torch.float16, device="cuda"))
+    for e in EXPONENTS:
+        x = _whole(_gen(e + 200), T, K, e)
+        y = torch.empty(T, N, device="cuda")
+        moe.moe_linear(ctx, x, w, y)
+        _same(y[:, :K], x, e, "x")
+        assert (y[:, K:] == 0).all()
+
+
+# (T, d, F) of the rows kernels, and of each tile
+@pytest.mark.parametrize("T,F,kind", [(3, 130, 0), (16, 130, 0), (40, 130, 0), (18, 4365, 2), (21, 8949, 2), (4099, 132, 2)])
+def test_fp32_factors_are_whole_in_the_gated_block(ctx, T, F, kind):
+    d = 128 if F < 4000 else 132
+    assert moe.moe_gated_plan(T, d, F, F32)[0] == kind
+    n = min(d, F)
+    eye = torch.zeros(F, d, device="cuda")
+    eye[:n].fill_diagonal_(1.0)
+    for e in EXPONENTS:
+        x = _whole(_gen(e + 300), T, d, e)
+        wg, wu = eye, 2 * eye
+        h, gate, up = (torch.empty(T, F, device="cuda") for _ in range(3))
+        moe.moe_gated(ctx, x, wg, wu, h, gate_out=gate, up_out=up)
+        _same(gate[:, :n], x[:, :n], e, "gate")
+        _same(up[:, :n] / 2, x[:, :n], e, "up")
+        # the weights' bits: tokens that are unit vectors
+        tokens = torch.zeros(T, d, device="cuda")
+        tokens[:min(T, d)].fill_diagonal_(1.0)
+        m = min(T, d)
+        wg, wu = _whole(_gen(e + 400), F, d, e), _whole(_gen(e + 500), F, d, e)
+        moe.moe_gated(ctx, tokens, wg, wu, h, gate_out=gate, up_out=up)
+        _same(gate[:m], wg[:, :m].t(), e, "w_gate")
+        _same(up[:m], wu[:, :m].t(), e, "w_up")
+
+
+@pytest.mark.parametrize("T,d,F", [(129, 2384, 115), (107, 116, 105), (141, 916, 1051), (145, 2373, 121)])
+def test_fp32_factors_are_whole_in_the_backward_pass(ctx, T, d, F):
+    """With gate 0 and up 2, dg is dh and du is 0: against identities dx is dh and
+    dw_gate its transpose; against unit vectors they are the weights and x."""
+    ws = torch.empty(moe.moe_gated_workspace(ctx, T, d, F, F32), dtype=torch.uint8, device="cuda")
+    zero, two = torch.zeros(T, F, device="cuda"), torch.full((T, F), 2.0, device="cuda")
+    dx, dwg, dwu = (torch.empty(s, device="cuda") for s in ((T, d), (F, d), (F, d)))
+
+    def backward(dh, x, wg):
+        moe.moe_gated_backward(ctx, dh, x, wg, wg, zero, two, dx=dx, dw_gate=dwg, dw_up=dwu, workspace=ws)
+
+    eye_w, eye_x, eye_h = torch.zeros(F, d, device="cuda"), torch.zeros(T, d, device="cuda"), torch.zeros(T, F, device="cuda")
+    a, b, c = min(F, d), min(T, d), min(T, F)
+    eye_w[:a].fill_diagonal_(1.0), eye_x[:b].fill_diagonal_(1.0), eye_h[:c].fill_diagonal_(1.0)
+    for e in EXPONENTS:
+        dh, x, wg = (_whole(_gen(e + i), *s, e) for i, s in ((600, (T, F)), (700, (T, d)), (800, (F, d))))
+        backward(dh, eye_x, eye_w)
+        _same(dx[:, :a], dh[:, :a], e, "dx")
+        _same(dwg[:, :b], dh[:b].t(), e, "dw_gate")
+        backward(eye_h, x, wg)
+        _same(dx[:c], wg[:c], e, "w_gate")
+        _same(dwg[:c], x[:c], e, "x")
+
+
+def test_fp32_products_of_whole_factors(ctx):
+    """One product a sum: what the six products of terms leave out is below 2^-24 of
+    it, and its additions round 6 times: 16 steps of 2^-24 hold, of which the two
+    terms of a shorter splitting would leave 2^7 of those out."""
+    for T, F, d in ((18, 4365, 132), (21, 8949, 132), (4099, 132, 132)):
+        assert moe.moe_gated_plan(T, d, F, F32)[0] == moe.MOE_PLAN_TILES
+        x = _whole(_gen(T), T, d, 0)
+        diagonal = _whole(_gen(F), 1, d, 0)[0]
+        w = torch.zeros(F, d, device="cuda")
+        w[:d] = torch.diag(diagonal)
+        h, gate, up = (torch.empty(T, F, device="cuda") for _ in range(3))
+        moe.moe_gated(ctx, x, w, w, h, gate_out=gate, up_out=up)
+        want = x.double() * diagonal.double()
+        assert ((gate[:, :d].double() - want).abs() <= 16 * U * want.abs()).all()
+
