@@ -489,8 +489,9 @@ moe_status moe_linear_dequant(moe_ctx* ctx, const moe_qmat* m, float* out, moe_s
  * Sums, scales and zero points are fp32 and neither x (fp32 x enters the matrix
  * cores as three bf16 terms, exact from 2^-110 up and to 2^-134 below that) nor a
  * weight is rounded, whatever the number of tokens.  A token's row that holds an infinity or NaN gives a row that is not
- * finite; other rows are not touched by it.  Finite x should stay below 2^120
- * (codes enter the sums of bf16 x as 16 + q). */
+ * finite; other rows are not touched by it.  Finite x should stay below 2^112
+ * (codes and zero points enter the sums of bf16 x as 16 + q and 16 + z, up to 271
+ * for each of a group's 128 columns, before s scales their difference). */
 moe_status moe_linear(moe_ctx* ctx, const void* x, int32_t x_dtype, int64_t ldx, int64_t T, const moe_qmat* w, void* y,
                       int32_t y_dtype, int64_t ldy, moe_stream stream);
 

@@ -192,3 +192,26 @@ def test_fp32_products_of_whole_factors(ctx):
         want = x.double() * diagonal.double()
         assert ((gate[:, :d].double() - want).abs() <= 16 * U * want.abs()).all()
 
+
+# ---- large x ----
+
+@pytest.mark.parametrize("group", [32, 128])
+@pytest.mark.parametrize("T,N", [(1, 4160), (9, 4160), (24, 4160), (40, 4160), (60, 4160), (300, 20800)])
+def test_x_below_2_to_112(ctx, T, N, group):
+    """The largest codes and zero points and x of one sign near the documented end:
+    (16 + 255) * 128 * 2^112 < 2^128, so no sum on the way to a result in range
+    overflows; the tiles (T = 300) sum q - z."""
+    K = 256
+    codes = torch.full((N, K // 2), 0xFF, dtype=torch.uint8, device="cuda")
+    scales = torch.full((N, K // group), 2.0 ** -12, device="cuda").half()
+    zeros = torch.full((N, K // group), 255, dtype=torch.uint8, device="cuda")
+    zeros[::2] = 0
+    w = moe.QuantMatrix(ctx, codes, scales, zeros)
+    for dt in (BF16, F32):
+        x = torch.full((T, K), 2.0 ** 112 * (1 - 2.0 ** -8), device="cuda").to(dt)
+        ref = x.double() @ _values((codes, scales, zeros), group)[0].t()
+        for yd in (BF16, F32):
+            y = torch.empty(T, N, dtype=yd, device="cuda")
+            moe.moe_linear(ctx, x, w, y)
+            tol = _bound(x, _values((codes, scales, zeros), group)[1]) + ref.abs() * (2.0 ** -8 if yd == BF16 else U)
+            assert ((y.double() - ref).abs() <= tol).all()
