@@ -60,7 +60,11 @@ __global__ __launch_bounds__(256) void reduce_kernel(ReduceArgs r) {
 }
 
 // dg and du into rows of whole 16-byte chunks (ld >= F), a chunk a thread.  In
-// bf16 they are rounded once, as the products that follow take them.
+// bf16 they are rounded once, as operands of the products that follow and as every
+// other tensor of such a block is.  The gradients' error against 64 bits is 0.0023
+// by that, where their own rounding makes it 0.0017; two terms of each would save
+// the difference at twice the products (4096 tokens 8192 x 2048 533 us, as many
+// products as two terms have 1040).
 template <bool BF16>
 __global__ __launch_bounds__(256) void gate_backward_kernel(const void* __restrict__ dh, int64_t lddh,
                                                             const void* __restrict__ gate, const void* __restrict__ up,
