@@ -75,7 +75,7 @@ hipError_t launch_linear_dequant(const QuantGeom& g, const void* data, float* ou
 // 384 tokens, 4096 x 512, groups of 128 8.2 / 11.9; 128 tokens, 8192 x 1024 9.5 /
 // 9.9; 106 tokens, gated 3360 x 2208, groups of 32 19.2 / 18.4; 128 tokens, gated
 // 8192 x 2048 22 / 27, 256 tokens 44 / 37; 512 tokens, 4096 x 4096, groups of 32 50
-// / 58; 2048 tokens, 4096 x 4096 190 / 88.
+// / 58; 2048 tokens, 4096 x 4096 190 / 84.
 DensePlan linear_plan(const LinearArgs& a, bool gated) {
     if (a.T > 64 && a.x_bf16 && a.y_bf16) {
         const float on_cu = (float)((a.row_groups + 3) / 4) * (float)((a.T + 63) / 64) / 256.f;

@@ -6,8 +6,8 @@
 // bf16: the matrix cores sum (q - z) x over a group, or the 64 columns of a step
 // where the group is longer, and the vector unit adds s times that to the result
 // in fp32.  No weight is rounded.  (Weights s (q - z) rounded to bf16 on the way
-// into LDS need no such addition: 2048 tokens 4096 x 4096 took 83 us, this way 88,
-// with groups of 32, two additions a step, 105; gated, 1000 tokens 5504 x 2048, 61,
+// into LDS need no such addition: 2048 tokens 4096 x 4096 took 83 us, this way 84,
+// with groups of 32, two additions a step, 103; gated, 1000 tokens 5504 x 2048, 61,
 // 71 and 90.  But the result's error against 64 bits grew from its own rounding's
 // 0.0017 to 0.0024, gated 0.0029, and a token's with the number of tokens beside
 // it.)  Bound by the three units in turn between a step's barriers: of 4800 cycles
@@ -226,7 +226,7 @@ __global__ __launch_bounds__(WM * WN * KW * 64, 2) void quant_tile_kernel(QuantT
         if constexpr (FAST) load_x(s0 + 1, 1);
         else fetch_x(s0 + 1);
     }
-    const bool first = WM * WN == 1 || wave < WM * WN / 2;
+    const bool first = wave < WM * WN / 2;
     auto step = [&](auto parity, int s) TILE_INLINE {
         constexpr int p = decltype(parity)::value;
         auto unpack = [&]() TILE_INLINE {
