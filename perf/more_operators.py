@@ -215,18 +215,17 @@ def _handles(case, state):
         state["y"] = torch.empty(state["x"].shape, dtype=state["x"].dtype, device="cuda")
     elif op == "append":
         state["cache"] = moe.KvCache(ctx, state["pages"], case["page"], case["Hkv"], case["D"], case["group"])
-        T = state["q"].shape[0]
-        state["batch"] = moe.KvBatch(ctx, T, state["offsets"], state["lengths"], state["table"])
+        state["batch"] = moe.KvBatch(ctx, state["offsets"], state["lengths"], state["table"], tokens=state["q"].shape[0], most_new=case["new"])
         state["q_out"] = torch.empty(state["q"].shape, dtype=state["q"].dtype, device="cuda")
         state["k_held"], state["v_held"] = (torch.empty(state["k"].shape, dtype=torch.bfloat16, device="cuda") for _ in range(2))
     elif op == "cached":
         cache = state["cache"] = moe.KvCache(ctx, state["pages"], case["page"], case["Hkv"], case["D"], case["group"])
         # the whole pool as sequences of one page each: appending the values that the codes stand for gives those codes
         pages, page = state["pages"], case["page"]
-        every = moe.KvBatch(ctx, pages * page, torch.arange(0, pages * page + 1, page, dtype=torch.int32, device="cuda"),
-                            torch.full((pages,), page, dtype=torch.int32, device="cuda"), torch.arange(pages, dtype=torch.int32, device="cuda").unsqueeze(1))
+        every = moe.KvBatch(ctx, torch.arange(0, pages * page + 1, page, dtype=torch.int32, device="cuda"), torch.full((pages,), page, dtype=torch.int32, device="cuda"),
+                            torch.arange(pages, dtype=torch.int32, device="cuda").unsqueeze(1), tokens=pages * page, most_new=page)
         moe.moe_kv_append(ctx, cache, every, _values(*state["keys"]).flatten(0, 1), _values(*state["values"]).flatten(0, 1))
-        state["batch"] = moe.KvBatch(ctx, state["q"].shape[0], state["offsets"], state["lengths"], state["table"])
+        state["batch"] = moe.KvBatch(ctx, state["offsets"], state["lengths"], state["table"], tokens=state["q"].shape[0], most_new=case["new"])
         state["out"] = torch.empty_like(state["q"])
         state["workspace"] = torch.empty(moe.moe_attention_cached_workspace(ctx, cache, state["batch"], case["H"]), dtype=torch.uint8, device="cuda")
     elif op == "attention":
