@@ -16,6 +16,11 @@
  *   moe_linear_gated gated feed-forward block with such weights (serving)
  *   moe_gated        the same block with bf16 or fp32 weights, and
  *   moe_gated_backward its backward pass (tuning)
+ * and the attention layer beside them:
+ *   moe_rotate       rotary positions, and their gradient
+ *   moe_kv_append    keys and values into a paged cache held in 4 bits, rotated on the way
+ *   moe_kv_read      the values that such a cache holds
+ *   moe_attention_cached attention over such a cache (serving)
  *
  * Conventions for every entry point:
  *  - Pointers named "device" are HIP device (or managed) memory; "host" is
@@ -548,6 +553,120 @@ moe_status moe_linear_plan(int64_t T, int64_t rows, int64_t cols, int32_t group,
                            int32_t gated, int32_t plan[6]);
 moe_status moe_gated_plan(int64_t T, int32_t d, int32_t F, int32_t dtype, int32_t backward, int32_t plan[6]);
 
+/* ---- attention ---------------------------------------------------------------
+ *
+ * Operators of a model's attention layers, under the dense layers' conventions:
+ * they use a device context for its device, error text and error word only, may
+ * overlap on different streams, allocate nothing, may be captured into a graph,
+ * and give equal bits for equal inputs.  Heads have head_dim channels: 64, 96,
+ * 128, 192 or 256.  Activations are [T, heads, head_dim] in fp32 or bf16 (dtype):
+ * heads and channels contiguous, tokens "ld" elements apart (at least
+ * heads * head_dim where there is more than one).  Packed sequences lie one after
+ * the other: sequence s has the tokens offsets[s] .. offsets[s + 1] - 1 (device
+ * int32 [n + 1], not descending, within 0 .. T).  Rows of no sequence are neither
+ * read nor written.  Offsets, lengths and pages are read by the kernels; one that
+ * cannot be is found there: it sets the error word (moe_check: MOE_EINVAL), and
+ * nothing outside the buffers is touched. */
+
+/* Rotary positions: channels 0 .. rot - 1 of a head are rot / 2 pairs, (i, i + rot/2)
+ * or, interleaved, (2 i, 2 i + 1); pair i of a token at position p is turned by the
+ * angle p * freqs[i]:  y1 = x1 c - x2 s, y2 = x1 s + x2 c, c = scale * cos,
+ * s = scale * sin.  The other channels are copied.  Angles are computed in 64 bits.
+ * freqs: device fp32 [rot / 2], radians a position.  rot: even, 2 .. head_dim. */
+typedef struct moe_rotary {
+    const float* freqs;
+    int32_t rot;
+    int32_t interleaved; /* 0 or 1 */
+    float scale;         /* finite */
+} moe_rotary;
+
+/* Frequencies for moe_rotary, on the host: base^(-2 i / rot), and for contexts that
+ * are `factor` times longer than those a model was trained on:
+ *   MOE_ROTARY_PLAIN   as they are (factor ignored)
+ *   MOE_ROTARY_LINEAR  divided by factor
+ *   MOE_ROTARY_BASE    of the base times factor^(rot / (rot - 2)), rot > 2: the
+ *                      highest stays, the lowest is divided by factor
+ *   MOE_ROTARY_RAMP    those that turn at least `fast` times within `context` (the
+ *                      trained length) stay, those that turn at most `slow` times are
+ *                      divided by factor, between them by the pair's place between
+ *                      the two (pairs' numbers, the ends rounded outwards); *scale
+ *                      becomes 0.1 ln(factor) + 1, else 1
+ * freqs: host [rot / 2], scale: host [1].  base > 1, factor >= 1, 0 < slow < fast,
+ * context >= 1 (the last three used by RAMP alone), else MOE_EINVAL. */
+enum { MOE_ROTARY_PLAIN = 0, MOE_ROTARY_LINEAR = 1, MOE_ROTARY_BASE = 2, MOE_ROTARY_RAMP = 3 };
+moe_status moe_rotary_freqs(int32_t rot, double base, int32_t kind, double factor, double context, double fast, double slow,
+                            float* freqs, float* scale);
+
+/* y = x rotated, or with inverse = 1 turned back (by -angle, times the same scale):
+ * also the gradient of x from that of y.  x, y: device [T, heads, head_dim];
+ * positions: device int32 [T].  y may be x itself, with the same ld (in place).
+ * T up to 2^22, heads up to 1024. */
+moe_status moe_rotate(moe_ctx* ctx, const void* x, int32_t dtype, int64_t ldx, int64_t T, int32_t heads, int32_t head_dim,
+                      const int32_t* positions, const moe_rotary* rotary, int32_t inverse, void* y, int64_t ldy,
+                      moe_stream stream);
+
+/* A paged cache of keys and values in 4 bits: `pages` pages of page_tokens tokens
+ * (16, 32, .. 1024) for all `heads` key heads of one layer.  For every token, head
+ * and `group` channels (32, 64 or 128, a divisor of head_dim):
+ *   lowest = fp16(min x), step = fp16((max x - lowest) / 15),
+ *   code = round((x - lowest) / step) in 0 .. 15,  value = lowest + step * code
+ * (halves to the even code; step 0: code 0).  A group that holds a NaN, an infinity or a value
+ * beyond 65504 in magnitude is kept as NaN.
+ * data: device, 16-byte aligned, moe_kv_bytes() bytes; needs no clearing. */
+typedef struct moe_kv_cache {
+    int64_t pages;
+    int32_t page_tokens, heads, head_dim, group;
+    void* data;
+} moe_kv_cache;
+size_t moe_kv_bytes(int64_t pages, int32_t page_tokens, int32_t heads, int32_t head_dim, int32_t group); /* 0: not valid */
+
+/* The sequences of a call.  Sequence s has new tokens offsets[s] .. offsets[s+1]-1
+ * of the packed tensors; it has lengths[s] tokens (device int32 [n]) in the cache
+ * once those are in it, the new ones last; its token at place i lies in page
+ * pages[s * max_pages + i / page_tokens] (device int32 [n, max_pages]).  Entries past
+ * a sequence's tokens are not read.  most_new: no sequence has more new tokens.
+ * n up to 65536, max_pages * page_tokens up to 2^30, tokens up to 2^22. */
+typedef struct moe_kv_batch {
+    const int32_t *offsets, *lengths, *pages;
+    int32_t n, max_pages;
+    int64_t tokens; /* rows of the packed tensors */
+    int64_t most_new;
+} moe_kv_batch;
+
+/* Write the new tokens' keys and values (device [tokens, heads, head_dim], ldk and
+ * ldv) into the cache.  With a rotary the keys are rotated on the way, in 64 bits,
+ * by positions[t] (device int32 [tokens]) or, if NULL, by their places in their
+ * sequences; and if q is given, the queries [tokens, q_heads, head_dim] are rotated
+ * into q_out (which may be q, with the same ld), as moe_rotate does (without a
+ * rotary: copied).  A token whose place has no page, or whose sequence cannot be,
+ * is left out (error word).  Two tokens of one call may not have the same place. */
+moe_status moe_kv_append(moe_ctx* ctx, const moe_kv_cache* cache, const moe_kv_batch* batch, const void* k, int64_t ldk,
+                         const void* v, int64_t ldv, int32_t dtype, const moe_rotary* rotary, const int32_t* positions,
+                         const void* q, int64_t ldq, int32_t q_heads, void* q_out, int64_t ldqo, moe_stream stream);
+
+/* The values held for the batch's new tokens, into k and v (device [tokens, heads,
+ * head_dim]): a batch whose offsets span whole sequences reads them whole.  Rows of
+ * a token without a page become NaN (error word). */
+moe_status moe_kv_read(moe_ctx* ctx, const moe_kv_cache* cache, const moe_kv_batch* batch, void* k, int64_t ldk, void* v,
+                       int64_t ldv, int32_t dtype, moe_stream stream);
+
+/* Attention of the batch's new tokens (already appended) over the cache: token i of
+ * n new ones of a sequence of L sees places 0 .. L - n + i, with window > 0 the last
+ * `window` of them:
+ *   out = sum_j p_j v_j,  p = softmax_j(scale * q.k_j)
+ * q, out: device [tokens, q_heads, head_dim] (dtype); q_heads is a multiple of the
+ * cache's heads, the query heads of a key head lie side by side.  scale > 0, finite.
+ * Sums and softmax are fp32; q and the cache's codes enter unrounded, p times the
+ * step in bf16 (q bf16) or as three bf16 terms (q fp32).  Every row of a sequence
+ * that reads a page outside the cache, or that cannot be (a length below its new
+ * tokens or above its pages, more than most_new of them) becomes NaN.  workspace:
+ * device, 256-byte aligned, moe_attention_cached_workspace() bytes or more, used
+ * until the call's work is done; calls that may run at the same time need one each. */
+size_t moe_attention_cached_workspace(const moe_kv_cache* cache, const moe_kv_batch* batch, int32_t q_heads); /* 0: not valid */
+moe_status moe_attention_cached(moe_ctx* ctx, const moe_kv_cache* cache, const moe_kv_batch* batch, const void* q, int64_t ldq,
+                                int32_t dtype, int32_t q_heads, float scale, int64_t window, void* out, int64_t ldo,
+                                void* workspace, size_t workspace_bytes, moe_stream stream);
+
 /* ---- inspection ------------------------------------------------------------- */
 
 /* Dequantise one device payload into device out [3 * d_ff * d_model] fp32 in
@@ -564,7 +683,8 @@ moe_status moe_stats(const moe_ctx* ctx, uint64_t out[5]);
 /* Synchronise `stream`, read and clear the error word: MOE_OK, MOE_EMISS,
  * MOE_ETIMEOUT (a decode launch's wait for its gate/up or router workgroups ran
  * out, about 200 ms; its rows are NaN; the counters are reset here), or MOE_EINVAL for an
- * out-of-range expert id met by moe_plan_union. */
+ * out-of-range expert id met by moe_plan_union or an offset, length or page that an
+ * attention call met. */
 moe_status moe_check(moe_ctx* ctx, moe_stream stream);
 
 /* Peak references for measurement (not part of the routed path; no context).

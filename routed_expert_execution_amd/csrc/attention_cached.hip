@@ -1,0 +1,32 @@
+// Attention over a paged cache held in 4 bits: how a call is cut and launched
+// (the kernels: attention_cached.h).
+#include <algorithm>
+
+#include "attention_cached.h"
+
+namespace moe {
+
+hipError_t launch_cached_f32(const CachedArgs& a, int split, hipStream_t s);
+
+// Few rows leave most of the card idle unless a sequence's tokens are cut: into so
+// many chunks that there are about 768 workgroups, three for each CU.
+CachedPlan cached_plan(const KvGeom& g, int n, int most_new, int max_pages, int q_heads, int bf16) {
+    CachedPlan p{};
+    p.tile_rows = 16;
+    const int64_t tiles = std::max<int64_t>(1, ((int64_t)most_new * (q_heads / g.heads) + p.tile_rows - 1) / p.tile_rows);
+    p.target = (int)std::max<int64_t>(1, 768 / (g.heads * tiles));
+    // sequences that cannot be longer than one round of a workgroup's waves are not cut
+    const int64_t longest = (int64_t)max_pages * g.page_tokens;
+    p.split = p.target > 1 && longest > cached::kStep * cached::kWaves;
+    if (!p.split) p.target = 1;
+    // (workgroups of a sequence past its own rows end at once; not too many of them)
+    p.row_tiles = (int)std::max<int64_t>(1, std::min<int64_t>(tiles, std::max<int64_t>(8192 / ((int64_t)g.heads * (n + p.target)), 256 / g.heads)));
+    p.bytes = p.split ? (size_t)2 * p.target * most_new * q_heads * (g.D + 2) * sizeof(float) : 0;
+    return p;
+}
+
+hipError_t launch_cached(const CachedArgs& a, int split, hipStream_t s) {
+    return a.bf16 ? cached::launch_by_width<true>(a, split, s) : launch_cached_f32(a, split, s);
+}
+
+}  // namespace moe

@@ -67,6 +67,7 @@ __host__ __device__ inline int q4_scale(int i) { return 16 * kTileBlocks + 2 * i
 constexpr int kErrMiss = 1;     // unmapped expert met by a kernel
 constexpr int kErrBadId = 4;    // expert id out of range in a plan input
 constexpr int kErrSync = 8;     // a decode workgroup's bounded wait for the hidden rows ran out
+constexpr int kErrCache = 16;  // a page, length or offset of an attention call that cannot be
 
 // ---- launchers (return hipError_t of the launch) ----
 

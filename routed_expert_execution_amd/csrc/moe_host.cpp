@@ -14,6 +14,7 @@
 #include <vector>
 
 #include "dense.h"
+#include "host.h"
 #include "internal.h"
 
 using moe::Geom;
@@ -115,9 +116,9 @@ struct moe_ctx {
     std::vector<uint64_t> slot_gen;   // slot -> generation of that mark
 };
 
-namespace {
+namespace moe {
+namespace host {
 
-moe_status fail(moe_ctx* c, moe_status st, const char* fmt, ...) __attribute__((format(printf, 3, 4)));
 moe_status fail(moe_ctx* c, moe_status st, const char* fmt, ...) {
     if (c) {
         char buf[512];
@@ -129,6 +130,20 @@ moe_status fail(moe_ctx* c, moe_status st, const char* fmt, ...) {
     }
     return st;
 }
+moe_status need_device(moe_ctx* c) {
+    if (!c) return MOE_EINVAL;
+    if (c->host_only) return fail(c, MOE_EINVAL, "host-only context has no device state");
+    return MOE_OK;
+}
+int device_of(const moe_ctx* c) { return c->cfg.device; }
+int* error_word(const moe_ctx* c) { return c->err_word; }
+
+}  // namespace host
+}  // namespace moe
+
+namespace {
+
+using namespace moe::host;
 
 #define HIP_TRY(ctx, call)                                                                   \
     do {                                                                                     \
@@ -161,23 +176,6 @@ bool cfg_valid(const moe_config* c, Geom* g, std::string* why) {
     }
     if (g) *g = gg;
     return true;
-}
-
-struct DeviceGuard {
-    int prev = -1;
-    bool changed = false;
-    explicit DeviceGuard(int dev) {
-        if (dev >= 0 && hipGetDevice(&prev) == hipSuccess && prev != dev) {
-            changed = hipSetDevice(dev) == hipSuccess;
-        }
-    }
-    ~DeviceGuard() { if (changed) (void)hipSetDevice(prev); }
-};
-
-moe_status need_device(moe_ctx* c) {
-    if (!c) return MOE_EINVAL;
-    if (c->host_only) return fail(c, MOE_EINVAL, "host-only context has no device state");
-    return MOE_OK;
 }
 
 // Q8_0 / Q4_0 repack between GGUF blocks (row-major, blocks along rows) and
@@ -1357,10 +1355,6 @@ moe_status moe_dequant(moe_ctx* c, const void* payload, int32_t prec, float* out
 // (arguments are judged before the context's device, so that a host-only context
 // names a bad argument too)
 
-static int elem_bytes(int32_t dtype) { return dtype == MOE_BF16 ? 2 : 4; }
-static bool dtype_valid(int32_t dtype) { return dtype == MOE_F32 || dtype == MOE_BF16; }
-static bool aligned_to(const void* p, size_t n) { return ((uintptr_t)p) % n == 0; }
-
 // (T, rows and widths such that no launch passes 65535 workgroups in y or 2^32
 // threads: tiles of more rows or columns than memory holds are not reached)
 constexpr int64_t kDenseMaxT = 1 << 20;
@@ -1570,6 +1564,7 @@ moe_status moe_check(moe_ctx* c, moe_stream stream) {
         return fail(c, MOE_ETIMEOUT, "a decode workgroup timed out waiting for the hidden rows or the logits (error word 0x%x)", w);
     }
     if (w & moe::kErrMiss) return fail(c, MOE_EMISS, "a kernel met an unmapped expert (error word 0x%x)", w);
+    if (w & moe::kErrCache) return fail(c, MOE_EINVAL, "an attention call met an offset, length or page that cannot be (error word 0x%x)", w);
     return fail(c, MOE_EINVAL, "a plan input held an expert id out of range (error word 0x%x)", w);
 }
 

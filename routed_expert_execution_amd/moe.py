@@ -23,6 +23,7 @@ MOE_F32, MOE_BF16 = 0, 1
 MOE_PREC_F32, MOE_PREC_BF16 = 0, 1
 MOE_MAX_STAGE_STREAMS = 8
 MOE_PLAN_ROWS, MOE_PLAN_SHARED_ROWS, MOE_PLAN_TILES = 0, 1, 2
+MOE_ROTARY_PLAIN, MOE_ROTARY_LINEAR, MOE_ROTARY_BASE, MOE_ROTARY_RAMP = 0, 1, 2, 3
 
 
 class MoeError(RuntimeError):
@@ -49,6 +50,20 @@ class moe_qmat(C.Structure):
                 ("data", C.c_void_p)]
 
 
+class moe_rotary(C.Structure):
+    _fields_ = [("freqs", C.c_void_p), ("rot", C.c_int32), ("interleaved", C.c_int32), ("scale", C.c_float)]
+
+
+class moe_kv_cache(C.Structure):
+    _fields_ = [("pages", C.c_int64), ("page_tokens", C.c_int32), ("heads", C.c_int32), ("head_dim", C.c_int32),
+                ("group", C.c_int32), ("data", C.c_void_p)]
+
+
+class moe_kv_batch(C.Structure):
+    _fields_ = [("offsets", C.c_void_p), ("lengths", C.c_void_p), ("pages", C.c_void_p), ("n", C.c_int32),
+                ("max_pages", C.c_int32), ("tokens", C.c_int64), ("most_new", C.c_int64)]
+
+
 def _load() -> C.CDLL:
     # torch ships its own HIP runtime.  Loading torch first makes libmoe's
     # libamdhip64.so.7 dependency resolve (by soname) to that same runtime;
@@ -61,6 +76,8 @@ def _load() -> C.CDLL:
     cfgp = C.POINTER(moe_config)
     planp = C.POINTER(moe_plan)
     qmatp = C.POINTER(moe_qmat)
+    F32, F64 = C.c_float, C.c_double
+    rotp, kvp, batchp = C.POINTER(moe_rotary), C.POINTER(moe_kv_cache), C.POINTER(moe_kv_batch)
     sig = {
         "moe_payload_bytes": (S, [cfgp]),
         "moe_plan_bytes": (C.c_int, [cfgp, I64, C.POINTER(S)]),
@@ -98,6 +115,13 @@ def _load() -> C.CDLL:
         "moe_gated_backward": (C.c_int, [P, P, I64, P, I32, I64, I64, I32, I32, P, P, P, P, P, P, P, P, S, P]),
         "moe_linear_plan": (C.c_int, [I64, I64, I64, I32, I32, I32, I32, C.POINTER(I32)]),
         "moe_gated_plan": (C.c_int, [I64, I32, I32, I32, I32, C.POINTER(I32)]),
+        "moe_rotary_freqs": (C.c_int, [I32, F64, I32, F64, F64, F64, F64, P, C.POINTER(F32)]),
+        "moe_rotate": (C.c_int, [P, P, I32, I64, I64, I32, I32, P, rotp, I32, P, I64, P]),
+        "moe_kv_bytes": (S, [I64, I32, I32, I32, I32]),
+        "moe_kv_append": (C.c_int, [P, kvp, batchp, P, I64, P, I64, I32, rotp, P, P, I64, I32, P, I64, P]),
+        "moe_kv_read": (C.c_int, [P, kvp, batchp, P, I64, P, I64, I32, P]),
+        "moe_attention_cached_workspace": (S, [kvp, batchp, I32]),
+        "moe_attention_cached": (C.c_int, [P, kvp, batchp, P, I64, I32, I32, F32, I64, P, I64, P, S, P]),
         "moe_stats": (C.c_int, [P, C.POINTER(C.c_uint64)]),
         "moe_check": (C.c_int, [P, P]),
         "moe_page_table": (C.c_int, [P, C.POINTER(P)]),
@@ -122,7 +146,8 @@ EXPORTS = ("moe_payload_bytes", "moe_plan_bytes", "moe_pack_expert", "moe_unpack
            "moe_route_ffn", "moe_dequant", "moe_stats", "moe_check", "moe_page_table", "moe_route_splits", "moe_hidden_rows", "moe_probe_read",
            "moe_probe_mfma", "moe_probe_lds", "moe_linear_bytes", "moe_linear_pack", "moe_linear_dequant", "moe_linear",
            "moe_linear_gated", "moe_gated", "moe_gated_workspace", "moe_gated_backward", "moe_linear_plan",
-           "moe_gated_plan")
+           "moe_gated_plan", "moe_rotary_freqs", "moe_rotate", "moe_kv_bytes", "moe_kv_append", "moe_kv_read",
+           "moe_attention_cached_workspace", "moe_attention_cached")
 
 
 def library() -> C.CDLL:
@@ -652,9 +677,9 @@ def moe_linear_gated(ctx: Context, x, w_gate: QuantMatrix, w_up: QuantMatrix, h,
                                      _stream_on(ctx, stream)))
 
 
-def _on_device(ctx: Context, w: QuantMatrix) -> None:
+def _on_device(ctx: Context, w, name: str = "matrix") -> None:
     if w.device != ctx.device:
-        raise ValueError(f"the matrix must be on cuda:{ctx.device}")
+        raise ValueError(f"the {name} must be on cuda:{ctx.device}")
 
 
 def moe_gated(ctx: Context, x, w_gate, w_up, h, gate_out=None, up_out=None, stream=None) -> None:
@@ -716,6 +741,171 @@ def moe_gated_plan(T: int, d: int, F: int, dtype, backward: bool = False) -> tup
     out = (C.c_int32 * 6)()
     _call(None, _lib.moe_gated_plan(T, d, F, _TYPE_CODES.get(dtype, -1), int(backward), out))
     return tuple(out)
+
+
+# ---- attention ----
+
+def _heads(ctx: Context, t, T: int, heads: int, D: int, name: str, dtype=None) -> tuple:
+    """(address, elements between tokens, type code) of a float32 or bfloat16
+    [T, heads, D] tensor on the context's GPU: the heads of a token contiguous,
+    tokens may lie apart."""
+    shape = t.shape
+    if len(shape) != 3 or shape[0] != T or shape[1] != heads or shape[2] != D:
+        raise ValueError(f"{name} must be [{T}, {heads}, {D}]")
+    kind = t.dtype
+    code = _TYPE_CODES.get(kind)
+    if code is None or (dtype is not None and kind != dtype):
+        raise ValueError(f"{name} must be {dtype or 'float32 or bfloat16'}")
+    ld, per_head, step = t.stride()
+    width = heads * D
+    if T <= 1:
+        ld = width
+    if step != 1 or (per_head != D and heads > 1) or ld < width:
+        raise ValueError(f"the heads of a token of {name} must be contiguous and tokens must not overlap")
+    if ctx.device < 0 or t.get_device() != ctx.device:
+        raise ValueError(f"{name} must be on cuda:{ctx.device}")
+    return t.data_ptr(), ld, code
+
+
+def _whole(ctx: Context, t, shape: tuple, name: str) -> int:
+    """Address of a contiguous int32 tensor on the context's GPU."""
+    if t.dtype != torch.int32 or t.shape != shape or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous int32 tensor of shape {list(shape)}")
+    if ctx.device < 0 or t.get_device() != ctx.device:
+        raise ValueError(f"{name} must be on cuda:{ctx.device}")
+    return t.data_ptr()
+
+
+def moe_rotary_freqs(rot: int, base: float = 10000.0, kind: int = MOE_ROTARY_PLAIN, factor: float = 1.0,
+                     context: float = 4096.0, fast: float = 32.0, slow: float = 1.0) -> tuple:
+    """(frequencies float32 [rot / 2], scale) for Rotary; kind MOE_ROTARY_*."""
+    out, scale = np.empty(max(1, rot // 2), dtype=np.float32), C.c_float()
+    if _lib.moe_rotary_freqs(rot, base, kind, factor, context, fast, slow, out.ctypes.data, C.byref(scale)) != MOE_OK:
+        raise ValueError("moe_rotary_freqs: bad arguments")
+    return out, scale.value
+
+
+class Rotary:
+    """Rotary positions: freqs float32 [rot / 2] on the context's GPU (radians a
+    position, kept referenced here), the layout of the pairs and the scale."""
+
+    def __init__(self, ctx: Context, freqs, interleaved: bool = False, scale: float = 1.0):
+        if freqs.dtype != torch.float32 or freqs.dim() != 1 or not freqs.is_contiguous() or freqs.numel() < 1:
+            raise ValueError("freqs must be a contiguous float32 tensor [rot / 2]")
+        if ctx.device < 0 or freqs.get_device() != ctx.device:
+            raise ValueError(f"freqs must be on cuda:{ctx.device}")
+        self.freqs, self.rot, self.device = freqs, 2 * freqs.numel(), ctx.device
+        self.c = moe_rotary(freqs.data_ptr(), self.rot, int(interleaved), scale)
+        self.ref = C.byref(self.c)
+
+
+def moe_rotate(ctx: Context, x, positions, rotary: Rotary, y, inverse: bool = False, stream=None) -> None:
+    """y = x rotated by positions (int32 [T]), or turned back.  x, y: float32 or
+    bfloat16 [T, heads, head_dim], tokens may lie apart; y may be x."""
+    T, H, D = x.shape
+    xp, ldx, code = _heads(ctx, x, T, H, D, "x")
+    yp, ldy, _ = _heads(ctx, y, T, H, D, "y", x.dtype)
+    _on_device(ctx, rotary, "rotary")
+    _call(ctx, _lib.moe_rotate(ctx.handle, xp, code, ldx, T, H, D, _whole(ctx, positions, (T,), "positions"), rotary.ref,
+                               int(inverse), yp, ldy, _stream_on(ctx, stream)))
+
+
+class KvCache:
+    """A paged cache of keys and values in 4 bits on the context's GPU
+    (moe_kv_cache), its memory owned here (or given: uint8, moe_kv_bytes bytes)."""
+
+    def __init__(self, ctx: Context, pages: int, page_tokens: int, heads: int, head_dim: int, group: int = 32, data=None):
+        n = int(_lib.moe_kv_bytes(pages, page_tokens, heads, head_dim, group))
+        if n == 0:
+            raise ValueError("unsupported cache: page_tokens a power of two in [16, 1024], head_dim 64, 96, 128, 192 or 256, "
+                             "group 32, 64 or 128 and a divisor of it")
+        if ctx.device < 0:
+            raise ValueError("a cache needs a device context")
+        if data is None:
+            data = torch.empty(n, dtype=torch.uint8, device=torch.device("cuda", ctx.device))
+        _check_dev(ctx, data)
+        if data.dtype != torch.uint8 or data.numel() < n:
+            raise ValueError(f"data must be uint8 of at least {n} bytes")
+        self.pages, self.page_tokens, self.heads, self.head_dim, self.group = pages, page_tokens, heads, head_dim, group
+        self.device, self.data = ctx.device, data
+        self.c = moe_kv_cache(pages, page_tokens, heads, head_dim, group, _ptr(data))
+        self.ref = C.byref(self.c)
+
+
+class KvBatch:
+    """The sequences of a call (moe_kv_batch): offsets int32 [n + 1] of their new
+    tokens in the packed tensors, lengths int32 [n] with these, pages int32 [n,
+    max_pages]; tokens: rows of the packed tensors; most_new: no sequence has more
+    new tokens (default: tokens).  The arrays are read when a call runs, so a
+    captured call sees what they hold at its replay."""
+
+    def __init__(self, ctx: Context, offsets, lengths, pages, tokens: int, most_new: int | None = None):
+        if pages.dim() != 2:
+            raise ValueError("pages must be [n, max_pages]")
+        n, most = pages.shape
+        self.offsets, self.lengths, self.pages, self.device = offsets, lengths, pages, ctx.device
+        self.tokens, self.most_new = tokens, tokens if most_new is None else most_new
+        self.c = moe_kv_batch(_whole(ctx, offsets, (n + 1,), "offsets"), _whole(ctx, lengths, (n,), "lengths"),
+                              _whole(ctx, pages, (n, most), "pages"), n, most, tokens, self.most_new)
+        self.ref = C.byref(self.c)
+
+
+def moe_kv_append(ctx: Context, cache: KvCache, batch: KvBatch, k, v, rotary: Rotary | None = None, positions=None,
+                  q=None, q_out=None, stream=None) -> None:
+    """The new tokens' keys and values [tokens, heads, head_dim] into the cache,
+    keys (and q into q_out, [tokens, q_heads, head_dim]) rotated on the way."""
+    _on_device(ctx, cache, "cache")
+    _on_device(ctx, batch, "batch")
+    if rotary is not None:
+        _on_device(ctx, rotary, "rotary")
+    T, H, D = batch.tokens, cache.heads, cache.head_dim
+    kp, ldk, code = _heads(ctx, k, T, H, D, "k")
+    vp, ldv, _ = _heads(ctx, v, T, H, D, "v", k.dtype)
+    pp = None if positions is None else _whole(ctx, positions, (T,), "positions")
+    qp = qo = None
+    ldq = ldqo = heads = 0
+    if q is not None or q_out is not None:
+        if q is None or q_out is None:
+            raise ValueError("q and q_out go together")
+        heads = q.shape[1]
+        qp, ldq, _ = _heads(ctx, q, T, heads, D, "q", k.dtype)
+        qo, ldqo, _ = _heads(ctx, q_out, T, heads, D, "q_out", k.dtype)
+    _call(ctx, _lib.moe_kv_append(ctx.handle, cache.ref, batch.ref, kp, ldk, vp, ldv, code, rotary.ref if rotary else None, pp,
+                                  qp, ldq, heads, qo, ldqo, _stream_on(ctx, stream)))
+
+
+def moe_kv_read(ctx: Context, cache: KvCache, batch: KvBatch, k, v, stream=None) -> None:
+    """The values held for the batch's new tokens into k and v [tokens, heads, head_dim]."""
+    _on_device(ctx, cache, "cache")
+    _on_device(ctx, batch, "batch")
+    T, H, D = batch.tokens, cache.heads, cache.head_dim
+    kp, ldk, code = _heads(ctx, k, T, H, D, "k")
+    vp, ldv, _ = _heads(ctx, v, T, H, D, "v", k.dtype)
+    _call(ctx, _lib.moe_kv_read(ctx.handle, cache.ref, batch.ref, kp, ldk, vp, ldv, code, _stream_on(ctx, stream)))
+
+
+def moe_attention_cached_workspace(ctx: Context, cache: KvCache, batch: KvBatch, q_heads: int) -> int:
+    """Bytes of moe_attention_cached's workspace."""
+    n = int(_lib.moe_attention_cached_workspace(cache.ref, batch.ref, q_heads))
+    if n == 0:
+        raise ValueError("bad sizes: q_heads must be a multiple of the cache's heads")
+    return n
+
+
+def moe_attention_cached(ctx: Context, cache: KvCache, batch: KvBatch, q, out, *, scale: float | None = None, window: int = 0,
+                         workspace, stream=None) -> None:
+    """out = attention of the batch's new tokens over the cache.  q, out: float32 or
+    bfloat16 [tokens, q_heads, head_dim]; scale: head_dim ** -0.5 unless given;
+    workspace: uint8, moe_attention_cached_workspace bytes."""
+    _on_device(ctx, cache, "cache")
+    _on_device(ctx, batch, "batch")
+    T, D, H = batch.tokens, cache.head_dim, q.shape[1]
+    qp, ldq, code = _heads(ctx, q, T, H, D, "q")
+    op, ldo, _ = _heads(ctx, out, T, H, D, "out", q.dtype)
+    _check_dev(ctx, workspace)
+    _call(ctx, _lib.moe_attention_cached(ctx.handle, cache.ref, batch.ref, qp, ldq, code, H, D ** -0.5 if scale is None else scale,
+                                         window, op, ldo, _ptr(workspace), workspace.numel() * workspace.element_size(),
+                                         _stream_on(ctx, stream)))
 
 
 def moe_stats(ctx: Context) -> dict:
