@@ -21,6 +21,8 @@
  *   moe_kv_append    keys and values into a paged cache held in 4 bits, rotated on the way
  *   moe_kv_read      the values that such a cache holds
  *   moe_attention_cached attention over such a cache (serving)
+ *   moe_attention    attention over packed sequences (prompts, tuning), and
+ *   moe_attention_backward its backward pass
  *
  * Conventions for every entry point:
  *  - Pointers named "device" are HIP device (or managed) memory; "host" is
@@ -566,7 +568,8 @@ moe_status moe_gated_plan(int64_t T, int32_t d, int32_t F, int32_t dtype, int32_
  * int32 [n + 1], not descending, within 0 .. T).  Rows of no sequence are neither
  * read nor written.  Offsets, lengths and pages are read by the kernels; one that
  * cannot be is found there: it sets the error word (moe_check: MOE_EINVAL), and
- * nothing outside the buffers is touched. */
+ * nothing outside the buffers is touched (where offsets descend, which rows are
+ * written is not said). */
 
 /* Rotary positions: channels 0 .. rot - 1 of a head are rot / 2 pairs, (i, i + rot/2)
  * or, interleaved, (2 i, 2 i + 1); pair i of a token at position p is turned by the
@@ -666,6 +669,55 @@ size_t moe_attention_cached_workspace(const moe_kv_cache* cache, const moe_kv_ba
 moe_status moe_attention_cached(moe_ctx* ctx, const moe_kv_cache* cache, const moe_kv_batch* batch, const void* q, int64_t ldq,
                                 int32_t dtype, int32_t q_heads, float scale, int64_t window, void* out, int64_t ldo,
                                 void* workspace, size_t workspace_bytes, moe_stream stream);
+
+/* Packed sequences for moe_attention: sequence s has the queries offsets_q[s] ..
+ * offsets_q[s+1]-1 of [tokens_q] and the keys and values offsets_k[s] ..
+ * offsets_k[s+1]-1 of [tokens_k] (for a prompt both are one array).  Where
+ * causal, query i of n sees keys 0 .. i + m - n of m (the last query sees all of
+ * them), with window > 0 (causal only) the last `window` of these; else every
+ * query sees every key of its sequence.  q_heads is a multiple of kv_heads (the
+ * query heads of a key head lie side by side).  scale > 0, finite.  n up to 65536,
+ * tokens up to 2^22. */
+typedef struct moe_attn {
+    const int32_t *offsets_q, *offsets_k; /* device [n + 1] */
+    int32_t n;
+    int32_t dtype; /* of every activation and gradient */
+    int32_t q_heads, kv_heads, head_dim;
+    int32_t causal; /* 0 or 1 */
+    float scale;
+    int64_t window; /* 0: none */
+    int64_t tokens_q, tokens_k;
+} moe_attn;
+
+/* out = softmax(scale * q k^T) v over the keys that a query sees.  q, out: device
+ * [tokens_q, q_heads, head_dim], k, v: device [tokens_k, kv_heads, head_dim].
+ * lse: device fp32 [tokens_q, q_heads] or NULL, the log of each row's sum of
+ * exponentials, which the backward pass needs.  A query that sees no key gets zeros
+ * and minus infinity.  Keys that a query does not see add nothing to its row, even
+ * where their values are not finite; a value that is not finite makes the rows that
+ * see it NaN in its channel.  Sums and softmax are fp32; the exponentials are
+ * rounded to bf16 before the second product (bf16) or enter as three bf16 terms, as
+ * every fp32 factor does (see moe_gated).  A sequence whose offsets cannot be gives
+ * NaN. */
+moe_status moe_attention(moe_ctx* ctx, const moe_attn* attn, const void* q, int64_t ldq, const void* k, int64_t ldk,
+                         const void* v, int64_t ldv, void* out, int64_t ldo, float* lse, moe_stream stream);
+
+/* Bytes of moe_attention_backward's workspace (0 if not valid). */
+size_t moe_attention_workspace(int64_t tokens_q, int32_t q_heads);
+
+/* Gradients of q, k and v from dout and what the forward pass took and gave:
+ *   P = exp(scale q k^T - lse), delta = rowsum(dout * out), dS = P (dout v^T - delta)
+ *   dq = scale dS k, dk = scale dS^T q, dv = P^T dout
+ * those of k and v summed over the query heads of a key head, all three written (not
+ * added to), every sum in fp32 and in one order.  P and dS are rounded to bf16 before
+ * the second products (bf16).  Rows and keys that do not see each other add nothing
+ * to each other's gradients, whatever they hold.  workspace: device, 256-byte
+ * aligned, moe_attention_workspace() bytes, used until the call's work is done;
+ * calls that may run at the same time need one each. */
+moe_status moe_attention_backward(moe_ctx* ctx, const moe_attn* attn, const void* dout, int64_t lddo, const void* q, int64_t ldq,
+                                  const void* k, int64_t ldk, const void* v, int64_t ldv, const void* out, int64_t ldo,
+                                  const float* lse, void* dq, int64_t lddq, void* dk, int64_t lddk, void* dv, int64_t lddv,
+                                  void* workspace, size_t workspace_bytes, moe_stream stream);
 
 /* ---- inspection ------------------------------------------------------------- */
 

@@ -17,7 +17,8 @@ LIB = os.path.join(PKG, "libmoe.so")
 
 SOURCES = ["moe_host.cpp", "route.hip", "plan.hip", "dequant.hip", "ffn_decode.hip", "ffn_prefill.hip", "probe.hip", "slots.hip", "scratch.hip",
            "linear.hip", "linear_bf16.hip", "linear_f32.hip", "linear_tiles.hip", "gated.hip",
-           "attention_host.cpp", "rotate.hip", "kv_cache.hip", "attention_cached.hip", "attention_cached_f32.hip"]
+           "attention_host.cpp", "rotate.hip", "kv_cache.hip", "attention_cached.hip", "attention_cached_f32.hip",
+           "attention_bf16.hip", "attention_f32.hip", "attention_backward_bf16.hip", "attention_backward_f32.hip"]
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 FLAGS = [

@@ -135,4 +135,29 @@ struct CachedPlan { int target, row_tiles, tile_rows, split; size_t bytes; };
 CachedPlan cached_plan(const KvGeom& g, int n, int most_new, int max_pages, int q_heads, int bf16);
 hipError_t launch_cached(const CachedArgs& a, int split, hipStream_t s);
 
+// Attention over packed sequences.
+struct PackedArgs {
+    const void *q, *k, *v;  // [Tq][q_heads][D], [Tk][kv_heads][D]; tokens ld* elements apart
+    int64_t ldq, ldk, ldv;
+    int bf16, D, q_heads, kv_heads, per_head;
+    int Tq, Tk, n;
+    const int32_t *offsets_q, *offsets_k;  // [n + 1]
+    int causal, window;                    // window: 0 none
+    float scale, scale_log2;               // scale / ln 2
+    void* out;                             // forward: written; backward: read
+    int64_t ldo;
+    float* lse;                            // [Tq][q_heads], forward: or null
+    int* err;
+    // backward
+    const void* dout;
+    int64_t lddo;
+    void *dq, *dk, *dv;
+    int64_t lddq, lddk, lddv;
+    float* delta;                          // [Tq][q_heads]
+};
+hipError_t launch_attention_bf16(const PackedArgs& a, hipStream_t s);
+hipError_t launch_attention_f32(const PackedArgs& a, hipStream_t s);
+hipError_t launch_attention_backward_bf16(const PackedArgs& a, hipStream_t s);
+hipError_t launch_attention_backward_f32(const PackedArgs& a, hipStream_t s);
+
 }  // namespace moe

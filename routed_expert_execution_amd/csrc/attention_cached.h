@@ -162,6 +162,7 @@ __global__ __launch_bounds__(kThreads, W <= 4 ? (BF16 ? 3 : 2) : W <= 6 ? 2 : 1)
     __shared__ __attribute__((aligned(16))) float pairs[kWaves][4][2][16 * W];
     __shared__ float joined[2][16][D + 4];
     __shared__ float2 stats[kWaves][16];
+    if (blockIdx.x == gridDim.x - 1 && blockIdx.y == 0) check_offsets(a.batch.offsets, a.batch.n, a.batch.T, a.err);
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), r16 = lane & 15, q4 = lane >> 4;
     Chunk c;
     if (!find_chunk<false>(a, blockIdx.x, &c)) return;

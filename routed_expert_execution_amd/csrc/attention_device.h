@@ -72,6 +72,14 @@ __device__ inline int wave_find(int n, int64_t at, Key key) {
     return lo;
 }
 
+// Sets the error word if any of the n sequences' offsets cannot be: by one workgroup
+// of a launch, for the sequences that no other workgroup meets.
+__device__ inline void check_offsets(const int32_t* offsets, int n, int T, int* err) {
+    bool bad = false;
+    for (int i = threadIdx.x; i < n; i += blockDim.x) bad |= offsets[i] < 0 || offsets[i + 1] < offsets[i] || offsets[i + 1] > T;
+    if (bad) atomicOr(err, kErrCache);
+}
+
 // The sequence and the place of packed token `token`; false where no sequence has
 // it, with `bad` where offsets or the length cannot be.
 struct TokenPlace { int seq; int64_t place; bool bad; };

@@ -243,4 +243,92 @@ moe_status moe_attention_cached(moe_ctx* c, const moe_kv_cache* cache, const moe
     LAUNCH(moe::launch_cached(a, p.split, (hipStream_t)stream));
 }
 
+// What both passes judge alike.
+static moe_status attn_check(moe_ctx* c, const char* fn, const moe_attn* t, moe::PackedArgs* a) {
+    CHECK(t, "%s: null description", fn);
+    CHECK(t->n >= 0 && t->n <= kMaxSequences && t->tokens_q >= 0 && t->tokens_q <= kMaxT && t->tokens_k >= 0 && t->tokens_k <= kMaxT,
+          "%s: n outside [0, 65536] or tokens outside [0, 2^22]", fn);
+    CHECK(t->n == 0 || (t->offsets_q && t->offsets_k), "%s: null offsets", fn);
+    CHECK(aligned_to(t->offsets_q, 4) && aligned_to(t->offsets_k, 4), "%s: misaligned offsets", fn);
+    CHECK(dtype_valid(t->dtype), "%s: bad type", fn);
+    CHECK(t->kv_heads >= 1 && t->kv_heads <= kMaxHeads && query_heads_valid(t->q_heads, t->kv_heads),
+          "%s: q_heads=%d not a multiple of kv_heads=%d in [1, 1024]", fn, t->q_heads, t->kv_heads);
+    CHECK(moe::head_dim_valid(t->head_dim), "%s: head_dim=%d not 64, 96, 128, 192 or 256", fn, t->head_dim);
+    CHECK(t->causal == 0 || t->causal == 1, "%s: causal must be 0 or 1", fn);
+    CHECK(t->window >= 0 && (t->window == 0 || t->causal), "%s: a window is not negative, and needs causal", fn);
+    CHECK(std::isfinite(t->scale) && t->scale > 0, "%s: scale must be finite and positive", fn);
+    *a = moe::PackedArgs{};
+    a->bf16 = t->dtype == MOE_BF16;
+    a->D = t->head_dim; a->q_heads = t->q_heads; a->kv_heads = t->kv_heads; a->per_head = t->q_heads / t->kv_heads;
+    a->Tq = (int)t->tokens_q; a->Tk = (int)t->tokens_k; a->n = t->n;
+    a->offsets_q = t->offsets_q; a->offsets_k = t->offsets_k;
+    a->causal = t->causal;
+    a->window = (int)(t->window < (1 << 23) ? t->window : 0);  // (none reaches further back)
+    a->scale = t->scale;
+    a->scale_log2 = (float)((double)t->scale * 1.4426950408889634);
+    // (a workgroup for each head of at least every 128 tokens, and two more a sequence: 2^31 at most)
+    CHECK((t->tokens_q / 128 + t->n) * t->q_heads < ((int64_t)1 << 31) / 256 && (t->tokens_k / 128 + t->n) * t->kv_heads < ((int64_t)1 << 31) / 256,
+          "%s: too many heads of too many tokens for one call", fn);
+    return MOE_OK;
+}
+
+moe_status moe_attention(moe_ctx* c, const moe_attn* t, const void* q, int64_t ldq, const void* k, int64_t ldk, const void* v,
+                         int64_t ldv, void* out, int64_t ldo, float* lse, moe_stream stream) {
+    const char* fn = "moe_attention";
+    if (!c) return MOE_EINVAL;
+    moe::PackedArgs a;
+    if (moe_status st = attn_check(c, fn, t, &a)) return st;
+    const int64_t Tq = t->tokens_q, Tk = t->tokens_k, qw = (int64_t)a.q_heads * a.D, kw = (int64_t)a.kv_heads * a.D;
+    if (moe_status st = tokens_check(c, fn, "q", q, t->dtype, Tq, qw, ldq)) return st;
+    if (moe_status st = tokens_check(c, fn, "k", k, t->dtype, Tk, kw, ldk)) return st;
+    if (moe_status st = tokens_check(c, fn, "v", v, t->dtype, Tk, kw, ldv)) return st;
+    if (moe_status st = tokens_check(c, fn, "out", out, t->dtype, Tq, qw, ldo)) return st;
+    CHECK(aligned_to(lse, 4), "%s: misaligned lse", fn);
+    if (moe_status st = need_device(c)) return st;
+    if (Tq == 0 || t->n == 0) return MOE_OK;
+    a.q = q; a.k = k; a.v = v; a.out = out; a.lse = lse;
+    a.ldq = Tq > 1 ? ldq : qw; a.ldk = Tk > 1 ? ldk : kw; a.ldv = Tk > 1 ? ldv : kw; a.ldo = Tq > 1 ? ldo : qw;
+    a.err = error_word(c);
+    DeviceGuard dg(device_of(c));
+    LAUNCH(a.bf16 ? moe::launch_attention_bf16(a, (hipStream_t)stream) : moe::launch_attention_f32(a, (hipStream_t)stream));
+}
+
+size_t moe_attention_workspace(int64_t tokens_q, int32_t q_heads) {
+    if (tokens_q < 0 || tokens_q > kMaxT || q_heads < 1 || q_heads > kMaxHeads) return 0;
+    const size_t n = (size_t)tokens_q * q_heads * sizeof(float);
+    return n < 256 ? 256 : n;
+}
+
+moe_status moe_attention_backward(moe_ctx* c, const moe_attn* t, const void* dout, int64_t lddo, const void* q, int64_t ldq,
+                                  const void* k, int64_t ldk, const void* v, int64_t ldv, const void* out, int64_t ldo,
+                                  const float* lse, void* dq, int64_t lddq, void* dk, int64_t lddk, void* dv, int64_t lddv,
+                                  void* workspace, size_t workspace_bytes, moe_stream stream) {
+    const char* fn = "moe_attention_backward";
+    if (!c) return MOE_EINVAL;
+    moe::PackedArgs a;
+    if (moe_status st = attn_check(c, fn, t, &a)) return st;
+    const int64_t Tq = t->tokens_q, Tk = t->tokens_k, qw = (int64_t)a.q_heads * a.D, kw = (int64_t)a.kv_heads * a.D;
+    if (moe_status st = tokens_check(c, fn, "dout", dout, t->dtype, Tq, qw, lddo)) return st;
+    if (moe_status st = tokens_check(c, fn, "q", q, t->dtype, Tq, qw, ldq)) return st;
+    if (moe_status st = tokens_check(c, fn, "k", k, t->dtype, Tk, kw, ldk)) return st;
+    if (moe_status st = tokens_check(c, fn, "v", v, t->dtype, Tk, kw, ldv)) return st;
+    if (moe_status st = tokens_check(c, fn, "out", out, t->dtype, Tq, qw, ldo)) return st;
+    if (moe_status st = tokens_check(c, fn, "dq", dq, t->dtype, Tq, qw, lddq)) return st;
+    if (moe_status st = tokens_check(c, fn, "dk", dk, t->dtype, Tk, kw, lddk)) return st;
+    if (moe_status st = tokens_check(c, fn, "dv", dv, t->dtype, Tk, kw, lddv)) return st;
+    CHECK(Tq == 0 || (lse && aligned_to(lse, 4)), "%s: null or misaligned lse", fn);
+    CHECK(workspace && aligned_to(workspace, 256), "%s: workspace must be 256-byte aligned", fn);
+    const size_t need = moe_attention_workspace(Tq, a.q_heads);
+    CHECK(workspace_bytes >= need, "%s: workspace of %zu bytes, %zu needed", fn, workspace_bytes, need);
+    if (moe_status st = need_device(c)) return st;
+    if (t->n == 0) return MOE_OK;
+    a.q = q; a.k = k; a.v = v; a.out = (void*)out; a.lse = (float*)lse; a.dout = dout; a.dq = dq; a.dk = dk; a.dv = dv;
+    a.ldq = Tq > 1 ? ldq : qw; a.ldo = Tq > 1 ? ldo : qw; a.lddo = Tq > 1 ? lddo : qw; a.lddq = Tq > 1 ? lddq : qw;
+    a.ldk = Tk > 1 ? ldk : kw; a.ldv = Tk > 1 ? ldv : kw; a.lddk = Tk > 1 ? lddk : kw; a.lddv = Tk > 1 ? lddv : kw;
+    a.delta = (float*)workspace;
+    a.err = error_word(c);
+    DeviceGuard dg(device_of(c));
+    LAUNCH(a.bf16 ? moe::launch_attention_backward_bf16(a, (hipStream_t)stream) : moe::launch_attention_backward_f32(a, (hipStream_t)stream));
+}
+
 }  // extern "C"

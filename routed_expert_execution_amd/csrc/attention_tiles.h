@@ -1,0 +1,242 @@
+// What the kernels of attention over packed sequences share: tiles of tokens in
+// LDS, operands of the matrix cores from them, and which keys a row sees.
+//
+// Products are taken so that a lane holds one row of a result: S^T = K Q^T has the
+// row (of queries) of lane % 32 and 16 keys in its registers.  The next product
+// sums over these keys, O^T = V^T P^T, and takes its operands' keys in the order in
+// which the registers hold them, so that P goes from one product into the next
+// without leaving the lane.  The backward products are laid out likewise.
+#pragma once
+
+#include "attention_device.h"
+#include "tile_gemm.h"
+
+namespace moe {
+namespace packed {
+
+using tile::f32x16;
+using tile::Fragment;
+using tile::mma;
+using tile::s16x4;
+using tile::s16x8;
+using tile::u32x4;
+typedef bf16x8_t bf16x8;
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+
+constexpr float kInf = __builtin_huge_valf(), kLog2e = 1.44269504088896f, kLn2 = 0.693147180559945f;
+
+// Key of result register i of a 32 x 32 block in lane half h: 8 (i / 4) + 4 h + i % 4.
+__device__ inline int reg_line(int i, int h) { return 8 * (i >> 2) + 4 * h + (i & 3); }
+
+// A tile of R lines (tokens) of D channels in LDS: 16-byte chunks, lines padded to a
+// power of two of them; chunk c of line r lies at c ^ x(r), such that 16 lines read
+// at one chunk, and the 4 lines x 32 bytes that a transposing read takes, lie in
+// different banks.
+template <bool BF16, int D>
+struct Tile {
+    static constexpr int kPer = BF16 ? 8 : 4;  // elements a chunk
+    static constexpr int kChunks = D / kPer;
+    static constexpr int kLine = kChunks <= 8 ? 8 : kChunks <= 16 ? 16 : kChunks <= 32 ? 32 : 64;
+    static constexpr int kLineBytes = kLine * 16;
+
+    __device__ static int at(int r, int c) {
+        const int x = kLine == 8 ? (r >> 1 & 3) * 2 ^ (r >> 3 & 1) : (r & 7) * 2 ^ (r >> 3 & 1);
+        return (r * kLine + (c ^ x)) << 4;
+    }
+    // Operand with a line a lane: lines r0 + lane % 32, channels 16 kk + 8 (lane / 32) + 0..7.
+    __device__ static void along(const char* lds, int r0, int kk, int lane, Fragment<BF16>& f) {
+        const int r = r0 + (lane & 31), h = lane >> 5;
+        if constexpr (BF16) {
+            f.raw = *(const bf16x8*)(lds + at(r, 2 * kk + h));
+        } else {
+#pragma unroll
+            for (int i = 0; i < 2; i++) {
+                const f32x4 v = *(const f32x4*)(lds + at(r, 4 * kk + 2 * h + i));
+#pragma unroll
+                for (int e = 0; e < 4; e++) f.raw[4 * i + e] = v[e];
+            }
+        }
+    }
+    // Operand with a channel a lane, c0 + lane % 32, over the 16 lines from r0 on in
+    // the order of result registers: r0 + reg_line(e, lane / 32).
+    __device__ static void across(const char* lds, int r0, int c0, int lane, Fragment<BF16>& f) {
+        const int h = lane >> 5;
+        if constexpr (BF16) {
+            const int r = r0 + 4 * h + (lane >> 2 & 3), col = c0 + 16 * (lane >> 4 & 1) + 4 * (lane & 3);
+            s16x8 v;
+#pragma unroll
+            for (int i = 0; i < 2; i++) {
+                typedef __attribute__((address_space(3))) s16x4 lds4;
+                const s16x4 t = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4*)(lds + at(r + 8 * i, col >> 3) + ((col & 7) << 1)));
+#pragma unroll
+                for (int e = 0; e < 4; e++) v[4 * i + e] = t[e];
+            }
+            f.raw = __builtin_bit_cast(bf16x8, v);
+        } else {
+            const int col = c0 + (lane & 31);
+#pragma unroll
+            for (int e = 0; e < 8; e++) f.raw[e] = *(const float*)(lds + at(r0 + reg_line(e, h), col >> 2) + ((col & 3) << 2));
+        }
+    }
+};
+
+// An operand straight from memory, a line a lane: as Tile::along, zero past the lines' end.
+template <bool BF16>
+__device__ inline void along_memory(const void* p, int64_t line, bool inside, int kk, int lane, Fragment<BF16>& f) {
+    float v[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+    if constexpr (BF16) {
+        u32x4 w = {0, 0, 0, 0};
+        if (inside) {
+            const Words4 m = *(const Words4*)((const uint16_t*)p + line + 16 * kk + 8 * (lane >> 5));
+            w = u32x4{m.v[0], m.v[1], m.v[2], m.v[3]};
+        }
+        f.raw = __builtin_bit_cast(bf16x8, w);
+    } else {
+        if (inside) load8<false>(p, line + 16 * kk + 8 * (lane >> 5), v);
+#pragma unroll
+        for (int e = 0; e < 8; e++) f.raw[e] = v[e];
+    }
+}
+
+// Eight fp32 values as an operand.
+__device__ inline void operand_of(const float (&v)[8], Fragment<true>& f) {
+#pragma unroll
+    for (int e = 0; e < 8; e++) f.raw[e] = (__bf16)v[e];
+}
+__device__ inline void operand_of(const float (&v)[8], Fragment<false>& f) {
+#pragma unroll
+    for (int e = 0; e < 8; e++) f.raw[e] = v[e];
+    f.split();
+}
+
+// R lines of a tensor on their way from memory into a tile by THREADS threads, a
+// chunk a thread at a time, zeros past `lines`.
+template <bool BF16, int D, int R, int THREADS>
+struct Staged {
+    typedef Tile<BF16, D> T;
+    static constexpr int kEach = (R * T::kChunks + THREADS - 1) / THREADS;
+    u32x4 v[kEach];
+    __device__ void load(const void* base, int64_t ld, int64_t first, int lines) {
+#pragma unroll
+        for (int i = 0; i < kEach; i++) {
+            const int n = threadIdx.x + i * THREADS, r = n / T::kChunks, c = n - r * T::kChunks;
+            v[i] = u32x4{0, 0, 0, 0};
+            if (r < min(R, lines)) {
+                const Words4 w = *(const Words4*)((const char*)base + ((first + r) * ld + c * T::kPer) * (BF16 ? 2 : 4));
+                v[i] = u32x4{w.v[0], w.v[1], w.v[2], w.v[3]};
+            }
+        }
+    }
+    __device__ void store(char* lds) const {
+#pragma unroll
+        for (int i = 0; i < kEach; i++) {
+            const int n = threadIdx.x + i * THREADS, r = n / T::kChunks, c = n - r * T::kChunks;
+            if (n < R * T::kChunks) *(u32x4*)(lds + T::at(r, c)) = v[i];
+        }
+    }
+    __device__ bool any_not_finite() const {
+        uint32_t bad = 0;
+#pragma unroll
+        for (int i = 0; i < kEach; i++)
+#pragma unroll
+            for (int e = 0; e < 4; e++) {
+                const uint32_t w = v[i][e];
+                if (BF16) bad |= (uint32_t)((w & 0x7F80u) == 0x7F80u) | (uint32_t)((w & 0x7F800000u) == 0x7F800000u);
+                else bad |= (uint32_t)((w & 0x7F800000u) == 0x7F800000u);
+            }
+        return bad;
+    }
+};
+
+// acc += a b where b's values are 0 for pairs that do not see each other, and a may
+// hold values that are not finite: 0 times these must add nothing.  They are taken
+// out, and results that see one become NaN.  seen: 1 or 0 for each of b's pairs.
+__device__ inline void mma_seen(f32x16& acc, const Fragment<true>& a, const Fragment<true>& b, const bf16x8& seen) {
+    // (in words and out of the compiler's sight: it takes a test of a bf16's bits for
+    // not finite to be false)
+    u32x4 w = __builtin_bit_cast(u32x4, a.raw), odd;
+    bool any = false;
+#pragma unroll
+    for (int e = 0; e < 4; e++) {
+        uint32_t v = w[e];
+        asm("" : "+v"(v));
+        const bool lo = (v & 0x7F80u) == 0x7F80u, hi = (v & 0x7F800000u) == 0x7F800000u;
+        any |= lo || hi;
+        odd[e] = (lo ? 0x3F80u : 0u) | (hi ? 0x3F800000u : 0u);
+        w[e] = (lo ? 0u : v & 0xFFFFu) | (hi ? 0u : v & 0xFFFF0000u);
+    }
+    Fragment<true> clean;
+    clean.raw = __builtin_bit_cast(bf16x8, w);
+    mma(acc, clean, b);
+    if (__any(any)) {
+        f32x16 n;
+#pragma unroll
+        for (int i = 0; i < 16; i++) n[i] = 0;
+        n = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, odd), seen, n, 0, 0, 0);
+#pragma unroll
+        for (int i = 0; i < 16; i++) acc[i] = n[i] > 0.f ? __uint_as_float(0x7FC00000u) : acc[i];
+    }
+}
+__device__ inline void mma_seen(f32x16& acc, const Fragment<false>& a, const Fragment<false>& b, const bf16x8& seen) {
+    Fragment<false> clean;
+    bf16x8 odd;
+    bool any = false;
+#pragma unroll
+    for (int e = 0; e < 8; e++) {
+        uint32_t v = __float_as_uint(a.raw[e]);
+        asm("" : "+v"(v));
+        const bool bad = (v & 0x7F800000u) == 0x7F800000u;
+        any |= bad;
+        odd[e] = (__bf16)(bad ? 1.f : 0.f);
+        clean.raw[e] = bad ? 0.f : a.raw[e];
+    }
+    clean.split();
+    mma(acc, clean, b);
+    if (__any(any)) {
+        f32x16 n;
+#pragma unroll
+        for (int i = 0; i < 16; i++) n[i] = 0;
+        n = __builtin_amdgcn_mfma_f32_32x32x16_bf16(odd, seen, n, 0, 0, 0);
+#pragma unroll
+        for (int i = 0; i < 16; i++) acc[i] = n[i] > 0.f ? __uint_as_float(0x7FC00000u) : acc[i];
+    }
+}
+
+// A sequence's rows of queries and keys; what lies outside the tensors is cut off
+// and makes it bad.
+struct Sequence {
+    int q0, rows, k0, keys;
+    bool bad;
+    int shift;  // row i sees keys up to i + shift if causal
+};
+__device__ inline int clamp_to(int v, int T) { return min(max(v, 0), T); }
+__device__ inline Sequence sequence_of(const PackedArgs& a, int s) {
+    const int qa = a.offsets_q[s], qb = a.offsets_q[s + 1], ka = a.offsets_k[s], kb = a.offsets_k[s + 1];
+    Sequence r;
+    r.bad = qa < 0 || qb < qa || qb > a.Tq || ka < 0 || kb < ka || kb > a.Tk;
+    r.q0 = clamp_to(qa, a.Tq);
+    r.rows = max(0, clamp_to(qb, a.Tq) - r.q0);
+    r.k0 = clamp_to(ka, a.Tk);
+    r.keys = max(0, clamp_to(kb, a.Tk) - r.k0);
+    r.shift = r.keys - r.rows;
+    return r;
+}
+// Tile `slot` of all sequences' tiles of B tokens: sequence s has the slots from
+// offsets[s] / B + s on, as many as it has tiles or one more, so that a slot's
+// sequence is found without a sum over the others.
+template <int B>
+__device__ inline bool find_tile(const int32_t* offsets, int n, int T, int slot, int* seq, int* local) {
+    auto first = [&](int i) { return (int64_t)(clamp_to(offsets[i], T) / B + i); };
+    *seq = __builtin_amdgcn_readfirstlane(wave_find(n, slot, first));
+    *local = __builtin_amdgcn_readfirstlane((int)(slot - first(*seq)));
+    return *local >= 0;
+}
+inline int64_t tile_slots(int T, int B, int n) { return (int64_t)T / B + n; }
+
+// Whether row i sees key j.
+__device__ inline bool sees(const PackedArgs& a, const Sequence& s, int i, int j) {
+    return j < s.keys && (!a.causal || j <= i + s.shift) && (!a.window || j > i + s.shift - a.window);
+}
+
+}  // namespace packed
+}  // namespace moe

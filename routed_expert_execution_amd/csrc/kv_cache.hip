@@ -82,6 +82,7 @@ __global__ __launch_bounds__(kThreads) void kv_append_kernel(KvAppendArgs a) {
     __shared__ double2 turns[128];
     __shared__ float2 turns_q[128];
     const int token = blockIdx.x;
+    if (token == (int)gridDim.x - 1 && blockIdx.y == 0) check_offsets(a.batch.offsets, a.batch.n, a.batch.T, a.err);
     TokenPlace at;
     if (!find_token(a.batch, token, &at)) {
         if (at.bad && threadIdx.x == 0) atomicOr(a.err, kErrCache);
@@ -187,6 +188,7 @@ __global__ __launch_bounds__(kThreads) void kv_append_kernel(KvAppendArgs a) {
 template <bool BF16>
 __global__ __launch_bounds__(kThreads) void kv_read_kernel(KvReadArgs a) {
     const int token = blockIdx.x;
+    if (token == (int)gridDim.x - 1 && blockIdx.y == 0) check_offsets(a.batch.offsets, a.batch.n, a.batch.T, a.err);
     TokenPlace at;
     if (!find_token(a.batch, token, &at)) {
         if (at.bad && threadIdx.x == 0) atomicOr(a.err, kErrCache);

@@ -64,6 +64,12 @@ class moe_kv_batch(C.Structure):
                 ("max_pages", C.c_int32), ("tokens", C.c_int64), ("most_new", C.c_int64)]
 
 
+class moe_attn(C.Structure):
+    _fields_ = [("offsets_q", C.c_void_p), ("offsets_k", C.c_void_p), ("n", C.c_int32), ("dtype", C.c_int32),
+                ("q_heads", C.c_int32), ("kv_heads", C.c_int32), ("head_dim", C.c_int32), ("causal", C.c_int32),
+                ("scale", C.c_float), ("window", C.c_int64), ("tokens_q", C.c_int64), ("tokens_k", C.c_int64)]
+
+
 def _load() -> C.CDLL:
     # torch ships its own HIP runtime.  Loading torch first makes libmoe's
     # libamdhip64.so.7 dependency resolve (by soname) to that same runtime;
@@ -77,6 +83,7 @@ def _load() -> C.CDLL:
     planp = C.POINTER(moe_plan)
     qmatp = C.POINTER(moe_qmat)
     F32, F64 = C.c_float, C.c_double
+    attnp = C.POINTER(moe_attn)
     rotp, kvp, batchp = C.POINTER(moe_rotary), C.POINTER(moe_kv_cache), C.POINTER(moe_kv_batch)
     sig = {
         "moe_payload_bytes": (S, [cfgp]),
@@ -122,6 +129,9 @@ def _load() -> C.CDLL:
         "moe_kv_read": (C.c_int, [P, kvp, batchp, P, I64, P, I64, I32, P]),
         "moe_attention_cached_workspace": (S, [kvp, batchp, I32]),
         "moe_attention_cached": (C.c_int, [P, kvp, batchp, P, I64, I32, I32, F32, I64, P, I64, P, S, P]),
+        "moe_attention": (C.c_int, [P, attnp, P, I64, P, I64, P, I64, P, I64, P, P]),
+        "moe_attention_workspace": (S, [I64, I32]),
+        "moe_attention_backward": (C.c_int, [P, attnp] + [P, I64] * 5 + [P] + [P, I64] * 3 + [P, S, P]),
         "moe_stats": (C.c_int, [P, C.POINTER(C.c_uint64)]),
         "moe_check": (C.c_int, [P, P]),
         "moe_page_table": (C.c_int, [P, C.POINTER(P)]),
@@ -147,7 +157,8 @@ EXPORTS = ("moe_payload_bytes", "moe_plan_bytes", "moe_pack_expert", "moe_unpack
            "moe_probe_mfma", "moe_probe_lds", "moe_linear_bytes", "moe_linear_pack", "moe_linear_dequant", "moe_linear",
            "moe_linear_gated", "moe_gated", "moe_gated_workspace", "moe_gated_backward", "moe_linear_plan",
            "moe_gated_plan", "moe_rotary_freqs", "moe_rotate", "moe_kv_bytes", "moe_kv_append", "moe_kv_read",
-           "moe_attention_cached_workspace", "moe_attention_cached")
+           "moe_attention_cached_workspace", "moe_attention_cached", "moe_attention", "moe_attention_workspace",
+           "moe_attention_backward")
 
 
 def library() -> C.CDLL:
@@ -906,6 +917,61 @@ def moe_attention_cached(ctx: Context, cache: KvCache, batch: KvBatch, q, out, *
     _call(ctx, _lib.moe_attention_cached(ctx.handle, cache.ref, batch.ref, qp, ldq, code, H, D ** -0.5 if scale is None else scale,
                                          window, op, ldo, _ptr(workspace), workspace.numel() * workspace.element_size(),
                                          _stream_on(ctx, stream)))
+
+
+def _attn(ctx: Context, q, k, offsets, offsets_k, causal: bool, window: int, scale) -> moe_attn:
+    """The sequences and heads of a call from q [tokens_q, q_heads, D] and k [tokens_k, kv_heads, D]."""
+    if offsets_k is None:
+        offsets_k = offsets
+    if offsets.dim() != 1 or offsets.numel() < 1:
+        raise ValueError("offsets must be int32 [n + 1]")
+    n = offsets.shape[0] - 1
+    Tq, H, D = q.shape
+    Tk, Hkv, _ = k.shape
+    return moe_attn(_whole(ctx, offsets, (n + 1,), "offsets"), _whole(ctx, offsets_k, (n + 1,), "offsets_k"), n,
+                    _TYPE_CODES.get(q.dtype, -1), H, Hkv, D, int(causal), D ** -0.5 if scale is None else scale, window, Tq, Tk)
+
+
+def moe_attention(ctx: Context, q, k, v, offsets, out, *, lse=None, offsets_k=None, causal: bool = True, window: int = 0,
+                  scale: float | None = None, stream=None) -> None:
+    """out = softmax(scale q k^T) v over packed sequences.  q, out: float32 or
+    bfloat16 [tokens_q, q_heads, D], k, v: [tokens_k, kv_heads, D], tokens may lie
+    apart; offsets (and offsets_k, where keys are others than the queries' tokens):
+    int32 [n + 1]; lse: float32 [tokens_q, q_heads], kept for the backward pass;
+    scale: D ** -0.5 unless given."""
+    (Tq, H, D), (Tk, Hkv, _), kind = q.shape, k.shape, q.dtype
+    qp, ldq, _ = _heads(ctx, q, Tq, H, D, "q")
+    kp, ldk, _ = _heads(ctx, k, Tk, Hkv, D, "k", kind)
+    vp, ldv, _ = _heads(ctx, v, Tk, Hkv, D, "v", kind)
+    op, ldo, _ = _heads(ctx, out, Tq, H, D, "out", kind)
+    lp = None if lse is None else _dense(ctx, lse, Tq, H, "lse", torch.float32)[0]
+    t = _attn(ctx, q, k, offsets, offsets_k, causal, window, scale)
+    _call(ctx, _lib.moe_attention(ctx.handle, C.byref(t), qp, ldq, kp, ldk, vp, ldv, op, ldo, lp, _stream_on(ctx, stream)))
+
+
+def moe_attention_workspace(ctx: Context, q, k=None) -> int:
+    """Bytes of moe_attention_backward's workspace for q [tokens_q, q_heads, D]."""
+    n = int(_lib.moe_attention_workspace(q.shape[0], q.shape[1]))
+    if n == 0:
+        raise ValueError("bad sizes")
+    return n
+
+
+def moe_attention_backward(ctx: Context, dout, q, k, v, out, lse, offsets, *, dq, dk, dv, workspace, offsets_k=None,
+                           causal: bool = True, window: int = 0, scale: float | None = None, stream=None) -> None:
+    """Gradients of moe_attention into dq, dk and dv from dout, its inputs, its out
+    and lse, all of q's type but lse; workspace: uint8, moe_attention_workspace bytes."""
+    (Tq, H, D), (Tk, Hkv, _), kind = q.shape, k.shape, q.dtype
+    args = []
+    for t, T, heads, name in ((dout, Tq, H, "dout"), (q, Tq, H, "q"), (k, Tk, Hkv, "k"), (v, Tk, Hkv, "v"), (out, Tq, H, "out")):
+        args += _heads(ctx, t, T, heads, D, name, kind)[:2]
+    args.append(_dense(ctx, lse, Tq, H, "lse", torch.float32)[0])
+    for t, T, heads, name in ((dq, Tq, H, "dq"), (dk, Tk, Hkv, "dk"), (dv, Tk, Hkv, "dv")):
+        args += _heads(ctx, t, T, heads, D, name, kind)[:2]
+    _check_dev(ctx, workspace)
+    t = _attn(ctx, q, k, offsets, offsets_k, causal, window, scale)
+    _call(ctx, _lib.moe_attention_backward(ctx.handle, C.byref(t), *args, _ptr(workspace),
+                                           workspace.numel() * workspace.element_size(), _stream_on(ctx, stream)))
 
 
 def moe_stats(ctx: Context) -> dict:

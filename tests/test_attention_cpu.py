@@ -62,6 +62,7 @@ def test_null_contexts_and_structs(ctx):
     assert lib.moe_kv_append(None, C.byref(m), C.byref(b), BASE, 128, BASE, 128, 1, None, None, None, 0, 0, None, 0, None) == moe.MOE_EINVAL
     assert lib.moe_kv_read(None, C.byref(m), C.byref(b), BASE, 128, BASE, 128, 1, None) == moe.MOE_EINVAL
     assert lib.moe_attention_cached(None, C.byref(m), C.byref(b), BASE, 128, 1, 2, 1.0, 0, BASE, 128, BASE, 1 << 16, None) == moe.MOE_EINVAL
+    _refused(ctx, lib.moe_attention(ctx.handle, None, BASE, 256, BASE, 128, BASE, 128, BASE, 256, None, None), "null description")
     _refused(ctx, lib.moe_kv_read(ctx.handle, None, C.byref(b), BASE, 128, BASE, 128, 1, None), "null cache")
     _refused(ctx, lib.moe_kv_read(ctx.handle, C.byref(m), None, BASE, 128, BASE, 128, 1, None), "bad batch")
     assert lib.moe_attention_cached_workspace(None, C.byref(b), 2) == 0 and lib.moe_attention_cached_workspace(C.byref(m), None, 2) == 0
@@ -114,6 +115,60 @@ def _cached(ctx, cache=None, batch=None, q=BASE, ldq=256, dtype=1, q_heads=4, sc
     (dict(window=-1), "window"), (dict(window=1 << 40), "host-only"), (dict(ws=None), "workspace"), (dict(ws=BASE + 128), "256-byte"), (dict(n=255), "needed")])
 def test_attention_cached_refuses(ctx, kw, text):
     _refused(ctx, _cached(ctx, **kw), text)
+
+
+ATTN = dict(offsets_q=BASE, offsets_k=BASE, n=2, dtype=1, q_heads=4, kv_heads=2, head_dim=64, causal=1, scale=0.125, window=0, tokens_q=8, tokens_k=9)
+PACKED = [(dict(n=-1), "n outside"), (dict(n=65537), "n outside"), (dict(tokens_q=-1), "tokens outside"), (dict(tokens_k=(1 << 22) + 1), "tokens outside"), (dict(offsets_q=None), "null offsets"),
+          (dict(offsets_k=None), "null offsets"), (dict(offsets_k=BASE + 2), "misaligned offsets"), (dict(dtype=2), "bad type"), (dict(q_heads=3), "multiple"), (dict(q_heads=0), "multiple"),
+          (dict(kv_heads=0), "multiple"), (dict(q_heads=2048, kv_heads=1), "multiple"), (dict(head_dim=80), "head_dim"), (dict(causal=2), "causal"), (dict(window=-1), "window"),
+          (dict(causal=0, window=5), "window"), (dict(scale=0.0), "scale"), (dict(scale=-1.0), "scale"), (dict(scale=math.nan), "scale"), ({}, "host-only"), (dict(window=1 << 50), "host-only"),
+          (dict(n=0, offsets_q=None, offsets_k=None), "host-only"), (dict(causal=0), "host-only"), (dict(n=65536, q_heads=1024, kv_heads=1024), "too many")]
+
+
+def _attn(**kw):
+    return moe.moe_attn(*(kw.get(name, ATTN[name]) for name, _ in moe.moe_attn._fields_))
+
+
+def _forward(ctx, attn=None, q=BASE, ldq=1 << 20, k=BASE, ldk=1 << 20, v=BASE, ldv=1 << 20, out=BASE, ldo=1 << 20, lse=None):
+    return moe.library().moe_attention(ctx.handle, C.byref(attn or _attn()), q, ldq, k, ldk, v, ldv, out, ldo, lse, None)
+
+
+def _backward(ctx, attn=None, lse=BASE, ws=BASE, n=1 << 40, **kw):
+    args = []
+    for name in ("dout", "q", "k", "v", "out"):
+        args += [kw.get(name, BASE), kw.get("ld" + name, 1 << 20)]
+    args.append(lse)
+    for name in ("dq", "dk", "dv"):
+        args += [kw.get(name, BASE), kw.get("ld" + name, 1 << 20)]
+    return moe.library().moe_attention_backward(ctx.handle, C.byref(attn or _attn()), *args, ws, n, None)
+
+
+@pytest.mark.parametrize("kw,text", PACKED)
+def test_packed_sequences_refused(ctx, kw, text):
+    _refused(ctx, _forward(ctx, _attn(**kw)), text)
+    _refused(ctx, _backward(ctx, _attn(**kw)), text)
+
+
+@pytest.mark.parametrize("kw,text", [(dict(q=None), "null q"), (dict(k=None), "null k"), (dict(v=None), "null v"), (dict(out=None), "null out"), (dict(q=BASE + 1), "misaligned q"),
+                                     (dict(ldq=255), "tokens of q"), (dict(ldk=127), "tokens of k"), (dict(ldv=0), "tokens of v"), (dict(ldo=255), "tokens of out"), (dict(lse=BASE + 2), "lse"),
+                                     (dict(lse=BASE), "host-only"), (dict(attn=_attn(tokens_q=0, tokens_k=0), q=None, k=None, v=None, out=None), "host-only")])
+def test_attention_refuses(ctx, kw, text):
+    _refused(ctx, _forward(ctx, **kw), text)
+
+
+@pytest.mark.parametrize("kw,text", [(dict(dout=None), "null dout"), (dict(lddout=255), "tokens of dout"), (dict(out=None), "null out"), (dict(dq=None), "null dq"), (dict(dk=None), "null dk"),
+                                     (dict(dv=None), "null dv"), (dict(lddk=127), "tokens of dk"), (dict(dv=BASE + 1), "misaligned dv"), (dict(lse=None), "lse"), (dict(ws=None), "workspace"),
+                                     (dict(ws=BASE + 16), "256-byte"), (dict(n=255), "needed"), (dict(q=None), "null q"), (dict(ldv=5), "tokens of v")])
+def test_attention_backward_refuses(ctx, kw, text):
+    _refused(ctx, _backward(ctx, **kw), text)
+
+
+def test_attention_without_a_context():
+    t = _attn()
+    assert moe.library().moe_attention(None, C.byref(t), BASE, 256, BASE, 128, BASE, 128, BASE, 256, None, None) == moe.MOE_EINVAL
+    assert moe.library().moe_attention_backward(None, C.byref(t), *[BASE, 256] * 5, BASE, *[BASE, 256] * 3, BASE, 1 << 20, None) == moe.MOE_EINVAL
+    f = moe.library().moe_attention_workspace
+    assert f(0, 1) == 256 and f(1000, 32) == 128000 and f(-1, 1) == 0 and f(1, 0) == 0 and f((1 << 22) + 1, 1) == 0
 
 
 def test_sizes():
