@@ -98,6 +98,7 @@ __global__ __launch_bounds__(kBackwardWaves * 64) void attention_dq_kernel(Packe
         put(begin, 0);
     }
     __syncthreads();
+    const uint32_t along_lane = T::along_lane(lane), across_lane = T::across_lane(lane);
     int buffer = 0;
     for (int k0 = begin; k0 < end; k0 += BK, buffer ^= 1) {
         const bool more = k0 + BK < end;
@@ -107,10 +108,12 @@ __global__ __launch_bounds__(kBackwardWaves * 64) void attention_dq_kernel(Packe
         }
         const char* kt = lds + 2 * buffer * B::kTileBytes;
         const char* vt = kt + B::kTileBytes;
+        const uint32_t ka = tile::lds_address(kt) + along_lane, va = tile::lds_address(vt) + along_lane, kx = tile::lds_address(kt) + across_lane;
         const bool none = wave_first >= s.rows || (a.causal && k0 > wave_last + s.shift) || (a.window && k0 + BK - 1 <= wave_first + s.shift - a.window);
         if (!none) {
             const bool masked = k0 + BK > s.keys || (a.causal && k0 + BK - 1 > wave_first + s.shift) || (a.window && k0 <= wave_last + s.shift - a.window);
             const bool odd = masked && odd_tile[buffer] == k0;
+            const Span span = keys_seen(a, s, row, k0, h);
 #pragma unroll
             for (int b = 0; b < KB; b++) {
                 f32x16 st, dp;
@@ -119,17 +122,17 @@ __global__ __launch_bounds__(kBackwardWaves * 64) void attention_dq_kernel(Packe
 #pragma unroll
                 for (int kk = 0; kk < KK; kk++) {
                     Fragment<BF16> f;
-                    T::along(kt, 32 * b, kk, lane, f);
+                    T::along(ka, 32 * b, kk, f);
                     f.split();
                     mma(st, f, q[kk]);
-                    T::along(vt, 32 * b, kk, lane, f);
+                    T::along(va, 32 * b, kk, f);
                     f.split();
                     mma(dp, f, g[kk]);
                 }
 #pragma unroll
                 for (int i = 0; i < 16; i++) {
                     const float ds = __builtin_amdgcn_exp2f(fmaf(st[i], a.scale_log2, -lse)) * (dp[i] - delta);
-                    st[i] = masked && !sees(a, s, row, k0 + 32 * b + reg_line(i, h)) ? 0.f : ds;
+                    st[i] = masked && !span.has(b, i) ? 0.f : ds;
                 }
 #pragma unroll
                 for (int n = 0; n < 2; n++) {
@@ -141,11 +144,11 @@ __global__ __launch_bounds__(kBackwardWaves * 64) void attention_dq_kernel(Packe
                     bf16x8 seen;
                     if (odd)
 #pragma unroll
-                        for (int e = 0; e < 8; e++) seen[e] = (__bf16)(sees(a, s, row, k0 + 32 * b + reg_line(8 * n + e, h)) ? 1.f : 0.f);
+                        for (int e = 0; e < 8; e++) seen[e] = (__bf16)(span.has(b, 8 * n + e) ? 1.f : 0.f);
 #pragma unroll
                     for (int d = 0; d < DB; d++) {
                         Fragment<BF16> f;
-                        T::across(kt, 32 * b + 16 * n, 32 * d, lane, f);
+                        T::across(kx, 32 * b + 16 * n, 32 * d, f);
                         if (odd) {
                             mma_seen(out[d], f, df, seen);
                         } else {
@@ -248,15 +251,19 @@ __global__ __launch_bounds__(kBackwardWaves * 64) void attention_dkv_kernel(Pack
         put(0, 0);
     }
     __syncthreads();
+    const uint32_t along_lane = T::along_lane(lane), across_lane = T::across_lane(lane);
     for (int t = 0; t < total; t++) {
         const int buffer = t & 1, r0 = row_of(t);
         if (t + 1 < total) get(t + 1);
         const char* qt = lds + 2 * buffer * B::kTileBytes;
         const char* gt = qt + B::kTileBytes;
+        const uint32_t qa = tile::lds_address(qt) + along_lane, ga = tile::lds_address(gt) + along_lane;
+        const uint32_t qx = tile::lds_address(qt) + across_lane, gx = tile::lds_address(gt) + across_lane;
         const bool none = wave_key >= s.keys || (a.causal && wave_key > r0 + BQ - 1 + s.shift) || (a.window && wave_last_key <= r0 + s.shift - a.window);
         if (!none) {
             const bool masked = (a.causal && wave_last_key > r0 + s.shift) || (a.window && wave_key <= r0 + BQ - 1 + s.shift - a.window);
             const bool odd = masked && odd_tile[buffer] == t;
+            const Span span = rows_seeing(a, s, key, r0, h);
 #pragma unroll
             for (int b = 0; b < RB; b++) {
                 f32x16 st, dp;
@@ -265,13 +272,13 @@ __global__ __launch_bounds__(kBackwardWaves * 64) void attention_dkv_kernel(Pack
 #pragma unroll
                 for (int kk = 0; kk < KK; kk++) {
                     Fragment<BF16> f, o;
-                    T::along(qt, 32 * b, kk, lane, f);
+                    T::along(qa, 32 * b, kk, f);
                     f.split();
                     o = k[kk];
                     o.split();
                     mma(st, f, o);
                     if constexpr (kDk) {
-                        T::along(gt, 32 * b, kk, lane, f);
+                        T::along(ga, 32 * b, kk, f);
                         f.split();
                         o = v[kk];
                         o.split();
@@ -285,7 +292,7 @@ __global__ __launch_bounds__(kBackwardWaves * 64) void attention_dkv_kernel(Pack
 #pragma unroll
                     for (int e = 0; e < 4; e++) {
                         const int i = 4 * j + e;
-                        const bool off = masked && !sees(a, s, r0 + 32 * b + reg_line(i, h), key);
+                        const bool off = masked && !span.has(b, i);
                         p[i] = __builtin_amdgcn_exp2f(fmaf(st[i], a.scale_log2, -lse[e]));
                         const float ds = p[i] * (dp[i] - delta[e]);
                         p[i] = off ? 0.f : p[i];
@@ -299,7 +306,7 @@ __global__ __launch_bounds__(kBackwardWaves * 64) void attention_dkv_kernel(Pack
                     bf16x8 seen;
                     if (odd)
 #pragma unroll
-                        for (int e = 0; e < 8; e++) seen[e] = (__bf16)(sees(a, s, r0 + 32 * b + reg_line(8 * n + e, h), key) ? 1.f : 0.f);
+                        for (int e = 0; e < 8; e++) seen[e] = (__bf16)(span.has(b, 8 * n + e) ? 1.f : 0.f);
                     if constexpr (kDv) {
 #pragma unroll
                         for (int e = 0; e < 8; e++) x[e] = p[8 * n + e];
@@ -314,7 +321,7 @@ __global__ __launch_bounds__(kBackwardWaves * 64) void attention_dkv_kernel(Pack
                     for (int d = 0; d < DB; d++) {
                         Fragment<BF16> f;
                         if constexpr (kDv) {
-                            T::across(gt, 32 * b + 16 * n, 32 * d, lane, f);
+                            T::across(gx, 32 * b + 16 * n, 32 * d, f);
                             if (odd) {
                                 mma_seen(dv[d], f, pf, seen);
                             } else {
@@ -323,7 +330,7 @@ __global__ __launch_bounds__(kBackwardWaves * 64) void attention_dkv_kernel(Pack
                             }
                         }
                         if constexpr (kDk) {
-                            T::across(qt, 32 * b + 16 * n, 32 * d, lane, f);
+                            T::across(qx, 32 * b + 16 * n, 32 * d, f);
                             if (odd) {
                                 mma_seen(dk[d], f, df, seen);
                             } else {

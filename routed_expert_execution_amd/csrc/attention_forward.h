@@ -10,19 +10,20 @@ namespace packed {
 
 constexpr int kForwardWaves = 4;
 template <bool BF16, int D> struct ForwardShape {
-    static constexpr int kWaves = kForwardWaves;
-    static constexpr int kRows = 32 * kWaves;              // a wave has 32 rows
+    static constexpr int kThreads = 64 * kForwardWaves;
+    static constexpr int kRows = 32 * kForwardWaves;          // a wave has 32 rows
     static constexpr int kKeys = BF16 && D <= 128 ? 64 : 32;  // of a tile
     static constexpr int kTileBytes = kKeys * Tile<BF16, D>::kLineBytes;
-    static constexpr int kLds = 4 * kTileBytes;            // keys and values, double
 };
 
-template <bool BF16, int D>
-__global__ __launch_bounds__(kForwardWaves * 64) void attention_kernel(PackedArgs a) {
+// DIRECT: tiles go straight from memory into LDS (lines
+// whole 16-byte chunks in memory); else through registers.
+template <bool BF16, int D, bool DIRECT>
+__global__ __launch_bounds__(kForwardWaves * 64, BF16 && D <= 128 ? 2 : 1) void attention_kernel(PackedArgs a) {
     typedef ForwardShape<BF16, D> F;
     typedef Tile<BF16, D> T;
-    constexpr int kThreads = F::kWaves * 64, BK = F::kKeys, KK = D / 16, DB = D / 32, KB = BK / 32;
-    __shared__ __attribute__((aligned(1024))) char lds[F::kLds];
+    constexpr int BK = F::kKeys, KK = D / 16, DB = D / 32, KB = BK / 32;
+    __shared__ __attribute__((aligned(1024))) char lds[4 * F::kTileBytes];
     __shared__ int odd_tile[2];  // the last tile whose values are not all finite, by buffer
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), h = lane >> 5;
 
@@ -39,10 +40,10 @@ __global__ __launch_bounds__(kForwardWaves * 64) void attention_kernel(PackedArg
     const Sequence s = sequence_of(a, seq);
     const int tiles = (s.rows + F::kRows - 1) / F::kRows;
     if (local >= tiles) return;
-    const int row0 = (tiles - 1 - local) * F::kRows, row = row0 + wave * 32 + (lane & 31);
-    const bool live = row < s.rows;
+    const int row0 = (tiles - 1 - local) * F::kRows, wave_first = row0 + wave * 32, row = wave_first + (lane & 31);
     if (s.bad && threadIdx.x == 0) atomicOr(a.err, kErrCache);
 
+    const bool live = row < s.rows;
     Fragment<BF16> q[KK];
     const int64_t line = (int64_t)(s.q0 + row) * a.ldq + (int64_t)head * D;
 #pragma unroll
@@ -55,145 +56,229 @@ __global__ __launch_bounds__(kForwardWaves * 64) void attention_kernel(PackedArg
     for (int d = 0; d < DB; d++)
 #pragma unroll
         for (int i = 0; i < 16; i++) out[d][i] = 0;
-    float m = -kInf, l = 0;  // of the row: m the largest q.k so far; l this lane's part of the sum
+    float m = -kInf, l = 0;  // of the row: m the largest q.k, about; l this lane's part of the sum
 
     // keys that any of the workgroup's rows, and of the wave's, sees
     const int last_row = min(row0 + F::kRows, s.rows) - 1;
     const int end = a.causal ? min(s.keys, last_row + s.shift + 1) : s.keys;
     const int begin = a.window ? max(0, row0 + s.shift - a.window + 1) / BK * BK : 0;
-    const int wave_first = row0 + wave * 32, wave_last = min(wave_first + 31, s.rows - 1);
+    const int wave_last = min(wave_first + 31, s.rows - 1);
 
     const char* kbase = (const char*)a.k + ((int64_t)s.k0 * a.ldk + (int64_t)kv_head * D) * (BF16 ? 2 : 4);
     const char* vbase = (const char*)a.v + ((int64_t)s.k0 * a.ldv + (int64_t)kv_head * D) * (BF16 ? 2 : 4);
     auto masked_tile = [&](int k0) {  // for some row of the workgroup
         return k0 + BK > s.keys || (a.causal && k0 + BK - 1 > row0 + s.shift) || (a.window && k0 <= last_row + s.shift - a.window);
     };
-    Staged<BF16, D, BK, kThreads> sk, sv;
-    auto put = [&](int k0, int buffer) {
-        sk.store(lds + 2 * buffer * F::kTileBytes);
-        sv.store(lds + (2 * buffer + 1) * F::kTileBytes);
-        if (masked_tile(k0) && sv.any_not_finite()) odd_tile[buffer] = k0;
-    };
+    Pipe<BF16, D, BK, F::kThreads, DIRECT> pk, pv;
     if (threadIdx.x < 2) odd_tile[threadIdx.x] = -1;
-    if (begin < end) {
-        sk.load(kbase, a.ldk, begin, s.keys - begin);
-        sv.load(vbase, a.ldv, begin, s.keys - begin);
-        __syncthreads();
-        put(begin, 0);
-    }
-    __syncthreads();
-    int buffer = 0;
-    for (int k0 = begin; k0 < end; k0 += BK, buffer ^= 1) {
-        const bool more = k0 + BK < end;
-        if (more) {
-            sk.load(kbase, a.ldk, k0 + BK, s.keys - k0 - BK);
-            sv.load(vbase, a.ldv, k0 + BK, s.keys - k0 - BK);
-        }
-        const char* kt = lds + 2 * buffer * F::kTileBytes;
-        const char* vt = kt + F::kTileBytes;
-        const bool none = wave_first >= s.rows || (a.causal && k0 > wave_last + s.shift) || (a.window && k0 + BK - 1 <= wave_first + s.shift - a.window);
-        if (!none) {
-            f32x16 st[KB];
+    // The products of a tile's scores run one tile ahead, beside the exponentials of the
+    // tile before: keys of tile t + 1 and values of tile t are in LDS at a time.
+    f32x16 st[KB], nx[KB];
+    auto scores = [&](uint32_t ka, f32x16 (&to)[KB]) __attribute__((always_inline)) {
 #pragma unroll
-            for (int b = 0; b < KB; b++) {
+        for (int b = 0; b < KB; b++) {
 #pragma unroll
-                for (int i = 0; i < 16; i++) st[b][i] = 0;
+            for (int i = 0; i < 16; i++) to[b][i] = 0;
 #pragma unroll
-                for (int kk = 0; kk < KK; kk++) {
-                    Fragment<BF16> f;
-                    T::along(kt, 32 * b, kk, lane, f);
-                    f.split();
-                    mma(st[b], f, q[kk]);
-                }
+            for (int kk = 0; kk < KK; kk++) {
+                Fragment<BF16> f;
+                T::along(ka, 32 * b, kk, f);
+                f.split();
+                mma(to[b], f, q[kk]);
+                __builtin_amdgcn_sched_barrier(0);  // (operands of one product at a time: registers are short)
             }
-            const bool masked = k0 + BK > s.keys || (a.causal && k0 + BK - 1 > wave_first + s.shift) || (a.window && k0 <= wave_last + s.shift - a.window);
-            if (masked) {
+        }
+    };
+    auto exponentials = [&](float base, int b, int g, Fragment<BF16>& pf) __attribute__((always_inline)) {
+        float p[8];
+#pragma unroll
+        for (int e = 0; e < 8; e++) {
+            p[e] = __builtin_amdgcn_exp2f(fmaf(st[b][8 * g + e], a.scale_log2, -base));
+            l += p[e];
+        }
+        operand_of(p, pf);
+    };
+    auto values = [&](uint32_t va, int b, int g, const Fragment<BF16>& pf) __attribute__((always_inline)) {
+#pragma unroll
+        for (int d = 0; d < DB; d++) {
+            Fragment<BF16> f;
+            T::across(va, 32 * b + 16 * g, 32 * d, f);
+            f.split();
+            mma(out[d], f, pf);
+            __builtin_amdgcn_sched_barrier(0);
+        }
+    };
+    auto in_range = [&](int k0) {  // some row of the wave sees a key of the tile
+        return k0 >= begin && k0 < end && wave_first < s.rows && !(a.causal && k0 > wave_last + s.shift) &&
+               !(a.window && k0 + BK - 1 <= wave_first + s.shift - a.window);
+    };
+    const uint32_t along_lane = T::along_lane(lane), across_lane = T::across_lane(lane);
+    int buffer = 0;
+    if (begin < end) pk.fetch(kbase, a.ldk, begin, s.keys - begin, lds);
+    // Tile k0's values and the next one's keys have arrived, and those after them are fetched.
+    auto advance = [&](int k0, bool check) __attribute__((always_inline)) {
+        char* kt = lds + 2 * buffer * F::kTileBytes;
+        const int next = k0 + BK;
+        if (next < end) pk.arrive(kt);
+        if (k0 >= begin) pv.arrive(kt + F::kTileBytes);
+        meet<DIRECT>();
+        if (check && k0 >= begin && masked_tile(k0)) {
+            if (tile_not_finite<BF16, D, BK, F::kThreads>(kt + F::kTileBytes)) odd_tile[buffer] = k0;
+            __syncthreads();
+        }
+        if (next + BK < end) pk.fetch(kbase, a.ldk, next + BK, s.keys - next - BK, lds + 2 * (buffer ^ 1) * F::kTileBytes);
+        if (next < end) pv.fetch(vbase, a.ldv, next, s.keys - next, lds + (2 * (buffer ^ 1) + 1) * F::kTileBytes);
+    };
+    // The next tile's scores, their maximum known, become this tile's.  The maximum that
+    // exponentials are taken against follows only where a row's would pass 2^8: sums in
+    // fp32 and factors in bf16 are as exact at any common scale.
+    auto follow = [&](float top) __attribute__((always_inline)) {
+        const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(top), __float_as_uint(top), false, false);
+        top = fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1]));
+        const float before = m;
+        const bool grown = (top - before) * a.scale_log2 > 8.f;
+        if (__any(grown)) {
+            m = grown ? top : before;
+            const float f = grown ? __builtin_amdgcn_exp2f((before - top) * a.scale_log2) : 1.f;
+            l *= f;
+#pragma unroll
+            for (int d = 0; d < DB; d++) out[d] *= f;
+        }
+#pragma unroll
+        for (int b = 0; b < KB; b++) st[b] = nx[b];
+    };
+    int k0 = begin - BK;
+    while (k0 < end) {
+        if constexpr (BF16) {
+            // Tiles that every row of the workgroup sees whole, as does the one after each:
+            // a product of the next scores, then some exponentials of this tile; a product
+            // with this tile's values, then some of the next scores' maximum.  The matrix
+            // cores run while the wave goes on; operands are read a product ahead.
+#pragma unroll 1
+            while (k0 >= begin && k0 + BK < end && !masked_tile(k0) && !masked_tile(k0 + BK)) {
+                advance(k0, false);
+                const uint32_t ka = tile::lds_address(lds + 2 * buffer * F::kTileBytes) + along_lane;
+                const uint32_t va = tile::lds_address(lds + (2 * buffer + 1) * F::kTileBytes) + across_lane;
+                const float base = m == -kInf ? 0.f : m * a.scale_log2;
+                constexpr int kScores = KB * KK, kValues = 2 * KB * DB, kPairs = 8 * KB;
+                Fragment<BF16> pf[2 * KB], f, f_next;
+                float sum = 0, top = -kInf;
+                T::along(ka, 0, 0, f);
 #pragma unroll
                 for (int b = 0; b < KB; b++)
 #pragma unroll
-                    for (int i = 0; i < 16; i++)
-                        if (!sees(a, s, row, k0 + 32 * b + reg_line(i, h))) st[b][i] = -kInf;
-            }
-            float top = st[0][0];
+                    for (int i = 0; i < 16; i++) nx[b][i] = 0;
 #pragma unroll
-            for (int b = 0; b < KB; b++)
+                for (int i = 0; i < kScores; i++) {
+                    if (i + 1 < kScores) T::along(ka, 32 * ((i + 1) / KK), (i + 1) % KK, f_next);
+                    else T::across(va, 0, 0, f_next);
+                    mma(nx[i / KK], f, q[i % KK]);
 #pragma unroll
-                for (int i = 0; i < 16; i++) top = fmaxf(top, st[b][i]);
-            const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(top), __float_as_uint(top), false, false);
-            top = fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1]));
-            const float before = m;
-            m = fmaxf(m, top);
-            const float base = m == -kInf ? 0.f : m * a.scale_log2;
-            if (__any(m != before)) {
-                const float f = __builtin_amdgcn_exp2f(fmaf(before, a.scale_log2, -base));
-                l *= f;
-#pragma unroll
-                for (int d = 0; d < DB; d++) out[d] *= f;
-            }
-            float sum = 0;
-#pragma unroll
-            for (int b = 0; b < KB; b++)
-#pragma unroll
-                for (int i = 0; i < 16; i++) {
-                    st[b][i] = __builtin_amdgcn_exp2f(fmaf(st[b][i], a.scale_log2, -base));
-                    sum += st[b][i];
+                    for (int p = (i * kPairs + kScores - 1) / kScores; p < ((i + 1) * kPairs + kScores - 1) / kScores; p++) {
+                        const int e = 2 * p % 16;
+                        const float x = __builtin_amdgcn_exp2f(fmaf(st[p / 8][e], a.scale_log2, -base)), y = __builtin_amdgcn_exp2f(fmaf(st[p / 8][e + 1], a.scale_log2, -base));
+                        sum += x + y;
+                        pf[p / 4].raw[e % 8] = (__bf16)x;
+                        pf[p / 4].raw[e % 8 + 1] = (__bf16)y;
+                    }
+                    f = f_next;
+                    __builtin_amdgcn_sched_barrier(0);
                 }
-            l += sum;
-            const bool odd = masked && odd_tile[buffer] == k0;
+                l += sum;
+#pragma unroll
+                for (int i = 0; i < kValues; i++) {
+                    if (i + 1 < kValues) T::across(va, 16 * ((i + 1) / DB), 32 * ((i + 1) % DB), f_next);
+                    mma(out[i % DB], f, pf[i / DB]);
+#pragma unroll
+                    for (int p = (i * kPairs + kValues - 1) / kValues; p < ((i + 1) * kPairs + kValues - 1) / kValues; p++) {
+                        const int e = 2 * p % 16;
+                        top = fmaxf(top, fmaxf(nx[p / 8][e], nx[p / 8][e + 1]));
+                    }
+                    f = f_next;
+                    __builtin_amdgcn_sched_barrier(0);
+                }
+                follow(top);
+                k0 += BK;
+                buffer ^= 1;
+            }
+        }
+        advance(k0, true);
+        const int next = k0 + BK;
+        const uint32_t ka = tile::lds_address(lds + 2 * buffer * F::kTileBytes) + along_lane;
+        const uint32_t va = tile::lds_address(lds + (2 * buffer + 1) * F::kTileBytes) + across_lane;
+        const bool ahead = in_range(next);
+        if (in_range(k0)) {
+            const bool odd = odd_tile[buffer] == k0;
+            const float base = m == -kInf ? 0.f : m * a.scale_log2;
+            const Span span = keys_seen(a, s, row, k0, h);
 #pragma unroll
             for (int b = 0; b < KB; b++)
 #pragma unroll
                 for (int g = 0; g < 2; g++) {
-                    float p[8];
-#pragma unroll
-                    for (int e = 0; e < 8; e++) p[e] = st[b][8 * g + e];
                     Fragment<BF16> pf;
-                    operand_of(p, pf);
+                    exponentials(base, b, g, pf);
                     if (odd) {
                         bf16x8 seen;
 #pragma unroll
-                        for (int e = 0; e < 8; e++) seen[e] = (__bf16)(sees(a, s, row, k0 + 32 * b + reg_line(8 * g + e, h)) ? 1.f : 0.f);
+                        for (int e = 0; e < 8; e++) seen[e] = (__bf16)(span.has(b, 8 * g + e) ? 1.f : 0.f);
 #pragma unroll
                         for (int d = 0; d < DB; d++) {
                             Fragment<BF16> f;
-                            T::across(vt, 32 * b + 16 * g, 32 * d, lane, f);
+                            T::across(va, 32 * b + 16 * g, 32 * d, f);
                             mma_seen(out[d], f, pf, seen);
+                            __builtin_amdgcn_sched_barrier(0);
                         }
                     } else {
-#pragma unroll
-                        for (int d = 0; d < DB; d++) {
-                            Fragment<BF16> f;
-                            T::across(vt, 32 * b + 16 * g, 32 * d, lane, f);
-                            f.split();
-                            mma(out[d], f, pf);
-                        }
+                        values(va, b, g, pf);
                     }
                 }
         }
-        if (more) put(k0 + BK, buffer ^ 1);
-        __syncthreads();
+        if (ahead) {
+            scores(ka, nx);
+            if (next + BK > s.keys || (a.causal && next + BK - 1 > wave_first + s.shift) || (a.window && next <= wave_last + s.shift - a.window)) {
+                const Span span = keys_seen(a, s, row, next, h);
+#pragma unroll
+                for (int b = 0; b < KB; b++)
+#pragma unroll
+                    for (int i = 0; i < 16; i++) nx[b][i] = span.has(b, i) ? nx[b][i] : -kInf;
+            }
+            float top = -kInf;
+#pragma unroll
+            for (int b = 0; b < KB; b++)
+#pragma unroll
+                for (int i = 0; i < 16; i++) top = fmaxf(top, nx[b][i]);
+            follow(top);
+        }
+        k0 += BK;
+        buffer ^= 1;
     }
-    if (!live) return;
+    const float nan = __uint_as_float(0x7FC00000u);
     const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(l), __float_as_uint(l), false, false);
-    l = __uint_as_float(r[0]) + __uint_as_float(r[1]);
+    const float sum = __uint_as_float(r[0]) + __uint_as_float(r[1]);
+    if (!live) return;
     // a row that sees nothing: 0, and minus infinity
-    const float nan = __uint_as_float(0x7FC00000u), by = s.bad ? nan : m == -kInf && l == 0.f ? 0.f : 1.0f / l;
-    const int64_t o = (int64_t)(s.q0 + row) * a.ldo + (int64_t)head * D;
+    const float by = s.bad ? nan : m == -kInf && sum == 0.f ? 0.f : 1.0f / sum;
+    const int64_t token = s.q0 + row, o = token * a.ldo + (int64_t)head * D;
 #pragma unroll
     for (int d = 0; d < DB; d++)
 #pragma unroll
         for (int j = 0; j < 4; j++)
 #pragma unroll
             for (int e = 0; e < 4; e++) store1<BF16>(a.out, o + 32 * d + 8 * j + 4 * h + e, out[d][4 * j + e] * by);
-    if (a.lse && h == 0) a.lse[(int64_t)(s.q0 + row) * a.q_heads + head] = s.bad ? nan : m == -kInf ? -kInf : fmaf(m, a.scale, __builtin_amdgcn_logf(l) * kLn2);
+    if (a.lse && h == 0) a.lse[token * a.q_heads + head] = s.bad ? nan : m == -kInf ? -kInf : fmaf(m, a.scale, __builtin_amdgcn_logf(sum) * kLn2);
 }
 
-template <bool BF16, int D>
-hipError_t launch_forward(const PackedArgs& a, hipStream_t s) {
+template <bool BF16, int D, bool DIRECT>
+hipError_t launch_shape(const PackedArgs& a, hipStream_t s) {
     typedef ForwardShape<BF16, D> F;
     const int64_t groups = tile_slots(a.Tq, F::kRows, a.n) * a.q_heads;
-    hipLaunchKernelGGL((attention_kernel<BF16, D>), dim3((unsigned)groups), dim3(F::kWaves * 64), 0, s, a);
+    hipLaunchKernelGGL((attention_kernel<BF16, D, DIRECT>), dim3((unsigned)groups), dim3(F::kThreads), 0, s, a);
     return hipGetLastError();
+}
+template <bool BF16, int D>
+hipError_t launch_forward(const PackedArgs& a, hipStream_t s) {
+    const bool direct = direct_lines(a.k, a.ldk, BF16) && direct_lines(a.v, a.ldv, BF16);
+    return direct ? launch_shape<BF16, D, true>(a, s) : launch_shape<BF16, D, false>(a, s);
 }
 template <bool BF16>
 hipError_t launch_forward_by_width(const PackedArgs& a, hipStream_t s) {

@@ -43,39 +43,48 @@ struct Tile {
         const int x = kLine == 8 ? (r >> 1 & 3) * 2 ^ (r >> 3 & 1) : (r & 7) * 2 ^ (r >> 3 & 1);
         return (r * kLine + (c ^ x)) << 4;
     }
-    // Operand with a line a lane: lines r0 + lane % 32, channels 16 kk + 8 (lane / 32) + 0..7.
-    __device__ static void along(const char* lds, int r0, int kk, int lane, Fragment<BF16>& f) {
-        const int r = r0 + (lane & 31), h = lane >> 5;
+    // Operands, read at the tile's LDS address plus the lane's part of it.  What differs
+    // between the reads of one lane is a constant: bits of the chunk's number, which the
+    // swizzle leaves where they are (xor), and whole lines (the instruction's offset).
+    // Lane's part of along(): line lane % 32, and of across(): lines 4 (lane / 32) + .. on.
+    __device__ static uint32_t along_lane(int lane) { return at(lane & 31, (BF16 ? 1 : 2) * (lane >> 5)); }
+    __device__ static uint32_t across_lane(int lane) {
+        const int h = lane >> 5;
+        if (BF16) return at(4 * h + (lane >> 2 & 3), 2 * (lane >> 4 & 1) + (lane >> 1 & 1)) + (lane & 1) * 8;
+        return at(4 * h, (lane & 31) >> 2) + (lane & 3) * 4;
+    }
+    // A line a lane: lines r0 + lane % 32 (r0 a multiple of 32), channels 16 kk + 8 (lane / 32) + 0..7.
+    __device__ static void along(uint32_t from, int r0, int kk, Fragment<BF16>& f) {
         if constexpr (BF16) {
-            f.raw = *(const bf16x8*)(lds + at(r, 2 * kk + h));
+            f.raw = *(__attribute__((address_space(3))) const bf16x8*)(uintptr_t)((from ^ (32 * kk)) + r0 * kLineBytes);
         } else {
 #pragma unroll
             for (int i = 0; i < 2; i++) {
-                const f32x4 v = *(const f32x4*)(lds + at(r, 4 * kk + 2 * h + i));
+                const f32x4 v = *(__attribute__((address_space(3))) const f32x4*)(uintptr_t)((from ^ (64 * kk + 16 * i)) + r0 * kLineBytes);
 #pragma unroll
                 for (int e = 0; e < 4; e++) f.raw[4 * i + e] = v[e];
             }
         }
     }
-    // Operand with a channel a lane, c0 + lane % 32, over the 16 lines from r0 on in
-    // the order of result registers: r0 + reg_line(e, lane / 32).
-    __device__ static void across(const char* lds, int r0, int c0, int lane, Fragment<BF16>& f) {
-        const int h = lane >> 5;
+    // A channel a lane, c0 + lane % 32 (c0 a multiple of 32), over the 16 lines from r0 on
+    // (a multiple of 16) in the order of result registers: r0 + reg_line(e, lane / 32).
+    __device__ static void across(uint32_t from, int r0, int c0, Fragment<BF16>& f) {
         if constexpr (BF16) {
-            const int r = r0 + 4 * h + (lane >> 2 & 3), col = c0 + 16 * (lane >> 4 & 1) + 4 * (lane & 3);
             s16x8 v;
 #pragma unroll
             for (int i = 0; i < 2; i++) {
                 typedef __attribute__((address_space(3))) s16x4 lds4;
-                const s16x4 t = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4*)(lds + at(r + 8 * i, col >> 3) + ((col & 7) << 1)));
+                const s16x4 t = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4*)(uintptr_t)((from ^ (2 * c0 ^ 16 * i)) + (r0 + 8 * i) * kLineBytes));
 #pragma unroll
                 for (int e = 0; e < 4; e++) v[4 * i + e] = t[e];
             }
             f.raw = __builtin_bit_cast(bf16x8, v);
         } else {
-            const int col = c0 + (lane & 31);
 #pragma unroll
-            for (int e = 0; e < 8; e++) f.raw[e] = *(const float*)(lds + at(r0 + reg_line(e, h), col >> 2) + ((col & 3) << 2));
+            for (int e = 0; e < 8; e++) {
+                const int i = e >> 2, j = e & 3;
+                f.raw[e] = *(__attribute__((address_space(3))) const float*)(uintptr_t)((from ^ (4 * c0 ^ 32 * j ^ 16 * i)) + (r0 + 8 * i + j) * kLineBytes);
+            }
         }
     }
 };
@@ -147,6 +156,67 @@ struct Staged {
         return bad;
     }
 };
+
+// The same tile fetched ahead: straight into LDS (DIRECT) or by registers on the way.
+// fetch() begins it, arrive() ends it; meet() lies between that and the first use.
+// DIRECT: lines past the last repeat it, where the others hold zeros; both are masked.
+template <bool BF16, int D, int R, int THREADS, bool DIRECT> struct Pipe;
+template <bool BF16, int D, int R, int THREADS> struct Pipe<BF16, D, R, THREADS, false> {
+    Staged<BF16, D, R, THREADS> s;
+    __device__ void fetch(const char* base, int64_t ld, int64_t first, int lines, char*) { s.load(base, ld, first, lines); }
+    __device__ void arrive(char* lds) const { s.store(lds); }
+};
+template <bool BF16, int D, int R, int THREADS> struct Pipe<BF16, D, R, THREADS, true> {
+    typedef Tile<BF16, D> T;
+    static constexpr int kEach = R * T::kLine / THREADS;
+    static_assert(R * T::kLine % THREADS == 0, "whole waves");
+    __device__ void fetch(const char* base, int64_t ld, int64_t first, int lines, char* lds) {
+        const uint32_t line_bytes = (uint32_t)ld * (BF16 ? 2 : 4);
+        const char* p = base + first * ld * (BF16 ? 2 : 4);
+        const uint32_t to = tile::lds_address(lds) + (threadIdx.x >> 6) * 1024;
+        // this lane's 16 bytes of LDS, and the line and chunk that belong there: of the
+        // next ones too, whole multiples of 16 lines on
+        constexpr int kStep = THREADS / T::kLine;
+        if (kStep % 16 == 0 && lines >= R) {
+            const int r = threadIdx.x / T::kLine, c = (T::at(r, threadIdx.x % T::kLine) >> 4) % T::kLine;
+            const uint32_t offset = r * line_bytes + (c < T::kChunks ? c : 0) * 16;
+#pragma unroll
+            for (int i = 0; i < kEach; i++) tile::load_lds16(to + i * THREADS * 16, offset, p + (int64_t)i * kStep * line_bytes);
+            return;
+        }
+#pragma unroll
+        for (int i = 0; i < kEach; i++) {
+            const int n = threadIdx.x + i * THREADS, r = n / T::kLine, c = (T::at(r, n % T::kLine) >> 4) % T::kLine;
+            tile::load_lds16(to + i * THREADS * 16, min(r, lines - 1) * line_bytes + (c < T::kChunks ? c : 0) * 16, p);
+        }
+    }
+    __device__ void arrive(char*) const {}
+};
+template <bool DIRECT> __device__ inline void meet() {
+    if (DIRECT) tile::wait_loads_and_meet();
+    else __syncthreads();
+}
+// Lines that may go straight into LDS: whole 16-byte chunks, a tile of 64 within 32 bits.
+inline bool direct_lines(const void* p, int64_t ld, bool bf16) {
+    const int64_t bytes = ld * (bf16 ? 2 : 4);
+    return (uintptr_t)p % 16 == 0 && bytes % 16 == 0 && bytes * 64 < ((int64_t)1 << 31);
+}
+// Whether a tile in LDS holds a value that is not finite (this thread's part of it).
+template <bool BF16, int D, int R, int THREADS>
+__device__ inline bool tile_not_finite(const char* lds) {
+    typedef Tile<BF16, D> T;
+    bool bad = false;
+#pragma unroll
+    for (int i = 0; i < (R * T::kChunks + THREADS - 1) / THREADS; i++) {
+        const int n = threadIdx.x + i * THREADS, r = n / T::kChunks, c = n - r * T::kChunks;
+        if (n < R * T::kChunks) {
+            const u32x4 v = *(const u32x4*)(lds + T::at(r, c));
+#pragma unroll
+            for (int e = 0; e < 4; e++) bad |= (BF16 && (v[e] & 0x7F80u) == 0x7F80u) || (v[e] & 0x7F800000u) == 0x7F800000u;
+        }
+    }
+    return bad;
+}
 
 // acc += a b where b's values are 0 for pairs that do not see each other, and a may
 // hold values that are not finite: 0 times these must add nothing.  They are taken
@@ -233,9 +303,22 @@ __device__ inline bool find_tile(const int32_t* offsets, int n, int T, int slot,
 }
 inline int64_t tile_slots(int T, int B, int n) { return (int64_t)T / B + n; }
 
-// Whether row i sees key j.
-__device__ inline bool sees(const PackedArgs& a, const Sequence& s, int i, int j) {
-    return j < s.keys && (!a.causal || j <= i + s.shift) && (!a.window || j > i + s.shift - a.window);
+// Which lines of a tile from `first` on a lane's row (or key) sees: those of the
+// result registers i of block b with lo <= 32 b + 8 (i / 4) + i % 4 < hi.
+struct Span {
+    int lo, hi;
+    __device__ bool has(int b, int i) const {
+        const int c = 32 * b + 8 * (i >> 2) + (i & 3);
+        return c >= lo && c < hi;
+    }
+};
+__device__ inline Span keys_seen(const PackedArgs& a, const Sequence& s, int row, int first, int h) {
+    const int off = first + 4 * h, last = row + s.shift;
+    return {a.window ? last - a.window + 1 - off : INT32_MIN, (a.causal ? min(s.keys, last + 1) : s.keys) - off};
+}
+__device__ inline Span rows_seeing(const PackedArgs& a, const Sequence& s, int key, int first, int h) {
+    const int off = first + 4 * h, own = key - s.shift;
+    return {a.causal ? own - off : INT32_MIN, (a.window ? min(s.rows, own + a.window) : s.rows) - off};
 }
 
 }  // namespace packed
