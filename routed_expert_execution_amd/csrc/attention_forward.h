@@ -134,7 +134,7 @@ __global__ __launch_bounds__(kForwardWaves * 64, BF16 && D <= 128 ? 2 : 1) void 
     // fp32 and factors in bf16 are as exact at any common scale.
     auto follow = [&](float top) __attribute__((always_inline)) {
         const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(top), __float_as_uint(top), false, false);
-        top = fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1]));
+        top = max_of(__uint_as_float(r[0]), __uint_as_float(r[1]));
         const float before = m;
         const bool grown = (top - before) * a.scale_log2 > 8.f;
         if (__any(grown)) {
@@ -161,18 +161,23 @@ __global__ __launch_bounds__(kForwardWaves * 64, BF16 && D <= 128 ? 2 : 1) void 
                 const uint32_t va = tile::lds_address(lds + (2 * buffer + 1) * F::kTileBytes) + across_lane;
                 const float base = m == -kInf ? 0.f : m * a.scale_log2;
                 constexpr int kScores = KB * KK, kValues = 2 * KB * DB, kPairs = 8 * KB;
-                Fragment<BF16> pf[2 * KB], f, f_next;
+                constexpr int kAhead = 2;  // products between an operand's read and its use
+                Fragment<BF16> pf[2 * KB], f[kAhead + 1];
                 float sum = 0, top = -kInf;
-                T::along(ka, 0, 0, f);
+                auto read = [&](int i) __attribute__((always_inline)) {
+                    if (i < kScores) T::along(ka, 32 * (i / KK), i % KK, f[i % (kAhead + 1)]);
+                    else if (i < kScores + kValues) T::across(va, 16 * ((i - kScores) / DB), 32 * ((i - kScores) % DB), f[i % (kAhead + 1)]);
+                };
+#pragma unroll
+                for (int i = 0; i < kAhead; i++) read(i);
 #pragma unroll
                 for (int b = 0; b < KB; b++)
 #pragma unroll
                     for (int i = 0; i < 16; i++) nx[b][i] = 0;
 #pragma unroll
                 for (int i = 0; i < kScores; i++) {
-                    if (i + 1 < kScores) T::along(ka, 32 * ((i + 1) / KK), (i + 1) % KK, f_next);
-                    else T::across(va, 0, 0, f_next);
-                    mma(nx[i / KK], f, q[i % KK]);
+                    read(i + kAhead);
+                    mma(nx[i / KK], f[i % (kAhead + 1)], q[i % KK]);
 #pragma unroll
                     for (int p = (i * kPairs + kScores - 1) / kScores; p < ((i + 1) * kPairs + kScores - 1) / kScores; p++) {
                         const int e = 2 * p % 16;
@@ -181,20 +186,18 @@ __global__ __launch_bounds__(kForwardWaves * 64, BF16 && D <= 128 ? 2 : 1) void 
                         pf[p / 4].raw[e % 8] = (__bf16)x;
                         pf[p / 4].raw[e % 8 + 1] = (__bf16)y;
                     }
-                    f = f_next;
                     __builtin_amdgcn_sched_barrier(0);
                 }
                 l += sum;
 #pragma unroll
                 for (int i = 0; i < kValues; i++) {
-                    if (i + 1 < kValues) T::across(va, 16 * ((i + 1) / DB), 32 * ((i + 1) % DB), f_next);
-                    mma(out[i % DB], f, pf[i / DB]);
+                    read(kScores + i + kAhead);
+                    mma(out[i % DB], f[(kScores + i) % (kAhead + 1)], pf[i / DB]);
 #pragma unroll
                     for (int p = (i * kPairs + kValues - 1) / kValues; p < ((i + 1) * kPairs + kValues - 1) / kValues; p++) {
                         const int e = 2 * p % 16;
-                        top = fmaxf(top, fmaxf(nx[p / 8][e], nx[p / 8][e + 1]));
+                        top = max_of(top, max_of(nx[p / 8][e], nx[p / 8][e + 1]));
                     }
-                    f = f_next;
                     __builtin_amdgcn_sched_barrier(0);
                 }
                 follow(top);
@@ -246,7 +249,7 @@ __global__ __launch_bounds__(kForwardWaves * 64, BF16 && D <= 128 ? 2 : 1) void 
 #pragma unroll
             for (int b = 0; b < KB; b++)
 #pragma unroll
-                for (int i = 0; i < 16; i++) top = fmaxf(top, nx[b][i]);
+                for (int i = 0; i < 16; i++) top = max_of(top, nx[b][i]);
             follow(top);
         }
         k0 += BK;

@@ -25,6 +25,10 @@ typedef float f32x4 __attribute__((ext_vector_type(4)));
 
 constexpr float kInf = __builtin_huge_valf(), kLog2e = 1.44269504088896f, kLn2 = 0.693147180559945f;
 
+// The larger, NaN where one is: one instruction for three values (fmaxf, which takes
+// the other one, has the compiler quieten each first).
+__device__ inline float max_of(float a, float b) { return __builtin_elementwise_maximum(a, b); }
+
 // Key of result register i of a 32 x 32 block in lane half h: 8 (i / 4) + 4 h + i % 4.
 __device__ inline int reg_line(int i, int h) { return 8 * (i >> 2) + 4 * h + (i & 3); }
 
