@@ -153,7 +153,7 @@ struct PackedArgs {
     int64_t lddo;
     void *dq, *dk, *dv;
     int64_t lddq, lddk, lddv;
-    float* delta;                          // [Tq][q_heads]
+    float2* rows;                          // workspace [q_heads][Tq]: lse / ln 2, delta
 };
 hipError_t launch_attention_bf16(const PackedArgs& a, hipStream_t s);
 hipError_t launch_attention_f32(const PackedArgs& a, hipStream_t s);

@@ -67,7 +67,7 @@ __global__ __launch_bounds__(kBackwardWaves * 64) void attention_dq_kernel(Packe
     float lse = kInf;  // (a row past the last: P = 0)
     if (live) {
         lse = a.lse[token * a.q_heads + head] * kLog2e;
-        if (h == 0) a.delta[token * a.q_heads + head] = delta;
+        if (h == 0) a.rows[(int64_t)head * a.Tq + token] = make_float2(lse, delta);
     }
     f32x16 out[DB];
 #pragma unroll
@@ -230,9 +230,10 @@ __global__ __launch_bounds__(kBackwardWaves * 64) void attention_dkv_kernel(Pack
         sg.load((const char*)a.dout + ((int64_t)s.q0 * a.lddo + (int64_t)head * D) * (BF16 ? 2 : 4), a.lddo, r0, s.rows - r0);
         if (threadIdx.x < BQ) {
             const int r = r0 + threadIdx.x;
-            const int64_t at = (int64_t)(s.q0 + r) * a.q_heads + head;
-            s_lse = r < s.rows ? a.lse[at] * kLog2e : kInf;  // (past the last row: P = 0)
-            s_delta = r < s.rows ? a.delta[at] : 0.f;
+            // (past the last row: P = 0)
+            const float2 of_row = r < s.rows ? a.rows[(int64_t)head * a.Tq + s.q0 + r] : make_float2(kInf, 0.f);
+            s_lse = of_row.x;
+            s_delta = of_row.y;
         }
     };
     auto put = [&](int t, int buffer) {
@@ -359,19 +360,442 @@ __global__ __launch_bounds__(kBackwardWaves * 64) void attention_dkv_kernel(Pack
             }
 }
 
+// The same two kernels for bf16 heads of up to 128 channels, where registers hold two
+// blocks' scores: the products of the next block's S and dP run beside this block's
+// exponentials, and the products with them follow, so that the matrix cores wait
+// neither for the vector unit nor for LDS.  A block is 32 keys (dQ) or 32 rows a wave
+// (dK, dV); three buffers, since a block's tile is read in two steps.
+// DIRECT: tiles go straight from memory into LDS.
+constexpr int kAhead = 2;  // products between an operand's read and its use
+
+template <int D, bool DIRECT>
+__global__ __launch_bounds__(kBackwardWaves * 64, 2) void attention_dq_beside_kernel(PackedArgs a) {
+    typedef Tile<true, D> T;
+    constexpr int kThreads = 64 * kBackwardWaves, kRows = 32 * kBackwardWaves, KK = D / 16, DB = D / 32, kBytes = 32 * T::kLineBytes;
+    __shared__ __attribute__((aligned(1024))) char lds[5 * kBytes];  // keys of three blocks, values of two
+    __shared__ int odd_block[3];
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), h = lane >> 5;
+    const int kv_head = blockIdx.x % a.kv_heads, rest = blockIdx.x / a.kv_heads;
+    const int head = kv_head * a.per_head + rest % a.per_head;
+    if (blockIdx.x == gridDim.x - 1) {
+        check_offsets(a.offsets_q, a.n, a.Tq, a.err);
+        check_offsets(a.offsets_k, a.n, a.Tk, a.err);
+    }
+    int seq, local;
+    if (!find_tile<kRows>(a.offsets_q, a.n, a.Tq, rest / a.per_head, &seq, &local)) return;
+    const Sequence s = sequence_of(a, seq);
+    const int tiles = (s.rows + kRows - 1) / kRows;
+    if (local >= tiles) return;
+    const int row0 = (tiles - 1 - local) * kRows, wave_first = row0 + wave * 32, row = wave_first + (lane & 31);
+    const bool live = row < s.rows;
+    if (s.bad && threadIdx.x == 0) atomicOr(a.err, kErrCache);
+
+    Fragment<true> q[KK], g[KK];
+    const int64_t token = s.q0 + row;
+    float delta = 0;
+#pragma unroll
+    for (int kk = 0; kk < KK; kk++) {
+        along_memory<true>(a.q, token * a.ldq + (int64_t)head * D, live, kk, lane, q[kk]);
+        along_memory<true>(a.dout, token * a.lddo + (int64_t)head * D, live, kk, lane, g[kk]);
+        Fragment<true> o;
+        along_memory<true>(a.out, token * a.ldo + (int64_t)head * D, live, kk, lane, o);
+#pragma unroll
+        for (int e = 0; e < 8; e++) delta = fmaf((float)g[kk].raw[e], (float)o.raw[e], delta);
+    }
+    {
+        const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(delta), __float_as_uint(delta), false, false);
+        delta = __uint_as_float(r[0]) + __uint_as_float(r[1]);
+    }
+    float lse = kInf;  // (a row past the last: P = 0)
+    if (live) {
+        lse = a.lse[token * a.q_heads + head] * kLog2e;
+        if (h == 0) a.rows[(int64_t)head * a.Tq + token] = make_float2(lse, delta);
+    }
+    f32x16 out[DB], st, dp, st_next, dp_next;
+#pragma unroll
+    for (int d = 0; d < DB; d++)
+#pragma unroll
+        for (int i = 0; i < 16; i++) out[d][i] = 0;
+
+    const int last_row = min(row0 + kRows, s.rows) - 1, wave_last = min(wave_first + 31, s.rows - 1);
+    const int end = a.causal ? min(s.keys, last_row + s.shift + 1) : s.keys;
+    const int begin = a.window ? max(0, row0 + s.shift - a.window + 1) / 32 * 32 : 0;
+    const int total = end > begin ? (end - begin + 31) / 32 : 0;
+    const char* kbase = (const char*)a.k + ((int64_t)s.k0 * a.ldk + (int64_t)kv_head * D) * 2;
+    const char* vbase = (const char*)a.v + ((int64_t)s.k0 * a.ldv + (int64_t)kv_head * D) * 2;
+    auto masked_block = [&](int t) {  // for some row of the workgroup
+        const int k0 = begin + 32 * t;
+        return k0 + 32 > s.keys || (a.causal && k0 + 31 > row0 + s.shift) || (a.window && k0 <= last_row + s.shift - a.window);
+    };
+    auto in_range = [&](int t) {  // for some row of the wave
+        const int k0 = begin + 32 * t;
+        return t >= 0 && t < total && wave_first < s.rows && !(a.causal && k0 > wave_last + s.shift) && !(a.window && k0 + 31 <= wave_first + s.shift - a.window);
+    };
+    Pipe<true, D, 32, kThreads, DIRECT> pk, pv;
+    auto keys_at = [&](int t) { return lds + (t % 3) * kBytes; };
+    auto values_at = [&](int t) { return lds + (3 + (t & 1)) * kBytes; };
+    auto fetch = [&](int t) __attribute__((always_inline)) {
+        const int k0 = begin + 32 * t;
+        pk.fetch(kbase, a.ldk, k0, s.keys - k0, keys_at(t));
+        pv.fetch(vbase, a.ldv, k0, s.keys - k0, values_at(t));
+    };
+    // Block t + 1 has arrived and t + 2 is fetched.
+    auto advance = [&](int t, bool check) __attribute__((always_inline)) {
+        if (t + 1 < total) {
+            pk.arrive(keys_at(t + 1));
+            pv.arrive(values_at(t + 1));
+        }
+        meet<DIRECT>();
+        if (check && t >= 0 && masked_block(t)) {
+            if (tile_not_finite<true, D, 32, kThreads>(keys_at(t))) odd_block[t % 3] = t;
+            __syncthreads();
+        }
+        if (t + 2 < total) fetch(t + 2);
+    };
+    if (threadIdx.x < 3) odd_block[threadIdx.x] = -1;
+    const uint32_t along_lane = T::along_lane(lane), across_lane = T::across_lane(lane);
+    if (total) fetch(0);
+    int t = -1;
+    while (t < total) {
+#pragma unroll 1
+        while (t >= 0 && t + 1 < total && !masked_block(t)) {
+            advance(t, false);
+            const uint32_t ka = tile::lds_address(keys_at(t + 1)) + along_lane, va = tile::lds_address(values_at(t + 1)) + along_lane;
+            const uint32_t kx = tile::lds_address(keys_at(t)) + across_lane;
+            constexpr int kScores = 2 * KK, kSums = 2 * DB, kPairs = 8;
+            Fragment<true> f[kAhead + 1], df[2];
+            auto read = [&](int i) __attribute__((always_inline)) {
+                if (i < kScores) T::along(i & 1 ? va : ka, 0, i / 2, f[i % (kAhead + 1)]);
+                else if (i < kScores + kSums) T::across(kx, 16 * ((i - kScores) / DB), 32 * ((i - kScores) % DB), f[i % (kAhead + 1)]);
+            };
+#pragma unroll
+            for (int i = 0; i < kAhead; i++) read(i);
+#pragma unroll
+            for (int i = 0; i < 16; i++) st_next[i] = dp_next[i] = 0;
+#pragma unroll
+            for (int i = 0; i < kScores; i++) {
+                read(i + kAhead);
+                if (i & 1) mma(dp_next, f[i % (kAhead + 1)], g[i / 2]);
+                else mma(st_next, f[i % (kAhead + 1)], q[i / 2]);
+#pragma unroll
+                for (int p = (i * kPairs + kScores - 1) / kScores; p < ((i + 1) * kPairs + kScores - 1) / kScores; p++)
+#pragma unroll
+                    for (int e = 2 * p; e < 2 * p + 2; e++)
+                        df[e / 8].raw[e % 8] = (__bf16)(__builtin_amdgcn_exp2f(fmaf(st[e], a.scale_log2, -lse)) * (dp[e] - delta));
+                __builtin_amdgcn_sched_barrier(0);
+            }
+#pragma unroll
+            for (int i = 0; i < kSums; i++) {
+                read(kScores + i + kAhead);
+                mma(out[i % DB], f[(kScores + i) % (kAhead + 1)], df[i / DB]);
+                __builtin_amdgcn_sched_barrier(0);
+            }
+            st = st_next;
+            dp = dp_next;
+            t++;
+        }
+        advance(t, true);
+        if (in_range(t)) {
+            const uint32_t kx = tile::lds_address(keys_at(t)) + across_lane;
+            const bool odd = odd_block[t % 3] == t;
+            const Span span = keys_seen(a, s, row, begin + 32 * t, h);
+#pragma unroll
+            for (int n = 0; n < 2; n++) {
+                Fragment<true> df;
+                bf16x8 seen;
+#pragma unroll
+                for (int e = 0; e < 8; e++) {
+                    const bool on = span.has(0, 8 * n + e);
+                    const float ds = __builtin_amdgcn_exp2f(fmaf(st[8 * n + e], a.scale_log2, -lse)) * (dp[8 * n + e] - delta);
+                    df.raw[e] = (__bf16)(on ? ds : 0.f);
+                    seen[e] = (__bf16)(on ? 1.f : 0.f);
+                }
+#pragma unroll
+                for (int d = 0; d < DB; d++) {
+                    Fragment<true> f;
+                    T::across(kx, 16 * n, 32 * d, f);
+                    if (odd) mma_seen(out[d], f, df, seen);
+                    else mma(out[d], f, df);
+                    __builtin_amdgcn_sched_barrier(0);
+                }
+            }
+        }
+        if (in_range(t + 1)) {
+            const uint32_t ka = tile::lds_address(keys_at(t + 1)) + along_lane, va = tile::lds_address(values_at(t + 1)) + along_lane;
+#pragma unroll
+            for (int i = 0; i < 16; i++) st[i] = dp[i] = 0;
+#pragma unroll
+            for (int kk = 0; kk < KK; kk++) {
+                Fragment<true> f;
+                T::along(ka, 0, kk, f);
+                mma(st, f, q[kk]);
+                T::along(va, 0, kk, f);
+                mma(dp, f, g[kk]);
+                __builtin_amdgcn_sched_barrier(0);
+            }
+        }
+        t++;
+    }
+    if (!live) return;
+    const float by = s.bad ? __uint_as_float(0x7FC00000u) : a.scale;
+    const int64_t o = token * a.lddq + (int64_t)head * D;
+#pragma unroll
+    for (int d = 0; d < DB; d++)
+#pragma unroll
+        for (int j = 0; j < 4; j++)
+#pragma unroll
+            for (int e = 0; e < 4; e++) store1<true>(a.dq, o + 32 * d + 8 * j + 4 * h + e, out[d][4 * j + e] * by);
+}
+
+// dK and dV: a workgroup has 64 keys; two waves take 32 of them each over the first
+// 32 of every 64 rows, two over the others, and their sums are added at the end.
+template <int D, bool DIRECT>
+__global__ __launch_bounds__(kBackwardWaves * 64) void attention_dkv_beside_kernel(PackedArgs a) {
+    typedef Tile<true, D> T;
+    constexpr int kThreads = 64 * kBackwardWaves, kKeys = 64, KK = D / 16, DB = D / 32, kBytes = 64 * T::kLineBytes;
+    __shared__ __attribute__((aligned(1024))) char lds[6 * kBytes];  // queries and their gradients, three steps
+    __shared__ __attribute__((aligned(1024))) float2 stats[3][64];
+    __shared__ int odd_step[3];
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), h = lane >> 5, part = wave >> 1;
+    const int kv_head = blockIdx.x % a.kv_heads;
+    int seq, local;
+    if (!find_tile<kKeys>(a.offsets_k, a.n, a.Tk, blockIdx.x / a.kv_heads, &seq, &local)) return;
+    const Sequence s = sequence_of(a, seq);
+    const int key0 = local * kKeys, wave_key = key0 + (wave & 1) * 32, key = wave_key + (lane & 31);
+    if (key0 >= s.keys) return;
+    const bool live = key < s.keys;
+    if (s.bad && threadIdx.x == 0) atomicOr(a.err, kErrCache);
+
+    Fragment<true> k[KK], v[KK];
+    const int64_t token = s.k0 + key;
+#pragma unroll
+    for (int kk = 0; kk < KK; kk++) {
+        along_memory<true>(a.k, token * a.ldk + (int64_t)kv_head * D, live, kk, lane, k[kk]);
+        along_memory<true>(a.v, token * a.ldv + (int64_t)kv_head * D, live, kk, lane, v[kk]);
+    }
+    f32x16 dk[DB], dv[DB], st, dp, st_next, dp_next;
+#pragma unroll
+    for (int i = 0; i < 16; i++)
+#pragma unroll
+        for (int d = 0; d < DB; d++) dk[d][i] = dv[d][i] = 0;
+
+    // rows that see any of the workgroup's keys, 64 a step, of one query head after the other
+    const int last_key = min(key0 + kKeys, s.keys) - 1, wave_last_key = min(wave_key + 31, s.keys - 1);
+    const int begin = a.causal ? max(0, key0 - s.shift) / 64 * 64 : 0;
+    const int end = (int)min((int64_t)s.rows, a.window ? (int64_t)last_key - s.shift + a.window : s.rows);
+    const int per = end > begin ? (end - begin + 63) / 64 : 0, total = per * a.per_head;
+    int fetch_head = kv_head * a.per_head, fetch_row = begin;  // of the next step to be fetched
+    auto masked_rows = [&](int r0) {  // for some key of the workgroup
+        return r0 + 64 > s.rows || (a.causal && last_key > r0 + s.shift) || (a.window && key0 <= r0 + 63 + s.shift - a.window);
+    };
+    Pipe<true, D, 64, kThreads, DIRECT> pq, pg;
+    float2 of_row;
+    auto queries_at = [&](int t) { return lds + (t % 3) * 2 * kBytes; };
+    auto fetch = [&](int t) __attribute__((always_inline)) {
+        pq.fetch((const char*)a.q + ((int64_t)s.q0 * a.ldq + (int64_t)fetch_head * D) * 2, a.ldq, fetch_row, s.rows - fetch_row, queries_at(t));
+        pg.fetch((const char*)a.dout + ((int64_t)s.q0 * a.lddo + (int64_t)fetch_head * D) * 2, a.lddo, fetch_row, s.rows - fetch_row, queries_at(t) + kBytes);
+        const float2* rows = a.rows + (int64_t)fetch_head * a.Tq + s.q0 + fetch_row;
+        const int most = s.rows - fetch_row - 1;  // (rows past the last are masked)
+        if (DIRECT) {
+            if (wave < 2) load_lds4(tile::lds_address(&stats[t % 3][32 * wave]), min(32 * wave + lane / 2, most) * 8 + (lane & 1) * 4, rows);
+        } else if (threadIdx.x < 64) {
+            of_row = rows[min((int)threadIdx.x, most)];
+        }
+        fetch_row += 64;
+        if (fetch_row >= end) {
+            fetch_row = begin;
+            fetch_head++;
+        }
+    };
+    // Step t + 1 has arrived and t + 2 is fetched.
+    auto advance = [&](int t, int r0, bool check) __attribute__((always_inline)) {
+        if (t + 1 < total) {
+            pq.arrive(queries_at(t + 1));
+            pg.arrive(queries_at(t + 1) + kBytes);
+            if (!DIRECT && threadIdx.x < 64) stats[(t + 1) % 3][threadIdx.x] = of_row;
+        }
+        meet<DIRECT>();
+        if (check && t >= 0 && masked_rows(r0)) {
+            const bool bad_q = tile_not_finite<true, D, 64, kThreads>(queries_at(t)), bad_g = tile_not_finite<true, D, 64, kThreads>(queries_at(t) + kBytes);
+            if (bad_q || bad_g) odd_step[t % 3] = t;
+            __syncthreads();
+        }
+        if (t + 2 < total) fetch(t + 2);
+    };
+    if (threadIdx.x < 3) odd_step[threadIdx.x] = -1;
+    const uint32_t along_lane = T::along_lane(lane) + part * 32 * T::kLineBytes, across_lane = T::across_lane(lane) + part * 32 * T::kLineBytes;
+    if (total) fetch(0);
+    int t = -1, r0 = begin - 64;  // step t's rows begin at r0
+    auto step_on = [&]() __attribute__((always_inline)) {
+        t++;
+        r0 += 64;
+        if (r0 >= end) r0 = begin;
+    };
+    while (t < total) {
+#pragma unroll 1
+        while (t >= 0 && t + 1 < total && !masked_rows(r0)) {
+            advance(t, r0, false);
+            const uint32_t qa = tile::lds_address(queries_at(t + 1)) + along_lane, qx = tile::lds_address(queries_at(t)) + across_lane;
+            const float2* rows = &stats[t % 3][32 * part + 4 * h];
+            constexpr int kScores = 2 * KK, kSums = 4 * DB, kPairs = 8;
+            Fragment<true> f[kAhead + 1], pf[2], df[2];
+            auto read = [&](int i) __attribute__((always_inline)) {
+                if (i < kScores) {
+                    T::along(i & 1 ? qa + kBytes : qa, 0, i / 2, f[i % (kAhead + 1)]);
+                } else if (i < kScores + kSums) {
+                    const int n = (i - kScores) / (2 * DB), d = (i - kScores) / 2 % DB;
+                    T::across(i & 1 ? qx : qx + kBytes, 16 * n, 32 * d, f[i % (kAhead + 1)]);
+                }
+            };
+            static_assert(kScores % 2 == 0, "values' gradients first");
+#pragma unroll
+            for (int i = 0; i < kAhead; i++) read(i);
+#pragma unroll
+            for (int i = 0; i < 16; i++) st_next[i] = dp_next[i] = 0;
+#pragma unroll
+            for (int i = 0; i < kScores; i++) {
+                read(i + kAhead);
+                if (i & 1) mma(dp_next, f[i % (kAhead + 1)], v[i / 2]);
+                else mma(st_next, f[i % (kAhead + 1)], k[i / 2]);
+#pragma unroll
+                for (int p = (i * kPairs + kScores - 1) / kScores; p < ((i + 1) * kPairs + kScores - 1) / kScores; p++) {
+                    const f32x4 two = *(const f32x4*)(rows + 8 * (p / 2) + 2 * (p & 1));  // of two rows
+#pragma unroll
+                    for (int e = 2 * p; e < 2 * p + 2; e++) {
+                        const float x = __builtin_amdgcn_exp2f(fmaf(st[e], a.scale_log2, -two[2 * (e & 1)]));
+                        pf[e / 8].raw[e % 8] = (__bf16)x;
+                        df[e / 8].raw[e % 8] = (__bf16)(x * (dp[e] - two[2 * (e & 1) + 1]));
+                    }
+                }
+                __builtin_amdgcn_sched_barrier(0);
+            }
+#pragma unroll
+            for (int i = 0; i < kSums; i++) {
+                read(kScores + i + kAhead);
+                const int n = i / (2 * DB), d = i / 2 % DB;
+                if (i & 1) mma(dk[d], f[(kScores + i) % (kAhead + 1)], df[n]);
+                else mma(dv[d], f[(kScores + i) % (kAhead + 1)], pf[n]);
+                __builtin_amdgcn_sched_barrier(0);
+            }
+            st = st_next;
+            dp = dp_next;
+            step_on();
+        }
+        advance(t, r0, true);
+        const int first = r0 + 32 * part;
+        auto in_range = [&](int t, int first) {  // some row of the wave sees some key of it
+            return t >= 0 && t < total && wave_key < s.keys && first < s.rows && !(a.causal && wave_key > first + 31 + s.shift) &&
+                   !(a.window && wave_last_key <= first + s.shift - a.window);
+        };
+        if (in_range(t, first)) {
+            const uint32_t qx = tile::lds_address(queries_at(t)) + across_lane;
+            const float2* rows = &stats[t % 3][32 * part + 4 * h];
+            const bool odd = odd_step[t % 3] == t;
+            const Span span = rows_seeing(a, s, key, first, h);
+#pragma unroll
+            for (int n = 0; n < 2; n++) {
+                Fragment<true> pf, df;
+                bf16x8 seen;
+#pragma unroll
+                for (int e = 0; e < 8; e++) {
+                    const int i = 8 * n + e;
+                    const float2 r = rows[8 * (i >> 2) + (i & 3)];
+                    const bool on = span.has(0, i);
+                    const float x = __builtin_amdgcn_exp2f(fmaf(st[i], a.scale_log2, -r.x));
+                    pf.raw[e] = (__bf16)(on ? x : 0.f);
+                    df.raw[e] = (__bf16)(on ? x * (dp[i] - r.y) : 0.f);
+                    seen[e] = (__bf16)(on ? 1.f : 0.f);
+                }
+#pragma unroll
+                for (int d = 0; d < DB; d++) {
+                    Fragment<true> f;
+                    T::across(qx + kBytes, 16 * n, 32 * d, f);
+                    if (odd) mma_seen(dv[d], f, pf, seen);
+                    else mma(dv[d], f, pf);
+                    T::across(qx, 16 * n, 32 * d, f);
+                    if (odd) mma_seen(dk[d], f, df, seen);
+                    else mma(dk[d], f, df);
+                    __builtin_amdgcn_sched_barrier(0);
+                }
+            }
+        }
+        step_on();
+        if (in_range(t, r0 + 32 * part)) {
+            const uint32_t qa = tile::lds_address(queries_at(t)) + along_lane;
+#pragma unroll
+            for (int i = 0; i < 16; i++) st[i] = dp[i] = 0;
+#pragma unroll
+            for (int kk = 0; kk < KK; kk++) {
+                Fragment<true> f;
+                T::along(qa, 0, kk, f);
+                mma(st, f, k[kk]);
+                T::along(qa + kBytes, 0, kk, f);
+                mma(dp, f, v[kk]);
+                __builtin_amdgcn_sched_barrier(0);
+            }
+        }
+    }
+    // the second rows' sums to the first rows' waves
+    __syncthreads();
+    f32x4* sums = (f32x4*)lds + (wave & 1) * 2 * DB * 4 * 64;
+    if (part == 1) {
+#pragma unroll
+        for (int d = 0; d < DB; d++)
+#pragma unroll
+            for (int j = 0; j < 4; j++) {
+                f32x4 x, y;
+#pragma unroll
+                for (int e = 0; e < 4; e++) {
+                    x[e] = dk[d][4 * j + e];
+                    y[e] = dv[d][4 * j + e];
+                }
+                sums[((2 * d) * 4 + j) * 64 + lane] = x;
+                sums[((2 * d + 1) * 4 + j) * 64 + lane] = y;
+            }
+    }
+    __syncthreads();
+    if (part == 1 || !live) return;
+    const float nan = __uint_as_float(0x7FC00000u);
+#pragma unroll
+    for (int d = 0; d < DB; d++)
+#pragma unroll
+        for (int j = 0; j < 4; j++) {
+            const f32x4 x = sums[((2 * d) * 4 + j) * 64 + lane], y = sums[((2 * d + 1) * 4 + j) * 64 + lane];
+#pragma unroll
+            for (int e = 0; e < 4; e++) {
+                const int at = 32 * d + 8 * j + 4 * h + e;
+                store1<true>(a.dk, token * a.lddk + (int64_t)kv_head * D + at, s.bad ? nan : (dk[d][4 * j + e] + x[e]) * a.scale);
+                store1<true>(a.dv, token * a.lddv + (int64_t)kv_head * D + at, s.bad ? nan : dv[d][4 * j + e] + y[e]);
+            }
+        }
+}
+
+template <int D, bool DIRECT>
+hipError_t launch_beside(const PackedArgs& a, hipStream_t s) {
+    const dim3 threads(64 * kBackwardWaves);
+    hipLaunchKernelGGL((attention_dq_beside_kernel<D, DIRECT>), dim3((unsigned)(tile_slots(a.Tq, 32 * kBackwardWaves, a.n) * a.q_heads)), threads, 0, s, a);
+    hipLaunchKernelGGL((attention_dkv_beside_kernel<D, DIRECT>), dim3((unsigned)(tile_slots(a.Tk, 64, a.n) * a.kv_heads)), threads, 0, s, a);
+    return hipGetLastError();
+}
+
 template <bool BF16, int D>
 hipError_t launch_backward(const PackedArgs& a, hipStream_t s) {
-    typedef BackwardShape<BF16, D> B;
-    const dim3 threads(B::kThreads);
-    const int64_t q_groups = tile_slots(a.Tq, B::kRows, a.n) * a.q_heads, k_groups = tile_slots(a.Tk, B::kRows, a.n) * a.kv_heads;
-    hipLaunchKernelGGL((attention_dq_kernel<BF16, D>), dim3((unsigned)q_groups), threads, 0, s, a);
-    if constexpr (BF16 || D <= 128) {
-        hipLaunchKernelGGL((attention_dkv_kernel<BF16, D, 3>), dim3((unsigned)k_groups), threads, 0, s, a);
+    if constexpr (BF16 && D <= 128) {
+        const bool direct = direct_lines(a.q, a.ldq, true) && direct_lines(a.k, a.ldk, true) && direct_lines(a.v, a.ldv, true) && direct_lines(a.dout, a.lddo, true);
+        return direct ? launch_beside<D, true>(a, s) : launch_beside<D, false>(a, s);
     } else {
-        hipLaunchKernelGGL((attention_dkv_kernel<BF16, D, 1>), dim3((unsigned)k_groups), threads, 0, s, a);
-        hipLaunchKernelGGL((attention_dkv_kernel<BF16, D, 2>), dim3((unsigned)k_groups), threads, 0, s, a);
+        typedef BackwardShape<BF16, D> B;
+        const dim3 threads(B::kThreads);
+        const int64_t q_groups = tile_slots(a.Tq, B::kRows, a.n) * a.q_heads, k_groups = tile_slots(a.Tk, B::kRows, a.n) * a.kv_heads;
+        hipLaunchKernelGGL((attention_dq_kernel<BF16, D>), dim3((unsigned)q_groups), threads, 0, s, a);
+        if constexpr (BF16 || D <= 128) {
+            hipLaunchKernelGGL((attention_dkv_kernel<BF16, D, 3>), dim3((unsigned)k_groups), threads, 0, s, a);
+        } else {
+            hipLaunchKernelGGL((attention_dkv_kernel<BF16, D, 1>), dim3((unsigned)k_groups), threads, 0, s, a);
+            hipLaunchKernelGGL((attention_dkv_kernel<BF16, D, 2>), dim3((unsigned)k_groups), threads, 0, s, a);
+        }
+        return hipGetLastError();
     }
-    return hipGetLastError();
 }
 template <bool BF16>
 hipError_t launch_backward_by_width(const PackedArgs& a, hipStream_t s) {

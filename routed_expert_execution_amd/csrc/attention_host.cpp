@@ -295,7 +295,7 @@ moe_status moe_attention(moe_ctx* c, const moe_attn* t, const void* q, int64_t l
 
 size_t moe_attention_workspace(int64_t tokens_q, int32_t q_heads) {
     if (tokens_q < 0 || tokens_q > kMaxT || q_heads < 1 || q_heads > kMaxHeads) return 0;
-    const size_t n = (size_t)tokens_q * q_heads * sizeof(float);
+    const size_t n = (size_t)tokens_q * q_heads * sizeof(float2);
     return n < 256 ? 256 : n;
 }
 
@@ -325,7 +325,7 @@ moe_status moe_attention_backward(moe_ctx* c, const moe_attn* t, const void* dou
     a.q = q; a.k = k; a.v = v; a.out = (void*)out; a.lse = (float*)lse; a.dout = dout; a.dq = dq; a.dk = dk; a.dv = dv;
     a.ldq = Tq > 1 ? ldq : qw; a.ldo = Tq > 1 ? ldo : qw; a.lddo = Tq > 1 ? lddo : qw; a.lddq = Tq > 1 ? lddq : qw;
     a.ldk = Tk > 1 ? ldk : kw; a.ldv = Tk > 1 ? ldv : kw; a.lddk = Tk > 1 ? lddk : kw; a.lddv = Tk > 1 ? lddv : kw;
-    a.delta = (float*)workspace;
+    a.rows = (float2*)workspace;
     a.err = error_word(c);
     DeviceGuard dg(device_of(c));
     LAUNCH(a.bf16 ? moe::launch_attention_backward_bf16(a, (hipStream_t)stream) : moe::launch_attention_backward_f32(a, (hipStream_t)stream));

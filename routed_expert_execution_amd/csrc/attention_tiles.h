@@ -200,6 +200,15 @@ template <bool DIRECT> __device__ inline void meet() {
     if (DIRECT) tile::wait_loads_and_meet();
     else __syncthreads();
 }
+// 4 bytes a lane from base + offset straight into LDS at `lds` + 4 * lane (see tile::load_lds16).
+__device__ inline void load_lds4(uint32_t lds, uint32_t offset, const void* base) {
+    asm volatile(
+        "s_nop 4\n\t"
+        "global_load_lds_dword %0, %1"
+        :
+        : "v"(offset), "s"(tile::uniform(base)), "{m0}"(__builtin_amdgcn_readfirstlane(lds))
+        : "memory");
+}
 // Lines that may go straight into LDS: whole 16-byte chunks, a tile of 64 within 32 bits.
 inline bool direct_lines(const void* p, int64_t ld, bool bf16) {
     const int64_t bytes = ld * (bf16 ? 2 : 4);
