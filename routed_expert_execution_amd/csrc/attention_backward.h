@@ -13,24 +13,78 @@
 namespace moe {
 namespace packed {
 
-constexpr int kBackwardWaves = 4;
-template <bool BF16, int D> struct BackwardShape {
-    static constexpr int kThreads = 64 * kBackwardWaves;
-    static constexpr int kRows = 32 * kBackwardWaves;       // of a workgroup's own tile, 32 a wave
-    static constexpr int kOther = BF16 && D <= 128 ? 64 : 32;  // of a tile that it passes over
-    static constexpr int kTileBytes = kOther * Tile<BF16, D>::kLineBytes;
+constexpr int kBackwardWaves = 4, kBackwardThreads = 64 * kBackwardWaves;
+
+// fp32, and bf16 heads of more than 128 channels.  A workgroup has 32 BLOCKS rows (dQ)
+// or keys (dK, dV) of its own and passes over the others 32 PARTS at a time, BLOCKS
+// PARTS = 4 waves, each with sums of its own that are added in order at the end: small
+// tiles, since few and short sequences have to fill the card and the products of fp32,
+// six of bf16 terms each, leave the time to load more.
+template <bool BF16, int D> struct PartsShape {
+    static constexpr int kParts = BF16 || D <= 128 ? 4 : 2, kBlocks = kBackwardWaves / kParts;
+    static constexpr int kOwn = 32 * kBlocks, kOther = 32 * kParts;
+    static constexpr int kTileBytes = kOther * Tile<BF16, D>::kLineBytes;  // 64 KiB at most
 };
 
-// dQ, and delta for the other kernel.  As the forward kernel: S^T = K Q^T and
-// dP^T = V dO^T with a row a lane, dQ^T = K^T dS^T.
-template <bool BF16, int D>
-__global__ __launch_bounds__(kBackwardWaves * 64) void attention_dq_kernel(PackedArgs a) {
-    typedef BackwardShape<BF16, D> B;
+// Sums of several waves: those of parts 1.. through LDS to part 0's, which adds them in
+// order.  N blocks of 16 registers; true for the waves that hold the result.
+template <int N, int PARTS, int BLOCKS>
+__device__ inline bool add_parts(f32x16 (&acc)[N], char* lds, int part, int block, int lane) {
+    f32x4* at = (f32x4*)lds;
+#pragma unroll 1
+    for (int p = 1; p < PARTS; p++) {
+        __syncthreads();
+        if (part == p)
+#pragma unroll
+            for (int n = 0; n < N; n++)
+#pragma unroll
+                for (int j = 0; j < 4; j++) at[((block * N + n) * 4 + j) * 64 + lane] = f32x4{acc[n][4 * j], acc[n][4 * j + 1], acc[n][4 * j + 2], acc[n][4 * j + 3]};
+        __syncthreads();
+        if (part == 0)
+#pragma unroll
+            for (int n = 0; n < N; n++)
+#pragma unroll
+                for (int j = 0; j < 4; j++) {
+                    const f32x4 v = at[((block * N + n) * 4 + j) * 64 + lane];
+#pragma unroll
+                    for (int e = 0; e < 4; e++) acc[n][4 * j + e] += v[e];
+                }
+    }
+    return part == 0;
+}
+
+// A tile into LDS, through registers a few chunks at a time or straight.
+template <bool BF16, int D, int R, bool DIRECT>
+__device__ inline void bring(const char* base, int64_t ld, int64_t first, int lines, char* lds) {
     typedef Tile<BF16, D> T;
-    constexpr int BK = B::kOther, KK = D / 16, DB = D / 32, KB = BK / 32;
-    __shared__ __attribute__((aligned(1024))) char lds[4 * B::kTileBytes];
-    __shared__ int odd_tile[2];
+    if constexpr (DIRECT) {
+        Pipe<BF16, D, R, kBackwardThreads, true> p;
+        p.fetch(base, ld, first, lines, lds);
+    } else {
+#pragma unroll 4
+        for (int n = threadIdx.x; n < R * T::kChunks; n += kBackwardThreads) {
+            const int r = n / T::kChunks, c = n - r * T::kChunks;
+            u32x4 v = {0, 0, 0, 0};
+            if (r < lines) {
+                const Words4 w = *(const Words4*)(base + ((first + r) * ld + c * T::kPer) * (BF16 ? 2 : 4));
+                v = u32x4{w.v[0], w.v[1], w.v[2], w.v[3]};
+            }
+            *(u32x4*)(lds + T::at(r, c)) = v;
+        }
+    }
+}
+
+// dQ, and delta for the other kernel: S^T = K Q^T and dP^T = V dO^T with a row a lane,
+// dQ^T = K^T dS^T.
+template <bool BF16, int D, bool DIRECT>
+__global__ __launch_bounds__(kBackwardThreads) void attention_dq_kernel(PackedArgs a) {
+    typedef PartsShape<BF16, D> B;
+    typedef Tile<BF16, D> T;
+    constexpr int BK = B::kOther, KK = D / 16, DB = D / 32;
+    __shared__ __attribute__((aligned(1024))) char lds[2 * B::kTileBytes];
+    __shared__ int odd_tile;
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), h = lane >> 5;
+    const int block = wave % B::kBlocks, part = wave / B::kBlocks;
     const int kv_head = blockIdx.x % a.kv_heads, rest = blockIdx.x / a.kv_heads;
     const int head = kv_head * a.per_head + rest % a.per_head;
     if (blockIdx.x == gridDim.x - 1) {
@@ -38,11 +92,11 @@ __global__ __launch_bounds__(kBackwardWaves * 64) void attention_dq_kernel(Packe
         check_offsets(a.offsets_k, a.n, a.Tk, a.err);
     }
     int seq, local;
-    if (!find_tile<B::kRows>(a.offsets_q, a.n, a.Tq, rest / a.per_head, &seq, &local)) return;
+    if (!find_tile<B::kOwn>(a.offsets_q, a.n, a.Tq, rest / a.per_head, &seq, &local)) return;
     const Sequence s = sequence_of(a, seq);
-    const int tiles = (s.rows + B::kRows - 1) / B::kRows;
+    const int tiles = (s.rows + B::kOwn - 1) / B::kOwn;
     if (local >= tiles) return;
-    const int row0 = (tiles - 1 - local) * B::kRows, row = row0 + wave * 32 + (lane & 31);
+    const int row0 = (tiles - 1 - local) * B::kOwn, wave_first = row0 + block * 32, row = wave_first + (lane & 31);
     const bool live = row < s.rows;
     if (s.bad && threadIdx.x == 0) atomicOr(a.err, kErrCache);
 
@@ -67,7 +121,7 @@ __global__ __launch_bounds__(kBackwardWaves * 64) void attention_dq_kernel(Packe
     float lse = kInf;  // (a row past the last: P = 0)
     if (live) {
         lse = a.lse[token * a.q_heads + head] * kLog2e;
-        if (h == 0) a.rows[(int64_t)head * a.Tq + token] = make_float2(lse, delta);
+        if (h == 0 && part == 0) a.rows[(int64_t)head * a.Tq + token] = make_float2(lse, delta);
     }
     f32x16 out[DB];
 #pragma unroll
@@ -75,94 +129,75 @@ __global__ __launch_bounds__(kBackwardWaves * 64) void attention_dq_kernel(Packe
 #pragma unroll
         for (int i = 0; i < 16; i++) out[d][i] = 0;
 
-    const int last_row = min(row0 + B::kRows, s.rows) - 1;
+    const int last_row = min(row0 + B::kOwn, s.rows) - 1, wave_last = min(wave_first + 31, s.rows - 1);
     const int end = a.causal ? min(s.keys, last_row + s.shift + 1) : s.keys;
-    const int begin = a.window ? max(0, row0 + s.shift - a.window + 1) / BK * BK : 0;
-    const int wave_first = row0 + wave * 32, wave_last = min(wave_first + 31, s.rows - 1);
+    const int begin = a.window ? max(0, row0 + s.shift - a.window + 1) / 32 * 32 : 0;
     const char* kbase = (const char*)a.k + ((int64_t)s.k0 * a.ldk + (int64_t)kv_head * D) * (BF16 ? 2 : 4);
     const char* vbase = (const char*)a.v + ((int64_t)s.k0 * a.ldv + (int64_t)kv_head * D) * (BF16 ? 2 : 4);
-    auto masked_tile = [&](int k0) {
-        return k0 + BK > s.keys || (a.causal && k0 + BK - 1 > row0 + s.shift) || (a.window && k0 <= last_row + s.shift - a.window);
-    };
-    Staged<BF16, D, BK, B::kThreads> sk, sv;
-    auto put = [&](int k0, int buffer) {
-        sk.store(lds + 2 * buffer * B::kTileBytes);
-        sv.store(lds + (2 * buffer + 1) * B::kTileBytes);
-        if (masked_tile(k0) && sk.any_not_finite()) odd_tile[buffer] = k0;
-    };
-    if (threadIdx.x < 2) odd_tile[threadIdx.x] = -1;
-    if (begin < end) {
-        sk.load(kbase, a.ldk, begin, s.keys - begin);
-        sv.load(vbase, a.ldv, begin, s.keys - begin);
+    char *kt = lds, *vt = lds + B::kTileBytes;
+    const uint32_t ka = tile::lds_address(kt) + T::along_lane(lane) + part * 32 * T::kLineBytes, va = ka + B::kTileBytes;
+    const uint32_t kx = tile::lds_address(kt) + T::across_lane(lane) + part * 32 * T::kLineBytes;
+    if (threadIdx.x == 0) odd_tile = -1;
+#pragma unroll 1
+    for (int t0 = begin; t0 < end; t0 += BK) {
         __syncthreads();
-        put(begin, 0);
-    }
-    __syncthreads();
-    const uint32_t along_lane = T::along_lane(lane), across_lane = T::across_lane(lane);
-    int buffer = 0;
-    for (int k0 = begin; k0 < end; k0 += BK, buffer ^= 1) {
-        const bool more = k0 + BK < end;
-        if (more) {
-            sk.load(kbase, a.ldk, k0 + BK, s.keys - k0 - BK);
-            sv.load(vbase, a.ldv, k0 + BK, s.keys - k0 - BK);
+        bring<BF16, D, BK, DIRECT>(kbase, a.ldk, t0, s.keys - t0, kt);
+        bring<BF16, D, BK, DIRECT>(vbase, a.ldv, t0, s.keys - t0, vt);
+        meet<DIRECT>();
+        if (t0 + BK > s.keys || (a.causal && t0 + BK - 1 > row0 + s.shift) || (a.window && t0 <= last_row + s.shift - a.window)) {
+            if (tile_not_finite<BF16, D, BK, kBackwardThreads>(kt)) odd_tile = t0;
+            __syncthreads();
         }
-        const char* kt = lds + 2 * buffer * B::kTileBytes;
-        const char* vt = kt + B::kTileBytes;
-        const uint32_t ka = tile::lds_address(kt) + along_lane, va = tile::lds_address(vt) + along_lane, kx = tile::lds_address(kt) + across_lane;
-        const bool none = wave_first >= s.rows || (a.causal && k0 > wave_last + s.shift) || (a.window && k0 + BK - 1 <= wave_first + s.shift - a.window);
-        if (!none) {
-            const bool masked = k0 + BK > s.keys || (a.causal && k0 + BK - 1 > wave_first + s.shift) || (a.window && k0 <= wave_last + s.shift - a.window);
-            const bool odd = masked && odd_tile[buffer] == k0;
-            const Span span = keys_seen(a, s, row, k0, h);
+        const int k0 = t0 + 32 * part;  // this wave's 32 keys
+        if (k0 >= s.keys || wave_first >= s.rows || (a.causal && k0 > wave_last + s.shift) || (a.window && k0 + 31 <= wave_first + s.shift - a.window)) continue;
+        const bool masked = k0 + 32 > s.keys || (a.causal && k0 + 31 > wave_first + s.shift) || (a.window && k0 <= wave_last + s.shift - a.window);
+        const bool odd = masked && odd_tile == t0;
+        const Span span = keys_seen(a, s, row, k0, h);
+        f32x16 st, dp;
 #pragma unroll
-            for (int b = 0; b < KB; b++) {
-                f32x16 st, dp;
+        for (int i = 0; i < 16; i++) st[i] = dp[i] = 0;
 #pragma unroll
-                for (int i = 0; i < 16; i++) st[i] = dp[i] = 0;
+        for (int kk = 0; kk < KK; kk++) {
+            Fragment<BF16> f, f2;
+            T::along(ka, 0, kk, f);
+            T::along(va, 0, kk, f2);
+            f.split();
+            f2.split();
+            mma(st, f, q[kk]);
+            mma(dp, f2, g[kk]);
+            if (!BF16) __builtin_amdgcn_sched_barrier(0);  // (terms of one step at a time: registers are short)
+        }
 #pragma unroll
-                for (int kk = 0; kk < KK; kk++) {
-                    Fragment<BF16> f;
-                    T::along(ka, 32 * b, kk, f);
+        for (int i = 0; i < 16; i++) {
+            const float ds = __builtin_amdgcn_exp2f(fmaf(st[i], a.scale_log2, -lse)) * (dp[i] - delta);
+            st[i] = masked && !span.has(0, i) ? 0.f : ds;
+        }
+#pragma unroll
+        for (int n = 0; n < 2; n++) {
+            float v[8];
+            bf16x8 seen;
+#pragma unroll
+            for (int e = 0; e < 8; e++) {
+                v[e] = st[8 * n + e];
+                seen[e] = (__bf16)(span.has(0, 8 * n + e) ? 1.f : 0.f);
+            }
+            Fragment<BF16> df;
+            operand_of(v, df);
+#pragma unroll
+            for (int d = 0; d < DB; d++) {
+                Fragment<BF16> f;
+                T::across(kx, 16 * n, 32 * d, f);
+                if (odd) {
+                    mma_seen(out[d], f, df, seen);
+                } else {
                     f.split();
-                    mma(st, f, q[kk]);
-                    T::along(va, 32 * b, kk, f);
-                    f.split();
-                    mma(dp, f, g[kk]);
+                    mma(out[d], f, df);
                 }
-#pragma unroll
-                for (int i = 0; i < 16; i++) {
-                    const float ds = __builtin_amdgcn_exp2f(fmaf(st[i], a.scale_log2, -lse)) * (dp[i] - delta);
-                    st[i] = masked && !span.has(b, i) ? 0.f : ds;
-                }
-#pragma unroll
-                for (int n = 0; n < 2; n++) {
-                    float v[8];
-#pragma unroll
-                    for (int e = 0; e < 8; e++) v[e] = st[8 * n + e];
-                    Fragment<BF16> df;
-                    operand_of(v, df);
-                    bf16x8 seen;
-                    if (odd)
-#pragma unroll
-                        for (int e = 0; e < 8; e++) seen[e] = (__bf16)(span.has(b, 8 * n + e) ? 1.f : 0.f);
-#pragma unroll
-                    for (int d = 0; d < DB; d++) {
-                        Fragment<BF16> f;
-                        T::across(kx, 32 * b + 16 * n, 32 * d, f);
-                        if (odd) {
-                            mma_seen(out[d], f, df, seen);
-                        } else {
-                            f.split();
-                            mma(out[d], f, df);
-                        }
-                    }
-                }
+                if (!BF16) __builtin_amdgcn_sched_barrier(0);
             }
         }
-        if (more) put(k0 + BK, buffer ^ 1);
-        __syncthreads();
     }
-    if (!live) return;
+    if (!add_parts<DB, B::kParts, B::kBlocks>(out, lds, part, block, lane) || !live) return;
     const float by = s.bad ? __uint_as_float(0x7FC00000u) : a.scale;
     const int64_t o = token * a.lddq + (int64_t)head * D;
 #pragma unroll
@@ -173,25 +208,26 @@ __global__ __launch_bounds__(kBackwardWaves * 64) void attention_dq_kernel(Packe
             for (int e = 0; e < 4; e++) store1<BF16>(a.dq, o + 32 * d + 8 * j + 4 * h + e, out[d][4 * j + e] * by);
 }
 
-// dK and dV.  A wave has 32 keys as operands in registers and passes over the rows
-// that see any of the workgroup's keys, of one query head after the other: S = Q K^T
-// and dP = dO V^T with a key a lane, dV^T = dO^T P, dK^T = Q^T dS.
+// dK and dV: a wave has 32 keys as operands in registers and passes over the rows that
+// see any of the workgroup's keys, of one query head after the other: S = Q K^T and
+// dP = dO V^T with a key a lane, dV^T = dO^T P, dK^T = Q^T dS.
 // WHAT: 3 both; 1 dV alone, 2 dK alone (where registers do not hold both).
-template <bool BF16, int D, int WHAT>
-__global__ __launch_bounds__(kBackwardWaves * 64) void attention_dkv_kernel(PackedArgs a) {
-    typedef BackwardShape<BF16, D> B;
+template <bool BF16, int D, int WHAT, bool DIRECT>
+__global__ __launch_bounds__(kBackwardThreads) void attention_dkv_kernel(PackedArgs a) {
+    typedef PartsShape<BF16, D> B;
     typedef Tile<BF16, D> T;
-    constexpr int BQ = B::kOther, KK = D / 16, DB = D / 32, RB = BQ / 32;
+    constexpr int BQ = B::kOther, KK = D / 16, DB = D / 32;
     constexpr bool kDv = WHAT & 1, kDk = WHAT & 2;
-    __shared__ __attribute__((aligned(1024))) char lds[4 * B::kTileBytes];
-    __shared__ __attribute__((aligned(16))) float row_lse[2][BQ], row_delta[2][BQ];
-    __shared__ int odd_tile[2];
+    __shared__ __attribute__((aligned(1024))) char lds[2 * B::kTileBytes];
+    __shared__ __attribute__((aligned(16))) float2 stats[BQ];
+    __shared__ int odd_tile;
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), h = lane >> 5;
+    const int block = wave % B::kBlocks, part = wave / B::kBlocks;
     const int kv_head = blockIdx.x % a.kv_heads;
     int seq, local;
-    if (!find_tile<B::kRows>(a.offsets_k, a.n, a.Tk, blockIdx.x / a.kv_heads, &seq, &local)) return;
+    if (!find_tile<B::kOwn>(a.offsets_k, a.n, a.Tk, blockIdx.x / a.kv_heads, &seq, &local)) return;
     const Sequence s = sequence_of(a, seq);
-    const int key0 = local * B::kRows, wave_key = key0 + wave * 32, key = wave_key + (lane & 31);
+    const int key0 = local * B::kOwn, wave_key = key0 + block * 32, key = wave_key + (lane & 31);
     if (key0 >= s.keys) return;
     const bool live = key < s.keys;
     if (s.bad && threadIdx.x == 0) atomicOr(a.err, kErrCache);
@@ -201,7 +237,11 @@ __global__ __launch_bounds__(kBackwardWaves * 64) void attention_dkv_kernel(Pack
 #pragma unroll
     for (int kk = 0; kk < KK; kk++) {
         along_memory<BF16>(a.k, token * a.ldk + (int64_t)kv_head * D, live, kk, lane, k[kk]);
-        if constexpr (kDk) along_memory<BF16>(a.v, token * a.ldv + (int64_t)kv_head * D, live, kk, lane, v[kk]);
+        k[kk].split();
+        if constexpr (kDk) {
+            along_memory<BF16>(a.v, token * a.ldv + (int64_t)kv_head * D, live, kk, lane, v[kk]);
+            v[kk].split();
+        }
     }
     f32x16 dk[kDk ? DB : 1], dv[kDv ? DB : 1];
 #pragma unroll
@@ -212,141 +252,110 @@ __global__ __launch_bounds__(kBackwardWaves * 64) void attention_dkv_kernel(Pack
         for (int d = 0; d < (kDv ? DB : 1); d++) dv[d][i] = 0;
     }
     // rows that see any of the workgroup's keys
-    const int last_key = min(key0 + B::kRows, s.keys) - 1;
-    const int begin = a.causal ? max(0, key0 - s.shift) / BQ * BQ : 0;
-    const int64_t end_row = a.window ? (int64_t)last_key - s.shift + a.window : s.rows;
-    const int end = (int)min((int64_t)s.rows, end_row);
-    const int per = end > begin ? (end - begin + BQ - 1) / BQ : 0, total = per * a.per_head;
-    const int wave_last_key = min(wave_key + 31, s.keys - 1);
-    auto row_of = [&](int t) { return begin + t % per * BQ; };
-    auto masked_tile = [&](int r0) {
-        return (a.causal && last_key > r0 + s.shift) || (a.window && key0 <= r0 + BQ - 1 + s.shift - a.window);
-    };
-    Staged<BF16, D, BQ, B::kThreads> sq, sg;
-    float s_lse = 0, s_delta = 0;
-    auto get = [&](int t) {
-        const int r0 = row_of(t), head = kv_head * a.per_head + t / per;
-        sq.load((const char*)a.q + ((int64_t)s.q0 * a.ldq + (int64_t)head * D) * (BF16 ? 2 : 4), a.ldq, r0, s.rows - r0);
-        sg.load((const char*)a.dout + ((int64_t)s.q0 * a.lddo + (int64_t)head * D) * (BF16 ? 2 : 4), a.lddo, r0, s.rows - r0);
-        if (threadIdx.x < BQ) {
-            const int r = r0 + threadIdx.x;
-            // (past the last row: P = 0)
-            const float2 of_row = r < s.rows ? a.rows[(int64_t)head * a.Tq + s.q0 + r] : make_float2(kInf, 0.f);
-            s_lse = of_row.x;
-            s_delta = of_row.y;
-        }
-    };
-    auto put = [&](int t, int buffer) {
-        sq.store(lds + 2 * buffer * B::kTileBytes);
-        sg.store(lds + (2 * buffer + 1) * B::kTileBytes);
-        if (threadIdx.x < BQ) {
-            row_lse[buffer][threadIdx.x] = s_lse;
-            row_delta[buffer][threadIdx.x] = s_delta;
-        }
-        if (masked_tile(row_of(t)) && (sq.any_not_finite() || sg.any_not_finite())) odd_tile[buffer] = t;
-    };
-    if (threadIdx.x < 2) odd_tile[threadIdx.x] = -1;
-    if (total) {
-        get(0);
-        __syncthreads();
-        put(0, 0);
-    }
-    __syncthreads();
-    const uint32_t along_lane = T::along_lane(lane), across_lane = T::across_lane(lane);
-    for (int t = 0; t < total; t++) {
-        const int buffer = t & 1, r0 = row_of(t);
-        if (t + 1 < total) get(t + 1);
-        const char* qt = lds + 2 * buffer * B::kTileBytes;
-        const char* gt = qt + B::kTileBytes;
-        const uint32_t qa = tile::lds_address(qt) + along_lane, ga = tile::lds_address(gt) + along_lane;
-        const uint32_t qx = tile::lds_address(qt) + across_lane, gx = tile::lds_address(gt) + across_lane;
-        const bool none = wave_key >= s.keys || (a.causal && wave_key > r0 + BQ - 1 + s.shift) || (a.window && wave_last_key <= r0 + s.shift - a.window);
-        if (!none) {
-            const bool masked = (a.causal && wave_last_key > r0 + s.shift) || (a.window && wave_key <= r0 + BQ - 1 + s.shift - a.window);
-            const bool odd = masked && odd_tile[buffer] == t;
+    const int last_key = min(key0 + B::kOwn, s.keys) - 1, wave_last_key = min(wave_key + 31, s.keys - 1);
+    const int begin = a.causal ? max(0, key0 - s.shift) / 32 * 32 : 0;
+    const int end = (int)min((int64_t)s.rows, a.window ? (int64_t)last_key - s.shift + a.window : s.rows);
+    char *qt = lds, *gt = lds + B::kTileBytes;
+    const uint32_t qa = tile::lds_address(qt) + T::along_lane(lane) + part * 32 * T::kLineBytes, ga = qa + B::kTileBytes;
+    const uint32_t qx = tile::lds_address(qt) + T::across_lane(lane) + part * 32 * T::kLineBytes, gx = qx + B::kTileBytes;
+    if (threadIdx.x == 0) odd_tile = -1;
+    int at = 0;  // a number for each tile
+#pragma unroll 1
+    for (int head = kv_head * a.per_head; head < (kv_head + 1) * a.per_head; head++)
+#pragma unroll 1
+        for (int t0 = begin; t0 < end; t0 += BQ, at++) {
+            __syncthreads();
+            bring<BF16, D, BQ, DIRECT>((const char*)a.q + ((int64_t)s.q0 * a.ldq + (int64_t)head * D) * (BF16 ? 2 : 4), a.ldq, t0, s.rows - t0, qt);
+            bring<BF16, D, BQ, DIRECT>((const char*)a.dout + ((int64_t)s.q0 * a.lddo + (int64_t)head * D) * (BF16 ? 2 : 4), a.lddo, t0, s.rows - t0, gt);
+            if (threadIdx.x < BQ) {
+                const int r = t0 + threadIdx.x;  // (past the last row: P = 0)
+                stats[threadIdx.x] = r < s.rows ? a.rows[(int64_t)head * a.Tq + s.q0 + r] : make_float2(kInf, 0.f);
+            }
+            meet<DIRECT>();
+            if (t0 + BQ > s.rows || (a.causal && last_key > t0 + s.shift) || (a.window && key0 <= t0 + BQ - 1 + s.shift - a.window)) {
+                const bool bad_q = tile_not_finite<BF16, D, BQ, kBackwardThreads>(qt), bad_g = tile_not_finite<BF16, D, BQ, kBackwardThreads>(gt);
+                if (bad_q || bad_g) odd_tile = at;
+                __syncthreads();
+            }
+            const int r0 = t0 + 32 * part;  // this wave's 32 rows
+            if (r0 >= s.rows || wave_key >= s.keys || (a.causal && wave_key > r0 + 31 + s.shift) || (a.window && wave_last_key <= r0 + s.shift - a.window)) continue;
+            const bool masked = r0 + 32 > s.rows || (a.causal && wave_last_key > r0 + s.shift) || (a.window && wave_key <= r0 + 31 + s.shift - a.window);
+            const bool odd = masked && odd_tile == at;
             const Span span = rows_seeing(a, s, key, r0, h);
+            f32x16 st, dp;
 #pragma unroll
-            for (int b = 0; b < RB; b++) {
-                f32x16 st, dp;
+            for (int i = 0; i < 16; i++) st[i] = dp[i] = 0;
 #pragma unroll
-                for (int i = 0; i < 16; i++) st[i] = dp[i] = 0;
-#pragma unroll
-                for (int kk = 0; kk < KK; kk++) {
-                    Fragment<BF16> f, o;
-                    T::along(qa, 32 * b, kk, f);
+            for (int kk = 0; kk < KK; kk++) {
+                Fragment<BF16> f;
+                T::along(qa, 0, kk, f);
+                f.split();
+                mma(st, f, k[kk]);
+                if constexpr (kDk) {
+                    T::along(ga, 0, kk, f);
                     f.split();
-                    o = k[kk];
-                    o.split();
-                    mma(st, f, o);
-                    if constexpr (kDk) {
-                        T::along(ga, 32 * b, kk, f);
-                        f.split();
-                        o = v[kk];
-                        o.split();
-                        mma(dp, f, o);
-                    }
+                    mma(dp, f, v[kk]);
                 }
-                float p[16];
+                if (!BF16) __builtin_amdgcn_sched_barrier(0);
+            }
+            float p[16];
 #pragma unroll
-                for (int j = 0; j < 4; j++) {
-                    const f32x4 lse = *(const f32x4*)&row_lse[buffer][32 * b + 8 * j + 4 * h], delta = *(const f32x4*)&row_delta[buffer][32 * b + 8 * j + 4 * h];
+            for (int j = 0; j < 4; j++)
 #pragma unroll
-                    for (int e = 0; e < 4; e++) {
-                        const int i = 4 * j + e;
-                        const bool off = masked && !span.has(b, i);
-                        p[i] = __builtin_amdgcn_exp2f(fmaf(st[i], a.scale_log2, -lse[e]));
-                        const float ds = p[i] * (dp[i] - delta[e]);
-                        p[i] = off ? 0.f : p[i];
-                        st[i] = off ? 0.f : ds;
-                    }
+                for (int e = 0; e < 4; e++) {
+                    const int i = 4 * j + e;
+                    const float2 of_row = stats[32 * part + 8 * j + 4 * h + e];
+                    const bool off = masked && !span.has(0, i);
+                    p[i] = __builtin_amdgcn_exp2f(fmaf(st[i], a.scale_log2, -of_row.x));
+                    const float ds = p[i] * (dp[i] - of_row.y);
+                    p[i] = off ? 0.f : p[i];
+                    st[i] = off ? 0.f : ds;
                 }
 #pragma unroll
-                for (int n = 0; n < 2; n++) {
-                    Fragment<BF16> pf, df;
-                    float x[8];
-                    bf16x8 seen;
-                    if (odd)
+            for (int n = 0; n < 2; n++) {
+                Fragment<BF16> pf, df;
+                float x[8];
+                bf16x8 seen;
 #pragma unroll
-                        for (int e = 0; e < 8; e++) seen[e] = (__bf16)(span.has(b, 8 * n + e) ? 1.f : 0.f);
+                for (int e = 0; e < 8; e++) seen[e] = (__bf16)(span.has(0, 8 * n + e) ? 1.f : 0.f);
+                if constexpr (kDv) {
+#pragma unroll
+                    for (int e = 0; e < 8; e++) x[e] = p[8 * n + e];
+                    operand_of(x, pf);
+                }
+                if constexpr (kDk) {
+#pragma unroll
+                    for (int e = 0; e < 8; e++) x[e] = st[8 * n + e];
+                    operand_of(x, df);
+                }
+#pragma unroll
+                for (int d = 0; d < DB; d++) {
+                    Fragment<BF16> f;
                     if constexpr (kDv) {
-#pragma unroll
-                        for (int e = 0; e < 8; e++) x[e] = p[8 * n + e];
-                        operand_of(x, pf);
+                        T::across(gx, 16 * n, 32 * d, f);
+                        if (odd) {
+                            mma_seen(dv[d], f, pf, seen);
+                        } else {
+                            f.split();
+                            mma(dv[d], f, pf);
+                        }
                     }
                     if constexpr (kDk) {
-#pragma unroll
-                        for (int e = 0; e < 8; e++) x[e] = st[8 * n + e];
-                        operand_of(x, df);
-                    }
-#pragma unroll
-                    for (int d = 0; d < DB; d++) {
-                        Fragment<BF16> f;
-                        if constexpr (kDv) {
-                            T::across(gx, 32 * b + 16 * n, 32 * d, f);
-                            if (odd) {
-                                mma_seen(dv[d], f, pf, seen);
-                            } else {
-                                f.split();
-                                mma(dv[d], f, pf);
-                            }
-                        }
-                        if constexpr (kDk) {
-                            T::across(qx, 32 * b + 16 * n, 32 * d, f);
-                            if (odd) {
-                                mma_seen(dk[d], f, df, seen);
-                            } else {
-                                f.split();
-                                mma(dk[d], f, df);
-                            }
+                        T::across(qx, 16 * n, 32 * d, f);
+                        if (odd) {
+                            mma_seen(dk[d], f, df, seen);
+                        } else {
+                            f.split();
+                            mma(dk[d], f, df);
                         }
                     }
+                    if (!BF16) __builtin_amdgcn_sched_barrier(0);
                 }
             }
         }
-        if (t + 1 < total) put(t + 1, buffer ^ 1);
-        __syncthreads();
-    }
-    if (!live) return;
+    if constexpr (kDk) add_parts<DB, B::kParts, B::kBlocks>(dk, lds, part, block, lane);
+    if constexpr (kDv) add_parts<DB, B::kParts, B::kBlocks>(dv, lds, part, block, lane);
+    if (part != 0 || !live) return;
     const float nan = __uint_as_float(0x7FC00000u);
 #pragma unroll
     for (int d = 0; d < DB; d++)
@@ -354,9 +363,9 @@ __global__ __launch_bounds__(kBackwardWaves * 64) void attention_dkv_kernel(Pack
         for (int j = 0; j < 4; j++)
 #pragma unroll
             for (int e = 0; e < 4; e++) {
-                const int at = 32 * d + 8 * j + 4 * h + e;
-                if constexpr (kDk) store1<BF16>(a.dk, token * a.lddk + (int64_t)kv_head * D + at, s.bad ? nan : dk[d][4 * j + e] * a.scale);
-                if constexpr (kDv) store1<BF16>(a.dv, token * a.lddv + (int64_t)kv_head * D + at, s.bad ? nan : dv[d][4 * j + e]);
+                const int c = 32 * d + 8 * j + 4 * h + e;
+                if constexpr (kDk) store1<BF16>(a.dk, token * a.lddk + (int64_t)kv_head * D + c, s.bad ? nan : dk[d][4 * j + e] * a.scale);
+                if constexpr (kDv) store1<BF16>(a.dv, token * a.lddv + (int64_t)kv_head * D + c, s.bad ? nan : dv[d][4 * j + e]);
             }
 }
 
@@ -778,24 +787,24 @@ hipError_t launch_beside(const PackedArgs& a, hipStream_t s) {
     return hipGetLastError();
 }
 
+template <bool BF16, int D, bool DIRECT>
+hipError_t launch_parts(const PackedArgs& a, hipStream_t s) {
+    typedef PartsShape<BF16, D> B;
+    const dim3 threads(kBackwardThreads), q_groups((unsigned)(tile_slots(a.Tq, B::kOwn, a.n) * a.q_heads)), k_groups((unsigned)(tile_slots(a.Tk, B::kOwn, a.n) * a.kv_heads));
+    hipLaunchKernelGGL((attention_dq_kernel<BF16, D, DIRECT>), q_groups, threads, 0, s, a);
+    if constexpr (BF16 || D <= 128) {
+        hipLaunchKernelGGL((attention_dkv_kernel<BF16, D, 3, DIRECT>), k_groups, threads, 0, s, a);
+    } else {
+        hipLaunchKernelGGL((attention_dkv_kernel<BF16, D, 1, DIRECT>), k_groups, threads, 0, s, a);
+        hipLaunchKernelGGL((attention_dkv_kernel<BF16, D, 2, DIRECT>), k_groups, threads, 0, s, a);
+    }
+    return hipGetLastError();
+}
 template <bool BF16, int D>
 hipError_t launch_backward(const PackedArgs& a, hipStream_t s) {
-    if constexpr (BF16 && D <= 128) {
-        const bool direct = direct_lines(a.q, a.ldq, true) && direct_lines(a.k, a.ldk, true) && direct_lines(a.v, a.ldv, true) && direct_lines(a.dout, a.lddo, true);
-        return direct ? launch_beside<D, true>(a, s) : launch_beside<D, false>(a, s);
-    } else {
-        typedef BackwardShape<BF16, D> B;
-        const dim3 threads(B::kThreads);
-        const int64_t q_groups = tile_slots(a.Tq, B::kRows, a.n) * a.q_heads, k_groups = tile_slots(a.Tk, B::kRows, a.n) * a.kv_heads;
-        hipLaunchKernelGGL((attention_dq_kernel<BF16, D>), dim3((unsigned)q_groups), threads, 0, s, a);
-        if constexpr (BF16 || D <= 128) {
-            hipLaunchKernelGGL((attention_dkv_kernel<BF16, D, 3>), dim3((unsigned)k_groups), threads, 0, s, a);
-        } else {
-            hipLaunchKernelGGL((attention_dkv_kernel<BF16, D, 1>), dim3((unsigned)k_groups), threads, 0, s, a);
-            hipLaunchKernelGGL((attention_dkv_kernel<BF16, D, 2>), dim3((unsigned)k_groups), threads, 0, s, a);
-        }
-        return hipGetLastError();
-    }
+    const bool direct = direct_lines(a.q, a.ldq, BF16) && direct_lines(a.k, a.ldk, BF16) && direct_lines(a.v, a.ldv, BF16) && direct_lines(a.dout, a.lddo, BF16);
+    if constexpr (BF16 && D <= 128) return direct ? launch_beside<D, true>(a, s) : launch_beside<D, false>(a, s);
+    else return direct ? launch_parts<BF16, D, true>(a, s) : launch_parts<BF16, D, false>(a, s);
 }
 template <bool BF16>
 hipError_t launch_backward_by_width(const PackedArgs& a, hipStream_t s) {

@@ -266,8 +266,8 @@ static moe_status attn_check(moe_ctx* c, const char* fn, const moe_attn* t, moe:
     a->window = (int)(t->window < (1 << 23) ? t->window : 0);  // (none reaches further back)
     a->scale = t->scale;
     a->scale_log2 = (float)((double)t->scale * 1.4426950408889634);
-    // (a workgroup for each head of at least every 128 tokens, and two more a sequence: 2^31 at most)
-    CHECK((t->tokens_q / 128 + t->n) * t->q_heads < ((int64_t)1 << 31) / 256 && (t->tokens_k / 128 + t->n) * t->kv_heads < ((int64_t)1 << 31) / 256,
+    // (a workgroup of 256 threads for each head of every 32 tokens at most, and one more a sequence: 2^32 threads)
+    CHECK((t->tokens_q / 32 + t->n) * t->q_heads < ((int64_t)1 << 24) && (t->tokens_k / 32 + t->n) * t->kv_heads < ((int64_t)1 << 24),
           "%s: too many heads of too many tokens for one call", fn);
     return MOE_OK;
 }

@@ -209,10 +209,10 @@ __device__ inline void load_lds4(uint32_t lds, uint32_t offset, const void* base
         : "v"(offset), "s"(tile::uniform(base)), "{m0}"(__builtin_amdgcn_readfirstlane(lds))
         : "memory");
 }
-// Lines that may go straight into LDS: whole 16-byte chunks, a tile of 64 within 32 bits.
+// Lines that may go straight into LDS: whole 16-byte chunks, a tile of 128 within 32 bits.
 inline bool direct_lines(const void* p, int64_t ld, bool bf16) {
     const int64_t bytes = ld * (bf16 ? 2 : 4);
-    return (uintptr_t)p % 16 == 0 && bytes % 16 == 0 && bytes * 64 < ((int64_t)1 << 31);
+    return (uintptr_t)p % 16 == 0 && bytes % 16 == 0 && bytes * 128 < ((int64_t)1 << 31);
 }
 // Whether a tile in LDS holds a value that is not finite (this thread's part of it).
 template <bool BF16, int D, int R, int THREADS>
