@@ -46,16 +46,13 @@ __device__ inline Sequence sequence_of(const CachedArgs& a, int s) {
 // of equal size, none over two sequences.  Every wave finds it for itself, 64
 // sequences a pass.  A sequence that is cut has more than 1 / target of all steps,
 // so there are fewer than `target` of them, with fewer than 2 target chunks.
-__device__ inline int64_t wave_sum(int64_t v) {
-    for (int m = 1; m < 64; m *= 2) v += __shfl_xor((long long)v, m);
-    return v;
-}
-__device__ inline int wave_scan(int v) {  // inclusive
-    const int lane = threadIdx.x & 63;
-    for (int m = 1; m < 64; m *= 2) {
-        const int o = __shfl_up(v, m);
-        if (lane >= m) v += o;
-    }
+__device__ inline uint32_t wave_scan(uint32_t v) {  // inclusive, within the registers
+    v += __builtin_amdgcn_update_dpp(0u, v, 0x111, 0xF, 0xF, false);  // from 1, 2, 4 and 8 lanes before, within 16
+    v += __builtin_amdgcn_update_dpp(0u, v, 0x112, 0xF, 0xF, false);
+    v += __builtin_amdgcn_update_dpp(0u, v, 0x114, 0xF, 0xF, false);
+    v += __builtin_amdgcn_update_dpp(0u, v, 0x118, 0xF, 0xF, false);
+    v += __builtin_amdgcn_update_dpp(0u, v, 0x142, 0xA, 0xF, false);  // the row before's last, then the half's
+    v += __builtin_amdgcn_update_dpp(0u, v, 0x143, 0xC, 0xF, false);
     return v;
 }
 __device__ inline int chunk_steps(int64_t total, int target) {
@@ -72,7 +69,7 @@ __device__ inline bool find_chunk(const CachedArgs& a, int w, Chunk* out) {
     for (int base = 0; base < n; base += 64) {
         q = Sequence{};
         if (base + lane < n) q = sequence_of(a, base + lane);
-        total += wave_sum(q.steps);
+        total += (uint32_t)__builtin_amdgcn_readlane(wave_scan(q.steps), 63);  // (64 times 2^25 at most)
     }
     const int steps = __builtin_amdgcn_readfirstlane(chunk_steps(total, a.target));
     int chunks_before = 0, cut_before = 0, slots_before = 0;
@@ -82,7 +79,7 @@ __device__ inline bool find_chunk(const CachedArgs& a, int w, Chunk* out) {
             if (base + lane < n) q = sequence_of(a, base + lane);
         }
         const int of = (q.steps + steps - 1) / steps, cut = of > 1;
-        const int chunks = wave_scan(of), cuts = wave_scan(cut), slots = wave_scan(cut ? of : 0);
+        const int chunks = wave_scan(of), cuts = CUT ? wave_scan(cut) : 0, slots = wave_scan(cut ? of : 0);
         const int mine = CUT ? cut_before + cuts : chunks_before + chunks;
         const uint64_t past = __ballot(mine > w);
         if (past) {
@@ -102,7 +99,7 @@ __device__ inline bool find_chunk(const CachedArgs& a, int w, Chunk* out) {
             return true;
         }
         chunks_before += __builtin_amdgcn_readlane(chunks, 63);
-        cut_before += __builtin_amdgcn_readlane(cuts, 63);
+        if (CUT) cut_before += __builtin_amdgcn_readlane(cuts, 63);
         slots_before += __builtin_amdgcn_readlane(slots, 63);
     }
     return false;
@@ -143,7 +140,7 @@ template <int N> __device__ inline void terms_of(const float (&v)[8], bf16x8_t (
     }
 }
 
-// W = D / 32.  A workgroup takes one chunk of a sequence's tokens, one key head and
+// W = D / 32, JP = group / 32.  A workgroup takes one chunk of a sequence's tokens, one key head and
 // 16 rows (new tokens times the query heads of that key head); its waves take the
 // chunk's steps of 32 tokens in turn, each with sums of its own, joined at the end.
 // Keys are the left operand of the first product, K Q^T, so that a lane holds four
@@ -153,13 +150,13 @@ template <int N> __device__ inline void terms_of(const float (&v)[8], bf16x8_t (
 // the step is rounded to bf16 and multiplies code - 8, which lies about zero as the
 // values do; the rest, lowest + 8 steps, is added in fp32.  (With code itself the
 // result was 0.0031 off, its own rounding being 0.0016.)
-template <int W, bool BF16>
+template <int W, int JP, bool BF16>
 __global__ __launch_bounds__(kThreads, W <= 4 ? (BF16 ? 3 : 2) : W <= 6 ? 2 : 1) void cached_kernel(CachedArgs a) {
     constexpr int N = BF16 ? 1 : 3;  // bf16 terms of a factor
-    constexpr int D = 32 * W;
-    constexpr int kParams = (16 * W + 63) / 64;  // words of one tile's steps a lane loads
+    constexpr int D = 32 * W, G = W / JP;
+    constexpr int kParams = (16 * G + 63) / 64;  // words of one tile's steps a lane loads
     // a step's (step, lowest) pairs: of keys the step and lowest - 16 steps, of values the step and lowest + 8 steps
-    __shared__ __attribute__((aligned(16))) float pairs[kWaves][4][2][16 * W];
+    __shared__ __attribute__((aligned(16))) float pairs[kWaves][4][2][16 * G];
     __shared__ float joined[2][16][D + 4];
     __shared__ float2 stats[kWaves][16];
     if (blockIdx.x == gridDim.x - 1 && blockIdx.y == 0) check_offsets(a.batch.offsets, a.batch.n, a.batch.T, a.err);
@@ -181,7 +178,9 @@ __global__ __launch_bounds__(kThreads, W <= 4 ? (BF16 ? 3 : 2) : W <= 6 ? 2 : 1)
         const int to = live ? c.length - c.rows_new + token + 1 : INT32_MAX, from = live && a.window ? max(0, to - a.window) : 0;
 
         bf16x8_t q[W][N];
-        float q_sum[W];
+        float q_sum[G];
+#pragma unroll
+        for (int g = 0; g < G; g++) q_sum[g] = 0;
 #pragma unroll
         for (int j = 0; j < W; j++) {
             float v[8] = {0, 0, 0, 0, 0, 0, 0, 0};
@@ -190,15 +189,14 @@ __global__ __launch_bounds__(kThreads, W <= 4 ? (BF16 ? 3 : 2) : W <= 6 ? 2 : 1)
             float s = 0;
 #pragma unroll
             for (int e = 0; e < 8; e++) s += v[e];
-            q_sum[j] = cross_row_sum(s);
+            q_sum[j / JP] += cross_row_sum(s);
         }
         f32x4 out[2 * W];
-        float low[W], m = -kInf, l = 0;
+        float low[G], m = -kInf, l = 0;
 #pragma unroll
-        for (int j = 0; j < W; j++) {
-            out[2 * j] = out[2 * j + 1] = f32x4{0, 0, 0, 0};
-            low[j] = 0;
-        }
+        for (int j = 0; j < 2 * W; j++) out[j] = f32x4{0, 0, 0, 0};
+#pragma unroll
+        for (int g = 0; g < G; g++) low[g] = 0;
         bool bad = c.bad;
 
         struct Loaded { uint32_t k[2][W], v[2][W], steps[4][kParams]; };
@@ -223,7 +221,7 @@ __global__ __launch_bounds__(kThreads, W <= 4 ? (BF16 ? 3 : 2) : W <= 6 ? 2 : 1)
                 const uint32_t *ks = (const uint32_t*)(p + 256 * W), *vs = (const uint32_t*)(pv + 256 * W);
 #pragma unroll
                 for (int n = 0; n < kParams; n++) {
-                    const int w = (min(q4 + 4 * n, W - 1) >> kv.group_shift) * 16 + r16;
+                    const int w = min(q4 + 4 * n, G - 1) * 16 + r16;
                     d.steps[i][n] = ks[w];
                     d.steps[2 + i][n] = vs[w];
                 }
@@ -242,7 +240,7 @@ __global__ __launch_bounds__(kThreads, W <= 4 ? (BF16 ? 3 : 2) : W <= 6 ? 2 : 1)
             for (int x = 0; x < 4; x++)
 #pragma unroll
                 for (int n = 0; n < kParams; n++)
-                    if (lane + 64 * n < 16 * W) {
+                    if (lane + 64 * n < 16 * G) {
                         // past the sequence's end nothing has been written: step and lowest 0
                         const uint32_t w = step * kStep + 16 * (x & 1) + r16 < c.length ? now.steps[x][n] : 0u;
                         const float by = f16_bits_to_f32(w & 0xFFFF);
@@ -264,13 +262,17 @@ __global__ __launch_bounds__(kThreads, W <= 4 ? (BF16 ? 3 : 2) : W <= 6 ? 2 : 1)
 #pragma unroll
             for (int i = 0; i < 2; i++)
 #pragma unroll
-                for (int j = 0; j < W; j++) {
-                    const u32x4 w = {codes16(now.k[i][j], 0, masks), codes16(now.k[i][j], 1, masks), codes16(now.k[i][j], 2, masks), codes16(now.k[i][j], 3, masks)};
-                    const f32x4 r = product<N>(__builtin_bit_cast(bf16x8_t, w), q[j], f32x4{0, 0, 0, 0});
-                    const int group = 16 * j + 4 * q4;
+                for (int g = 0; g < G; g++) {
+                    f32x4 r = {0, 0, 0, 0};
+#pragma unroll
+                    for (int j = g * JP; j < (g + 1) * JP; j++) {
+                        const u32x4 w = {codes16(now.k[i][j], 0, masks), codes16(now.k[i][j], 1, masks), codes16(now.k[i][j], 2, masks), codes16(now.k[i][j], 3, masks)};
+                        r = product<N>(__builtin_bit_cast(bf16x8_t, w), q[j], r);
+                    }
+                    const int group = 16 * g + 4 * q4;
                     const f32x4 by = *(const f32x4*)&pairs[wave][i][0][group], less = *(const f32x4*)&pairs[wave][i][1][group];
 #pragma unroll
-                    for (int e = 0; e < 4; e++) s[4 * i + e] = fmaf(by[e], r[e], fmaf(less[e], q_sum[j], s[4 * i + e]));
+                    for (int e = 0; e < 4; e++) s[4 * i + e] = fmaf(by[e], r[e], fmaf(less[e], q_sum[g], s[4 * i + e]));
                     __builtin_amdgcn_sched_barrier(0);
                 }
             const int at = step * kStep;
@@ -290,19 +292,20 @@ __global__ __launch_bounds__(kThreads, W <= 4 ? (BF16 ? 3 : 2) : W <= 6 ? 2 : 1)
 #pragma unroll
             for (int e = 1; e < 8; e++) top = fmaxf(top, s[e]);
             top = cross_row_max(top) * a.scale_log2;
+            // (followed only where exponentials would pass 2^8: sums in fp32 and factors in
+            // bf16 are as exact at any common scale)
             const float before = m;
-            m = fmaxf(m, top);
-            const float base = m == -kInf ? 0.f : m;
-            if (__any(m != before)) {
-                const float f = __builtin_amdgcn_exp2f(before - base);
+            const bool grown = top - before > 8.f;
+            if (__any(grown)) {
+                m = grown ? top : before;
+                const float f = grown ? __builtin_amdgcn_exp2f(before - top) : 1.f;
                 l *= f;
 #pragma unroll
-                for (int j = 0; j < W; j++) {
-                    out[2 * j] *= f;
-                    out[2 * j + 1] *= f;
-                    low[j] *= f;
-                }
+                for (int j = 0; j < 2 * W; j++) out[j] *= f;
+#pragma unroll
+                for (int g = 0; g < G; g++) low[g] *= f;
             }
+            const float base = m == -kInf ? 0.f : m;
             float p[8];
 #pragma unroll
             for (int e = 0; e < 8; e++) {
@@ -311,11 +314,11 @@ __global__ __launch_bounds__(kThreads, W <= 4 ? (BF16 ? 3 : 2) : W <= 6 ? 2 : 1)
             }
             auto values = [&](auto masked) {
 #pragma unroll
-                for (int j = 0; j < W; j++) {
+                for (int g = 0; g < G; g++) {
                     float scaled[8];
 #pragma unroll
                     for (int i = 0; i < 2; i++) {
-                        const int group = 16 * j + 4 * q4;
+                        const int group = 16 * g + 4 * q4;
                         const f32x4 by = *(const f32x4*)&pairs[wave][2 + i][0][group], middle = *(const f32x4*)&pairs[wave][2 + i][1][group];
 #pragma unroll
                         for (int e = 0; e < 4; e++) {
@@ -323,24 +326,27 @@ __global__ __launch_bounds__(kThreads, W <= 4 ? (BF16 ? 3 : 2) : W <= 6 ? 2 : 1)
                             if constexpr (masked.value) {  // a token that the row does not see adds nothing
                                 const bool on = seen >> (4 * i + e) & 1;
                                 scaled[4 * i + e] = on ? scaled[4 * i + e] : 0.f;
-                                low[j] = on ? fmaf(p[4 * i + e], middle[e], low[j]) : low[j];
+                                low[g] = on ? fmaf(p[4 * i + e], middle[e], low[g]) : low[g];
                             } else {
-                                low[j] = fmaf(p[4 * i + e], middle[e], low[j]);
+                                low[g] = fmaf(p[4 * i + e], middle[e], low[g]);
                             }
                         }
                     }
                     bf16x8_t b[N];
                     terms_of<N>(scaled, b);
-                    uint32_t w0 = now.v[0][j], w1 = now.v[1][j];
-                    if constexpr (masked.value) asm("" : "+v"(w0), "+v"(w1));  // (so that the two branches' codes are not made before them)
-                    const u32x4 lo = {codes16(w0, 0, masks), codes16(w0, 2, masks), codes16(w1, 0, masks), codes16(w1, 2, masks)};
-                    const u32x4 hi = {codes16(w0, 1, masks), codes16(w0, 3, masks), codes16(w1, 1, masks), codes16(w1, 3, masks)};
-                    const u32x4 bias = {0xC1C0C1C0u, 0xC1C0C1C0u, 0xC1C0C1C0u, 0xC1C0C1C0u};  // -24: code - 8 of 16 + code
-                    out[2 * j] = product<N>(__builtin_bit_cast(bf16x8_t, bias), b, out[2 * j]);
-                    out[2 * j + 1] = product<N>(__builtin_bit_cast(bf16x8_t, bias), b, out[2 * j + 1]);
-                    out[2 * j] = product<N>(__builtin_bit_cast(bf16x8_t, lo), b, out[2 * j]);
-                    out[2 * j + 1] = product<N>(__builtin_bit_cast(bf16x8_t, hi), b, out[2 * j + 1]);
-                    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+                    for (int j = g * JP; j < (g + 1) * JP; j++) {
+                        uint32_t w0 = now.v[0][j], w1 = now.v[1][j];
+                        if constexpr (masked.value) asm("" : "+v"(w0), "+v"(w1));  // (so that the two branches' codes are not made before them)
+                        const u32x4 lo = {codes16(w0, 0, masks), codes16(w0, 2, masks), codes16(w1, 0, masks), codes16(w1, 2, masks)};
+                        const u32x4 hi = {codes16(w0, 1, masks), codes16(w0, 3, masks), codes16(w1, 1, masks), codes16(w1, 3, masks)};
+                        const u32x4 bias = {0xC1C0C1C0u, 0xC1C0C1C0u, 0xC1C0C1C0u, 0xC1C0C1C0u};  // -24: code - 8 of 16 + code
+                        out[2 * j] = product<N>(__builtin_bit_cast(bf16x8_t, bias), b, out[2 * j]);
+                        out[2 * j + 1] = product<N>(__builtin_bit_cast(bf16x8_t, bias), b, out[2 * j + 1]);
+                        out[2 * j] = product<N>(__builtin_bit_cast(bf16x8_t, lo), b, out[2 * j]);
+                        out[2 * j + 1] = product<N>(__builtin_bit_cast(bf16x8_t, hi), b, out[2 * j + 1]);
+                        __builtin_amdgcn_sched_barrier(0);
+                    }
                 }
             };
             if (all_seen || !__any(!fine)) values(std::false_type{});
@@ -362,11 +368,9 @@ __global__ __launch_bounds__(kThreads, W <= 4 ? (BF16 ? 3 : 2) : W <= 6 ? 2 : 1)
         for (int w = 0; w < kWaves; w++) sum += stats[w][r16].y * __builtin_amdgcn_exp2f(stats[w][r16].x - base);
         const float f = __builtin_amdgcn_exp2f(m - base);
 #pragma unroll
-        for (int j = 0; j < W; j++) {
-            const float add = cross_row_sum(low[j]);
+        for (int g = 0; g < G; g++) low[g] = cross_row_sum(low[g]);
 #pragma unroll
-            for (int h = 0; h < 2; h++) out[2 * j + h] = (out[2 * j + h] + add) * f;
-        }
+        for (int j = 0; j < 2 * W; j++) out[j] = (out[j] + low[j / 2 / JP]) * f;
 #pragma unroll
         for (int half = 2; half >= 1; half /= 2) {
             if (wave >= half && wave < 2 * half)
@@ -396,75 +400,95 @@ __global__ __launch_bounds__(kThreads, W <= 4 ? (BF16 ? 3 : 2) : W <= 6 ? 2 : 1)
     }
 }
 
-// Rows of the sequences that were cut: their chunks' sums, in the chunks' order.
-// A workgroup takes a row at a time, each of its waves every fourth chunk.
-template <int W, bool BF16>
-__global__ __launch_bounds__(kThreads) void cached_join_kernel(CachedArgs a) {
-    constexpr int D = 32 * W, kEach = (D + 63) / 64;
-    __shared__ float sums[kWaves][D];
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+// Rows of the sequences that were cut: their chunks' sums, in the chunks' order.  Rows
+// of up to 16 chunks are taken by a wave each, with more by a workgroup, each of its
+// waves every 16th chunk: a row has up to `target` of them, of D fp32 values, and they
+// are read at once.
+constexpr int kJoinWaves = 16, kJoinThreads = 64 * kJoinWaves;
+template <bool BF16>
+__global__ __launch_bounds__(kJoinThreads) void cached_join_kernel(CachedArgs a) {
+    __shared__ float sums[kJoinWaves][256];
+    const int D = a.cache.D, lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     Chunk c;
     if (!find_chunk<true>(a, blockIdx.x, &c)) return;
     const int64_t per_chunk = (int64_t)a.batch.most_new * a.q_heads;
-    for (int row = blockIdx.y; row < c.rows_new * a.q_heads; row += gridDim.y) {
+    const int rows = c.rows_new * a.q_heads, d0 = min(4 * lane, D - 4);  // (four channels a lane, past the last the last again)
+    auto join = [&](int row, int first, int every, float* sum) -> f32x4 {  // this wave's chunks, to the row's scale
         const int64_t at = (int64_t)c.slot * per_chunk + row;
-        float m = -kInf;
+        float m = -kInf, l = 0;
         for (int i = lane; i < c.of; i += 64) m = fmaxf(m, a.part_ml[at + i * per_chunk].x);
 #pragma unroll
         for (int x = 1; x < 64; x *= 2) m = fmaxf(m, __shfl_xor(m, x));
         const float base = m == -kInf ? 0.f : m;
-        float sum = 0, l = 0;
-        for (int i = 0; i < c.of; i += 64) {
-            if (i + lane < c.of) {
-                const float2 ml = a.part_ml[at + (i + lane) * per_chunk];
-                l += ml.y * __builtin_amdgcn_exp2f(ml.x - base);
-            }
+        for (int i = lane; i < c.of; i += 64) {
+            const float2 ml = a.part_ml[at + i * per_chunk];
+            l += ml.y * __builtin_amdgcn_exp2f(ml.x - base);
         }
-        sum = seg_sum<64>(l);
-        float v[kEach];
-#pragma unroll
-        for (int k = 0; k < kEach; k++) v[k] = 0;
+        *sum = seg_sum<64>(l);
+        f32x4 v = {0, 0, 0, 0};
 #pragma unroll 4
-        for (int i = wave; i < c.of; i += kWaves) {
+        for (int i = first; i < c.of; i += every) {
             const float f = __builtin_amdgcn_exp2f(a.part_ml[at + i * per_chunk].x - base);
-#pragma unroll
-            for (int k = 0; k < kEach; k++)
-                if (lane + 64 * k < D) v[k] = fmaf(f, a.part[(at + i * per_chunk) * D + lane + 64 * k], v[k]);
+            v += f * *(const f32x4*)&a.part[(at + i * per_chunk) * D + d0];
         }
-#pragma unroll
-        for (int k = 0; k < kEach; k++)
-            if (lane + 64 * k < D) sums[wave][lane + 64 * k] = v[k];
-        __syncthreads();
+        return v;
+    };
+    auto out_at = [&](int row) {
         const int token = row / a.q_heads, q_head = row - token * a.q_heads;
-        for (int d = threadIdx.x; d < D; d += kThreads) {
+        return (int64_t)(c.begin + token) * a.ldo + (int64_t)q_head * D;
+    };
+    if (c.of <= kJoinWaves) {
+        for (int row = blockIdx.y * kJoinWaves + wave; row < rows; row += gridDim.y * kJoinWaves) {
+            float sum;
+            const f32x4 v = join(row, 0, 1, &sum);
+            if (4 * lane < D)
+#pragma unroll
+                for (int e = 0; e < 4; e++) store1<BF16>(a.out, out_at(row) + d0 + e, v[e] / sum);
+        }
+        return;
+    }
+    for (int row = blockIdx.y; row < rows; row += gridDim.y) {
+        float sum;
+        const f32x4 v = join(row, wave, kJoinWaves, &sum);
+        if (4 * lane < D) *(f32x4*)&sums[wave][d0] = v;
+        __syncthreads();
+        if (threadIdx.x < D) {
             float o = 0;
 #pragma unroll
-            for (int w = 0; w < kWaves; w++) o += sums[w][d];
-            store1<BF16>(a.out, (int64_t)(c.begin + token) * a.ldo + (int64_t)q_head * D + d, o / sum);
+            for (int w = 0; w < kJoinWaves; w++) o += sums[w][threadIdx.x];
+            store1<BF16>(a.out, out_at(row) + threadIdx.x, o / sum);
         }
         __syncthreads();
     }
 }
 
-template <int W, bool BF16>
+template <int W, int JP, bool BF16>
 hipError_t launch(const CachedArgs& a, int split, hipStream_t s) {
     const dim3 grid(a.batch.n + (split ? a.target : 0), a.cache.heads * a.row_tiles);
-    hipLaunchKernelGGL((cached_kernel<W, BF16>), grid, dim3(kThreads), 0, s, a);
+    hipLaunchKernelGGL((cached_kernel<W, JP, BF16>), grid, dim3(kThreads), 0, s, a);
     if (split) {
-        const int rows = a.batch.most_new * a.q_heads;
-        const int share = rows < 4096 / a.target ? rows : 4096 / a.target > 1 ? 4096 / a.target : 1;
-        hipLaunchKernelGGL((cached_join_kernel<W, BF16>), dim3(a.target, share), dim3(kThreads), 0, s, a);
+        // (fewer than `target` sequences are cut)
+        const int cut = a.batch.n < a.target ? a.batch.n : a.target, rows = a.batch.most_new * a.q_heads, share = 512 / cut;
+        hipLaunchKernelGGL((cached_join_kernel<BF16>), dim3(cut, rows < share ? rows : share < 1 ? 1 : share), dim3(kJoinThreads), 0, s, a);
     }
     return hipGetLastError();
+}
+template <int W, bool BF16>
+hipError_t launch_by_group(const CachedArgs& a, int split, hipStream_t s) {
+    if constexpr (W % 2 == 0)
+        if (a.cache.group_shift == 1) return launch<W, 2, BF16>(a, split, s);
+    if constexpr (W % 4 == 0)
+        if (a.cache.group_shift == 2) return launch<W, 4, BF16>(a, split, s);
+    return launch<W, 1, BF16>(a, split, s);
 }
 template <bool BF16>
 hipError_t launch_by_width(const CachedArgs& a, int split, hipStream_t s) {
     switch (a.cache.words) {
-        case 2: return launch<2, BF16>(a, split, s);
-        case 3: return launch<3, BF16>(a, split, s);
-        case 4: return launch<4, BF16>(a, split, s);
-        case 6: return launch<6, BF16>(a, split, s);
-        default: return launch<8, BF16>(a, split, s);
+        case 2: return launch_by_group<2, BF16>(a, split, s);
+        case 3: return launch_by_group<3, BF16>(a, split, s);
+        case 4: return launch_by_group<4, BF16>(a, split, s);
+        case 6: return launch_by_group<6, BF16>(a, split, s);
+        default: return launch_by_group<8, BF16>(a, split, s);
     }
 }
 
