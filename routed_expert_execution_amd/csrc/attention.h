@@ -124,14 +124,14 @@ struct CachedArgs {
     int window;                   // 0: none
     void* out;
     int64_t ldo;
-    int target;                   // into how many chunks the call is cut, about
-    int row_tiles;                // gridDim.y / heads
+    int places, rounds, target;   // chunks the card takes at a time, rounds of them at most; into how many the call is cut at most, about
+    int row_tiles;                // workgroups that share a chunk's rows of one key head
     float* part;                  // [2 target][most_new * q_heads][D]
     float2* part_ml;              // [2 target][most_new * q_heads] running maximum and sum
     int* err;
 };
 // How a call is cut, by sizes alone.
-struct CachedPlan { int target, row_tiles, tile_rows, split; size_t bytes; };
+struct CachedPlan { int places, rounds, target, row_tiles, tile_rows, split; size_t bytes; };
 CachedPlan cached_plan(const KvGeom& g, int n, int most_new, int max_pages, int q_heads, int bf16);
 hipError_t launch_cached(const CachedArgs& a, int split, hipStream_t s);
 

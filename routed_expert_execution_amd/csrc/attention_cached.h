@@ -55,7 +55,10 @@ __device__ inline uint32_t wave_scan(uint32_t v) {  // inclusive, within the reg
     v += __builtin_amdgcn_update_dpp(0u, v, 0x143, 0xC, 0xF, false);
     return v;
 }
-__device__ inline int chunk_steps(int64_t total, int target) {
+__device__ inline int chunk_steps(int64_t total, const CachedArgs& a) {
+    // a chunk for each place of the card, or a few where there is work for several
+    // rounds: the last of them leaves less of the card idle
+    const int64_t rounds = min(max(total * a.row_tiles / ((int64_t)a.places * 24), (int64_t)1), (int64_t)a.rounds), target = a.places * rounds;
     const int64_t c = (total + target - 1) / target;
     return (int)((max(c, (int64_t)1) + kWaves - 1) / kWaves * kWaves);
 }
@@ -71,7 +74,7 @@ __device__ inline bool find_chunk(const CachedArgs& a, int w, Chunk* out) {
         if (base + lane < n) q = sequence_of(a, base + lane);
         total += (uint32_t)__builtin_amdgcn_readlane(wave_scan(q.steps), 63);  // (64 times 2^25 at most)
     }
-    const int steps = __builtin_amdgcn_readfirstlane(chunk_steps(total, a.target));
+    const int steps = __builtin_amdgcn_readfirstlane(chunk_steps(total, a));
     int chunks_before = 0, cut_before = 0, slots_before = 0;
     for (int base = 0; base < n; base += 64) {
         if (n > 64) {
@@ -159,23 +162,65 @@ __global__ __launch_bounds__(kThreads, W <= 4 ? (BF16 ? 3 : 2) : W <= 6 ? 2 : 1)
     __shared__ __attribute__((aligned(16))) float pairs[kWaves][4][2][16 * G];
     __shared__ float joined[2][16][D + 4];
     __shared__ float2 stats[kWaves][16];
-    if (blockIdx.x == gridDim.x - 1 && blockIdx.y == 0) check_offsets(a.batch.offsets, a.batch.n, a.batch.T, a.err);
+    if (blockIdx.x == gridDim.x - 1) check_offsets(a.batch.offsets, a.batch.n, a.batch.T, a.err);
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), r16 = lane & 15, q4 = lane >> 4;
-    Chunk c;
-    if (!find_chunk<false>(a, blockIdx.x, &c)) return;
+    // (all of a chunk's workgroups side by side: those of chunks that there are not come last)
     const KvView& kv = a.cache;
-    const int head = blockIdx.y % kv.heads, rows = c.rows_new * a.per_head;
+    const int units = kv.heads * a.row_tiles, unit = blockIdx.x % units, head = unit % kv.heads;
+    Chunk c;
+    if (!find_chunk<false>(a, blockIdx.x / units, &c)) return;
+    const int rows = c.rows_new * a.per_head;
     if (c.bad && threadIdx.x == 0) atomicOr(a.err, kErrCache);
     const CodeMasks masks = code_masks();
     const int32_t* table = a.batch.pages + (int64_t)c.seq * a.batch.max_pages;
     const int last_step = c.first + c.steps;
+    const uint32_t head_bytes = (uint32_t)kv.tile_bytes << (kv.page_shift - 4), page_bytes = head_bytes * kv.heads;
+    const uint8_t* heads_at = kv.data + (uint64_t)head * head_bytes;
 
 #pragma unroll 1
-    for (int tile = blockIdx.y / kv.heads; tile * 16 < rows; tile += a.row_tiles) {
+    for (int tile = unit / kv.heads; tile * 16 < rows; tile += a.row_tiles) {
         const int row = tile * 16 + r16, token = row / a.per_head, q_head = head * a.per_head + row - token * a.per_head;
         const bool live = row < rows;
         // the row sees places from .. to - 1 (one past the last row all of them: it masks no step, and nothing of it is stored)
         const int to = live ? c.length - c.rows_new + token + 1 : INT32_MAX, from = live && a.window ? max(0, to - a.window) : 0;
+
+        // (the first step's tokens on their way before the queries are waited for)
+        bool bad = c.bad;
+
+        struct Loaded { uint32_t k[2][W], v[2][W], steps[4][kParams]; };
+        auto page_of = [&](int step, int i) -> int {  // wave-uniform
+            const int at = step * kStep + 16 * i;
+            return step < last_step && at < c.length ? table[at >> kv.page_shift] : 0;
+        };
+        auto load = [&](int step, const int (&pages)[2], Loaded& d) {
+#pragma unroll
+            for (int i = 0; i < 2; i++) {
+                const int at = step * kStep + 16 * i;
+                int page = pages[i];
+                if (page < 0 || page >= kv.pages) {
+                    bad = true;
+                    page = 0;
+                }
+                const uint32_t in = at & ((1 << kv.page_shift) - 1);
+                const uint8_t* p = heads_at + (uint64_t)(uint32_t)page * page_bytes + (in >> 4) * (uint32_t)kv.tile_bytes;
+                const uint8_t* pv = p + kv.tile_bytes / 2;
+                __builtin_memcpy(d.k[i], p + lane * 4 * W, 4 * W);
+                __builtin_memcpy(d.v[i], pv + lane * 4 * W, 4 * W);
+                const uint32_t *ks = (const uint32_t*)(p + 256 * W), *vs = (const uint32_t*)(pv + 256 * W);
+#pragma unroll
+                for (int n = 0; n < kParams; n++) {
+                    const int w = min(q4 + 4 * n, G - 1) * 16 + r16;
+                    d.steps[i][n] = ks[w];
+                    d.steps[2 + i][n] = vs[w];
+                }
+            }
+        };
+        Loaded now, next;
+        int step = c.first + wave;
+        int pages[2] = {page_of(step, 0), page_of(step, 1)};
+        if (step < last_step) load(step, pages, now);
+        pages[0] = page_of(step + kWaves, 0);
+        pages[1] = page_of(step + kWaves, 1);
 
         bf16x8_t q[W][N];
         float q_sum[G];
@@ -197,42 +242,6 @@ __global__ __launch_bounds__(kThreads, W <= 4 ? (BF16 ? 3 : 2) : W <= 6 ? 2 : 1)
         for (int j = 0; j < 2 * W; j++) out[j] = f32x4{0, 0, 0, 0};
 #pragma unroll
         for (int g = 0; g < G; g++) low[g] = 0;
-        bool bad = c.bad;
-
-        struct Loaded { uint32_t k[2][W], v[2][W], steps[4][kParams]; };
-        auto page_of = [&](int step, int i) -> int {  // wave-uniform
-            const int at = step * kStep + 16 * i;
-            return step < last_step && at < c.length ? table[at >> kv.page_shift] : 0;
-        };
-        auto load = [&](int step, const int (&pages)[2], Loaded& d) {
-#pragma unroll
-            for (int i = 0; i < 2; i++) {
-                const int at = step * kStep + 16 * i;
-                int page = pages[i];
-                if (page < 0 || page >= kv.pages) {
-                    bad = true;
-                    page = 0;
-                }
-                const int in = at & ((1 << kv.page_shift) - 1);
-                const uint8_t* p = kv.data + (((int64_t)page * kv.heads + head) * (1 << (kv.page_shift - 4)) + (in >> 4)) * kv.tile_bytes;
-                const uint8_t* pv = p + kv.tile_bytes / 2;
-                __builtin_memcpy(d.k[i], p + lane * 4 * W, 4 * W);
-                __builtin_memcpy(d.v[i], pv + lane * 4 * W, 4 * W);
-                const uint32_t *ks = (const uint32_t*)(p + 256 * W), *vs = (const uint32_t*)(pv + 256 * W);
-#pragma unroll
-                for (int n = 0; n < kParams; n++) {
-                    const int w = min(q4 + 4 * n, G - 1) * 16 + r16;
-                    d.steps[i][n] = ks[w];
-                    d.steps[2 + i][n] = vs[w];
-                }
-            }
-        };
-        Loaded now, next;
-        int step = c.first + wave;
-        int pages[2] = {page_of(step, 0), page_of(step, 1)};
-        if (step < last_step) load(step, pages, now);
-        pages[0] = page_of(step + kWaves, 0);
-        pages[1] = page_of(step + kWaves, 1);
 #pragma unroll 1
         for (; step < last_step; step += kWaves) {
             bool fine = true;  // no value of the step is NaN
@@ -464,7 +473,7 @@ __global__ __launch_bounds__(kJoinThreads) void cached_join_kernel(CachedArgs a)
 
 template <int W, int JP, bool BF16>
 hipError_t launch(const CachedArgs& a, int split, hipStream_t s) {
-    const dim3 grid(a.batch.n + (split ? a.target : 0), a.cache.heads * a.row_tiles);
+    const dim3 grid((a.batch.n + (split ? a.target : 0)) * a.cache.heads * a.row_tiles);
     hipLaunchKernelGGL((cached_kernel<W, JP, BF16>), grid, dim3(kThreads), 0, s, a);
     if (split) {
         // (fewer than `target` sequences are cut)

@@ -225,9 +225,10 @@ moe_status moe_attention_cached(moe_ctx* c, const moe_kv_cache* cache, const moe
     CHECK(workspace && aligned_to(workspace, 256), "%s: workspace must be 256-byte aligned", fn);
     const size_t need = moe_attention_cached_workspace(cache, batch, q_heads);
     CHECK(workspace_bytes >= need, "%s: workspace of %zu bytes, %zu needed", fn, workspace_bytes, need);
+    const moe::CachedPlan p = moe::cached_plan(g, batch->n, (int)batch->most_new, batch->max_pages, q_heads, dtype == MOE_BF16);
+    CHECK(((int64_t)batch->n + p.target) * g.heads * p.row_tiles < (1 << 24), "%s: too many heads of too many sequences for one call", fn);
     if (moe_status st = need_device(c)) return st;
     if (T == 0 || batch->n == 0) return MOE_OK;
-    const moe::CachedPlan p = moe::cached_plan(g, batch->n, (int)batch->most_new, batch->max_pages, q_heads, dtype == MOE_BF16);
     a.cache = moe::kv_view(g, cache->data);
     a.q = q; a.ldq = T > 1 ? ldq : width;
     a.bf16 = dtype == MOE_BF16;
@@ -235,7 +236,7 @@ moe_status moe_attention_cached(moe_ctx* c, const moe_kv_cache* cache, const moe
     a.scale_log2 = (float)((double)scale * 1.4426950408889634);
     a.window = (int)(window < (1 << 30) ? window : 0);  // (none reaches further back)
     a.out = out; a.ldo = T > 1 ? ldo : width;
-    a.target = p.target; a.row_tiles = p.row_tiles;
+    a.places = p.places; a.rounds = p.rounds; a.target = p.target; a.row_tiles = p.row_tiles;
     a.part = (float*)workspace;
     a.part_ml = (float2*)(a.part + (size_t)2 * p.target * batch->most_new * q_heads * g.D);
     a.err = error_word(c);
