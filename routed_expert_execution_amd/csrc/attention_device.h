@@ -17,23 +17,31 @@ template <bool BF16> __device__ inline void store1(void* p, int64_t i, float v) 
     if (BF16) ((__bf16*)p)[i] = (__bf16)v;
     else ((float*)p)[i] = v;
 }
-// Eight elements from index i on (16 or 32 bytes, aligned as elements are).
-template <bool BF16> __device__ inline void load8(const void* p, int64_t i, float (&v)[8]) {
-    if (BF16) {
-        const Words4 w = *(const Words4*)((const uint16_t*)p + i);
+// Eight elements from index i on (16 or 32 bytes, aligned as elements are), as they lie
+// in memory and as values.
+template <bool BF16> struct Raw8 {
+    Words4 w[BF16 ? 1 : 2];
+    __device__ void load(const void* p, int64_t i) {
+        w[0] = *(const Words4*)((const char*)p + i * (BF16 ? 2 : 4));
+        if constexpr (!BF16) w[1] = *(const Words4*)((const float*)p + i + 4);
+    }
+    __device__ void get(float (&v)[8]) const {
 #pragma unroll
         for (int e = 0; e < 4; e++) {
-            v[2 * e] = __uint_as_float(w.v[e] << 16);
-            v[2 * e + 1] = __uint_as_float(w.v[e] & 0xFFFF0000u);
-        }
-    } else {
-#pragma unroll
-        for (int h = 0; h < 2; h++) {
-            const Words4 w = *(const Words4*)((const float*)p + i + 4 * h);
-#pragma unroll
-            for (int e = 0; e < 4; e++) v[4 * h + e] = __uint_as_float(w.v[e]);
+            if constexpr (BF16) {
+                v[2 * e] = __uint_as_float(w[0].v[e] << 16);
+                v[2 * e + 1] = __uint_as_float(w[0].v[e] & 0xFFFF0000u);
+            } else {
+                v[e] = __uint_as_float(w[0].v[e]);
+                v[4 + e] = __uint_as_float(w[1].v[e]);
+            }
         }
     }
+};
+template <bool BF16> __device__ inline void load8(const void* p, int64_t i, float (&v)[8]) {
+    Raw8<BF16> r;
+    r.load(p, i);
+    r.get(v);
 }
 template <bool BF16> __device__ inline void store8(void* p, int64_t i, const float (&v)[8]) {
     if (BF16) {

@@ -9,54 +9,74 @@
 namespace moe {
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 256, kTokens = 4;  // of a workgroup, where there are many tokens
 
-__device__ inline double shuffle_xor(double v, int mask) {
-    const uint64_t b = __builtin_bit_cast(uint64_t, v);
-    const uint32_t lo = __shfl_xor((int)(uint32_t)b, mask), hi = __shfl_xor((int)(uint32_t)(b >> 32), mask);
-    return __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
+// Reductions over a group's neighbouring threads (N = group / 8 of them, aligned), by
+// the partner exchanges of seg_sum.
+template <int CTRL> __device__ inline double dpp_f64(double v) { return __builtin_bit_cast(double, dpp_u64<CTRL>(__builtin_bit_cast(uint64_t, v))); }
+template <typename F> __device__ inline float over_group(float v, int n, F f) {
+    v = f(v, dpp_f<0xB1>(v));
+    v = f(v, dpp_f<0x4E>(v));
+    if (n > 4) v = f(v, dpp_f<0x141>(v));
+    if (n > 8) v = f(v, dpp_f<0x140>(v));
+    return v;
 }
 
-// Eight channels of a thread to codes, with the others of its group on the
-// neighbouring threads (group / 8 of them, aligned).  In 64 bits throughout: which
-// of two codes a value next to their border gets is then decided by the value and
-// not by roundings on the way, and 64 bits cost little beside the bytes.
+// Eight channels of a thread to codes.  Which of two values next to their border a step
+// or a code takes is decided in 64 bits, by the value and not by roundings on the way;
+// but only there, and 32 bits say where that is: the quotients are within 2^-21 of
+// theirs, relative, of 15 at most.
 // Returns eight codes, four bits each; *steps the word that stands for the group.
 __device__ inline uint32_t to_codes(const double (&x)[8], int group, uint32_t* steps) {
-    double lo = x[0], hi = x[0];
-    int fine = 1;
+    const int n = group / 8;
+    float xf[8], lo, hi;
+    bool fine = true;
 #pragma unroll
     for (int i = 0; i < 8; i++) {
-        lo = fmin(lo, x[i]);
-        hi = fmax(hi, x[i]);
-        fine &= (int)(fabs(x[i]) <= 65504.0);  // (false for a NaN)
+        xf[i] = (float)x[i];
+        lo = i ? fminf(lo, xf[i]) : xf[i];
+        hi = i ? fmaxf(hi, xf[i]) : xf[i];
+        fine &= fabs(x[i]) <= 65504.0;  // (false for a NaN)
     }
-    for (int m = 1; m < group / 8; m *= 2) {
-        lo = fmin(lo, shuffle_xor(lo, m));
-        hi = fmax(hi, shuffle_xor(hi, m));
-        fine &= __shfl_xor(fine, m);
+    lo = over_group(lo, n, [](float a, float b) { return fminf(a, b); });
+    hi = over_group(hi, n, [](float a, float b) { return fmaxf(a, b); });
+    const bool all_fine = over_group(fine ? 1.f : 0.f, n, [](float a, float b) { return fminf(a, b); }) != 0.f;
+    const _Float16 low16 = (_Float16)lo;  // (rounding keeps order: the fp32 of the lowest value)
+    const float low = (float)low16;
+    // the step, and whether its rounding to fp16 is certain: not within 2^-20 of it of a
+    // border, which lies half way between two fp16 values
+    float exact_step = (hi - low) / 15.0f;
+    const float slack = fabsf(exact_step) * 0x1p-20f + fabsf(low) * 0x1p-26f;
+    if (__any((_Float16)(exact_step - slack) != (_Float16)(exact_step + slack))) {
+        double top = x[0];
+#pragma unroll
+        for (int i = 1; i < 8; i++) top = fmax(top, x[i]);
+        top = fmax(top, dpp_f64<0xB1>(top));
+        top = fmax(top, dpp_f64<0x4E>(top));
+        if (n > 4) top = fmax(top, dpp_f64<0x141>(top));
+        if (n > 8) top = fmax(top, dpp_f64<0x140>(top));
+        exact_step = (float)((top - (double)low) / 15.0);
     }
-    if (!fine) {  // the whole group reads back as NaN
-        *steps = 0x7E007E00u;
-        return 0;
-    }
-    const _Float16 low16 = (_Float16)(float)lo;
-    const double low = (double)low16;
-    const _Float16 step16 = (_Float16)(float)((hi - low) / 15.0);
-    const double step = (double)step16;
-    *steps = (uint32_t)__builtin_bit_cast(uint16_t, step16) | (uint32_t)__builtin_bit_cast(uint16_t, low16) << 16;
-    if (!(step > 0.0)) return 0;
-    const float inverse = 1.0f / (float)step;
+    const _Float16 step16 = (_Float16)exact_step;
+    const float step = (float)step16;
+    // a group with a value that is none reads back as NaN
+    *steps = all_fine ? (uint32_t)__builtin_bit_cast(uint16_t, step16) | (uint32_t)__builtin_bit_cast(uint16_t, low16) << 16 : 0x7E007E00u;
+    const bool some = all_fine && step > 0.f;
+    const float inverse = some ? 1.0f / step : 0.f;
     uint32_t codes = 0;
 #pragma unroll
     for (int i = 0; i < 8; i++) {
-        // a guess that is off by one at most, then by what it leaves: halves go to the even code
-        const double d = x[i] - low;
-        int q = (int)rintf(fminf(fmaxf((float)d * inverse, 0.f), 15.f));
-        const double left = 2.0 * fma(-(double)q, step, d);
-        if (left > step || (left == step && (q & 1))) q++;
-        else if (left < -step || (left == -step && (q & 1))) q--;
-        codes |= (uint32_t)min(max(q, 0), 15) << (4 * i);
+        const float t = fminf(fmaxf((xf[i] - low) * inverse, 0.f), 15.f);
+        float q = rintf(t);
+        const bool near = some && fabsf(fabsf(t - q) - 0.5f) < 1e-4f;
+        if (__any(near)) {  // halves go to the even code
+            const double left = 2.0 * fma(-(double)q, (double)step, x[i] - (double)low);
+            const bool odd = (int)q & 1;
+            if (near && (left > (double)step || (left == (double)step && odd))) q += 1.f;
+            else if (near && (left < -(double)step || (left == -(double)step && odd))) q -= 1.f;
+            q = fminf(fmaxf(q, 0.f), 15.f);
+        }
+        codes |= (uint32_t)(int)(some ? q : 0.f) << (4 * i);
     }
     return codes;
 }
@@ -66,146 +86,188 @@ __device__ inline uint8_t* tile_at(const KvView& c, int page, int head, int in_p
 }
 __device__ inline int value_byte(int t) { return (t & 1) * 2 + (t >> 1 & 1); }  // place of token t % 4 in its word
 
-// The page and the place in it; false where there is none.
-__device__ inline bool find_page(const KvView& c, const KvBatchView& b, const TokenPlace& p, int* page, int* in_page) {
-    if (p.bad || p.place < 0 || p.place >= (int64_t)b.max_pages << c.page_shift) return false;
-    *page = b.pages[(int64_t)p.seq * b.max_pages + (p.place >> c.page_shift)];
-    *in_page = (int)(p.place & ((1 << c.page_shift) - 1));
-    return *page >= 0 && *page < c.pages;
+// What a workgroup knows of each of its tokens.
+struct TokenInfo { int place, page, in_page, has; };  // has: 0 no sequence, 1 one, 2 and a page
+__device__ inline TokenInfo info_of(const KvView& c, const KvBatchView& b, int token, int* err) {
+    TokenInfo t{};
+    TokenPlace p;
+    if (!find_token(b, token, &p)) {
+        if (p.bad && (threadIdx.x & 63) == 0) atomicOr(err, kErrCache);
+        return t;
+    }
+    t.has = 1;
+    t.place = (int)p.place;
+    if (!p.bad && p.place >= 0 && p.place < (int64_t)b.max_pages << c.page_shift) {
+        t.page = b.pages[(int64_t)p.seq * b.max_pages + (p.place >> c.page_shift)];
+        t.in_page = (int)(p.place & ((1 << c.page_shift) - 1));
+        if (t.page >= 0 && t.page < c.pages) t.has = 2;
+    }
+    if (t.has != 2 && (threadIdx.x & 63) == 0) atomicOr(err, kErrCache);
+    return t;
 }
 
-// One token a workgroup (gridDim.y of them share few tokens' heads): its angles
-// once into LDS, then eight channels a thread of keys, of values, and eight pairs
-// of queries.
+// The first token of a workgroup.  Tokens side by side share lines of the cache, which
+// is written a few bytes a token: where there are many tokens, workgroups that go to one
+// XCD (every eighth) take a run of them, so that its L2 has whole lines to write back.
+__device__ inline int first_token(int tokens) {
+    if (tokens == 1) return blockIdx.x;
+    const int per = gridDim.x / 8;  // (a multiple of 8 workgroups)
+    return (blockIdx.x % 8 * per + blockIdx.x / 8) * tokens;
+}
+
+// `tokens` tokens a workgroup (or gridDim.y workgroups for one, where tokens are few):
+// a wave finds each one's place; their angles once into LDS; then eight channels a
+// thread of keys, of values, and eight pairs of queries.  Bound by bytes in flight
+// (leaving out the codes' arithmetic, their stores or the cosines changes nothing):
+// five prompts, 32 query and 8 key heads of 128 in bf16, 85 us, 2.5 TB/s of all that is
+// read and written; 64 single tokens 6.5 us, the launch and one read after another.
 template <bool BF16>
-__global__ __launch_bounds__(kThreads) void kv_append_kernel(KvAppendArgs a) {
-    __shared__ double2 turns[128];
-    __shared__ float2 turns_q[128];
-    const int token = blockIdx.x;
-    if (token == (int)gridDim.x - 1 && blockIdx.y == 0) check_offsets(a.batch.offsets, a.batch.n, a.batch.T, a.err);
-    TokenPlace at;
-    if (!find_token(a.batch, token, &at)) {
-        if (at.bad && threadIdx.x == 0) atomicOr(a.err, kErrCache);
-        return;
-    }
-    int page = 0, in_page = 0;
-    const bool kept = find_page(a.cache, a.batch, at, &page, &in_page);
-    if (!kept && threadIdx.x == 0) atomicOr(a.err, kErrCache);
-    const RotaryView r = a.rotary;
-    if (r.freqs) {
-        const int position = a.positions ? a.positions[token] : (int)at.place;
-        for (int i = threadIdx.x; i < r.half; i += kThreads) {
-            double c, s;
-            turn_of(position, r.freqs[i], &c, &s);
-            c *= r.scale;
-            s *= r.scale;
-            turns[i] = make_double2(c, s);
-            turns_q[i] = make_float2((float)c, (float)s);
-        }
+__global__ __launch_bounds__(kThreads) void kv_append_kernel(KvAppendArgs a, int tokens) {
+    __shared__ double2 turns[kTokens][128];
+    __shared__ float2 turns_q[kTokens][128];
+    __shared__ TokenInfo infos[kTokens];
+    const int first = first_token(tokens), count = min(tokens, a.batch.T - first), wave = threadIdx.x >> 6;
+    if (blockIdx.x == gridDim.x - 1 && blockIdx.y == 0) check_offsets(a.batch.offsets, a.batch.n, a.batch.T, a.err);
+    if (wave < count) {
+        const TokenInfo t = info_of(a.cache, a.batch, first + wave, a.err);
+        if ((threadIdx.x & 63) == 0) infos[wave] = t;
     }
     __syncthreads();
+    const RotaryView r = a.rotary;
+    if (r.freqs) {
+        for (int i = threadIdx.x; i < count * r.half; i += kThreads) {
+            const int t = i / r.half, p = i - t * r.half;
+            double c, s;
+            turn_of(a.positions ? a.positions[first + t] : infos[t].place, r.freqs[p], &c, &s);
+            c *= r.scale;
+            s *= r.scale;
+            turns[t][p] = make_double2(c, s);
+            turns_q[t][p] = make_float2((float)c, (float)s);
+        }
+        __syncthreads();
+    }
     const KvView& c = a.cache;
     const int per_row = c.D / 8, keys = c.heads * per_row, group = 32 << c.group_shift;
     const int units = a.q ? rotate_units(r.half, c.D, a.q == a.q_out) : 0;
     const int total = 2 * keys + a.q_heads * units;
+    // A thread does the same unit of all tokens, and all of them are read before the
+    // first is worked on: a workgroup is bound by the time that a read takes.
     // (whole groups of channels lie on neighbouring threads: keys is a multiple of group / 8)
     for (int i = blockIdx.y * kThreads + threadIdx.x; i < total; i += gridDim.y * kThreads) {
         if (i >= 2 * keys) {
             const int h = (i - 2 * keys) / units, u = (i - 2 * keys) - h * units;
-            rotate_unit<BF16>(a.q, token * a.ldq + (int64_t)h * c.D, a.q_out, token * a.ldqo + (int64_t)h * c.D, c.D, r, u, turns_q);
+            RotateUnit<BF16> unit(r, c.D, u);
+#pragma unroll
+            for (int t = 0; t < kTokens; t++)
+                if (t < count && infos[t].has) unit.load(t, a.q, (first + t) * a.ldq + (int64_t)h * c.D);
+#pragma unroll
+            for (int t = 0; t < kTokens; t++)
+                if (t < count && infos[t].has) unit.finish(t, a.q, (first + t) * a.ldq + (int64_t)h * c.D, a.q_out, (first + t) * a.ldqo + (int64_t)h * c.D, turns_q[t]);
             continue;
         }
-        if (!kept) continue;
         const bool value = i >= keys;
         const int row = value ? i - keys : i, head = row / per_row, chunk = row - head * per_row, c0 = 8 * chunk;
         const void* p = value ? a.v : a.k;
-        const int64_t base = token * (value ? a.ldv : a.ldk) + (int64_t)head * c.D;
-        float own[8];
-        load8<BF16>(p, base + c0, own);
-        double x[8];
+        const int64_t ld = value ? a.ldv : a.ldk, in_row = (int64_t)head * c.D;
+        const bool turned = !value && r.freqs && c0 < 2 * r.half, halves = turned && !r.interleaved;
+        Raw8<BF16> own[kTokens], other[kTokens];  // the chunk, and its channels' partners
 #pragma unroll
-        for (int e = 0; e < 8; e++) x[e] = (double)own[e];
-        if (!value && r.freqs && c0 < 2 * r.half) {
-            if (r.interleaved) {
+        for (int t = 0; t < kTokens; t++)
+            if (t < count && infos[t].has == 2) {
+                own[t].load(p, (first + t) * ld + in_row + c0);
+                if (halves && r.half % 8 == 0) other[t].load(p, (first + t) * ld + in_row + (c0 < r.half ? c0 + r.half : c0 - r.half));
+            }
+#pragma unroll
+        for (int t = 0; t < kTokens; t++) {
+            if (t >= count || infos[t].has != 2) continue;
+            const TokenInfo info = infos[t];
+            float mine[8], partner[8];
+            own[t].get(mine);
+            double x[8];
+#pragma unroll
+            for (int e = 0; e < 8; e++) x[e] = (double)mine[e];
+            if (turned && r.interleaved) {
 #pragma unroll
                 for (int e = 0; e < 8; e += 2)
                     if (c0 + e < 2 * r.half) {
-                        const double2 t = turns[(c0 + e) / 2];
+                        const double2 w = turns[t][(c0 + e) / 2];
                         const double v0 = x[e], v1 = x[e + 1];
-                        x[e] = v0 * t.x - v1 * t.y;
-                        x[e + 1] = v0 * t.y + v1 * t.x;
+                        x[e] = v0 * w.x - v1 * w.y;
+                        x[e + 1] = v0 * w.y + v1 * w.x;
                     }
-            } else {
-                float other[8];  // the channels' partners
+            } else if (halves) {
                 if (r.half % 8 == 0) {
-                    load8<BF16>(p, base + (c0 < r.half ? c0 + r.half : c0 - r.half), other);
+                    other[t].get(partner);
                 } else {
 #pragma unroll
                     for (int e = 0; e < 8; e++) {
                         const int ch = c0 + e;
-                        other[e] = ch < 2 * r.half ? load1<BF16>(p, base + (ch < r.half ? ch + r.half : ch - r.half)) : 0.f;
+                        partner[e] = ch < 2 * r.half ? load1<BF16>(p, (first + t) * ld + in_row + (ch < r.half ? ch + r.half : ch - r.half)) : 0.f;
                     }
                 }
 #pragma unroll
                 for (int e = 0; e < 8; e++) {
                     const int ch = c0 + e;
                     if (ch < r.half) {
-                        const double2 t = turns[ch];
-                        x[e] = x[e] * t.x - (double)other[e] * t.y;
+                        const double2 w = turns[t][ch];
+                        x[e] = x[e] * w.x - (double)partner[e] * w.y;
                     } else if (ch < 2 * r.half) {
-                        const double2 t = turns[ch - r.half];
-                        x[e] = (double)other[e] * t.y + x[e] * t.x;
+                        const double2 w = turns[t][ch - r.half];
+                        x[e] = (double)partner[e] * w.y + x[e] * w.x;
                     }
                 }
             }
-        }
-        uint32_t steps;
-        const uint32_t codes = to_codes(x, group, &steps);
-        uint8_t* tile = tile_at(c, page, head, in_page) + (value ? c.tile_bytes / 2 : 0);
-        const int in = in_page & 15, j = chunk >> 2;
-        if (chunk % (group / 8) == 0) ((uint32_t*)(tile + 256 * c.words))[c0 / group * 16 + in] = steps;
-        if (!value) {
-            uint32_t w = 0;
+            uint32_t steps;
+            const uint32_t codes = to_codes(x, group, &steps);
+            uint8_t* tile = tile_at(c, info.page, head, info.in_page) + (value ? c.tile_bytes / 2 : 0);
+            const int in = info.in_page & 15, j = chunk >> 2;
+            if (chunk % (group / 8) == 0) ((uint32_t*)(tile + 256 * c.words))[c0 / group * 16 + in] = steps;
+            // channels 16 apart share a byte of the values: the threads of each pair write half of theirs
+            const uint32_t theirs = __builtin_amdgcn_update_dpp(0u, codes, 0x4E, 0xF, 0xF, false);
+            if (!value) {
+                uint32_t w = 0;
 #pragma unroll
-            for (int e = 0; e < 8; e++) w |= (codes >> (4 * e) & 15) << (4 * (e >> 1) + 16 * (e & 1));
-            ((uint32_t*)tile)[((chunk & 3) * 16 + in) * c.words + j] = w;
-        } else {
-            // channels 16 apart share a byte: the threads of each pair write half of theirs
-            const uint32_t theirs = __shfl_xor((int)codes, 2);
-            const bool high = chunk & 2;
-            const uint32_t lo = high ? theirs : codes, hi = high ? codes : theirs;
+                for (int e = 0; e < 8; e++) w |= (codes >> (4 * e) & 15) << (4 * (e >> 1) + 16 * (e & 1));
+                ((uint32_t*)tile)[((chunk & 3) * 16 + in) * c.words + j] = w;
+            } else {
+                const bool high = chunk & 2;
+                const uint32_t lo = high ? theirs : codes, hi = high ? codes : theirs;
 #pragma unroll
-            for (int e = 0; e < 4; e++) {
-                const int k = e + (high ? 4 : 0), n = 8 * (chunk & 1) + k;
-                tile[(((in >> 2) * 16 + n) * c.words + j) * 4 + value_byte(in & 3)] =
-                    (uint8_t)((lo >> (4 * k) & 15) | (hi >> (4 * k) & 15) << 4);
+                for (int e = 0; e < 4; e++) {
+                    const int k = e + (high ? 4 : 0), n = 8 * (chunk & 1) + k;
+                    tile[(((in >> 2) * 16 + n) * c.words + j) * 4 + value_byte(in & 3)] =
+                        (uint8_t)((lo >> (4 * k) & 15) | (hi >> (4 * k) & 15) << 4);
+                }
             }
         }
     }
 }
 
-// The values kept for each packed token, eight channels a thread.
+// The values kept for each packed token, eight channels a thread: the five prompts'
+// 20 us, the single tokens' 3 us.
 template <bool BF16>
-__global__ __launch_bounds__(kThreads) void kv_read_kernel(KvReadArgs a) {
-    const int token = blockIdx.x;
-    if (token == (int)gridDim.x - 1 && blockIdx.y == 0) check_offsets(a.batch.offsets, a.batch.n, a.batch.T, a.err);
-    TokenPlace at;
-    if (!find_token(a.batch, token, &at)) {
-        if (at.bad && threadIdx.x == 0) atomicOr(a.err, kErrCache);
-        return;
+__global__ __launch_bounds__(kThreads) void kv_read_kernel(KvReadArgs a, int tokens) {
+    __shared__ TokenInfo infos[kTokens];
+    const int first = first_token(tokens), count = min(tokens, a.batch.T - first), wave = threadIdx.x >> 6;
+    if (blockIdx.x == gridDim.x - 1 && blockIdx.y == 0) check_offsets(a.batch.offsets, a.batch.n, a.batch.T, a.err);
+    if (wave < count) {
+        const TokenInfo t = info_of(a.cache, a.batch, first + wave, a.err);
+        if ((threadIdx.x & 63) == 0) infos[wave] = t;
     }
-    int page = 0, in_page = 0;
-    const bool kept = find_page(a.cache, a.batch, at, &page, &in_page);
-    if (!kept && threadIdx.x == 0) atomicOr(a.err, kErrCache);
+    __syncthreads();
     const KvView& c = a.cache;
     const int per_row = c.D / 8, keys = c.heads * per_row;
-    for (int i = blockIdx.y * kThreads + threadIdx.x; i < 2 * keys; i += gridDim.y * kThreads) {
-        const bool value = i >= keys;
-        const int row = value ? i - keys : i, head = row / per_row, chunk = row - head * per_row;
-        const int in = in_page & 15, j = chunk >> 2;
+    for (int i = blockIdx.y * kThreads + threadIdx.x; i < count * 2 * keys; i += gridDim.y * kThreads) {
+        const int t = i / (2 * keys), u = i - t * 2 * keys;
+        const TokenInfo info = infos[t];
+        const int64_t token = first + t;
+        if (info.has == 0) continue;
+        const bool value = u >= keys;
+        const int row = value ? u - keys : u, head = row / per_row, chunk = row - head * per_row;
+        const int in = info.in_page & 15, j = chunk >> 2;
         float x[8];
-        if (kept) {
-            const uint8_t* tile = tile_at(c, page, head, in_page) + (value ? c.tile_bytes / 2 : 0);
+        if (info.has == 2) {
+            const uint8_t* tile = tile_at(c, info.page, head, info.in_page) + (value ? c.tile_bytes / 2 : 0);
             const uint32_t steps = ((const uint32_t*)(tile + 256 * c.words))[(chunk >> (2 + c.group_shift)) * 16 + in];
             const float step = f16_bits_to_f32(steps & 0xFFFF), low = f16_bits_to_f32(steps >> 16);
             if (!value) {
@@ -228,25 +290,32 @@ __global__ __launch_bounds__(kThreads) void kv_read_kernel(KvReadArgs a) {
     }
 }
 
-// Workgroups for one token's work: enough to fill the card where there are few tokens.
-int share_of(int total, int T) {
-    return std::max(1, std::min((total + kThreads - 1) / kThreads, 1024 / std::max(1, T)));
+// Tokens a workgroup takes, and workgroups that share them: enough to fill the card
+// where there are few.  8192 tokens of 32 query and 8 key heads of 128: four tokens each
+// 56 us, one 70; 2048 of 8 and 2 of 64: four 17 us, one 13.
+dim3 grid_of(int total, int T, int* tokens) {
+    *tokens = T >= 4096 ? kTokens : 1;
+    const int share = std::max(1, std::min((total + kThreads - 1) / kThreads, 1024 / T));
+    const int groups = (T + *tokens - 1) / *tokens;
+    return dim3(*tokens == 1 ? groups : (groups + 7) / 8 * 8, share);
 }
 
 }  // namespace
 
 hipError_t launch_kv_append(const KvAppendArgs& a, hipStream_t s) {
     const int total = 2 * a.cache.heads * a.cache.D / 8 + (a.q ? a.q_heads * rotate_units(a.rotary.half, a.cache.D, a.q == a.q_out) : 0);
-    const dim3 grid(a.batch.T, share_of(total, a.batch.T));
-    if (a.bf16) hipLaunchKernelGGL((kv_append_kernel<true>), grid, dim3(kThreads), 0, s, a);
-    else hipLaunchKernelGGL((kv_append_kernel<false>), grid, dim3(kThreads), 0, s, a);
+    int tokens;
+    const dim3 grid = grid_of(total, a.batch.T, &tokens);
+    if (a.bf16) hipLaunchKernelGGL((kv_append_kernel<true>), grid, dim3(kThreads), 0, s, a, tokens);
+    else hipLaunchKernelGGL((kv_append_kernel<false>), grid, dim3(kThreads), 0, s, a, tokens);
     return hipGetLastError();
 }
 
 hipError_t launch_kv_read(const KvReadArgs& a, hipStream_t s) {
-    const dim3 grid(a.batch.T, share_of(2 * a.cache.heads * a.cache.D / 8, a.batch.T));
-    if (a.bf16) hipLaunchKernelGGL((kv_read_kernel<true>), grid, dim3(kThreads), 0, s, a);
-    else hipLaunchKernelGGL((kv_read_kernel<false>), grid, dim3(kThreads), 0, s, a);
+    int tokens;
+    const dim3 grid = grid_of(2 * a.cache.heads * a.cache.D / 8, a.batch.T, &tokens);
+    if (a.bf16) hipLaunchKernelGGL((kv_read_kernel<true>), grid, dim3(kThreads), 0, s, a, tokens);
+    else hipLaunchKernelGGL((kv_read_kernel<false>), grid, dim3(kThreads), 0, s, a, tokens);
     return hipGetLastError();
 }
 

