@@ -660,11 +660,13 @@ moe_status moe_kv_read(moe_ctx* ctx, const moe_kv_cache* cache, const moe_kv_bat
  * q, out: device [tokens, q_heads, head_dim] (dtype); q_heads is a multiple of the
  * cache's heads, the query heads of a key head lie side by side.  scale > 0, finite.
  * Sums and softmax are fp32; q and the cache's codes enter unrounded, p times the
- * step in bf16 (q bf16) or as three bf16 terms (q fp32).  Every row of a sequence
- * that reads a page outside the cache, or that cannot be (a length below its new
- * tokens or above its pages, more than most_new of them) becomes NaN.  workspace:
- * device, 256-byte aligned, moe_attention_cached_workspace() bytes or more, used
- * until the call's work is done; calls that may run at the same time need one each. */
+ * step in bf16 (q bf16) or as three bf16 terms (q fp32).  Rows of a sequence that
+ * cannot be (a length below its new tokens or above its pages, more than most_new of
+ * them) and rows that see a place on a page outside the cache become NaN; other rows of
+ * a sequence with such a page may.  (tokens * q_heads / heads / 16 + n) * (max_pages *
+ * page_tokens / 128), each rounded up, stays below 2^31.  workspace: device, 256-byte
+ * aligned, moe_attention_cached_workspace() bytes or more, used until the call's work
+ * is done; calls that may run at the same time need one each. */
 size_t moe_attention_cached_workspace(const moe_kv_cache* cache, const moe_kv_batch* batch, int32_t q_heads); /* 0: not valid */
 moe_status moe_attention_cached(moe_ctx* ctx, const moe_kv_cache* cache, const moe_kv_batch* batch, const void* q, int64_t ldq,
                                 int32_t dtype, int32_t q_heads, float scale, int64_t window, void* out, int64_t ldo,

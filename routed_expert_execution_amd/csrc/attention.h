@@ -124,16 +124,17 @@ struct CachedArgs {
     int window;                   // 0: none
     void* out;
     int64_t ldo;
-    int places, rounds, target;   // chunks the card takes at a time, rounds of them at most; into how many the call is cut at most, about
-    int row_tiles;                // workgroups that share a chunk's rows of one key head
-    float* part;                  // [2 target][most_new * q_heads][D]
-    float2* part_ml;              // [2 target][most_new * q_heads] running maximum and sum
+    int places, part_rows;        // runs that the call's work is cut into; rows kept of a part of a row tile
+    float* part;                  // [2 places][cache.heads][part_rows][D]
+    float2* part_ml;              // [2 places][cache.heads][part_rows] running maximum and sum
     int* err;
 };
 // How a call is cut, by sizes alone.
-struct CachedPlan { int places, rounds, target, row_tiles, tile_rows, split; size_t bytes; };
-CachedPlan cached_plan(const KvGeom& g, int n, int most_new, int max_pages, int q_heads, int bf16);
-hipError_t launch_cached(const CachedArgs& a, int split, hipStream_t s);
+struct CachedPlan { int places, part_rows, split; int64_t tiles, line; size_t bytes; };
+CachedPlan cached_plan(const KvGeom& g, int n, int64_t tokens, int most_new, int max_pages, int q_heads, int bf16);
+// Workgroups of a CU at a time, by the registers that a row of 32 `words` channels takes.
+constexpr int cached_per_cu(int words, bool bf16) { return words <= 4 ? (bf16 ? 3 : 2) : words <= 6 && bf16 ? 2 : 1; }
+hipError_t launch_cached(const CachedArgs& a, const CachedPlan& p, hipStream_t s);
 
 // Attention over packed sequences.
 struct PackedArgs {

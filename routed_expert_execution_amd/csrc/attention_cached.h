@@ -3,6 +3,7 @@
 // with the running maximum m and both sums kept while the cache is read once.
 #pragma once
 
+#include <algorithm>
 #include <type_traits>
 
 #include "attention_device.h"
@@ -16,17 +17,21 @@ typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 constexpr int kWaves = 4, kThreads = 64 * kWaves, kStep = 32;  // tokens a wave takes at a time
 constexpr float kInf = __builtin_huge_valf();
 
-// Where a chunk lies.
-struct Chunk {
-    int seq, begin, rows_new, length, first, steps;  // first: step of 32 tokens it begins with
-    int index, of;                                    // chunk of the sequence, how many it has
-    int slot;                                         // its place among the partial results
-    bool bad;
+// The work of a call, for one key head: its row tiles (16 rows of a sequence's new
+// tokens and the query heads of the key head), each through its sequence's rounds, one
+// after another.  A round: a step of 32 tokens for each wave.  The line of all of them is
+// cut into a.places runs of equal length, one for a workgroup; a tile that lies in
+// several runs is joined from its parts afterwards.  (Chunks of one sequence each, a
+// fourth of a run long where there was work for it, took 290 us where this takes 234: 40
+// sequences of 1000 to 40000 tokens; 69 and 49: 64 of 2048; 631 and 210: one of 128 new
+// tokens beside 63 single ones, of 8192.)
+struct Work {
+    int seq, begin, rows_new, length, first;  // first: the step that the sequence's rounds begin with
+    int tile, rounds, start;                  // the tile's place on the line is [start, start + rounds)
+    bool bad;                                 // not what it may be: its rows are NaN
 };
-
-// A sequence as every chunk sees it: steps that its new tokens read, 1 where it is
-// not what it may be (one chunk then says so), 0 without new tokens.
-struct Sequence { int begin, rows_new, length, first, steps; bool bad; };
+// Sequence s: its tiles (none without new tokens) and each one's rounds.
+struct Sequence { int begin, rows_new, length, first, tiles, rounds; bool bad; };
 __device__ inline Sequence sequence_of(const CachedArgs& a, int s) {
     Sequence r;
     const int begin = a.batch.offsets[s], end = a.batch.offsets[s + 1], length = a.batch.lengths[s];
@@ -36,77 +41,73 @@ __device__ inline Sequence sequence_of(const CachedArgs& a, int s) {
     r.bad |= length < r.rows_new || length > (int64_t)a.batch.max_pages << a.cache.page_shift || r.rows_new > a.batch.most_new;
     r.length = r.bad ? 0 : length;
     const int first = a.window ? max(0, length - r.rows_new - a.window + 1) : 0;
-    r.first = first / kStep;
-    r.steps = r.bad ? 1 : r.rows_new ? (length + kStep - 1) / kStep - r.first : 0;
-    if (r.bad && !r.rows_new) r.steps = 0;
+    r.first = r.bad ? 0 : first / kStep;
+    r.rounds = r.bad ? 1 : ((length + kStep - 1) / kStep - r.first + kWaves - 1) / kWaves;
+    r.tiles = (int)(((int64_t)r.rows_new * a.per_head + 15) / 16);
     return r;
 }
 
-// Chunk `w` of the call: all steps of all sequences cut into about `target` chunks
-// of equal size, none over two sequences.  Every wave finds it for itself, 64
-// sequences a pass.  A sequence that is cut has more than 1 / target of all steps,
-// so there are fewer than `target` of them, with fewer than 2 target chunks.
-__device__ inline uint32_t wave_scan(uint32_t v) {  // inclusive, within the registers
-    v += __builtin_amdgcn_update_dpp(0u, v, 0x111, 0xF, 0xF, false);  // from 1, 2, 4 and 8 lanes before, within 16
-    v += __builtin_amdgcn_update_dpp(0u, v, 0x112, 0xF, 0xF, false);
-    v += __builtin_amdgcn_update_dpp(0u, v, 0x114, 0xF, 0xF, false);
-    v += __builtin_amdgcn_update_dpp(0u, v, 0x118, 0xF, 0xF, false);
-    v += __builtin_amdgcn_update_dpp(0u, v, 0x142, 0xA, 0xF, false);  // the row before's last, then the half's
-    v += __builtin_amdgcn_update_dpp(0u, v, 0x143, 0xC, 0xF, false);
+__device__ inline uint32_t wave_scan(uint32_t v) {  // inclusive, within the registers; stays at 2^32 - 1 once it is there
+    auto add = [&](uint32_t x) { v = __builtin_elementwise_add_sat(v, x); };
+    add(__builtin_amdgcn_update_dpp(0u, v, 0x111, 0xF, 0xF, false));  // from 1, 2, 4 and 8 lanes before, within 16
+    add(__builtin_amdgcn_update_dpp(0u, v, 0x112, 0xF, 0xF, false));
+    add(__builtin_amdgcn_update_dpp(0u, v, 0x114, 0xF, 0xF, false));
+    add(__builtin_amdgcn_update_dpp(0u, v, 0x118, 0xF, 0xF, false));
+    add(__builtin_amdgcn_update_dpp(0u, v, 0x142, 0xA, 0xF, false));  // the row before's last, then the half's
+    add(__builtin_amdgcn_update_dpp(0u, v, 0x143, 0xC, 0xF, false));
     return v;
 }
-__device__ inline int chunk_steps(int64_t total, const CachedArgs& a) {
-    // a chunk for each place of the card, or a few where there is work for several
-    // rounds: the last of them leaves less of the card idle
-    const int64_t rounds = min(max(total * a.row_tiles / ((int64_t)a.places * 24), (int64_t)1), (int64_t)a.rounds), target = a.places * rounds;
-    const int64_t c = (total + target - 1) / target;
-    return (int)((max(c, (int64_t)1) + kWaves - 1) / kWaves * kWaves);
-}
-// which(chunks so far, chunks of it, cut sequences so far): the wanted sequence.
-// CUT: `w` counts the sequences that are cut, in place of chunks.
-template <bool CUT>
-__device__ inline bool find_chunk(const CachedArgs& a, int w, Chunk* out) {
+// Length of the line (and the sequences of the last 64 on the lanes), 0 where it passes 2^31: with good offsets and lengths it does not
+// (the host sees to that), with others the call only reports them.
+__device__ inline uint32_t line_of(const CachedArgs& a, Sequence* last) {
     const int lane = threadIdx.x & 63, n = a.batch.n;
-    Sequence q{};
-    int64_t total = 0;
+    uint64_t total = 0;
     for (int base = 0; base < n; base += 64) {
-        q = Sequence{};
+        Sequence q{};
         if (base + lane < n) q = sequence_of(a, base + lane);
-        total += (uint32_t)__builtin_amdgcn_readlane(wave_scan(q.steps), 63);  // (64 times 2^25 at most)
+        *last = q;
+        const uint32_t cost = (uint32_t)min((uint64_t)(uint32_t)q.tiles * (uint32_t)q.rounds, (uint64_t)1 << 31);
+        total += (uint32_t)__builtin_amdgcn_readlane(wave_scan(cost), 63);
     }
-    const int steps = __builtin_amdgcn_readfirstlane(chunk_steps(total, a));
-    int chunks_before = 0, cut_before = 0, slots_before = 0;
+    return total < (1u << 31) ? (uint32_t)total : 0;
+}
+// The tile at place `at` of the line, or the call's tile `at` (TILES).  Every wave finds
+// it for itself, 64 sequences a pass.  all: the sequences, where there are no more than
+// 64 and they are at hand.
+template <bool TILES>
+__device__ inline bool find_work(const CachedArgs& a, uint32_t at, Work* out, const Sequence* all) {
+    const int lane = threadIdx.x & 63, n = a.batch.n;
+    uint32_t before = 0, tiles_before = 0;
     for (int base = 0; base < n; base += 64) {
-        if (n > 64) {
-            q = Sequence{};
-            if (base + lane < n) q = sequence_of(a, base + lane);
-        }
-        const int of = (q.steps + steps - 1) / steps, cut = of > 1;
-        const int chunks = wave_scan(of), cuts = CUT ? wave_scan(cut) : 0, slots = wave_scan(cut ? of : 0);
-        const int mine = CUT ? cut_before + cuts : chunks_before + chunks;
-        const uint64_t past = __ballot(mine > w);
+        Sequence q{};
+        if (all && n <= 64) q = *all;
+        else if (base + lane < n) q = sequence_of(a, base + lane);
+        const uint32_t line = wave_scan((uint32_t)q.tiles * (uint32_t)q.rounds), tiles = TILES ? wave_scan(q.tiles) : 0;
+        const uint64_t past = __ballot((TILES ? tiles_before + tiles : before + line) > at);
         if (past) {
             const int k = __ffsll((unsigned long long)past) - 1;
-            out->seq = base + k;
             auto of_k = [&](int v) { return __builtin_amdgcn_readlane(v, k); };  // (wave-uniform, in scalar registers)
+            out->seq = base + k;
             out->begin = of_k(q.begin);
             out->rows_new = of_k(q.rows_new);
             out->length = of_k(q.length);
+            out->first = of_k(q.first);
+            out->rounds = of_k(q.rounds);
             out->bad = of_k((int)q.bad);
-            out->of = of_k(of);
-            out->index = CUT ? 0 : w - (chunks_before + of_k(chunks) - out->of);
-            out->slot = slots_before + of_k(slots) - (out->of > 1 ? out->of : 0) + out->index;
-            const int all = of_k(q.steps);
-            out->first = of_k(q.first) + out->index * steps;
-            out->steps = min(steps, all - out->index * steps);
+            const uint32_t count = of_k(q.tiles), from = before + of_k(line) - count * out->rounds;
+            out->tile = __builtin_amdgcn_readfirstlane(TILES ? at - (tiles_before + of_k(tiles) - count) : (at - from) / out->rounds);
+            out->start = from + out->tile * out->rounds;
             return true;
         }
-        chunks_before += __builtin_amdgcn_readlane(chunks, 63);
-        if (CUT) cut_before += __builtin_amdgcn_readlane(cuts, 63);
-        slots_before += __builtin_amdgcn_readlane(slots, 63);
+        before += __builtin_amdgcn_readlane(line, 63);
+        if (TILES) tiles_before += __builtin_amdgcn_readlane(tiles, 63);
     }
     return false;
 }
+__device__ inline uint32_t run_of(const CachedArgs& a, uint32_t line) { return max((line + a.places - 1) / a.places, 1u); }
+// Where the part of a tile that lies in run w is kept: a run has at most two that are
+// not whole tiles, one that it begins with and one that it ends with.
+__device__ inline int part_of(uint32_t run, int w, uint32_t start) { return 2 * w + (start > w * run); }
 
 // Codes as bf16 16 + code, two to a word: part 0..3 takes bits 4 part..4 part + 3
 // of each half word.
@@ -143,18 +144,21 @@ template <int N> __device__ inline void terms_of(const float (&v)[8], bf16x8_t (
     }
 }
 
-// W = D / 32, JP = group / 32.  A workgroup takes one chunk of a sequence's tokens, one key head and
-// 16 rows (new tokens times the query heads of that key head); its waves take the
-// chunk's steps of 32 tokens in turn, each with sums of its own, joined at the end.
+// W = D / 32, JP = group / 32.  A workgroup takes a run for one key head; the waves take
+// the steps of 32 tokens of each tile's part in turn, each with sums of its own, joined
+// at its end.
 // Keys are the left operand of the first product, K Q^T, so that a lane holds four
 // tokens of one row; these are, as they lie, the right operand of the second one,
 // V^T P^T.  Neither goes through LDS.  Codes enter as they are held: the (step,
 // lowest) pairs scale the first product's result and the second one's P.  P times
 // the step is rounded to bf16 and multiplies code - 8, which lies about zero as the
 // values do; the rest, lowest + 8 steps, is added in fp32.  (With code itself the
-// result was 0.0031 off, its own rounding being 0.0016.)
+// result was 0.0031 off, its own rounding being 0.0016.)  Bound by the cache's bytes
+// where sequences are long: 64 of up to 16000 tokens, 64 query and 8 key heads of 128,
+// 128 us (3.8 TB/s); one of 130001 tokens, 32 and 8, 44 us (3.8 TB/s); by latency where
+// they are short: one of 777 tokens 7.5 us, the first read and one round.
 template <int W, int JP, bool BF16>
-__global__ __launch_bounds__(kThreads, W <= 4 ? (BF16 ? 3 : 2) : W <= 6 ? 2 : 1) void cached_kernel(CachedArgs a) {
+__global__ __launch_bounds__(kThreads, cached_per_cu(W, BF16)) void cached_kernel(CachedArgs a) {
     constexpr int N = BF16 ? 1 : 3;  // bf16 terms of a factor
     constexpr int D = 32 * W, G = W / JP;
     constexpr int kParams = (16 * G + 63) / 64;  // words of one tile's steps a lane loads
@@ -163,26 +167,45 @@ __global__ __launch_bounds__(kThreads, W <= 4 ? (BF16 ? 3 : 2) : W <= 6 ? 2 : 1)
     __shared__ float joined[2][16][D + 4];
     __shared__ float2 stats[kWaves][16];
     if (blockIdx.x == gridDim.x - 1) check_offsets(a.batch.offsets, a.batch.n, a.batch.T, a.err);
-    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), r16 = lane & 15, q4 = lane >> 4;
-    // (all of a chunk's workgroups side by side: those of chunks that there are not come last)
     const KvView& kv = a.cache;
-    const int units = kv.heads * a.row_tiles, unit = blockIdx.x % units, head = unit % kv.heads;
-    Chunk c;
-    if (!find_chunk<false>(a, blockIdx.x / units, &c)) return;
-    const int rows = c.rows_new * a.per_head;
-    if (c.bad && threadIdx.x == 0) atomicOr(a.err, kErrCache);
+    const int head = blockIdx.x % kv.heads, run_index = blockIdx.x / kv.heads;
+    Sequence sequences;
+    const uint32_t line = line_of(a, &sequences), run = __builtin_amdgcn_readfirstlane(run_of(a, line));
     const CodeMasks masks = code_masks();
-    const int32_t* table = a.batch.pages + (int64_t)c.seq * a.batch.max_pages;
-    const int last_step = c.first + c.steps;
     const uint32_t head_bytes = (uint32_t)kv.tile_bytes << (kv.page_shift - 4), page_bytes = head_bytes * kv.heads;
     const uint8_t* heads_at = kv.data + (uint64_t)head * head_bytes;
 
+    const uint32_t run_end = min((run_index + 1) * (uint64_t)run, (uint64_t)line);
+    uint32_t place = run_index * (uint64_t)run < run_end ? run_index * run : run_end;
+    Work c;
+    if (place >= run_end || !find_work<false>(a, place, &c, &sequences)) return;
 #pragma unroll 1
-    for (int tile = unit / kv.heads; tile * 16 < rows; tile += a.row_tiles) {
-        const int row = tile * 16 + r16, token = row / a.per_head, q_head = head * a.per_head + row - token * a.per_head;
-        const bool live = row < rows;
+    for (;;) {
+        // (what follows from the lane is worked out for each part: it is not kept beside the sums)
+        int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+        asm volatile("" : "+v"(lane), "+s"(wave));
+        const int r16 = lane & 15, q4 = lane >> 4;
+        const uint32_t part_end = min(run_end, (uint32_t)(c.start + c.rounds));
+        const bool whole = place == (uint32_t)c.start && part_end == (uint32_t)(c.start + c.rounds);
+        const int32_t* table = a.batch.pages + (int64_t)c.seq * a.batch.max_pages;
+        const int rows = c.rows_new * a.per_head;
+        const bool live = c.tile * 16 + r16 < rows;
+        const int token = (c.tile * 16 + r16) / a.per_head;
+        auto row_at = [&](int64_t ld) {  // (worked out where it is used: it is not kept through the loop)
+            int row = c.tile * 16 + r16;
+            asm("" : "+v"(row));
+            const int of_token = row / a.per_head;
+            return (int64_t)(c.begin + of_token) * ld + (int64_t)(head * a.per_head + row - of_token * a.per_head) * D;
+        };
         // the row sees places from .. to - 1 (one past the last row all of them: it masks no step, and nothing of it is stored)
-        const int to = live ? c.length - c.rows_new + token + 1 : INT32_MAX, from = live && a.window ? max(0, to - a.window) : 0;
+        const int old = c.length - c.rows_new, to = live ? old + token + 1 : INT32_MAX, from = live && a.window ? max(0, to - a.window) : 0;
+        // the part's steps, less those at its ends that no row of the tile sees
+        const int first_token = __builtin_amdgcn_readfirstlane(c.tile * 16 / a.per_head), last_token = __builtin_amdgcn_readfirstlane(min(c.tile * 16 + 15, rows - 1) / a.per_head);
+        const int last_step = min(c.first + (int)(part_end - c.start) * kWaves, (old + last_token + kStep) / kStep);
+        int step = c.first + (int)(place - c.start) * kWaves;
+        if (a.window) step += max(0, (old + first_token - a.window + 1) / kStep - step) / kWaves * kWaves;
+        step += wave;
+        if (c.bad && threadIdx.x == 0) atomicOr(a.err, kErrCache);
 
         // (the first step's tokens on their way before the queries are waited for)
         bool bad = c.bad;
@@ -216,20 +239,20 @@ __global__ __launch_bounds__(kThreads, W <= 4 ? (BF16 ? 3 : 2) : W <= 6 ? 2 : 1)
             }
         };
         Loaded now, next;
-        int step = c.first + wave;
         int pages[2] = {page_of(step, 0), page_of(step, 1)};
         if (step < last_step) load(step, pages, now);
         pages[0] = page_of(step + kWaves, 0);
         pages[1] = page_of(step + kWaves, 1);
 
         bf16x8_t q[W][N];
+        const int64_t q_at = row_at(a.ldq);
         float q_sum[G];
 #pragma unroll
         for (int g = 0; g < G; g++) q_sum[g] = 0;
 #pragma unroll
         for (int j = 0; j < W; j++) {
             float v[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-            if (live) load8<BF16>(a.q, (int64_t)(c.begin + token) * a.ldq + (int64_t)q_head * D + 32 * j + 8 * q4, v);
+            if (live) load8<BF16>(a.q, q_at + 32 * j + 8 * q4, v);
             terms_of<N>(v, q[j]);
             float s = 0;
 #pragma unroll
@@ -392,61 +415,94 @@ __global__ __launch_bounds__(kThreads, W <= 4 ? (BF16 ? 3 : 2) : W <= 6 ? 2 : 1)
             __syncthreads();
         }
         if (wave == 0 && live) {
-            if (c.of == 1) {
+            if (whole) {
                 const float by = 1.0f / sum;
+                const int64_t at = row_at(a.ldo);
 #pragma unroll
                 for (int j = 0; j < 2 * W; j++)
 #pragma unroll
                     for (int e = 0; e < 4; e++)
-                        store1<BF16>(a.out, (int64_t)(c.begin + token) * a.ldo + (int64_t)q_head * D + 16 * j + 4 * q4 + e, out[j][e] * by);
+                        store1<BF16>(a.out, at + 16 * j + 4 * q4 + e, out[j][e] * by);
             } else {
-                const int64_t at = (int64_t)c.slot * a.batch.most_new * a.q_heads + (int64_t)token * a.q_heads + q_head;
+                const int64_t at = ((int64_t)part_of(run, run_index, place) * kv.heads + head) * a.part_rows + r16;
 #pragma unroll
                 for (int j = 0; j < 2 * W; j++) *(f32x4*)&a.part[at * D + 16 * j + 4 * q4] = out[j];
                 if (q4 == 0) a.part_ml[at] = make_float2(all, sum);
             }
         }
+        place = part_end;
+        if (place >= run_end || !find_work<false>(a, place, &c, nullptr)) return;
     }
 }
 
-// Rows of the sequences that were cut: their chunks' sums, in the chunks' order.  Rows
-// of up to 16 chunks are taken by a wave each, with more by a workgroup, each of its
-// waves every 16th chunk: a row has up to `target` of them, of D fp32 values, and they
-// are read at once.
+// Rows of the tiles that were cut: their parts' sums, in the parts' order.  Rows of up to
+// 16 parts are taken by a wave each, with more by a workgroup, each of its waves every
+// 16th part: a row has up to a.places of them, of D fp32 values, and they are read at once.
+// 6 to 9 us for the same calls, most of it one read after another.
+// BY_TILE: a workgroup's tile is the call's tile blockIdx.x; otherwise the one that the
+// end of run blockIdx.x cuts, if that is its first cut.
 constexpr int kJoinWaves = 16, kJoinThreads = 64 * kJoinWaves;
-template <bool BF16>
+template <bool BF16, bool BY_TILE>
 __global__ __launch_bounds__(kJoinThreads) void cached_join_kernel(CachedArgs a) {
     __shared__ float sums[kJoinWaves][256];
-    const int D = a.cache.D, lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    Chunk c;
-    if (!find_chunk<true>(a, blockIdx.x, &c)) return;
-    const int64_t per_chunk = (int64_t)a.batch.most_new * a.q_heads;
-    const int rows = c.rows_new * a.q_heads, d0 = min(4 * lane, D - 4);  // (four channels a lane, past the last the last again)
-    auto join = [&](int row, int first, int every, float* sum) -> f32x4 {  // this wave's chunks, to the row's scale
-        const int64_t at = (int64_t)c.slot * per_chunk + row;
-        float m = -kInf, l = 0;
-        for (int i = lane; i < c.of; i += 64) m = fmaxf(m, a.part_ml[at + i * per_chunk].x);
+    const int D = a.cache.D, heads = a.cache.heads, lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    Sequence sequences;
+    const uint32_t line = line_of(a, &sequences), run = __builtin_amdgcn_readfirstlane(run_of(a, line));
+    Work c;
+    const uint64_t cut = (blockIdx.x + 1) * (uint64_t)run;
+    if (line == 0 || (!BY_TILE && cut >= line) || !find_work<BY_TILE>(a, BY_TILE ? blockIdx.x : (uint32_t)cut, &c, &sequences)) return;
+    const uint32_t start = c.start, end = start + c.rounds;
+    if (!BY_TILE && (start >= cut || start + run < cut)) return;
+    const int run_0 = start / run, of = (end - 1) / run - run_0 + 1;
+    if (of == 1) return;
+    const int live = min(16, c.rows_new * a.per_head - c.tile * 16), rows = live * heads;
+    const int d0 = min(4 * lane, D - 4);  // (four channels a lane, past the last the last again)
+    const int64_t per_part = (int64_t)heads * a.part_rows;
+    // the place of a row's part i: the first's, then every second one from the next run on
+    auto join = [&](int row, int first, int every, float* sum) -> f32x4 {  // this wave's parts, to the row's scale
+        const int head = row / live, r = row - head * live;
+        const int64_t at = (int64_t)head * a.part_rows + r;
+        auto place = [&](int i) { return at + (i ? 2 * (run_0 + i) : part_of(run, run_0, start)) * per_part; };
+        constexpr int kBatch = 4;
+        f32x4 part[kBatch];  // the next ones, on their way before the stats are waited for
+        auto load = [&](int i) {
+#pragma unroll
+            for (int x = 0; x < kBatch; x++)
+                if (i + x * every < of) part[x] = *(const f32x4*)&a.part[place(i + x * every) * D + d0];
+        };
+        load(first);
+        auto stats_of = [&](int i) { return i < of ? a.part_ml[place(i)] : make_float2(-kInf, 0.f); };
+        float2 ml = stats_of(lane);  // 64 parts at a time, one a lane
+        float m = ml.x, l = 0;
+        for (int i = lane + 64; i < of; i += 64) m = fmaxf(m, a.part_ml[place(i)].x);
 #pragma unroll
         for (int x = 1; x < 64; x *= 2) m = fmaxf(m, __shfl_xor(m, x));
         const float base = m == -kInf ? 0.f : m;
-        for (int i = lane; i < c.of; i += 64) {
-            const float2 ml = a.part_ml[at + i * per_chunk];
-            l += ml.y * __builtin_amdgcn_exp2f(ml.x - base);
+        f32x4 v = {0, 0, 0, 0};
+        int i = first;
+        for (int i0 = 0;;) {
+            const float f = __builtin_amdgcn_exp2f(ml.x - base);
+            l += ml.y * f;
+            const int end = min(i0 + 64, of);
+            while (i < end) {
+#pragma unroll
+                for (int x = 0; x < kBatch; x++)
+                    if (i + x * every < end) v += __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(f), i + x * every - i0)) * part[x];
+                i += kBatch * every;  // (divides 64)
+                load(i);
+            }
+            i0 += 64;
+            if (i0 >= of) break;
+            ml = stats_of(i0 + lane);
         }
         *sum = seg_sum<64>(l);
-        f32x4 v = {0, 0, 0, 0};
-#pragma unroll 4
-        for (int i = first; i < c.of; i += every) {
-            const float f = __builtin_amdgcn_exp2f(a.part_ml[at + i * per_chunk].x - base);
-            v += f * *(const f32x4*)&a.part[(at + i * per_chunk) * D + d0];
-        }
         return v;
     };
     auto out_at = [&](int row) {
-        const int token = row / a.q_heads, q_head = row - token * a.q_heads;
-        return (int64_t)(c.begin + token) * a.ldo + (int64_t)q_head * D;
+        const int head = row / live, r = c.tile * 16 + row - head * live, token = r / a.per_head;
+        return (int64_t)(c.begin + token) * a.ldo + (int64_t)(head * a.per_head + r - token * a.per_head) * D;
     };
-    if (c.of <= kJoinWaves) {
+    if (of <= kJoinWaves) {
         for (int row = blockIdx.y * kJoinWaves + wave; row < rows; row += gridDim.y * kJoinWaves) {
             float sum;
             const f32x4 v = join(row, 0, 1, &sum);
@@ -472,32 +528,33 @@ __global__ __launch_bounds__(kJoinThreads) void cached_join_kernel(CachedArgs a)
 }
 
 template <int W, int JP, bool BF16>
-hipError_t launch(const CachedArgs& a, int split, hipStream_t s) {
-    const dim3 grid((a.batch.n + (split ? a.target : 0)) * a.cache.heads * a.row_tiles);
-    hipLaunchKernelGGL((cached_kernel<W, JP, BF16>), grid, dim3(kThreads), 0, s, a);
-    if (split) {
-        // (fewer than `target` sequences are cut)
-        const int cut = a.batch.n < a.target ? a.batch.n : a.target, rows = a.batch.most_new * a.q_heads, share = 512 / cut;
-        hipLaunchKernelGGL((cached_join_kernel<BF16>), dim3(cut, rows < share ? rows : share < 1 ? 1 : share), dim3(kJoinThreads), 0, s, a);
+hipError_t launch(const CachedArgs& a, const CachedPlan& p, hipStream_t s) {
+    hipLaunchKernelGGL((cached_kernel<W, JP, BF16>), dim3(p.places * a.cache.heads), dim3(kThreads), 0, s, a);
+    if (p.split) {
+        const int cuts = p.places - 1, rows = a.part_rows * a.cache.heads;
+        const bool by_tile = p.tiles <= cuts;
+        const dim3 grid(by_tile ? (int)p.tiles : cuts, std::max(1, std::min(rows, 512 / (by_tile ? (int)p.tiles : cuts))));
+        if (by_tile) hipLaunchKernelGGL((cached_join_kernel<BF16, true>), grid, dim3(kJoinThreads), 0, s, a);
+        else hipLaunchKernelGGL((cached_join_kernel<BF16, false>), grid, dim3(kJoinThreads), 0, s, a);
     }
     return hipGetLastError();
 }
 template <int W, bool BF16>
-hipError_t launch_by_group(const CachedArgs& a, int split, hipStream_t s) {
+hipError_t launch_by_group(const CachedArgs& a, const CachedPlan& p, hipStream_t s) {
     if constexpr (W % 2 == 0)
-        if (a.cache.group_shift == 1) return launch<W, 2, BF16>(a, split, s);
+        if (a.cache.group_shift == 1) return launch<W, 2, BF16>(a, p, s);
     if constexpr (W % 4 == 0)
-        if (a.cache.group_shift == 2) return launch<W, 4, BF16>(a, split, s);
-    return launch<W, 1, BF16>(a, split, s);
+        if (a.cache.group_shift == 2) return launch<W, 4, BF16>(a, p, s);
+    return launch<W, 1, BF16>(a, p, s);
 }
 template <bool BF16>
-hipError_t launch_by_width(const CachedArgs& a, int split, hipStream_t s) {
+hipError_t launch_by_width(const CachedArgs& a, const CachedPlan& p, hipStream_t s) {
     switch (a.cache.words) {
-        case 2: return launch_by_group<2, BF16>(a, split, s);
-        case 3: return launch_by_group<3, BF16>(a, split, s);
-        case 4: return launch_by_group<4, BF16>(a, split, s);
-        case 6: return launch_by_group<6, BF16>(a, split, s);
-        default: return launch_by_group<8, BF16>(a, split, s);
+        case 2: return launch_by_group<2, BF16>(a, p, s);
+        case 3: return launch_by_group<3, BF16>(a, p, s);
+        case 4: return launch_by_group<4, BF16>(a, p, s);
+        case 6: return launch_by_group<6, BF16>(a, p, s);
+        default: return launch_by_group<8, BF16>(a, p, s);
     }
 }
 

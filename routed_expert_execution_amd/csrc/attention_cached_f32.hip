@@ -4,6 +4,6 @@
 
 namespace moe {
 
-hipError_t launch_cached_f32(const CachedArgs& a, int split, hipStream_t s) { return cached::launch_by_width<false>(a, split, s); }
+hipError_t launch_cached_f32(const CachedArgs& a, const CachedPlan& p, hipStream_t s) { return cached::launch_by_width<false>(a, p, s); }
 
 }  // namespace moe

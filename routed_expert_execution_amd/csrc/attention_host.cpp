@@ -202,7 +202,7 @@ size_t moe_attention_cached_workspace(const moe_kv_cache* m, const moe_kv_batch*
     if (!m || !g.init(m->pages, m->page_tokens, m->heads, m->head_dim, m->group) || !batch_sizes(b, g.page_tokens) ||
         !query_heads_valid(q_heads, g.heads))
         return 0;
-    const size_t n = moe::cached_plan(g, b->n, (int)b->most_new, b->max_pages, q_heads, 0).bytes;
+    const size_t n = moe::cached_plan(g, b->n, b->tokens, (int)b->most_new, b->max_pages, q_heads, 1).bytes;
     return n < 256 ? 256 : n;
 }
 
@@ -225,23 +225,23 @@ moe_status moe_attention_cached(moe_ctx* c, const moe_kv_cache* cache, const moe
     CHECK(workspace && aligned_to(workspace, 256), "%s: workspace must be 256-byte aligned", fn);
     const size_t need = moe_attention_cached_workspace(cache, batch, q_heads);
     CHECK(workspace_bytes >= need, "%s: workspace of %zu bytes, %zu needed", fn, workspace_bytes, need);
-    const moe::CachedPlan p = moe::cached_plan(g, batch->n, (int)batch->most_new, batch->max_pages, q_heads, dtype == MOE_BF16);
-    CHECK(((int64_t)batch->n + p.target) * g.heads * p.row_tiles < (1 << 24), "%s: too many heads of too many sequences for one call", fn);
+    a.bf16 = dtype == MOE_BF16;
+    const moe::CachedPlan p = moe::cached_plan(g, batch->n, T, (int)batch->most_new, batch->max_pages, q_heads, a.bf16);
+    CHECK(p.line < ((int64_t)1 << 31), "%s: too many tokens over too long a page table for one call", fn);
     if (moe_status st = need_device(c)) return st;
     if (T == 0 || batch->n == 0) return MOE_OK;
     a.cache = moe::kv_view(g, cache->data);
     a.q = q; a.ldq = T > 1 ? ldq : width;
-    a.bf16 = dtype == MOE_BF16;
     a.q_heads = q_heads; a.per_head = q_heads / g.heads;
     a.scale_log2 = (float)((double)scale * 1.4426950408889634);
     a.window = (int)(window < (1 << 30) ? window : 0);  // (none reaches further back)
     a.out = out; a.ldo = T > 1 ? ldo : width;
-    a.places = p.places; a.rounds = p.rounds; a.target = p.target; a.row_tiles = p.row_tiles;
+    a.places = p.places; a.part_rows = p.part_rows;
     a.part = (float*)workspace;
-    a.part_ml = (float2*)(a.part + (size_t)2 * p.target * batch->most_new * q_heads * g.D);
+    a.part_ml = (float2*)(a.part + (size_t)2 * p.places * g.heads * p.part_rows * g.D);
     a.err = error_word(c);
     DeviceGuard dg(device_of(c));
-    LAUNCH(moe::launch_cached(a, p.split, (hipStream_t)stream));
+    LAUNCH(moe::launch_cached(a, p, (hipStream_t)stream));
 }
 
 // What both passes judge alike.

@@ -112,7 +112,8 @@ def _cached(ctx, cache=None, batch=None, q=BASE, ldq=256, dtype=1, q_heads=4, sc
 @pytest.mark.parametrize("kw,text", CACHE + [
     (dict(q_heads=3), "multiple"), (dict(q_heads=0), "multiple"), (dict(q_heads=1026), "multiple"), (dict(q=None), "null q"), (dict(out=None), "null out"), (dict(ldq=255), "tokens of q"),
     (dict(ldo=255), "tokens of out"), (dict(scale=0.0), "scale"), (dict(scale=-1.0), "scale"), (dict(scale=math.inf), "scale"), (dict(scale=math.nan), "scale"),
-    (dict(cache=_cache(heads=1024), batch=_batch(n=65536), q_heads=1024, ldq=1 << 20, ldo=1 << 20, n=1 << 40), "too many"),
+    (dict(cache=_cache(heads=1024), batch=_batch(n=65536), q_heads=1024, ldq=1 << 20, ldo=1 << 20, n=1 << 40), "host-only"),
+    (dict(batch=_batch(max_pages=1 << 20, tokens=1 << 18), n=1 << 40), "too many"), (dict(batch=_batch(max_pages=1 << 20, tokens=1 << 16), n=1 << 40), "host-only"),
     (dict(window=-1), "window"), (dict(window=1 << 40), "host-only"), (dict(ws=None), "workspace"), (dict(ws=BASE + 128), "256-byte"), (dict(n=255), "needed")])
 def test_attention_cached_refuses(ctx, kw, text):
     _refused(ctx, _cached(ctx, **kw), text)

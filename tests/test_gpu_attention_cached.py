@@ -64,7 +64,11 @@ CASES = [
     ([70], [100], 16, 2, 1, 64, 64, 0, BF16, 0), ([33, 1], [33, 900], 128, 10, 2, 256, 128, 0, F32, 0), ([1, 1], [2000, 100], 16, 8, 2, 128, 32, 100, BF16, 0),
     ([9, 2], [500, 37], 32, 4, 2, 96, 32, 33, F32, 0), ([5], [1000], 64, 8, 2, 192, 32, 1, BF16, 0), ([1] * 70, [i * 7 % 400 + 1 for i in range(70)], 16, 4, 2, 64, 32, 0, BF16, 0),
     ([1] * 130, [2000 if i == 77 else 9 for i in range(130)], 16, 4, 2, 128, 64, 0, BF16, 0), ([1], [6000], 16, 128, 1, 192, 32, 0, F32, 0),
-    ([1, 300], [4000, 300], 64, 2, 1, 64, 32, 0, BF16, 0), ([1], [100000], 256, 2, 1, 64, 64, 0, BF16, 0), ([1], [40000], 64, 2, 1, 96, 32, 0, F32, 0)]
+    ([1, 300], [4000, 300], 64, 2, 1, 64, 32, 0, BF16, 0), ([1], [100000], 256, 2, 1, 64, 64, 0, BF16, 0), ([1], [40000], 64, 2, 1, 96, 32, 0, F32, 0),
+    # a prompt's part beside single tokens, more sequences than a wave has lanes: a run is several sequences' tiles
+    ([1] * 40 + [90] + [1] * 40 + [0, 17], [i * 37 % 700 + 1 for i in range(40)] + [2500] + [i * 53 % 900 + 1 for i in range(40)] + [5, 1700], 16, 8, 2, 64, 32, 0, BF16, 0),
+    ([1] * 70 + [33, 2], [i * 29 % 500 + 1 for i in range(70)] + [1500, 800], 64, 12, 4, 128, 64, 200, F32, 0),
+    ([1, 1, 1, 260, 1], [9000, 1, 128, 4000, 129], 32, 8, 2, 128, 128, 0, BF16, 0), ([500], [500], 16, 16, 16, 128, 32, 0, BF16, 0), ([500], [900], 16, 4, 4, 96, 32, 70, BF16, 0)]
 
 
 @pytest.mark.parametrize("new,lengths,page,heads,Hkv,D,group,window,dtype,gap", CASES)
