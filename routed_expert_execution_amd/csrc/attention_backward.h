@@ -8,6 +8,8 @@
 // products in place of five.
 #pragma once
 
+#include <type_traits>
+
 #include "attention_tiles.h"
 
 namespace moe {
@@ -373,16 +375,20 @@ __global__ __launch_bounds__(kBackwardThreads) void attention_dkv_kernel(PackedA
 // blocks' scores: the products of the next block's S and dP run beside this block's
 // exponentials, and the products with them follow, so that the matrix cores wait
 // neither for the vector unit nor for LDS.  A block is 32 keys (dQ) or 32 rows a wave
-// (dK, dV); three buffers, since a block's tile is read in two steps.
+// (dK, dV).
 // DIRECT: tiles go straight from memory into LDS.
+// Four sequences of up to 4096 tokens, 16 query and 4 key heads of 128, causal: dQ 193 us,
+// dK and dV 355 us, the matrix cores busy for a third of the time; what is left is the
+// vector unit's work (instructions of two waves to a unit), and, of dK and dV, that the
+// longest sequence's first keys take 256 steps where the average CU has 195.
 constexpr int kAhead = 2;  // products between an operand's read and its use
 
 template <int D, bool DIRECT>
 __global__ __launch_bounds__(kBackwardWaves * 64, 2) void attention_dq_beside_kernel(PackedArgs a) {
     typedef Tile<true, D> T;
     constexpr int kThreads = 64 * kBackwardWaves, kRows = 32 * kBackwardWaves, KK = D / 16, DB = D / 32, kBytes = 32 * T::kLineBytes;
-    __shared__ __attribute__((aligned(1024))) char lds[5 * kBytes];  // keys of three blocks, values of two
-    __shared__ int odd_block[3];
+    __shared__ __attribute__((aligned(1024))) char lds[8 * kBytes];  // keys and values, four blocks (three would do: their number's low bits say where)
+    __shared__ int odd_block[4];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), h = lane >> 5;
     const int kv_head = blockIdx.x % a.kv_heads, rest = blockIdx.x / a.kv_heads;
     const int head = kv_head * a.per_head + rest % a.per_head;
@@ -430,38 +436,57 @@ __global__ __launch_bounds__(kBackwardWaves * 64, 2) void attention_dq_beside_ke
     const int end = a.causal ? min(s.keys, last_row + s.shift + 1) : s.keys;
     const int begin = a.window ? max(0, row0 + s.shift - a.window + 1) / 32 * 32 : 0;
     const int total = end > begin ? (end - begin + 31) / 32 : 0;
-    const char* kbase = (const char*)a.k + ((int64_t)s.k0 * a.ldk + (int64_t)kv_head * D) * 2;
-    const char* vbase = (const char*)a.v + ((int64_t)s.k0 * a.ldv + (int64_t)kv_head * D) * 2;
-    auto masked_block = [&](int t) {  // for some row of the workgroup
+    // a block whose keys all the workgroup's rows see begins with one of these keys
+    const int clear_from = a.window ? last_row + s.shift - a.window + 1 : INT32_MIN;
+    const int clear_to = min(s.keys - 32, a.causal ? row0 + s.shift - 31 : INT32_MAX);
+    auto masked_block = [&](int t) {
         const int k0 = begin + 32 * t;
-        return k0 + 32 > s.keys || (a.causal && k0 + 31 > row0 + s.shift) || (a.window && k0 <= last_row + s.shift - a.window);
+        return k0 < clear_from || k0 > clear_to;
     };
     auto in_range = [&](int t) {  // for some row of the wave
         const int k0 = begin + 32 * t;
         return t >= 0 && t < total && wave_first < s.rows && !(a.causal && k0 > wave_last + s.shift) && !(a.window && k0 + 31 <= wave_first + s.shift - a.window);
     };
-    Pipe<true, D, 32, kThreads, DIRECT> pk, pv;
-    auto keys_at = [&](int t) { return lds + (t % 3) * kBytes; };
-    auto values_at = [&](int t) { return lds + (3 + (t & 1)) * kBytes; };
+    Pipe<true, D, 32, kThreads, false> pk, pv;
+    LinesToLds<D, 32, kThreads> to_k, to_v;
+    auto keys_at = [&](int t) { return lds + (t & 3) * 2 * kBytes; };
+    auto values_at = [&](int t) { return lds + (t & 3) * 2 * kBytes + kBytes; };
+    // what is fetched next
+    int fetch_key = begin;
+    const char* k_at = (const char*)a.k + (((int64_t)s.k0 + begin) * a.ldk + (int64_t)kv_head * D) * 2;
+    const char* v_at = (const char*)a.v + (((int64_t)s.k0 + begin) * a.ldv + (int64_t)kv_head * D) * 2;
+    auto places = [&](int keys) __attribute__((always_inline)) {
+        to_k.places(a.ldk, keys);
+        to_v.places(a.ldv, keys);
+    };
+    if (DIRECT && total) places(s.keys - begin);
     auto fetch = [&](int t) __attribute__((always_inline)) {
-        const int k0 = begin + 32 * t;
-        pk.fetch(kbase, a.ldk, k0, s.keys - k0, keys_at(t));
-        pv.fetch(vbase, a.ldv, k0, s.keys - k0, values_at(t));
+        if constexpr (DIRECT) {
+            if (t > 0 && fetch_key + 32 > s.keys) places(s.keys - fetch_key);
+            to_k.fetch(k_at, tile::lds_address(keys_at(t)), wave);
+            to_v.fetch(v_at, tile::lds_address(values_at(t)), wave);
+        } else {
+            pk.fetch(k_at, a.ldk, 0, s.keys - fetch_key, nullptr);
+            pv.fetch(v_at, a.ldv, 0, s.keys - fetch_key, nullptr);
+        }
+        fetch_key += 32;
+        k_at += 64 * a.ldk;
+        v_at += 64 * a.ldv;
     };
     // Block t + 1 has arrived and t + 2 is fetched.
     auto advance = [&](int t, bool check) __attribute__((always_inline)) {
-        if (t + 1 < total) {
+        if (!DIRECT && t + 1 < total) {
             pk.arrive(keys_at(t + 1));
             pv.arrive(values_at(t + 1));
         }
         meet<DIRECT>();
         if (check && t >= 0 && masked_block(t)) {
-            if (tile_not_finite<true, D, 32, kThreads>(keys_at(t))) odd_block[t % 3] = t;
+            if (tile_not_finite<true, D, 32, kThreads>(keys_at(t))) odd_block[t & 3] = t;
             __syncthreads();
         }
         if (t + 2 < total) fetch(t + 2);
     };
-    if (threadIdx.x < 3) odd_block[threadIdx.x] = -1;
+    if (threadIdx.x < 4) odd_block[threadIdx.x] = -1;
     const uint32_t along_lane = T::along_lane(lane), across_lane = T::across_lane(lane);
     if (total) fetch(0);
     int t = -1;
@@ -506,7 +531,7 @@ __global__ __launch_bounds__(kBackwardWaves * 64, 2) void attention_dq_beside_ke
         advance(t, true);
         if (in_range(t)) {
             const uint32_t kx = tile::lds_address(keys_at(t)) + across_lane;
-            const bool odd = odd_block[t % 3] == t;
+            const bool odd = odd_block[t & 3] == t;
             const Span span = keys_seen(a, s, row, begin + 32 * t, h);
 #pragma unroll
             for (int n = 0; n < 2; n++) {
@@ -556,16 +581,20 @@ __global__ __launch_bounds__(kBackwardWaves * 64, 2) void attention_dq_beside_ke
             for (int e = 0; e < 4; e++) store1<true>(a.dq, o + 32 * d + 8 * j + 4 * h + e, out[d][4 * j + e] * by);
 }
 
-// dK and dV: a workgroup has 64 keys; two waves take 32 of them each over the first
-// 32 of every 64 rows, two over the others, and their sums are added at the end.
+// dK and dV: a workgroup has 64 keys and passes over the rows 64 at a time; of the four
+// 32 x 32 blocks of these one wave adds to dK, another to dV, and the two over the same
+// keys are added at the end.  S is computed by both, five products in place of four, but
+// a wave's registers then leave room for a second one to each unit.  (With both sums in a
+// wave, and one wave to a unit, the unit stood still for most of the time: 432 us for 355.)
+constexpr int kBesideThreads = 512;
 template <int D, bool DIRECT>
-__global__ __launch_bounds__(kBackwardWaves * 64) void attention_dkv_beside_kernel(PackedArgs a) {
+__global__ __launch_bounds__(kBesideThreads, 2) void attention_dkv_beside_kernel(PackedArgs a) {
     typedef Tile<true, D> T;
-    constexpr int kThreads = 64 * kBackwardWaves, kKeys = 64, KK = D / 16, DB = D / 32, kBytes = 64 * T::kLineBytes;
-    __shared__ __attribute__((aligned(1024))) char lds[6 * kBytes];  // queries and their gradients, three steps
-    __shared__ __attribute__((aligned(1024))) float2 stats[3][64];
-    __shared__ int odd_step[3];
-    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), h = lane >> 5, part = wave >> 1;
+    constexpr int kThreads = kBesideThreads, kKeys = 64, KK = D / 16, DB = D / 32, kBytes = 64 * T::kLineBytes;
+    __shared__ __attribute__((aligned(1024))) char lds[8 * kBytes];  // queries and their gradients, four steps
+    __shared__ __attribute__((aligned(1024))) float2 stats[4][64];
+    __shared__ int odd_step[4];
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), h = lane >> 5, part = wave >> 1 & 1;
     const int kv_head = blockIdx.x % a.kv_heads;
     int seq, local;
     if (!find_tile<kKeys>(a.offsets_k, a.n, a.Tk, blockIdx.x / a.kv_heads, &seq, &local)) return;
@@ -574,216 +603,274 @@ __global__ __launch_bounds__(kBackwardWaves * 64) void attention_dkv_beside_kern
     if (key0 >= s.keys) return;
     const bool live = key < s.keys;
     if (s.bad && threadIdx.x == 0) atomicOr(a.err, kErrCache);
-
-    Fragment<true> k[KK], v[KK];
     const int64_t token = s.k0 + key;
-#pragma unroll
-    for (int kk = 0; kk < KK; kk++) {
-        along_memory<true>(a.k, token * a.ldk + (int64_t)kv_head * D, live, kk, lane, k[kk]);
-        along_memory<true>(a.v, token * a.ldv + (int64_t)kv_head * D, live, kk, lane, v[kk]);
-    }
-    f32x16 dk[DB], dv[DB], st, dp, st_next, dp_next;
-#pragma unroll
-    for (int i = 0; i < 16; i++)
-#pragma unroll
-        for (int d = 0; d < DB; d++) dk[d][i] = dv[d][i] = 0;
 
-    // rows that see any of the workgroup's keys, 64 a step, of one query head after the other
+    // rows that see any of the workgroup's keys, 64 a step, the last ones first and the query
+    // heads in turn: workgroups that run at the same time read the same rows
     const int last_key = min(key0 + kKeys, s.keys) - 1, wave_last_key = min(wave_key + 31, s.keys - 1);
     const int begin = a.causal ? max(0, key0 - s.shift) / 64 * 64 : 0;
     const int end = (int)min((int64_t)s.rows, a.window ? (int64_t)last_key - s.shift + a.window : s.rows);
     const int per = end > begin ? (end - begin + 63) / 64 : 0, total = per * a.per_head;
-    int fetch_head = kv_head * a.per_head, fetch_row = begin;  // of the next step to be fetched
-    auto masked_rows = [&](int r0) {  // for some key of the workgroup
-        return r0 + 64 > s.rows || (a.causal && last_key > r0 + s.shift) || (a.window && key0 <= r0 + 63 + s.shift - a.window);
-    };
-    Pipe<true, D, 64, kThreads, DIRECT> pq, pg;
+    const int first_head = kv_head * a.per_head, first_row = begin + (per - 1) * 64;
+    int fetch_head = first_head, fetch_row = first_row;  // of the next step to be fetched
+    // a step whose rows all see all of the workgroup's keys begins with one of these rows
+    const int clear_from = a.causal ? last_key - s.shift : INT32_MIN;
+    const int clear_to = min(s.rows - 64, a.window ? key0 - 64 - s.shift + a.window : INT32_MAX);
+    auto masked_rows = [&](int r0) { return r0 < clear_from || r0 > clear_to; };
+    Pipe<true, D, 64, kThreads, false> pq, pg;
     float2 of_row;
-    auto queries_at = [&](int t) { return lds + (t % 3) * 2 * kBytes; };
+    auto queries_at = [&](int t) { return lds + (t & 3) * 2 * kBytes; };
+    // what is fetched next: the first of 64 rows of queries, of their gradients and of
+    // their L and delta, and this lane's places from there (rows past the last repeat it)
+    const char* q_at = (const char*)a.q + (((int64_t)s.q0 + first_row) * a.ldq + (int64_t)first_head * D) * 2;
+    const char* g_at = (const char*)a.dout + (((int64_t)s.q0 + first_row) * a.lddo + (int64_t)first_head * D) * 2;
+    const float2* stats_at = a.rows + (int64_t)first_head * a.Tq + s.q0 + first_row;
+    LinesToLds<D, 64, kThreads> to_q, to_g;
+    uint32_t stats_place;
+    auto places = [&](int rows) __attribute__((always_inline)) {
+        to_q.places(a.ldq, rows);
+        to_g.places(a.lddo, rows);
+        stats_place = min(32 * wave + lane / 2, rows - 1) * 8 + (lane & 1) * 4;
+    };
+    if (DIRECT) places(s.rows - first_row);
     auto fetch = [&](int t) __attribute__((always_inline)) {
-        pq.fetch((const char*)a.q + ((int64_t)s.q0 * a.ldq + (int64_t)fetch_head * D) * 2, a.ldq, fetch_row, s.rows - fetch_row, queries_at(t));
-        pg.fetch((const char*)a.dout + ((int64_t)s.q0 * a.lddo + (int64_t)fetch_head * D) * 2, a.lddo, fetch_row, s.rows - fetch_row, queries_at(t) + kBytes);
-        const float2* rows = a.rows + (int64_t)fetch_head * a.Tq + s.q0 + fetch_row;
-        const int most = s.rows - fetch_row - 1;  // (rows past the last are masked)
-        if (DIRECT) {
-            if (wave < 2) load_lds4(tile::lds_address(&stats[t % 3][32 * wave]), min(32 * wave + lane / 2, most) * 8 + (lane & 1) * 4, rows);
-        } else if (threadIdx.x < 64) {
-            of_row = rows[min((int)threadIdx.x, most)];
+        if constexpr (DIRECT) {
+            to_q.fetch(q_at, tile::lds_address(queries_at(t)), wave);
+            to_g.fetch(g_at, tile::lds_address(queries_at(t)) + kBytes, wave);
+            if (wave < 2) load_lds4(tile::lds_address(&stats[t & 3][32 * wave]), stats_place, stats_at);
+        } else {
+            pq.fetch(q_at, a.ldq, 0, s.rows - fetch_row, nullptr);
+            pg.fetch(g_at, a.lddo, 0, s.rows - fetch_row, nullptr);
+            if (threadIdx.x < 64) of_row = stats_at[min((int)threadIdx.x, s.rows - fetch_row - 1)];
         }
-        fetch_row += 64;
-        if (fetch_row >= end) {
-            fetch_row = begin;
-            fetch_head++;
+        q_at += D * 2;
+        g_at += D * 2;
+        stats_at += a.Tq;
+        if (++fetch_head == first_head + a.per_head) {
+            q_at -= (64 * a.ldq + a.per_head * D) * 2;
+            g_at -= (64 * a.lddo + a.per_head * D) * 2;
+            stats_at -= 64 + (int64_t)a.per_head * a.Tq;
+            fetch_head = first_head;
+            fetch_row -= 64;
+            if (DIRECT) places(64);
         }
     };
     // Step t + 1 has arrived and t + 2 is fetched.
     auto advance = [&](int t, int r0, bool check) __attribute__((always_inline)) {
         if (t + 1 < total) {
-            pq.arrive(queries_at(t + 1));
-            pg.arrive(queries_at(t + 1) + kBytes);
-            if (!DIRECT && threadIdx.x < 64) stats[(t + 1) % 3][threadIdx.x] = of_row;
+            if (!DIRECT) {
+                pq.arrive(queries_at(t + 1));
+                pg.arrive(queries_at(t + 1) + kBytes);
+            }
+            if (!DIRECT && threadIdx.x < 64) stats[(t + 1) & 3][threadIdx.x] = of_row;
         }
         meet<DIRECT>();
         if (check && t >= 0 && masked_rows(r0)) {
             const bool bad_q = tile_not_finite<true, D, 64, kThreads>(queries_at(t)), bad_g = tile_not_finite<true, D, 64, kThreads>(queries_at(t) + kBytes);
-            if (bad_q || bad_g) odd_step[t % 3] = t;
+            if (bad_q || bad_g) odd_step[t & 3] = t;
             __syncthreads();
         }
         if (t + 2 < total) fetch(t + 2);
     };
-    if (threadIdx.x < 3) odd_step[threadIdx.x] = -1;
+    if (threadIdx.x < 4) odd_step[threadIdx.x] = -1;
     const uint32_t along_lane = T::along_lane(lane) + part * 32 * T::kLineBytes, across_lane = T::across_lane(lane) + part * 32 * T::kLineBytes;
     if (total) fetch(0);
-    int t = -1, r0 = begin - 64;  // step t's rows begin at r0
-    auto step_on = [&]() __attribute__((always_inline)) {
-        t++;
-        r0 += 64;
-        if (r0 >= end) r0 = begin;
-    };
-    while (t < total) {
-#pragma unroll 1
-        while (t >= 0 && t + 1 < total && !masked_rows(r0)) {
-            advance(t, r0, false);
-            const uint32_t qa = tile::lds_address(queries_at(t + 1)) + along_lane, qx = tile::lds_address(queries_at(t)) + across_lane;
-            const float2* rows = &stats[t % 3][32 * part + 4 * h];
-            constexpr int kScores = 2 * KK, kSums = 4 * DB, kPairs = 8;
-            Fragment<true> f[kAhead + 1], pf[2], df[2];
+
+    auto pass = [&](auto which) __attribute__((always_inline)) {
+        constexpr bool kDK = which.value;  // dK, or dV
+        Fragment<true> k[KK], v[kDK ? KK : 1];
+#pragma unroll
+        for (int kk = 0; kk < KK; kk++) {
+            along_memory<true>(a.k, token * a.ldk + (int64_t)kv_head * D, live, kk, lane, k[kk]);
+            if constexpr (kDK) along_memory<true>(a.v, token * a.ldv + (int64_t)kv_head * D, live, kk, lane, v[kk]);
+        }
+        f32x16 sum[DB], st, dp, st_next, dp_next;
+#pragma unroll
+        for (int i = 0; i < 16; i++)
+#pragma unroll
+            for (int d = 0; d < DB; d++) sum[d][i] = 0;
+        int t = -1, r0 = first_row, left = a.per_head + 1;  // step t's rows begin at r0, `left` steps of them are left
+        auto step_on = [&]() __attribute__((always_inline)) {
+            t++;
+            if (--left == 0) {
+                left = a.per_head;
+                r0 -= 64;
+            }
+        };
+        while (t < total) {
+            constexpr int kScores = (kDK ? 2 : 1) * KK, kSums = 2 * DB, kPairs = 8;
+            Fragment<true> f[kAhead + 1], pf[2];
+            uint32_t qa, qx;
             auto read = [&](int i) __attribute__((always_inline)) {
-                if (i < kScores) {
-                    T::along(i & 1 ? qa + kBytes : qa, 0, i / 2, f[i % (kAhead + 1)]);
-                } else if (i < kScores + kSums) {
-                    const int n = (i - kScores) / (2 * DB), d = (i - kScores) / 2 % DB;
-                    T::across(i & 1 ? qx : qx + kBytes, 16 * n, 32 * d, f[i % (kAhead + 1)]);
+                if (kDK) T::along(i & 1 ? qa + kBytes : qa, 0, i / 2, f[i % (kAhead + 1)]);
+                else T::along(qa, 0, i, f[i % (kAhead + 1)]);
+            };
+            auto read_across = [&](int i, int at) __attribute__((always_inline)) { T::across(qx, 16 * (i / DB), 32 * (i % DB), f[(at + i) % (kAhead + 1)]); };
+            auto scores = [&](int t) __attribute__((always_inline)) {  // of step t + 1, beside step t's exponentials
+                const float2* rows = &stats[t & 3][32 * part + 4 * h];
+                f32x4 two[3];  // L and delta of two rows
+                auto read_stats = [&](int p) __attribute__((always_inline)) {
+                    if (p < kPairs) two[p % 3] = *(const f32x4*)(rows + 8 * (p / 2) + 2 * (p & 1));
+                };
+                read_stats(0);
+                read_stats(1);
+#pragma unroll
+                for (int i = 0; i < kAhead; i++) read(i);
+#pragma unroll
+                for (int i = 0; i < 16; i++) {
+                    st_next[i] = 0;
+                    if (kDK) dp_next[i] = 0;
+                }
+#pragma unroll
+                for (int i = 0; i < kScores; i++) {
+                    if (i + kAhead < kScores) read(i + kAhead);
+                    else if (kDK) read_across(i + kAhead - kScores, kScores);
+                    if constexpr (kDK) {
+                        if (i & 1) mma(dp_next, f[i % (kAhead + 1)], v[i / 2]);
+                        else mma(st_next, f[i % (kAhead + 1)], k[i / 2]);
+                    } else {
+                        mma(st_next, f[i % (kAhead + 1)], k[i]);
+                    }
+#pragma unroll
+                    for (int p = (i * kPairs + kScores - 1) / kScores; p < ((i + 1) * kPairs + kScores - 1) / kScores; p++) {
+                        read_stats(p + 2);
+                        const f32x4 of = two[p % 3];
+#pragma unroll
+                        for (int e = 2 * p; e < 2 * p + 2; e++) {
+                            float x = __builtin_amdgcn_exp2f(fmaf(st[e], a.scale_log2, -of[2 * (e & 1)]));
+                            if (kDK) x *= dp[e] - of[2 * (e & 1) + 1];
+                            pf[e / 8].raw[e % 8] = (__bf16)x;
+                        }
+                    }
+                    __builtin_amdgcn_sched_barrier(0);
+                }
+                st = st_next;
+                if (kDK) dp = dp_next;
+            };
+            auto sums = [&](int at) __attribute__((always_inline)) {
+#pragma unroll
+                for (int i = 0; i < kSums; i++) {
+                    if (i + kAhead < kSums) read_across(i + kAhead, at);
+                    mma(sum[i % DB], f[(at + i) % (kAhead + 1)], pf[i / DB]);
+                    __builtin_amdgcn_sched_barrier(0);
                 }
             };
-            static_assert(kScores % 2 == 0, "values' gradients first");
+            // dK's waves sum at the end of a step; dV's at the beginning of the next one, so
+            // that of a unit's two waves one sums while the other's vector work is done
+            bool held = false;
+            auto held_sums = [&](int t) __attribute__((always_inline)) {
+                if (kDK || !held) return;
+                qx = tile::lds_address(queries_at(t)) + kBytes + across_lane;
 #pragma unroll
-            for (int i = 0; i < kAhead; i++) read(i);
+                for (int i = 0; i < kAhead; i++) read_across(i, 0);
+                sums(0);
+                held = false;
+            };
+#pragma unroll 1
+            while (t >= 0 && t + 1 < total && !masked_rows(r0)) {
+                advance(t, r0, false);
+                held_sums(t - 1);
+                qa = tile::lds_address(queries_at(t + 1)) + along_lane;
+                if (kDK) qx = tile::lds_address(queries_at(t)) + across_lane;
+                scores(t);
+                if (kDK) sums(kScores);
+                else held = true;
+                step_on();
+            }
+            held_sums(t - 1);
+            advance(t, r0, true);
+            const int first = r0 + 32 * part;
+            auto in_range = [&](int t, int first) {  // some row of the wave sees some key of it
+                return t >= 0 && t < total && wave_key < s.keys && first < s.rows && !(a.causal && wave_key > first + 31 + s.shift) &&
+                       !(a.window && wave_last_key <= first + s.shift - a.window);
+            };
+            if (in_range(t, first)) {
+                const uint32_t qx = tile::lds_address(queries_at(t)) + (kDK ? 0 : kBytes) + across_lane;
+                const float2* rows = &stats[t & 3][32 * part + 4 * h];
+                const bool odd = odd_step[t & 3] == t;
+                const Span span = rows_seeing(a, s, key, first, h);
 #pragma unroll
-            for (int i = 0; i < 16; i++) st_next[i] = dp_next[i] = 0;
+                for (int n = 0; n < 2; n++) {
+                    Fragment<true> pf;
+                    bf16x8 seen;
 #pragma unroll
-            for (int i = 0; i < kScores; i++) {
-                read(i + kAhead);
-                if (i & 1) mma(dp_next, f[i % (kAhead + 1)], v[i / 2]);
-                else mma(st_next, f[i % (kAhead + 1)], k[i / 2]);
+                    for (int e = 0; e < 8; e++) {
+                        const int i = 8 * n + e;
+                        const float2 r = rows[8 * (i >> 2) + (i & 3)];
+                        const bool on = span.has(0, i);
+                        float x = __builtin_amdgcn_exp2f(fmaf(st[i], a.scale_log2, -r.x));
+                        if (kDK) x *= dp[i] - r.y;
+                        pf.raw[e] = (__bf16)(on ? x : 0.f);
+                        seen[e] = (__bf16)(on ? 1.f : 0.f);
+                    }
 #pragma unroll
-                for (int p = (i * kPairs + kScores - 1) / kScores; p < ((i + 1) * kPairs + kScores - 1) / kScores; p++) {
-                    const f32x4 two = *(const f32x4*)(rows + 8 * (p / 2) + 2 * (p & 1));  // of two rows
-#pragma unroll
-                    for (int e = 2 * p; e < 2 * p + 2; e++) {
-                        const float x = __builtin_amdgcn_exp2f(fmaf(st[e], a.scale_log2, -two[2 * (e & 1)]));
-                        pf[e / 8].raw[e % 8] = (__bf16)x;
-                        df[e / 8].raw[e % 8] = (__bf16)(x * (dp[e] - two[2 * (e & 1) + 1]));
+                    for (int d = 0; d < DB; d++) {
+                        Fragment<true> f;
+                        T::across(qx, 16 * n, 32 * d, f);
+                        if (odd) mma_seen(sum[d], f, pf, seen);
+                        else mma(sum[d], f, pf);
+                        __builtin_amdgcn_sched_barrier(0);
                     }
                 }
-                __builtin_amdgcn_sched_barrier(0);
             }
-#pragma unroll
-            for (int i = 0; i < kSums; i++) {
-                read(kScores + i + kAhead);
-                const int n = i / (2 * DB), d = i / 2 % DB;
-                if (i & 1) mma(dk[d], f[(kScores + i) % (kAhead + 1)], df[n]);
-                else mma(dv[d], f[(kScores + i) % (kAhead + 1)], pf[n]);
-                __builtin_amdgcn_sched_barrier(0);
-            }
-            st = st_next;
-            dp = dp_next;
             step_on();
-        }
-        advance(t, r0, true);
-        const int first = r0 + 32 * part;
-        auto in_range = [&](int t, int first) {  // some row of the wave sees some key of it
-            return t >= 0 && t < total && wave_key < s.keys && first < s.rows && !(a.causal && wave_key > first + 31 + s.shift) &&
-                   !(a.window && wave_last_key <= first + s.shift - a.window);
-        };
-        if (in_range(t, first)) {
-            const uint32_t qx = tile::lds_address(queries_at(t)) + across_lane;
-            const float2* rows = &stats[t % 3][32 * part + 4 * h];
-            const bool odd = odd_step[t % 3] == t;
-            const Span span = rows_seeing(a, s, key, first, h);
+            if (in_range(t, r0 + 32 * part)) {
+                const uint32_t qa = tile::lds_address(queries_at(t)) + along_lane;
 #pragma unroll
-            for (int n = 0; n < 2; n++) {
-                Fragment<true> pf, df;
-                bf16x8 seen;
-#pragma unroll
-                for (int e = 0; e < 8; e++) {
-                    const int i = 8 * n + e;
-                    const float2 r = rows[8 * (i >> 2) + (i & 3)];
-                    const bool on = span.has(0, i);
-                    const float x = __builtin_amdgcn_exp2f(fmaf(st[i], a.scale_log2, -r.x));
-                    pf.raw[e] = (__bf16)(on ? x : 0.f);
-                    df.raw[e] = (__bf16)(on ? x * (dp[i] - r.y) : 0.f);
-                    seen[e] = (__bf16)(on ? 1.f : 0.f);
+                for (int i = 0; i < 16; i++) {
+                    st[i] = 0;
+                    if (kDK) dp[i] = 0;
                 }
 #pragma unroll
-                for (int d = 0; d < DB; d++) {
+                for (int kk = 0; kk < KK; kk++) {
                     Fragment<true> f;
-                    T::across(qx + kBytes, 16 * n, 32 * d, f);
-                    if (odd) mma_seen(dv[d], f, pf, seen);
-                    else mma(dv[d], f, pf);
-                    T::across(qx, 16 * n, 32 * d, f);
-                    if (odd) mma_seen(dk[d], f, df, seen);
-                    else mma(dk[d], f, df);
+                    T::along(qa, 0, kk, f);
+                    mma(st, f, k[kk]);
+                    if constexpr (kDK) {
+                        T::along(qa + kBytes, 0, kk, f);
+                        mma(dp, f, v[kk]);
+                    }
                     __builtin_amdgcn_sched_barrier(0);
                 }
             }
         }
-        step_on();
-        if (in_range(t, r0 + 32 * part)) {
-            const uint32_t qa = tile::lds_address(queries_at(t)) + along_lane;
+        // the second rows' sums to the first rows' waves
+        __syncthreads();
+        f32x4* sums = (f32x4*)lds + ((wave & 1) * 2 + kDK) * DB * 4 * 64;
+        if (part == 1) {
 #pragma unroll
-            for (int i = 0; i < 16; i++) st[i] = dp[i] = 0;
+            for (int d = 0; d < DB; d++)
 #pragma unroll
-            for (int kk = 0; kk < KK; kk++) {
-                Fragment<true> f;
-                T::along(qa, 0, kk, f);
-                mma(st, f, k[kk]);
-                T::along(qa + kBytes, 0, kk, f);
-                mma(dp, f, v[kk]);
-                __builtin_amdgcn_sched_barrier(0);
-            }
+                for (int j = 0; j < 4; j++) {
+                    f32x4 x;
+#pragma unroll
+                    for (int e = 0; e < 4; e++) x[e] = sum[d][4 * j + e];
+                    sums[(d * 4 + j) * 64 + lane] = x;
+                }
         }
-    }
-    // the second rows' sums to the first rows' waves
-    __syncthreads();
-    f32x4* sums = (f32x4*)lds + (wave & 1) * 2 * DB * 4 * 64;
-    if (part == 1) {
+        __syncthreads();
+        if (part == 1 || !live) return;
+        const float by = s.bad ? __uint_as_float(0x7FC00000u) : kDK ? a.scale : 1.f;
+        void* out = kDK ? a.dk : a.dv;
+        const int64_t o = token * (kDK ? a.lddk : a.lddv) + (int64_t)kv_head * D;
 #pragma unroll
         for (int d = 0; d < DB; d++)
 #pragma unroll
             for (int j = 0; j < 4; j++) {
-                f32x4 x, y;
+                const f32x4 x = sums[(d * 4 + j) * 64 + lane];
 #pragma unroll
-                for (int e = 0; e < 4; e++) {
-                    x[e] = dk[d][4 * j + e];
-                    y[e] = dv[d][4 * j + e];
-                }
-                sums[((2 * d) * 4 + j) * 64 + lane] = x;
-                sums[((2 * d + 1) * 4 + j) * 64 + lane] = y;
+                for (int e = 0; e < 4; e++) store1<true>(out, o + 32 * d + 8 * j + 4 * h + e, (sum[d][4 * j + e] + x[e]) * by);
             }
-    }
-    __syncthreads();
-    if (part == 1 || !live) return;
-    const float nan = __uint_as_float(0x7FC00000u);
-#pragma unroll
-    for (int d = 0; d < DB; d++)
-#pragma unroll
-        for (int j = 0; j < 4; j++) {
-            const f32x4 x = sums[((2 * d) * 4 + j) * 64 + lane], y = sums[((2 * d + 1) * 4 + j) * 64 + lane];
-#pragma unroll
-            for (int e = 0; e < 4; e++) {
-                const int at = 32 * d + 8 * j + 4 * h + e;
-                store1<true>(a.dk, token * a.lddk + (int64_t)kv_head * D + at, s.bad ? nan : (dk[d][4 * j + e] + x[e]) * a.scale);
-                store1<true>(a.dv, token * a.lddv + (int64_t)kv_head * D + at, s.bad ? nan : dv[d][4 * j + e] + y[e]);
-            }
-        }
+    };
+    if (wave < 4) pass(std::true_type{});
+    else pass(std::false_type{});
 }
 
 template <int D, bool DIRECT>
 hipError_t launch_beside(const PackedArgs& a, hipStream_t s) {
     const dim3 threads(64 * kBackwardWaves);
     hipLaunchKernelGGL((attention_dq_beside_kernel<D, DIRECT>), dim3((unsigned)(tile_slots(a.Tq, 32 * kBackwardWaves, a.n) * a.q_heads)), threads, 0, s, a);
-    hipLaunchKernelGGL((attention_dkv_beside_kernel<D, DIRECT>), dim3((unsigned)(tile_slots(a.Tk, 64, a.n) * a.kv_heads)), threads, 0, s, a);
+    hipLaunchKernelGGL((attention_dkv_beside_kernel<D, DIRECT>), dim3((unsigned)(tile_slots(a.Tk, 64, a.n) * a.kv_heads)), dim3(kBesideThreads), 0, s, a);
     return hipGetLastError();
 }
 

@@ -66,10 +66,37 @@ __global__ __launch_bounds__(kForwardWaves * 64, BF16 && D <= 128 ? 2 : 1) void 
 
     const char* kbase = (const char*)a.k + ((int64_t)s.k0 * a.ldk + (int64_t)kv_head * D) * (BF16 ? 2 : 4);
     const char* vbase = (const char*)a.v + ((int64_t)s.k0 * a.ldv + (int64_t)kv_head * D) * (BF16 ? 2 : 4);
-    auto masked_tile = [&](int k0) {  // for some row of the workgroup
-        return k0 + BK > s.keys || (a.causal && k0 + BK - 1 > row0 + s.shift) || (a.window && k0 <= last_row + s.shift - a.window);
-    };
+    // a tile whose keys all the workgroup's rows see begins with one of these keys
+    const int clear_from = a.window ? last_row + s.shift - a.window + 1 : INT32_MIN;
+    const int clear_to = min(s.keys - BK, a.causal ? row0 + s.shift - BK + 1 : INT32_MAX);
+    auto masked_tile = [&](int k0) { return k0 < clear_from || k0 > clear_to; };
+    // tiles of bf16 heads of up to 128 channels that go straight into LDS are stepped through
+    constexpr bool kLines = BF16 && D <= 128 && DIRECT;
     Pipe<BF16, D, BK, F::kThreads, DIRECT> pk, pv;
+    LinesToLds<kLines ? D : 64, 64, F::kThreads> to_k, to_v;
+    const char *k_at = kbase + (int64_t)begin * a.ldk * 2, *v_at = vbase + (int64_t)begin * a.ldv * 2;
+    if (kLines && begin < end) {
+        to_k.places(a.ldk, s.keys - begin);
+        to_v.places(a.ldv, s.keys - begin);
+    }
+    auto fetch_keys = [&](int k0, char* to) __attribute__((always_inline)) {
+        if constexpr (kLines) {
+            if (k0 > begin && k0 + BK > s.keys) to_k.places(a.ldk, s.keys - k0);
+            to_k.fetch(k_at, tile::lds_address(to), wave);
+            k_at += BK * 2 * a.ldk;
+        } else {
+            pk.fetch(kbase, a.ldk, k0, s.keys - k0, to);
+        }
+    };
+    auto fetch_values = [&](int k0, char* to) __attribute__((always_inline)) {
+        if constexpr (kLines) {
+            if (k0 > begin && k0 + BK > s.keys) to_v.places(a.ldv, s.keys - k0);
+            to_v.fetch(v_at, tile::lds_address(to), wave);
+            v_at += BK * 2 * a.ldv;
+        } else {
+            pv.fetch(vbase, a.ldv, k0, s.keys - k0, to);
+        }
+    };
     if (threadIdx.x < 2) odd_tile[threadIdx.x] = -1;
     // The products of a tile's scores run one tile ahead, beside the exponentials of the
     // tile before: keys of tile t + 1 and values of tile t are in LDS at a time.
@@ -114,7 +141,7 @@ __global__ __launch_bounds__(kForwardWaves * 64, BF16 && D <= 128 ? 2 : 1) void 
     };
     const uint32_t along_lane = T::along_lane(lane), across_lane = T::across_lane(lane);
     int buffer = 0;
-    if (begin < end) pk.fetch(kbase, a.ldk, begin, s.keys - begin, lds);
+    if (begin < end) fetch_keys(begin, lds);
     // Tile k0's values and the next one's keys have arrived, and those after them are fetched.
     auto advance = [&](int k0, bool check) __attribute__((always_inline)) {
         char* kt = lds + 2 * buffer * F::kTileBytes;
@@ -126,8 +153,8 @@ __global__ __launch_bounds__(kForwardWaves * 64, BF16 && D <= 128 ? 2 : 1) void 
             if (tile_not_finite<BF16, D, BK, F::kThreads>(kt + F::kTileBytes)) odd_tile[buffer] = k0;
             __syncthreads();
         }
-        if (next + BK < end) pk.fetch(kbase, a.ldk, next + BK, s.keys - next - BK, lds + 2 * (buffer ^ 1) * F::kTileBytes);
-        if (next < end) pv.fetch(vbase, a.ldv, next, s.keys - next, lds + (2 * (buffer ^ 1) + 1) * F::kTileBytes);
+        if (next + BK < end) fetch_keys(next + BK, lds + 2 * (buffer ^ 1) * F::kTileBytes);
+        if (next < end) fetch_values(next, lds + (2 * (buffer ^ 1) + 1) * F::kTileBytes);
     };
     // The next tile's scores, their maximum known, become this tile's.  The maximum that
     // exponentials are taken against follows only where a row's would pass 2^8: sums in
@@ -155,7 +182,7 @@ __global__ __launch_bounds__(kForwardWaves * 64, BF16 && D <= 128 ? 2 : 1) void 
             // with this tile's values, then some of the next scores' maximum.  The matrix
             // cores run while the wave goes on; operands are read a product ahead.
 #pragma unroll 1
-            while (k0 >= begin && k0 + BK < end && !masked_tile(k0) && !masked_tile(k0 + BK)) {
+            while (k0 >= begin && k0 + BK < end && k0 >= clear_from && k0 + BK <= clear_to) {
                 advance(k0, false);
                 const uint32_t ka = tile::lds_address(lds + 2 * buffer * F::kTileBytes) + along_lane;
                 const uint32_t va = tile::lds_address(lds + (2 * buffer + 1) * F::kTileBytes) + across_lane;

@@ -196,6 +196,40 @@ template <bool BF16, int D, int R, int THREADS> struct Pipe<BF16, D, R, THREADS,
     }
     __device__ void arrive(char*) const {}
 };
+// Lines of a bf16 tensor straight into a tile of LDS, for loops that step through it: the
+// lane's places from the first line on are kept, and a wave's loads are one block, with
+// one wait for the scalar registers of their address (see tile::load_lds16).
+template <int D, int R, int THREADS> struct LinesToLds {
+    typedef Tile<true, D> T;
+    static constexpr int kEach = R * T::kLine / THREADS;
+    static_assert(R * T::kLine % THREADS == 0 && (kEach == 1 || kEach == 2 || kEach == 4), "the blocks below");
+    uint32_t at[kEach];
+    __device__ void places(int64_t ld, int lines) {  // lines past the last repeat it
+#pragma unroll
+        for (int i = 0; i < kEach; i++) {
+            const int n = threadIdx.x + i * THREADS, r = n / T::kLine, c = (T::at(r, n % T::kLine) >> 4) % T::kLine;
+            at[i] = min(r, lines - 1) * (uint32_t)ld * 2 + (c < T::kChunks ? c : 0) * 16;
+        }
+    }
+    __device__ void fetch(const char* first, uint32_t lds, int wave) const {
+        uint32_t to = __builtin_amdgcn_readfirstlane(lds + wave * 1024);
+        const void* p = tile::uniform(first);
+        if constexpr (kEach == 1)
+            asm volatile("s_nop 4\n\tglobal_load_lds_dwordx4 %1, %2" : "+{m0}"(to) : "v"(at[0]), "s"(p) : "memory");
+        else if constexpr (kEach == 2)
+            asm volatile(
+                "s_nop 4\n\tglobal_load_lds_dwordx4 %1, %3\n\t"
+                "s_add_u32 m0, m0, %4\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %2, %3"
+                : "+{m0}"(to) : "v"(at[0]), "v"(at[1]), "s"(p), "i"(THREADS * 16) : "memory", "scc");
+        else
+            asm volatile(
+                "s_nop 4\n\tglobal_load_lds_dwordx4 %1, %5\n\t"
+                "s_add_u32 m0, m0, %6\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %2, %5\n\t"
+                "s_add_u32 m0, m0, %6\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %3, %5\n\t"
+                "s_add_u32 m0, m0, %6\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %4, %5"
+                : "+{m0}"(to) : "v"(at[0]), "v"(at[1]), "v"(at[2]), "v"(at[3]), "s"(p), "i"(THREADS * 16) : "memory", "scc");
+    }
+};
 template <bool DIRECT> __device__ inline void meet() {
     if (DIRECT) tile::wait_loads_and_meet();
     else __syncthreads();
