@@ -21,7 +21,9 @@ constexpr int kBackwardWaves = 4, kBackwardThreads = 64 * kBackwardWaves;
 // or keys (dK, dV) of its own and passes over the others 32 PARTS at a time, BLOCKS
 // PARTS = 4 waves, each with sums of its own that are added in order at the end: small
 // tiles, since few and short sequences have to fill the card and the products of fp32,
-// six of bf16 terms each, leave the time to load more.
+// six of bf16 terms each, leave the time to load more.  Two sequences of 611 and 54 tokens,
+// 6 and 3 heads of 96 in fp32: dQ 37 us, dK and dV 86 us, ten steps one after the other; of
+// a step's 6 us the products take a third.  fp32 heads of 192 and 256 channels spill.
 template <bool BF16, int D> struct PartsShape {
     static constexpr int kParts = BF16 || D <= 128 ? 4 : 2, kBlocks = kBackwardWaves / kParts;
     static constexpr int kOwn = 32 * kBlocks, kOther = 32 * kParts;
@@ -73,6 +75,23 @@ __device__ inline void bring(const char* base, int64_t ld, int64_t first, int li
             }
             *(u32x4*)(lds + T::at(r, c)) = v;
         }
+    }
+}
+
+// N products with an operand each from LDS, the second next one's read and the next one's
+// terms made beside a product.
+template <int N, bool BF16, typename Read, typename Use>
+__device__ inline void in_turn(Read read, Use use) {
+    Fragment<BF16> f[3];
+    read(0, f[0]);
+    if (N > 1) read(1, f[1]);
+    f[0].split();
+#pragma unroll
+    for (int i = 0; i < N; i++) {
+        if (i + 2 < N) read(i + 2, f[(i + 2) % 3]);
+        if (i + 1 < N) f[(i + 1) % 3].split();
+        use(i, f[i % 3]);
+        __builtin_amdgcn_sched_barrier(0);
     }
 }
 
@@ -158,43 +177,36 @@ __global__ __launch_bounds__(kBackwardThreads) void attention_dq_kernel(PackedAr
         f32x16 st, dp;
 #pragma unroll
         for (int i = 0; i < 16; i++) st[i] = dp[i] = 0;
-#pragma unroll
-        for (int kk = 0; kk < KK; kk++) {
-            Fragment<BF16> f, f2;
-            T::along(ka, 0, kk, f);
-            T::along(va, 0, kk, f2);
-            f.split();
-            f2.split();
-            mma(st, f, q[kk]);
-            mma(dp, f2, g[kk]);
-            if (!BF16) __builtin_amdgcn_sched_barrier(0);  // (terms of one step at a time: registers are short)
-        }
+        in_turn<2 * KK, BF16>([&](int i, Fragment<BF16>& f) { T::along(i & 1 ? va : ka, 0, i / 2, f); },
+                              [&](int i, const Fragment<BF16>& f) { mma(i & 1 ? dp : st, f, i & 1 ? g[i / 2] : q[i / 2]); });
 #pragma unroll
         for (int i = 0; i < 16; i++) {
             const float ds = __builtin_amdgcn_exp2f(fmaf(st[i], a.scale_log2, -lse)) * (dp[i] - delta);
             st[i] = masked && !span.has(0, i) ? 0.f : ds;
         }
+        Fragment<BF16> df[2];
 #pragma unroll
         for (int n = 0; n < 2; n++) {
             float v[8];
+#pragma unroll
+            for (int e = 0; e < 8; e++) v[e] = st[8 * n + e];
+            operand_of(v, df[n]);
+        }
+        if (!odd) {
+            in_turn<2 * DB, BF16>([&](int i, Fragment<BF16>& f) { T::across(kx, 16 * (i / DB), 32 * (i % DB), f); },
+                                  [&](int i, const Fragment<BF16>& f) { mma(out[i % DB], f, df[i / DB]); });
+            continue;
+        }
+#pragma unroll
+        for (int n = 0; n < 2; n++) {
             bf16x8 seen;
 #pragma unroll
-            for (int e = 0; e < 8; e++) {
-                v[e] = st[8 * n + e];
-                seen[e] = (__bf16)(span.has(0, 8 * n + e) ? 1.f : 0.f);
-            }
-            Fragment<BF16> df;
-            operand_of(v, df);
+            for (int e = 0; e < 8; e++) seen[e] = (__bf16)(span.has(0, 8 * n + e) ? 1.f : 0.f);
 #pragma unroll
             for (int d = 0; d < DB; d++) {
                 Fragment<BF16> f;
                 T::across(kx, 16 * n, 32 * d, f);
-                if (odd) {
-                    mma_seen(out[d], f, df, seen);
-                } else {
-                    f.split();
-                    mma(out[d], f, df);
-                }
+                mma_seen(out[d], f, df[n], seen);
                 if (!BF16) __builtin_amdgcn_sched_barrier(0);
             }
         }
@@ -287,19 +299,11 @@ __global__ __launch_bounds__(kBackwardThreads) void attention_dkv_kernel(PackedA
             f32x16 st, dp;
 #pragma unroll
             for (int i = 0; i < 16; i++) st[i] = dp[i] = 0;
-#pragma unroll
-            for (int kk = 0; kk < KK; kk++) {
-                Fragment<BF16> f;
-                T::along(qa, 0, kk, f);
-                f.split();
-                mma(st, f, k[kk]);
-                if constexpr (kDk) {
-                    T::along(ga, 0, kk, f);
-                    f.split();
-                    mma(dp, f, v[kk]);
-                }
-                if (!BF16) __builtin_amdgcn_sched_barrier(0);
-            }
+            if constexpr (kDk)
+                in_turn<2 * KK, BF16>([&](int i, Fragment<BF16>& f) { T::along(i & 1 ? ga : qa, 0, i / 2, f); },
+                                      [&](int i, const Fragment<BF16>& f) { mma(i & 1 ? dp : st, f, i & 1 ? v[i / 2] : k[i / 2]); });
+            else
+                in_turn<KK, BF16>([&](int i, Fragment<BF16>& f) { T::along(qa, 0, i, f); }, [&](int i, const Fragment<BF16>& f) { mma(st, f, k[i]); });
             float p[16];
 #pragma unroll
             for (int j = 0; j < 4; j++)
@@ -313,46 +317,44 @@ __global__ __launch_bounds__(kBackwardThreads) void attention_dkv_kernel(PackedA
                     p[i] = off ? 0.f : p[i];
                     st[i] = off ? 0.f : ds;
                 }
+            Fragment<BF16> pf[2], df[2];
 #pragma unroll
             for (int n = 0; n < 2; n++) {
-                Fragment<BF16> pf, df;
                 float x[8];
-                bf16x8 seen;
-#pragma unroll
-                for (int e = 0; e < 8; e++) seen[e] = (__bf16)(span.has(0, 8 * n + e) ? 1.f : 0.f);
                 if constexpr (kDv) {
 #pragma unroll
                     for (int e = 0; e < 8; e++) x[e] = p[8 * n + e];
-                    operand_of(x, pf);
+                    operand_of(x, pf[n]);
                 }
                 if constexpr (kDk) {
 #pragma unroll
                     for (int e = 0; e < 8; e++) x[e] = st[8 * n + e];
-                    operand_of(x, df);
+                    operand_of(x, df[n]);
                 }
+            }
+            // products i: of dV and dK in turn, or of the one of them
+            constexpr int kBoth = kDv && kDk ? 2 : 1;
+            auto is_dv = [](int i) { return kBoth == 2 ? i % 2 == 0 : kDv; };
+            auto read = [&](int i, Fragment<BF16>& f) { T::across(is_dv(i) ? gx : qx, 16 * (i / kBoth / DB), 32 * (i / kBoth % DB), f); };
+            if (!odd) {
+                in_turn<2 * DB * kBoth, BF16>(read, [&](int i, const Fragment<BF16>& f) {
+                    const int n = i / kBoth / DB, d = i / kBoth % DB;
+                    if (is_dv(i)) mma(dv[kDv ? d : 0], f, pf[n]);
+                    else mma(dk[kDk ? d : 0], f, df[n]);
+                });
+                continue;
+            }
 #pragma unroll
-                for (int d = 0; d < DB; d++) {
-                    Fragment<BF16> f;
-                    if constexpr (kDv) {
-                        T::across(gx, 16 * n, 32 * d, f);
-                        if (odd) {
-                            mma_seen(dv[d], f, pf, seen);
-                        } else {
-                            f.split();
-                            mma(dv[d], f, pf);
-                        }
-                    }
-                    if constexpr (kDk) {
-                        T::across(qx, 16 * n, 32 * d, f);
-                        if (odd) {
-                            mma_seen(dk[d], f, df, seen);
-                        } else {
-                            f.split();
-                            mma(dk[d], f, df);
-                        }
-                    }
-                    if (!BF16) __builtin_amdgcn_sched_barrier(0);
-                }
+            for (int i = 0; i < 2 * DB * kBoth; i++) {
+                const int n = i / kBoth / DB, d = i / kBoth % DB;
+                bf16x8 seen;
+#pragma unroll
+                for (int e = 0; e < 8; e++) seen[e] = (__bf16)(span.has(0, 8 * n + e) ? 1.f : 0.f);
+                Fragment<BF16> f;
+                read(i, f);
+                if (is_dv(i)) mma_seen(dv[kDv ? d : 0], f, pf[n], seen);
+                else mma_seen(dk[kDk ? d : 0], f, df[n], seen);
+                if (!BF16) __builtin_amdgcn_sched_barrier(0);
             }
         }
     if constexpr (kDk) add_parts<DB, B::kParts, B::kBlocks>(dk, lds, part, block, lane);
@@ -879,7 +881,10 @@ hipError_t launch_parts(const PackedArgs& a, hipStream_t s) {
     typedef PartsShape<BF16, D> B;
     const dim3 threads(kBackwardThreads), q_groups((unsigned)(tile_slots(a.Tq, B::kOwn, a.n) * a.q_heads)), k_groups((unsigned)(tile_slots(a.Tk, B::kOwn, a.n) * a.kv_heads));
     hipLaunchKernelGGL((attention_dq_kernel<BF16, D, DIRECT>), q_groups, threads, 0, s, a);
-    if constexpr (BF16 || D <= 128) {
+    // Both sums in a wave up to 96 channels; past that they, the operands and what is on its way
+    // do not fit into its registers: 3548 tokens of 16 and 4 heads of 128 in fp32 1.4 ms that way,
+    // 1.1 ms so; of 256 in bf16 1.8 and 0.8 ms (products: five in place of four).
+    if constexpr (D <= 96) {
         hipLaunchKernelGGL((attention_dkv_kernel<BF16, D, 3, DIRECT>), k_groups, threads, 0, s, a);
     } else {
         hipLaunchKernelGGL((attention_dkv_kernel<BF16, D, 1, DIRECT>), k_groups, threads, 0, s, a);
