@@ -380,8 +380,8 @@ __global__ __launch_bounds__(kBackwardThreads) void attention_dkv_kernel(PackedA
 // (dK, dV).
 // DIRECT: tiles go straight from memory into LDS.
 // Four sequences of up to 4096 tokens, 16 query and 4 key heads of 128, causal: dQ 193 us,
-// dK and dV 355 us, the matrix cores busy for a third of the time; what is left is the
-// vector unit's work (instructions of two waves to a unit), and, of dK and dV, that the
+// dK and dV 360 us, the matrix cores busy for 0.46 of it; what is left is the vector unit's
+// work, reads of LDS behind a step's barrier and, of dK and dV, that the
 // longest sequence's first keys take 256 steps where the average CU has 195.
 constexpr int kAhead = 2;  // products between an operand's read and its use
 
@@ -587,7 +587,7 @@ __global__ __launch_bounds__(kBackwardWaves * 64, 2) void attention_dq_beside_ke
 // 32 x 32 blocks of these one wave adds to dK, another to dV, and the two over the same
 // keys are added at the end.  S is computed by both, five products in place of four, but
 // a wave's registers then leave room for a second one to each unit.  (With both sums in a
-// wave, and one wave to a unit, the unit stood still for most of the time: 432 us for 355.)
+// wave, and one wave to a unit, the unit stood still for most of the time: 432 us for 360.)
 constexpr int kBesideThreads = 512;
 template <int D, bool DIRECT>
 __global__ __launch_bounds__(kBesideThreads, 2) void attention_dkv_beside_kernel(PackedArgs a) {

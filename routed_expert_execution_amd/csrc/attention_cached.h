@@ -72,13 +72,14 @@ __device__ inline uint32_t line_of(const CachedArgs& a, Sequence* last) {
     return total < (1u << 31) ? (uint32_t)total : 0;
 }
 // The tile at place `at` of the line, or the call's tile `at` (TILES).  Every wave finds
-// it for itself, 64 sequences a pass.  all: the sequences, where there are no more than
-// 64 and they are at hand.
+// it for itself, 64 sequences a pass, from where it found the one before (which does not
+// lie after it).  all: the sequences, where there are no more than 64 and they are at hand.
+struct Found { int base; uint32_t line, tiles; };  // a multiple of 64 sequences, and what lies before them
 template <bool TILES>
-__device__ inline bool find_work(const CachedArgs& a, uint32_t at, Work* out, const Sequence* all) {
+__device__ inline bool find_work(const CachedArgs& a, uint32_t at, Work* out, Found* found, const Sequence* all) {
     const int lane = threadIdx.x & 63, n = a.batch.n;
-    uint32_t before = 0, tiles_before = 0;
-    for (int base = 0; base < n; base += 64) {
+    uint32_t before = found->line, tiles_before = found->tiles;
+    for (int base = found->base; base < n; base += 64) {
         Sequence q{};
         if (all && n <= 64) q = *all;
         else if (base + lane < n) q = sequence_of(a, base + lane);
@@ -97,6 +98,7 @@ __device__ inline bool find_work(const CachedArgs& a, uint32_t at, Work* out, co
             const uint32_t count = of_k(q.tiles), from = before + of_k(line) - count * out->rounds;
             out->tile = __builtin_amdgcn_readfirstlane(TILES ? at - (tiles_before + of_k(tiles) - count) : (at - from) / out->rounds);
             out->start = from + out->tile * out->rounds;
+            *found = Found{base, before, tiles_before};
             return true;
         }
         before += __builtin_amdgcn_readlane(line, 63);
@@ -178,7 +180,8 @@ __global__ __launch_bounds__(kThreads, cached_per_cu(W, BF16)) void cached_kerne
     const uint32_t run_end = min((run_index + 1) * (uint64_t)run, (uint64_t)line);
     uint32_t place = run_index * (uint64_t)run < run_end ? run_index * run : run_end;
     Work c;
-    if (place >= run_end || !find_work<false>(a, place, &c, &sequences)) return;
+    Found found{};
+    if (place >= run_end || !find_work<false>(a, place, &c, &found, &sequences)) return;
 #pragma unroll 1
     for (;;) {
         // (what follows from the lane is worked out for each part: it is not kept beside the sums)
@@ -431,7 +434,7 @@ __global__ __launch_bounds__(kThreads, cached_per_cu(W, BF16)) void cached_kerne
             }
         }
         place = part_end;
-        if (place >= run_end || !find_work<false>(a, place, &c, nullptr)) return;
+        if (place >= run_end || !find_work<false>(a, place, &c, &found, nullptr)) return;
     }
 }
 
@@ -449,8 +452,9 @@ __global__ __launch_bounds__(kJoinThreads) void cached_join_kernel(CachedArgs a)
     Sequence sequences;
     const uint32_t line = line_of(a, &sequences), run = __builtin_amdgcn_readfirstlane(run_of(a, line));
     Work c;
+    Found found{};
     const uint64_t cut = (blockIdx.x + 1) * (uint64_t)run;
-    if (line == 0 || (!BY_TILE && cut >= line) || !find_work<BY_TILE>(a, BY_TILE ? blockIdx.x : (uint32_t)cut, &c, &sequences)) return;
+    if (line == 0 || (!BY_TILE && cut >= line) || !find_work<BY_TILE>(a, BY_TILE ? blockIdx.x : (uint32_t)cut, &c, &found, &sequences)) return;
     const uint32_t start = c.start, end = start + c.rounds;
     if (!BY_TILE && (start >= cut || start + run < cut)) return;
     const int run_0 = start / run, of = (end - 1) / run - run_0 + 1;
