@@ -627,7 +627,8 @@ size_t moe_kv_bytes(int64_t pages, int32_t page_tokens, int32_t heads, int32_t h
  * of the packed tensors; it has lengths[s] tokens (device int32 [n]) in the cache
  * once those are in it, the new ones last; its token at place i lies in page
  * pages[s * max_pages + i / page_tokens] (device int32 [n, max_pages]).  Entries past
- * a sequence's tokens are not read.  most_new: no sequence has more new tokens.
+ * a sequence's tokens are not read, nor by moe_attention_cached those of pages that lie
+ * before the windows of all its new tokens.  most_new: no sequence has more new tokens.
  * n up to 65536, max_pages * page_tokens up to 2^30, tokens up to 2^22. */
 typedef struct moe_kv_batch {
     const int32_t *offsets, *lengths, *pages;
@@ -664,9 +665,10 @@ moe_status moe_kv_read(moe_ctx* ctx, const moe_kv_cache* cache, const moe_kv_bat
  * cannot be (a length below its new tokens or above its pages, more than most_new of
  * them) and rows that see a place on a page outside the cache become NaN; other rows of
  * a sequence with such a page may.  (tokens * q_heads / heads / 16 + n) * (max_pages *
- * page_tokens / 128), each rounded up, stays below 2^31.  workspace: device, 256-byte
- * aligned, moe_attention_cached_workspace() bytes or more, used until the call's work
- * is done; calls that may run at the same time need one each. */
+ * page_tokens / 128), each rounded up, stays below 2^31, and the first factor below
+ * 2^27.  workspace: device, 256-byte aligned, moe_attention_cached_workspace() bytes
+ * or more, used until the call's work is done; calls that may run at the same time
+ * need one each. */
 size_t moe_attention_cached_workspace(const moe_kv_cache* cache, const moe_kv_batch* batch, int32_t q_heads); /* 0: not valid */
 moe_status moe_attention_cached(moe_ctx* ctx, const moe_kv_cache* cache, const moe_kv_batch* batch, const void* q, int64_t ldq,
                                 int32_t dtype, int32_t q_heads, float scale, int64_t window, void* out, int64_t ldo,

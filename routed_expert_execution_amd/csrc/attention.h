@@ -119,7 +119,7 @@ struct CachedArgs {
     KvBatchView batch;
     const void* q;
     int64_t ldq;
-    int bf16, q_heads, per_head;  // per_head: query heads of one key head
+    int bf16, per_head;           // per_head: query heads of one key head
     float scale_log2;             // scale / ln 2: the exponentials are powers of two
     int window;                   // 0: none
     void* out;

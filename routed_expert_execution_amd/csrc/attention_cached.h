@@ -206,7 +206,8 @@ __global__ __launch_bounds__(kThreads, cached_per_cu(W, BF16)) void cached_kerne
         const int first_token = __builtin_amdgcn_readfirstlane(c.tile * 16 / a.per_head), last_token = __builtin_amdgcn_readfirstlane(min(c.tile * 16 + 15, rows - 1) / a.per_head);
         const int last_step = min(c.first + (int)(part_end - c.start) * kWaves, (old + last_token + kStep) / kStep);
         int step = c.first + (int)(place - c.start) * kWaves;
-        if (a.window) step += max(0, (old + first_token - a.window + 1) / kStep - step) / kWaves * kWaves;
+        const int tile_from = a.window ? old + first_token - a.window + 1 : 0;  // what lies before is seen by none: its pages may be gone
+        step += max(0, tile_from / kStep - step) / kWaves * kWaves;
         step += wave;
         if (c.bad && threadIdx.x == 0) atomicOr(a.err, kErrCache);
 
@@ -216,7 +217,7 @@ __global__ __launch_bounds__(kThreads, cached_per_cu(W, BF16)) void cached_kerne
         struct Loaded { uint32_t k[2][W], v[2][W], steps[4][kParams]; };
         auto page_of = [&](int step, int i) -> int {  // wave-uniform
             const int at = step * kStep + 16 * i;
-            return step < last_step && at < c.length ? table[at >> kv.page_shift] : 0;
+            return step < last_step && at < c.length && at + 16 > tile_from ? table[at >> kv.page_shift] : 0;
         };
         auto load = [&](int step, const int (&pages)[2], Loaded& d) {
 #pragma unroll

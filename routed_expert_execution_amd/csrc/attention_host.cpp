@@ -227,12 +227,12 @@ moe_status moe_attention_cached(moe_ctx* c, const moe_kv_cache* cache, const moe
     CHECK(workspace_bytes >= need, "%s: workspace of %zu bytes, %zu needed", fn, workspace_bytes, need);
     a.bf16 = dtype == MOE_BF16;
     const moe::CachedPlan p = moe::cached_plan(g, batch->n, T, (int)batch->most_new, batch->max_pages, q_heads, a.bf16);
-    CHECK(p.line < ((int64_t)1 << 31), "%s: too many tokens over too long a page table for one call", fn);
+    CHECK(p.line < ((int64_t)1 << 31) && p.tiles < (1 << 27), "%s: too many tokens over too long a page table for one call", fn);
     if (moe_status st = need_device(c)) return st;
     if (T == 0 || batch->n == 0) return MOE_OK;
     a.cache = moe::kv_view(g, cache->data);
     a.q = q; a.ldq = T > 1 ? ldq : width;
-    a.q_heads = q_heads; a.per_head = q_heads / g.heads;
+    a.per_head = q_heads / g.heads;
     a.scale_log2 = (float)((double)scale * 1.4426950408889634);
     a.window = (int)(window < (1 << 30) ? window : 0);  // (none reaches further back)
     a.out = out; a.ldo = T > 1 ? ldo : width;

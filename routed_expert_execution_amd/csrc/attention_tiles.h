@@ -147,18 +147,6 @@ struct Staged {
             if (n < R * T::kChunks) *(u32x4*)(lds + T::at(r, c)) = v[i];
         }
     }
-    __device__ bool any_not_finite() const {
-        uint32_t bad = 0;
-#pragma unroll
-        for (int i = 0; i < kEach; i++)
-#pragma unroll
-            for (int e = 0; e < 4; e++) {
-                const uint32_t w = v[i][e];
-                if (BF16) bad |= (uint32_t)((w & 0x7F80u) == 0x7F80u) | (uint32_t)((w & 0x7F800000u) == 0x7F800000u);
-                else bad |= (uint32_t)((w & 0x7F800000u) == 0x7F800000u);
-            }
-        return bad;
-    }
 };
 
 // The same tile fetched ahead: straight into LDS (DIRECT) or by registers on the way.

@@ -130,7 +130,11 @@ CASES = [
     ([333], None, 4, 4, 128, True, 1, BF16, 0), ([150], None, 2, 1, 96, True, 64, F32, 0), ([40, 7], [170, 300], 4, 2, 128, True, 0, BF16, 0),
     ([170, 5], [40, 5], 4, 2, 128, True, 0, BF16, 0), ([170, 5], [40, 9], 2, 1, 96, False, 0, F32, 0), ([3, 4, 0], [0, 70, 9], 2, 2, 64, True, 0, BF16, 0),
     ([100], [300], 2, 1, 64, True, 130, F32, 0), ([500], [130], 2, 1, 64, True, 40, BF16, 0), ([700], None, 7, 1, 64, True, 0, BF16, 0),
-    ([5] * 70, None, 2, 1, 64, True, 0, BF16, 0), ([1, 700], [400, 3], 2, 2, 256, False, 0, BF16, 0), ([161], None, 2, 2, 96, False, 0, BF16, 0)]
+    ([5] * 70, None, 2, 1, 64, True, 0, BF16, 0), ([1, 700], [400, 3], 2, 2, 256, False, 0, BF16, 0), ([161], None, 2, 2, 96, False, 0, BF16, 0),
+    # long enough for steps without a mask, an odd and an even number of them, between others
+    ([1100, 70], None, 6, 2, 128, True, 0, BF16, 0), ([900], None, 4, 4, 96, False, 0, BF16, 8), ([777], None, 8, 1, 64, True, 300, BF16, 0),
+    ([640], [1000], 3, 1, 128, True, 0, BF16, 5), ([900, 450], None, 2, 1, 128, True, 500, BF16, 3), ([1000], [300], 4, 2, 64, False, 0, BF16, 0),
+    ([400], None, 4, 2, 192, True, 0, F32, 0), ([300, 100], None, 2, 1, 256, True, 0, F32, 3), ([520], None, 4, 1, 128, True, 200, F32, 0), ([600], None, 2, 1, 256, True, 0, BF16, 0)]
 
 
 @pytest.mark.parametrize("lq,lk,heads,Hkv,D,causal,window,dtype,gap", CASES)

@@ -68,7 +68,8 @@ CASES = [
     # a prompt's part beside single tokens, more sequences than a wave has lanes: a run is several sequences' tiles
     ([1] * 40 + [90] + [1] * 40 + [0, 17], [i * 37 % 700 + 1 for i in range(40)] + [2500] + [i * 53 % 900 + 1 for i in range(40)] + [5, 1700], 16, 8, 2, 64, 32, 0, BF16, 0),
     ([1] * 70 + [33, 2], [i * 29 % 500 + 1 for i in range(70)] + [1500, 800], 64, 12, 4, 128, 64, 200, F32, 0),
-    ([1, 1, 1, 260, 1], [9000, 1, 128, 4000, 129], 32, 8, 2, 128, 128, 0, BF16, 0), ([500], [500], 16, 16, 16, 128, 32, 0, BF16, 0), ([500], [900], 16, 4, 4, 96, 32, 70, BF16, 0)]
+    ([1, 1, 1, 260, 1], [9000, 1, 128, 4000, 129], 32, 8, 2, 128, 128, 0, BF16, 0), ([500], [500], 16, 16, 16, 128, 32, 0, BF16, 0), ([500], [900], 16, 4, 4, 96, 32, 70, BF16, 0),
+    ([i % 3 for i in range(700)], [i * 31 % 190 + 2 for i in range(700)], 16, 2, 1, 64, 32, 0, BF16, 0)]
 
 
 @pytest.mark.parametrize("new,lengths,page,heads,Hkv,D,group,window,dtype,gap", CASES)
@@ -178,6 +179,19 @@ def test_uninitialised_memory_is_not_read(ctx):
         moe.moe_kv_append(ctx, cache, batch, *x)
         out = _call(ctx, cache, batch, A.normal(g, length, 2, 64, F32))
         assert out.isfinite().all()
+
+
+@pytest.mark.parametrize("new,lengths,page,window,dtype", [([1], [400], 16, 50, BF16), ([3, 1], [1000, 333], 16, 17, F32), ([40], [700], 32, 100, BF16), ([1], [129], 64, 1, BF16)])
+def test_pages_before_the_window_may_be_gone(ctx, new, lengths, page, window, dtype):
+    g = A.gen(21)
+    table, pages = A.page_table(g, lengths, page)
+    held = A.Held(ctx, g, pages, page, 1, 64, 32)
+    q = A.normal(g, sum(new), 4, 64, dtype)
+    out = _call(ctx, held.cache, moe.KvBatch(ctx, A.offsets(new), A.ints(lengths), table, tokens=sum(new), most_new=max(new)), q, window=window)
+    for s, (n, length) in enumerate(zip(new, lengths)):
+        table[s, :max(0, length - n - window + 1) // page] = -1
+    gone = _call(ctx, held.cache, moe.KvBatch(ctx, A.offsets(new), A.ints(lengths), table, tokens=sum(new), most_new=max(new)), q, window=window)
+    assert moe.moe_check(ctx) == moe.MOE_OK and torch.equal(gone, out)
 
 
 def test_places_that_cannot_be(ctx):
