@@ -124,6 +124,12 @@ __device__ inline uint32_t codes16(uint32_t w, int part, const CodeMasks& c) {
     const uint32_t v = part == 0 ? w << 3 : part == 1 ? w >> 1 : part == 2 ? w >> 5 : w >> 9;
     return (v & c.mask) | c.bias;
 }
+// The same less 24: code - 8, which lies about zero as the values do.
+__device__ inline uint32_t codes8(uint32_t w, int part, const CodeMasks& c) {
+    const uint32_t v = codes16(w, part, c);
+    const float lo = __uint_as_float(v << 16) - 24.f, hi = __uint_as_float(v & 0xFFFF0000u) - 24.f;  // (exact, in bf16 too)
+    return __float_as_uint(lo) >> 16 | (__float_as_uint(hi) & 0xFFFF0000u);
+}
 // Maximum over the four 16-lane rows.
 __device__ inline float cross_row_max(float v) {
     auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
@@ -162,9 +168,12 @@ template <int N> __device__ inline void terms_of(const float (&v)[8], bf16x8_t (
 template <int W, int JP, bool BF16>
 __global__ __launch_bounds__(kThreads, cached_per_cu(W, BF16)) void cached_kernel(CachedArgs a) {
     constexpr int N = BF16 ? 1 : 3;  // bf16 terms of a factor
+    // fp32: both products take code - 8, whose sums lose nothing to an offset; bf16, where
+    // that is far below the rounding of P: 16 + code, and -24 by a product of its own in the second
+    constexpr bool kCentred = !BF16;
     constexpr int D = 32 * W, G = W / JP;
     constexpr int kParams = (16 * G + 63) / 64;  // words of one tile's steps a lane loads
-    // a step's (step, lowest) pairs: of keys the step and lowest - 16 steps, of values the step and lowest + 8 steps
+    // a step's (step, lowest) pairs: the step, and lowest + 8 steps (bf16: of keys lowest - 16 steps)
     __shared__ __attribute__((aligned(16))) float pairs[kWaves][4][2][16 * G];
     __shared__ float joined[2][16][D + 4];
     __shared__ float2 stats[kWaves][16];
@@ -174,6 +183,7 @@ __global__ __launch_bounds__(kThreads, cached_per_cu(W, BF16)) void cached_kerne
     Sequence sequences;
     const uint32_t line = line_of(a, &sequences), run = __builtin_amdgcn_readfirstlane(run_of(a, line));
     const CodeMasks masks = code_masks();
+    auto code = [&](uint32_t w, int part) { return kCentred ? codes8(w, part, masks) : codes16(w, part, masks); };
     const uint32_t head_bytes = (uint32_t)kv.tile_bytes << (kv.page_shift - 4), page_bytes = head_bytes * kv.heads;
     const uint8_t* heads_at = kv.data + (uint64_t)head * head_bytes;
 
@@ -281,7 +291,7 @@ __global__ __launch_bounds__(kThreads, cached_per_cu(W, BF16)) void cached_kerne
                         const uint32_t w = step * kStep + 16 * (x & 1) + r16 < c.length ? now.steps[x][n] : 0u;
                         const float by = f16_bits_to_f32(w & 0xFFFF);
                         pairs[wave][x][0][lane + 64 * n] = by;
-                        const float rest = fmaf(x < 2 ? -16.f : 8.f, by, f16_bits_to_f32(w >> 16));
+                        const float rest = fmaf(x < 2 && !kCentred ? -16.f : 8.f, by, f16_bits_to_f32(w >> 16));
                         pairs[wave][x][1][lane + 64 * n] = rest;
                         if (x >= 2) fine &= rest == rest;
                     }
@@ -302,7 +312,7 @@ __global__ __launch_bounds__(kThreads, cached_per_cu(W, BF16)) void cached_kerne
                     f32x4 r = {0, 0, 0, 0};
 #pragma unroll
                     for (int j = g * JP; j < (g + 1) * JP; j++) {
-                        const u32x4 w = {codes16(now.k[i][j], 0, masks), codes16(now.k[i][j], 1, masks), codes16(now.k[i][j], 2, masks), codes16(now.k[i][j], 3, masks)};
+                        const u32x4 w = {code(now.k[i][j], 0), code(now.k[i][j], 1), code(now.k[i][j], 2), code(now.k[i][j], 3)};
                         r = product<N>(__builtin_bit_cast(bf16x8_t, w), q[j], r);
                     }
                     const int group = 16 * g + 4 * q4;
@@ -374,11 +384,13 @@ __global__ __launch_bounds__(kThreads, cached_per_cu(W, BF16)) void cached_kerne
                     for (int j = g * JP; j < (g + 1) * JP; j++) {
                         uint32_t w0 = now.v[0][j], w1 = now.v[1][j];
                         if constexpr (masked.value) asm("" : "+v"(w0), "+v"(w1));  // (so that the two branches' codes are not made before them)
-                        const u32x4 lo = {codes16(w0, 0, masks), codes16(w0, 2, masks), codes16(w1, 0, masks), codes16(w1, 2, masks)};
-                        const u32x4 hi = {codes16(w0, 1, masks), codes16(w0, 3, masks), codes16(w1, 1, masks), codes16(w1, 3, masks)};
-                        const u32x4 bias = {0xC1C0C1C0u, 0xC1C0C1C0u, 0xC1C0C1C0u, 0xC1C0C1C0u};  // -24: code - 8 of 16 + code
-                        out[2 * j] = product<N>(__builtin_bit_cast(bf16x8_t, bias), b, out[2 * j]);
-                        out[2 * j + 1] = product<N>(__builtin_bit_cast(bf16x8_t, bias), b, out[2 * j + 1]);
+                        const u32x4 lo = {code(w0, 0), code(w0, 2), code(w1, 0), code(w1, 2)};
+                        const u32x4 hi = {code(w0, 1), code(w0, 3), code(w1, 1), code(w1, 3)};
+                        if constexpr (!kCentred) {
+                            const u32x4 bias = {0xC1C0C1C0u, 0xC1C0C1C0u, 0xC1C0C1C0u, 0xC1C0C1C0u};  // -24: code - 8 of 16 + code
+                            out[2 * j] = product<N>(__builtin_bit_cast(bf16x8_t, bias), b, out[2 * j]);
+                            out[2 * j + 1] = product<N>(__builtin_bit_cast(bf16x8_t, bias), b, out[2 * j + 1]);
+                        }
                         out[2 * j] = product<N>(__builtin_bit_cast(bf16x8_t, lo), b, out[2 * j]);
                         out[2 * j + 1] = product<N>(__builtin_bit_cast(bf16x8_t, hi), b, out[2 * j + 1]);
                         __builtin_amdgcn_sched_barrier(0);
