@@ -2,12 +2,13 @@
 // exponentials L and the outputs O that the forward pass has kept:
 //   P = exp(scale Q K^T - L),  dV = P^T dO,  dP = dO V^T,  delta = rowsum(dO O),
 //   dS = P (dP - delta),  dQ = scale dS K,  dK = scale dS^T Q.
-// Two kernels, each with results of its own rows only, so that sums have one order
-// and nothing is added in memory: dQ over tiles of queries, dK and dV over tiles of
-// keys (with all query heads of the key head).  S and dP are computed in both: seven
-// products in place of five.
+// delta first, then one launch of workgroups with results of their own rows only, so that
+// sums have one order and nothing is added in memory: dQ over tiles of queries, dK and dV
+// over tiles of keys (with all query heads of the key head).  S and dP are computed in
+// each: seven or eight products in place of five.
 #pragma once
 
+#include <algorithm>
 #include <type_traits>
 
 #include "attention_tiles.h"
@@ -22,8 +23,9 @@ constexpr int kBackwardWaves = 4, kBackwardThreads = 64 * kBackwardWaves;
 // PARTS = 4 waves, each with sums of its own that are added in order at the end: small
 // tiles, since few and short sequences have to fill the card and the products of fp32,
 // six of bf16 terms each, leave the time to load more.  Two sequences of 611 and 54 tokens,
-// 6 and 3 heads of 96 in fp32: dQ 37 us, dK and dV 86 us, ten steps one after the other; of
-// a step's 6 us the products take a third.  fp32 heads of 192 and 256 channels spill.
+// 6 and 3 heads of 96 in fp32: 65 us (one launch after the other, dK and dV together: 123),
+// ten steps one after the other, of whose 4 us the products take half.  fp32 heads of 192
+// and 256 channels spill.
 template <bool BF16, int D> struct PartsShape {
     static constexpr int kParts = BF16 || D <= 128 ? 4 : 2, kBlocks = kBackwardWaves / kParts;
     static constexpr int kOwn = 32 * kBlocks, kOther = 32 * kParts;
@@ -95,23 +97,42 @@ __device__ inline void in_turn(Read read, Use use) {
     }
 }
 
-// dQ, and delta for the other kernel: S^T = K Q^T and dP^T = V dO^T with a row a lane,
+// What the others need of each row: L / ln 2 and delta = rowsum(dO O), by 16 or 32 lanes a
+// row.  Bound by bytes: 8532 rows of 16 heads of 128 in bf16 14 us.
+constexpr int kRowsThreads = 256;
+template <bool BF16, int D>
+__global__ __launch_bounds__(kRowsThreads) void attention_rows_kernel(PackedArgs a) {
+    constexpr int kLanes = D <= 128 ? 16 : 32, kRows = kRowsThreads / kLanes;
+    const int c = threadIdx.x % kLanes;
+    // (rows of no sequence are not read)
+    const int64_t from = (int64_t)clamp_to(a.offsets_q[0], a.Tq) * a.q_heads, to = (int64_t)clamp_to(a.offsets_q[a.n], a.Tq) * a.q_heads;
+    for (int64_t first = from + (int64_t)blockIdx.x * kRows; first < to; first += (int64_t)gridDim.x * kRows) {
+        const int64_t at = first + threadIdx.x / kLanes, token = at / a.q_heads;
+        const int head = (int)(at - token * a.q_heads);
+        float delta = 0;
+        if (at < to && c < D / 8) {
+            float o[8], g[8];
+            load8<BF16>(a.out, token * a.ldo + (int64_t)head * D + 8 * c, o);
+            load8<BF16>(a.dout, token * a.lddo + (int64_t)head * D + 8 * c, g);
+#pragma unroll
+            for (int e = 0; e < 8; e++) delta = fmaf(g[e], o[e], delta);
+        }
+        delta = seg_sum<kLanes>(delta);
+        if (at < to && c == 0) a.rows[(int64_t)head * a.Tq + token] = make_float2(a.lse[at] * kLog2e, delta);
+    }
+}
+
+// dQ: S^T = K Q^T and dP^T = V dO^T with a row a lane,
 // dQ^T = K^T dS^T.
 template <bool BF16, int D, bool DIRECT>
-__global__ __launch_bounds__(kBackwardThreads) void attention_dq_kernel(PackedArgs a) {
+__device__ inline void attention_dq_parts(const PackedArgs& a, int group, char* lds, int& odd_tile) {
     typedef PartsShape<BF16, D> B;
     typedef Tile<BF16, D> T;
     constexpr int BK = B::kOther, KK = D / 16, DB = D / 32;
-    __shared__ __attribute__((aligned(1024))) char lds[2 * B::kTileBytes];
-    __shared__ int odd_tile;
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), h = lane >> 5;
     const int block = wave % B::kBlocks, part = wave / B::kBlocks;
-    const int kv_head = blockIdx.x % a.kv_heads, rest = blockIdx.x / a.kv_heads;
+    const int kv_head = group % a.kv_heads, rest = group / a.kv_heads;
     const int head = kv_head * a.per_head + rest % a.per_head;
-    if (blockIdx.x == gridDim.x - 1) {
-        check_offsets(a.offsets_q, a.n, a.Tq, a.err);
-        check_offsets(a.offsets_k, a.n, a.Tk, a.err);
-    }
     int seq, local;
     if (!find_tile<B::kOwn>(a.offsets_q, a.n, a.Tq, rest / a.per_head, &seq, &local)) return;
     const Sequence s = sequence_of(a, seq);
@@ -123,26 +144,15 @@ __global__ __launch_bounds__(kBackwardThreads) void attention_dq_kernel(PackedAr
 
     Fragment<BF16> q[KK], g[KK];
     const int64_t token = s.q0 + row;
-    float delta = 0;
+    float2 of_row = make_float2(kInf, 0.f);  // (a row past the last: P = 0)
+    if (live) of_row = a.rows[(int64_t)head * a.Tq + token];
+    const float lse = of_row.x, delta = of_row.y;
 #pragma unroll
     for (int kk = 0; kk < KK; kk++) {
         along_memory<BF16>(a.q, token * a.ldq + (int64_t)head * D, live, kk, lane, q[kk]);
         along_memory<BF16>(a.dout, token * a.lddo + (int64_t)head * D, live, kk, lane, g[kk]);
-        Fragment<BF16> o;
-        along_memory<BF16>(a.out, token * a.ldo + (int64_t)head * D, live, kk, lane, o);
-#pragma unroll
-        for (int e = 0; e < 8; e++) delta = fmaf((float)g[kk].raw[e], (float)o.raw[e], delta);
         q[kk].split();
         g[kk].split();
-    }
-    {
-        const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(delta), __float_as_uint(delta), false, false);
-        delta = __uint_as_float(r[0]) + __uint_as_float(r[1]);
-    }
-    float lse = kInf;  // (a row past the last: P = 0)
-    if (live) {
-        lse = a.lse[token * a.q_heads + head] * kLog2e;
-        if (h == 0 && part == 0) a.rows[(int64_t)head * a.Tq + token] = make_float2(lse, delta);
     }
     f32x16 out[DB];
 #pragma unroll
@@ -227,19 +237,16 @@ __global__ __launch_bounds__(kBackwardThreads) void attention_dq_kernel(PackedAr
 // dP = dO V^T with a key a lane, dV^T = dO^T P, dK^T = Q^T dS.
 // WHAT: 3 both; 1 dV alone, 2 dK alone (where registers do not hold both).
 template <bool BF16, int D, int WHAT, bool DIRECT>
-__global__ __launch_bounds__(kBackwardThreads) void attention_dkv_kernel(PackedArgs a) {
+__device__ inline void attention_dkv_parts(const PackedArgs& a, int group, char* lds, float2* stats, int& odd_tile) {
     typedef PartsShape<BF16, D> B;
     typedef Tile<BF16, D> T;
     constexpr int BQ = B::kOther, KK = D / 16, DB = D / 32;
     constexpr bool kDv = WHAT & 1, kDk = WHAT & 2;
-    __shared__ __attribute__((aligned(1024))) char lds[2 * B::kTileBytes];
-    __shared__ __attribute__((aligned(16))) float2 stats[BQ];
-    __shared__ int odd_tile;
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), h = lane >> 5;
     const int block = wave % B::kBlocks, part = wave / B::kBlocks;
-    const int kv_head = blockIdx.x % a.kv_heads;
+    const int kv_head = group % a.kv_heads;
     int seq, local;
-    if (!find_tile<B::kOwn>(a.offsets_k, a.n, a.Tk, blockIdx.x / a.kv_heads, &seq, &local)) return;
+    if (!find_tile<B::kOwn>(a.offsets_k, a.n, a.Tk, group / a.kv_heads, &seq, &local)) return;
     const Sequence s = sequence_of(a, seq);
     const int key0 = local * B::kOwn, wave_key = key0 + block * 32, key = wave_key + (lane & 31);
     if (key0 >= s.keys) return;
@@ -373,31 +380,58 @@ __global__ __launch_bounds__(kBackwardThreads) void attention_dkv_kernel(PackedA
             }
 }
 
-// The same two kernels for bf16 heads of up to 128 channels, where registers hold two
+// All in one launch, those that take longest first, so that the card is full.  ROLES: 1,
+// dK and dV by one workgroup; 2, by one each, five products in place of four: past 96
+// channels, where a wave's registers do not hold both sums, the operands and what is on its
+// way (with launches of their own, 3548 tokens of 16 and 4 heads of 128 in fp32 1.4 ms with 1,
+// 1.1 ms with 2; of 256 in bf16 1.8 and 0.8 ms), and where there are few workgroups (of 96 channels, 1 and 2: 665
+// tokens of 6 and 3 heads, 198 of them, 103 and 79 us; 1000 of 16 and 4, 640, 255 and 193;
+// four times 700 of 6 and 3, 819, 169 and 182; 2000 of 16 and 4, 1260, 498 and 559).
+template <bool BF16, int D, int ROLES, bool DIRECT>
+__global__ __launch_bounds__(kBackwardThreads) void attention_parts_kernel(PackedArgs a, int dkv_groups) {
+    typedef PartsShape<BF16, D> B;
+    __shared__ __attribute__((aligned(1024))) char lds[2 * B::kTileBytes];
+    __shared__ __attribute__((aligned(16))) float2 stats[B::kOther];
+    __shared__ int odd_tile;
+    int group = blockIdx.y * gridDim.x + blockIdx.x;
+    if (blockIdx.x == gridDim.x - 1 && blockIdx.y == gridDim.y - 1) {
+        check_offsets(a.offsets_q, a.n, a.Tq, a.err);
+        check_offsets(a.offsets_k, a.n, a.Tk, a.err);
+    }
+    if (group >= ROLES * dkv_groups) {
+        attention_dq_parts<BF16, D, DIRECT>(a, group - ROLES * dkv_groups, lds, odd_tile);
+    } else if constexpr (ROLES == 1) {
+        attention_dkv_parts<BF16, D, 3, DIRECT>(a, group, lds, stats, odd_tile);
+    } else {
+        if (group < dkv_groups) attention_dkv_parts<BF16, D, 2, DIRECT>(a, group, lds, stats, odd_tile);
+        else attention_dkv_parts<BF16, D, 1, DIRECT>(a, group - dkv_groups, lds, stats, odd_tile);
+    }
+}
+
+// The same for bf16 heads of up to 128 channels, where registers hold two
 // blocks' scores: the products of the next block's S and dP run beside this block's
 // exponentials, and the products with them follow, so that the matrix cores wait
 // neither for the vector unit nor for LDS.  A block is 32 keys (dQ) or 32 rows a wave
 // (dK, dV).
 // DIRECT: tiles go straight from memory into LDS.
-// Four sequences of up to 4096 tokens, 16 query and 4 key heads of 128, causal: dQ 193 us,
-// dK and dV 360 us, the matrix cores busy for 0.46 of it; what is left is the vector unit's
-// work, reads of LDS behind a step's barrier and, of dK and dV, that the
-// longest sequence's first keys take 256 steps where the average CU has 195.
+// Four sequences of up to 4096 tokens, 16 query and 4 key heads of 128, causal: 511 us (dQ
+// after dK and dV in launches of their own 193 and 360, the matrix cores busy for 0.46 of
+// it; 3548 tokens 230 for 190, 665 tokens 72 for 50); what is left is the vector unit's
+// work, reads of LDS behind a step's barrier, and the eight products in place of five.
 constexpr int kAhead = 2;  // products between an operand's read and its use
 
+constexpr int kBesideThreads = 512;
+// dQ: a workgroup has 256 rows, a wave 32 of them.
+template <int D> struct DqShape {
+    static constexpr int kBytes = 32 * Tile<true, D>::kLineBytes, kLds = 8 * kBytes;  // keys and values, four blocks (three would do: their number's low bits say where)
+};
 template <int D, bool DIRECT>
-__global__ __launch_bounds__(kBackwardWaves * 64, 2) void attention_dq_beside_kernel(PackedArgs a) {
+__device__ inline void attention_dq_beside(const PackedArgs& a, int group, char* lds, int* odd_block) {
     typedef Tile<true, D> T;
-    constexpr int kThreads = 64 * kBackwardWaves, kRows = 32 * kBackwardWaves, KK = D / 16, DB = D / 32, kBytes = 32 * T::kLineBytes;
-    __shared__ __attribute__((aligned(1024))) char lds[8 * kBytes];  // keys and values, four blocks (three would do: their number's low bits say where)
-    __shared__ int odd_block[4];
+    constexpr int kThreads = kBesideThreads, kRows = kThreads / 2, KK = D / 16, DB = D / 32, kBytes = DqShape<D>::kBytes;
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), h = lane >> 5;
-    const int kv_head = blockIdx.x % a.kv_heads, rest = blockIdx.x / a.kv_heads;
+    const int kv_head = group % a.kv_heads, rest = group / a.kv_heads;
     const int head = kv_head * a.per_head + rest % a.per_head;
-    if (blockIdx.x == gridDim.x - 1) {
-        check_offsets(a.offsets_q, a.n, a.Tq, a.err);
-        check_offsets(a.offsets_k, a.n, a.Tk, a.err);
-    }
     int seq, local;
     if (!find_tile<kRows>(a.offsets_q, a.n, a.Tq, rest / a.per_head, &seq, &local)) return;
     const Sequence s = sequence_of(a, seq);
@@ -409,24 +443,13 @@ __global__ __launch_bounds__(kBackwardWaves * 64, 2) void attention_dq_beside_ke
 
     Fragment<true> q[KK], g[KK];
     const int64_t token = s.q0 + row;
-    float delta = 0;
+    float2 of_row = make_float2(kInf, 0.f);  // (a row past the last: P = 0)
+    if (live) of_row = a.rows[(int64_t)head * a.Tq + token];
+    const float lse = of_row.x, delta = of_row.y;
 #pragma unroll
     for (int kk = 0; kk < KK; kk++) {
         along_memory<true>(a.q, token * a.ldq + (int64_t)head * D, live, kk, lane, q[kk]);
         along_memory<true>(a.dout, token * a.lddo + (int64_t)head * D, live, kk, lane, g[kk]);
-        Fragment<true> o;
-        along_memory<true>(a.out, token * a.ldo + (int64_t)head * D, live, kk, lane, o);
-#pragma unroll
-        for (int e = 0; e < 8; e++) delta = fmaf((float)g[kk].raw[e], (float)o.raw[e], delta);
-    }
-    {
-        const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(delta), __float_as_uint(delta), false, false);
-        delta = __uint_as_float(r[0]) + __uint_as_float(r[1]);
-    }
-    float lse = kInf;  // (a row past the last: P = 0)
-    if (live) {
-        lse = a.lse[token * a.q_heads + head] * kLog2e;
-        if (h == 0) a.rows[(int64_t)head * a.Tq + token] = make_float2(lse, delta);
     }
     f32x16 out[DB], st, dp, st_next, dp_next;
 #pragma unroll
@@ -588,18 +611,17 @@ __global__ __launch_bounds__(kBackwardWaves * 64, 2) void attention_dq_beside_ke
 // keys are added at the end.  S is computed by both, five products in place of four, but
 // a wave's registers then leave room for a second one to each unit.  (With both sums in a
 // wave, and one wave to a unit, the unit stood still for most of the time: 432 us for 360.)
-constexpr int kBesideThreads = 512;
+template <int D> struct DkvShape {
+    static constexpr int kBytes = 64 * Tile<true, D>::kLineBytes, kLds = 8 * kBytes;  // queries and their gradients, four steps
+};
 template <int D, bool DIRECT>
-__global__ __launch_bounds__(kBesideThreads, 2) void attention_dkv_beside_kernel(PackedArgs a) {
+__device__ inline void attention_dkv_beside(const PackedArgs& a, int group, char* lds, float2 (*stats)[64], int* odd_step) {
     typedef Tile<true, D> T;
-    constexpr int kThreads = kBesideThreads, kKeys = 64, KK = D / 16, DB = D / 32, kBytes = 64 * T::kLineBytes;
-    __shared__ __attribute__((aligned(1024))) char lds[8 * kBytes];  // queries and their gradients, four steps
-    __shared__ __attribute__((aligned(1024))) float2 stats[4][64];
-    __shared__ int odd_step[4];
+    constexpr int kThreads = kBesideThreads, kKeys = 64, KK = D / 16, DB = D / 32, kBytes = DkvShape<D>::kBytes;
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), h = lane >> 5, part = wave >> 1 & 1;
-    const int kv_head = blockIdx.x % a.kv_heads;
+    const int kv_head = group % a.kv_heads;
     int seq, local;
-    if (!find_tile<kKeys>(a.offsets_k, a.n, a.Tk, blockIdx.x / a.kv_heads, &seq, &local)) return;
+    if (!find_tile<kKeys>(a.offsets_k, a.n, a.Tk, group / a.kv_heads, &seq, &local)) return;
     const Sequence s = sequence_of(a, seq);
     const int key0 = local * kKeys, wave_key = key0 + (wave & 1) * 32, key = wave_key + (lane & 31);
     if (key0 >= s.keys) return;
@@ -868,35 +890,59 @@ __global__ __launch_bounds__(kBesideThreads, 2) void attention_dkv_beside_kernel
     else pass(std::false_type{});
 }
 
+// In one launch, as above.
 template <int D, bool DIRECT>
-hipError_t launch_beside(const PackedArgs& a, hipStream_t s) {
-    const dim3 threads(64 * kBackwardWaves);
-    hipLaunchKernelGGL((attention_dq_beside_kernel<D, DIRECT>), dim3((unsigned)(tile_slots(a.Tq, 32 * kBackwardWaves, a.n) * a.q_heads)), threads, 0, s, a);
-    hipLaunchKernelGGL((attention_dkv_beside_kernel<D, DIRECT>), dim3((unsigned)(tile_slots(a.Tk, 64, a.n) * a.kv_heads)), dim3(kBesideThreads), 0, s, a);
-    return hipGetLastError();
+__global__ __launch_bounds__(kBesideThreads, 2) void attention_backward_kernel(PackedArgs a, int dkv_groups) {
+    static_assert(DqShape<D>::kLds <= DkvShape<D>::kLds, "shared");
+    __shared__ __attribute__((aligned(1024))) char lds[DkvShape<D>::kLds];
+    __shared__ __attribute__((aligned(1024))) float2 stats[4][64];
+    __shared__ int odd[4];
+    const int group = blockIdx.y * gridDim.x + blockIdx.x;
+    if (blockIdx.x == gridDim.x - 1 && blockIdx.y == gridDim.y - 1) {
+        check_offsets(a.offsets_q, a.n, a.Tq, a.err);
+        check_offsets(a.offsets_k, a.n, a.Tk, a.err);
+    }
+    if (group < dkv_groups) attention_dkv_beside<D, DIRECT>(a, group, lds, stats, odd);
+    else attention_dq_beside<D, DIRECT>(a, group - dkv_groups, lds, odd);
 }
 
+inline dim3 grid_of(int64_t groups) {  // (threads of a grid's row: 32 bits)
+    const int64_t across = 1 << 20;
+    return dim3((unsigned)std::min(groups, across), (unsigned)((groups + across - 1) / across));
+}
+template <bool BF16, int D>
+void launch_rows(const PackedArgs& a, hipStream_t s) {
+    const int64_t groups = ((int64_t)a.Tq * a.q_heads + 7) / 8;
+    hipLaunchKernelGGL((attention_rows_kernel<BF16, D>), dim3((unsigned)std::min<int64_t>(groups, 8192)), dim3(kRowsThreads), 0, s, a);
+}
+template <int D, bool DIRECT>
+void launch_beside(const PackedArgs& a, hipStream_t s) {
+    const int64_t dkv = tile_slots(a.Tk, 64, a.n) * a.kv_heads, dq = tile_slots(a.Tq, kBesideThreads / 2, a.n) * a.q_heads;
+    hipLaunchKernelGGL((attention_backward_kernel<D, DIRECT>), grid_of(dkv + dq), dim3(kBesideThreads), 0, s, a, (int)dkv);
+}
 template <bool BF16, int D, bool DIRECT>
-hipError_t launch_parts(const PackedArgs& a, hipStream_t s) {
+void launch_parts(const PackedArgs& a, hipStream_t s) {
     typedef PartsShape<BF16, D> B;
-    const dim3 threads(kBackwardThreads), q_groups((unsigned)(tile_slots(a.Tq, B::kOwn, a.n) * a.q_heads)), k_groups((unsigned)(tile_slots(a.Tk, B::kOwn, a.n) * a.kv_heads));
-    hipLaunchKernelGGL((attention_dq_kernel<BF16, D, DIRECT>), q_groups, threads, 0, s, a);
-    // Both sums in a wave up to 96 channels; past that they, the operands and what is on its way
-    // do not fit into its registers: 3548 tokens of 16 and 4 heads of 128 in fp32 1.4 ms that way,
-    // 1.1 ms so; of 256 in bf16 1.8 and 0.8 ms (products: five in place of four).
-    if constexpr (D <= 96) {
-        hipLaunchKernelGGL((attention_dkv_kernel<BF16, D, 3, DIRECT>), k_groups, threads, 0, s, a);
-    } else {
-        hipLaunchKernelGGL((attention_dkv_kernel<BF16, D, 1, DIRECT>), k_groups, threads, 0, s, a);
-        hipLaunchKernelGGL((attention_dkv_kernel<BF16, D, 2, DIRECT>), k_groups, threads, 0, s, a);
-    }
-    return hipGetLastError();
+    const int64_t dkv = tile_slots(a.Tk, B::kOwn, a.n) * a.kv_heads, dq = tile_slots(a.Tq, B::kOwn, a.n) * a.q_heads;
+    if constexpr (D <= 96)
+        if (dkv + dq >= 700) {
+            hipLaunchKernelGGL((attention_parts_kernel<BF16, D, 1, DIRECT>), grid_of(dkv + dq), dim3(kBackwardThreads), 0, s, a, (int)dkv);
+            return;
+        }
+    hipLaunchKernelGGL((attention_parts_kernel<BF16, D, 2, DIRECT>), grid_of(2 * dkv + dq), dim3(kBackwardThreads), 0, s, a, (int)dkv);
 }
 template <bool BF16, int D>
 hipError_t launch_backward(const PackedArgs& a, hipStream_t s) {
     const bool direct = direct_lines(a.q, a.ldq, BF16) && direct_lines(a.k, a.ldk, BF16) && direct_lines(a.v, a.ldv, BF16) && direct_lines(a.dout, a.lddo, BF16);
-    if constexpr (BF16 && D <= 128) return direct ? launch_beside<D, true>(a, s) : launch_beside<D, false>(a, s);
-    else return direct ? launch_parts<BF16, D, true>(a, s) : launch_parts<BF16, D, false>(a, s);
+    launch_rows<BF16, D>(a, s);
+    if constexpr (BF16 && D <= 128) {
+        if (direct) launch_beside<D, true>(a, s);
+        else launch_beside<D, false>(a, s);
+    } else {
+        if (direct) launch_parts<BF16, D, true>(a, s);
+        else launch_parts<BF16, D, false>(a, s);
+    }
+    return hipGetLastError();
 }
 template <bool BF16>
 hipError_t launch_backward_by_width(const PackedArgs& a, hipStream_t s) {

@@ -189,8 +189,9 @@ template <bool BF16, int D, int R, int THREADS> struct Pipe<BF16, D, R, THREADS,
 // one wait for the scalar registers of their address (see tile::load_lds16).
 template <int D, int R, int THREADS> struct LinesToLds {
     typedef Tile<true, D> T;
-    static constexpr int kEach = R * T::kLine / THREADS;
-    static_assert(R * T::kLine % THREADS == 0 && (kEach == 1 || kEach == 2 || kEach == 4), "the blocks below");
+    static constexpr int kLoading = R * T::kLine < THREADS ? R * T::kLine : THREADS;  // threads that do
+    static constexpr int kEach = R * T::kLine / kLoading;
+    static_assert(R * T::kLine % kLoading == 0 && (kEach == 1 || kEach == 2 || kEach == 4), "the blocks below");
     uint32_t at[kEach];
     __device__ void places(int64_t ld, int lines) {  // lines past the last repeat it
 #pragma unroll
@@ -200,6 +201,7 @@ template <int D, int R, int THREADS> struct LinesToLds {
         }
     }
     __device__ void fetch(const char* first, uint32_t lds, int wave) const {
+        if (kLoading < THREADS && wave >= kLoading / 64) return;
         uint32_t to = __builtin_amdgcn_readfirstlane(lds + wave * 1024);
         const void* p = tile::uniform(first);
         if constexpr (kEach == 1)

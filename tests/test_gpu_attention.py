@@ -134,7 +134,9 @@ CASES = [
     # long enough for steps without a mask, an odd and an even number of them, between others
     ([1100, 70], None, 6, 2, 128, True, 0, BF16, 0), ([900], None, 4, 4, 96, False, 0, BF16, 8), ([777], None, 8, 1, 64, True, 300, BF16, 0),
     ([640], [1000], 3, 1, 128, True, 0, BF16, 5), ([900, 450], None, 2, 1, 128, True, 500, BF16, 3), ([1000], [300], 4, 2, 64, False, 0, BF16, 0),
-    ([400], None, 4, 2, 192, True, 0, F32, 0), ([300, 100], None, 2, 1, 256, True, 0, F32, 3), ([520], None, 4, 1, 128, True, 200, F32, 0), ([600], None, 2, 1, 256, True, 0, BF16, 0)]
+    ([400], None, 4, 2, 192, True, 0, F32, 0), ([300, 100], None, 2, 1, 256, True, 0, F32, 3), ([520], None, 4, 1, 128, True, 200, F32, 0), ([600], None, 2, 1, 256, True, 0, BF16, 0),
+    # workgroups enough for dK and dV by one each, in fp32
+    ([700, 333], None, 16, 8, 64, True, 0, F32, 0), ([600, 500], None, 16, 8, 96, False, 0, F32, 4)]
 
 
 @pytest.mark.parametrize("lq,lk,heads,Hkv,D,causal,window,dtype,gap", CASES)
