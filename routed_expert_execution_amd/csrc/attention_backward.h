@@ -11,92 +11,15 @@
 #include <algorithm>
 #include <type_traits>
 
-#include "attention_tiles.h"
+#include "attention_parts.h"
 
 namespace moe {
 namespace packed {
 
-constexpr int kBackwardWaves = 4, kBackwardThreads = 64 * kBackwardWaves;
-
-// fp32, and bf16 heads of more than 128 channels.  A workgroup has 32 BLOCKS rows (dQ)
-// or keys (dK, dV) of its own and passes over the others 32 PARTS at a time, BLOCKS
-// PARTS = 4 waves, each with sums of its own that are added in order at the end: small
-// tiles, since few and short sequences have to fill the card and the products of fp32,
-// six of bf16 terms each, leave the time to load more.  Two sequences of 611 and 54 tokens,
-// 6 and 3 heads of 96 in fp32: 65 us (one launch after the other, dK and dV together: 123),
-// ten steps one after the other, of whose 4 us the products take half.  fp32 heads of 192
-// and 256 channels spill.
-template <bool BF16, int D> struct PartsShape {
-    static constexpr int kParts = BF16 || D <= 128 ? 4 : 2, kBlocks = kBackwardWaves / kParts;
-    static constexpr int kOwn = 32 * kBlocks, kOther = 32 * kParts;
-    static constexpr int kTileBytes = kOther * Tile<BF16, D>::kLineBytes;  // 64 KiB at most
-};
-
-// Sums of several waves: those of parts 1.. through LDS to part 0's, which adds them in
-// order.  N blocks of 16 registers; true for the waves that hold the result.
-template <int N, int PARTS, int BLOCKS>
-__device__ inline bool add_parts(f32x16 (&acc)[N], char* lds, int part, int block, int lane) {
-    f32x4* at = (f32x4*)lds;
-#pragma unroll 1
-    for (int p = 1; p < PARTS; p++) {
-        __syncthreads();
-        if (part == p)
-#pragma unroll
-            for (int n = 0; n < N; n++)
-#pragma unroll
-                for (int j = 0; j < 4; j++) at[((block * N + n) * 4 + j) * 64 + lane] = f32x4{acc[n][4 * j], acc[n][4 * j + 1], acc[n][4 * j + 2], acc[n][4 * j + 3]};
-        __syncthreads();
-        if (part == 0)
-#pragma unroll
-            for (int n = 0; n < N; n++)
-#pragma unroll
-                for (int j = 0; j < 4; j++) {
-                    const f32x4 v = at[((block * N + n) * 4 + j) * 64 + lane];
-#pragma unroll
-                    for (int e = 0; e < 4; e++) acc[n][4 * j + e] += v[e];
-                }
-    }
-    return part == 0;
-}
-
-// A tile into LDS, through registers a few chunks at a time or straight.
-template <bool BF16, int D, int R, bool DIRECT>
-__device__ inline void bring(const char* base, int64_t ld, int64_t first, int lines, char* lds) {
-    typedef Tile<BF16, D> T;
-    if constexpr (DIRECT) {
-        Pipe<BF16, D, R, kBackwardThreads, true> p;
-        p.fetch(base, ld, first, lines, lds);
-    } else {
-#pragma unroll 4
-        for (int n = threadIdx.x; n < R * T::kChunks; n += kBackwardThreads) {
-            const int r = n / T::kChunks, c = n - r * T::kChunks;
-            u32x4 v = {0, 0, 0, 0};
-            if (r < lines) {
-                const Words4 w = *(const Words4*)(base + ((first + r) * ld + c * T::kPer) * (BF16 ? 2 : 4));
-                v = u32x4{w.v[0], w.v[1], w.v[2], w.v[3]};
-            }
-            *(u32x4*)(lds + T::at(r, c)) = v;
-        }
-    }
-}
-
-// N products with an operand each from LDS, the second next one's read and the next one's
-// terms made beside a product.
-template <int N, bool BF16, typename Read, typename Use>
-__device__ inline void in_turn(Read read, Use use) {
-    Fragment<BF16> f[3];
-    read(0, f[0]);
-    if (N > 1) read(1, f[1]);
-    f[0].split();
-#pragma unroll
-    for (int i = 0; i < N; i++) {
-        if (i + 2 < N) read(i + 2, f[(i + 2) % 3]);
-        if (i + 1 < N) f[(i + 1) % 3].split();
-        use(i, f[i % 3]);
-        __builtin_amdgcn_sched_barrier(0);
-    }
-}
-
+// fp32, and bf16 heads of more than 128 channels, by PartsShape.  Two sequences of 611 and
+// 54 tokens, 6 and 3 heads of 96 in fp32: 65 us (one launch after the other, dK and dV
+// together: 123), ten steps one after the other, of whose 4 us the products take half.  fp32
+// heads of 192 and 256 channels spill.
 // What the others need of each row: L / ln 2 and delta = rowsum(dO O), by 16 or 32 lanes a
 // row.  Bound by bytes: 8532 rows of 16 heads of 128 in bf16 14 us.
 constexpr int kRowsThreads = 256;
@@ -176,7 +99,7 @@ __device__ inline void attention_dq_parts(const PackedArgs& a, int group, char* 
         bring<BF16, D, BK, DIRECT>(vbase, a.ldv, t0, s.keys - t0, vt);
         meet<DIRECT>();
         if (t0 + BK > s.keys || (a.causal && t0 + BK - 1 > row0 + s.shift) || (a.window && t0 <= last_row + s.shift - a.window)) {
-            if (tile_not_finite<BF16, D, BK, kBackwardThreads>(kt)) odd_tile = t0;
+            if (tile_not_finite<BF16, D, BK, kPartsThreads>(kt)) odd_tile = t0;
             __syncthreads();
         }
         const int k0 = t0 + 32 * part;  // this wave's 32 keys
@@ -294,7 +217,7 @@ __device__ inline void attention_dkv_parts(const PackedArgs& a, int group, char*
             }
             meet<DIRECT>();
             if (t0 + BQ > s.rows || (a.causal && last_key > t0 + s.shift) || (a.window && key0 <= t0 + BQ - 1 + s.shift - a.window)) {
-                const bool bad_q = tile_not_finite<BF16, D, BQ, kBackwardThreads>(qt), bad_g = tile_not_finite<BF16, D, BQ, kBackwardThreads>(gt);
+                const bool bad_q = tile_not_finite<BF16, D, BQ, kPartsThreads>(qt), bad_g = tile_not_finite<BF16, D, BQ, kPartsThreads>(gt);
                 if (bad_q || bad_g) odd_tile = at;
                 __syncthreads();
             }
@@ -388,7 +311,7 @@ __device__ inline void attention_dkv_parts(const PackedArgs& a, int group, char*
 // tokens of 6 and 3 heads, 198 of them, 103 and 79 us; 1000 of 16 and 4, 640, 255 and 193;
 // four times 700 of 6 and 3, 819, 169 and 182; 2000 of 16 and 4, 1260, 498 and 559).
 template <bool BF16, int D, int ROLES, bool DIRECT>
-__global__ __launch_bounds__(kBackwardThreads) void attention_parts_kernel(PackedArgs a, int dkv_groups) {
+__global__ __launch_bounds__(kPartsThreads) void attention_parts_kernel(PackedArgs a, int dkv_groups) {
     typedef PartsShape<BF16, D> B;
     __shared__ __attribute__((aligned(1024))) char lds[2 * B::kTileBytes];
     __shared__ __attribute__((aligned(16))) float2 stats[B::kOther];
@@ -926,10 +849,10 @@ void launch_parts(const PackedArgs& a, hipStream_t s) {
     const int64_t dkv = tile_slots(a.Tk, B::kOwn, a.n) * a.kv_heads, dq = tile_slots(a.Tq, B::kOwn, a.n) * a.q_heads;
     if constexpr (D <= 96)
         if (dkv + dq >= 700) {
-            hipLaunchKernelGGL((attention_parts_kernel<BF16, D, 1, DIRECT>), grid_of(dkv + dq), dim3(kBackwardThreads), 0, s, a, (int)dkv);
+            hipLaunchKernelGGL((attention_parts_kernel<BF16, D, 1, DIRECT>), grid_of(dkv + dq), dim3(kPartsThreads), 0, s, a, (int)dkv);
             return;
         }
-    hipLaunchKernelGGL((attention_parts_kernel<BF16, D, 2, DIRECT>), grid_of(2 * dkv + dq), dim3(kBackwardThreads), 0, s, a, (int)dkv);
+    hipLaunchKernelGGL((attention_parts_kernel<BF16, D, 2, DIRECT>), grid_of(2 * dkv + dq), dim3(kPartsThreads), 0, s, a, (int)dkv);
 }
 template <bool BF16, int D>
 hipError_t launch_backward(const PackedArgs& a, hipStream_t s) {

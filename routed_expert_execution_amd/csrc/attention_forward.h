@@ -3,7 +3,9 @@
 // One pass over the keys with a running maximum and sum.
 #pragma once
 
-#include "attention_tiles.h"
+#include <algorithm>
+
+#include "attention_parts.h"
 
 namespace moe {
 namespace packed {
@@ -298,11 +300,176 @@ __global__ __launch_bounds__(kForwardWaves * 64, BF16 && D <= 128 ? 2 : 1) void 
     if (a.lse && h == 0) a.lse[token * a.q_heads + head] = s.bad ? nan : m == -kInf ? -kInf : fmaf(m, a.scale, __builtin_amdgcn_logf(sum) * kLn2);
 }
 
+// The same for few rows, by PartsShape: 32 (or 64) rows a workgroup, its waves over parts of
+// the keys, each with a maximum and sums of its own that are joined at the end.  The next
+// tile is on its way where LDS holds two.  Figures at its launch.
+template <bool BF16, int D, bool DIRECT>
+__global__ __launch_bounds__(kPartsThreads) void attention_few_kernel(PackedArgs a) {
+    typedef PartsShape<BF16, D> B;
+    typedef Tile<BF16, D> T;
+    constexpr int BK = B::kOther, KK = D / 16, DB = D / 32, kBuffers = B::kTileBytes <= 32768 ? 2 : 1;
+    __shared__ __attribute__((aligned(1024))) char lds[2 * kBuffers * B::kTileBytes];
+    __shared__ float2 stats[kPartsWaves][32];
+    __shared__ int odd_tile;
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), h = lane >> 5;
+    const int block = wave % B::kBlocks, part = wave / B::kBlocks;
+    const int kv_head = blockIdx.x % a.kv_heads, rest = blockIdx.x / a.kv_heads;
+    const int head = kv_head * a.per_head + rest % a.per_head;
+    if (blockIdx.x == gridDim.x - 1) {
+        check_offsets(a.offsets_q, a.n, a.Tq, a.err);
+        check_offsets(a.offsets_k, a.n, a.Tk, a.err);
+    }
+    int seq, local;
+    if (!find_tile<B::kOwn>(a.offsets_q, a.n, a.Tq, rest / a.per_head, &seq, &local)) return;
+    const Sequence s = sequence_of(a, seq);
+    const int tiles = (s.rows + B::kOwn - 1) / B::kOwn;
+    if (local >= tiles) return;
+    const int row0 = (tiles - 1 - local) * B::kOwn, wave_first = row0 + block * 32, row = wave_first + (lane & 31);
+    const bool live = row < s.rows;
+    if (s.bad && threadIdx.x == 0) atomicOr(a.err, kErrCache);
+
+    const int last_row = min(row0 + B::kOwn, s.rows) - 1, wave_last = min(wave_first + 31, s.rows - 1);
+    const int end = a.causal ? min(s.keys, last_row + s.shift + 1) : s.keys;
+    const int begin = a.window ? max(0, row0 + s.shift - a.window + 1) / 32 * 32 : 0;
+    const char* kbase = (const char*)a.k + ((int64_t)s.k0 * a.ldk + (int64_t)kv_head * D) * (BF16 ? 2 : 4);
+    const char* vbase = (const char*)a.v + ((int64_t)s.k0 * a.ldv + (int64_t)kv_head * D) * (BF16 ? 2 : 4);
+    Pipe<BF16, D, BK, kPartsThreads, DIRECT> pk, pv;
+    int buffer = 0;
+    auto fetch = [&](int t0, int b) __attribute__((always_inline)) {
+        pk.fetch(kbase, a.ldk, t0, s.keys - t0, lds + 2 * b * B::kTileBytes);
+        pv.fetch(vbase, a.ldv, t0, s.keys - t0, lds + (2 * b + 1) * B::kTileBytes);
+    };
+    if (kBuffers == 2 && begin < end) fetch(begin, 0);
+
+    Fragment<BF16> q[KK];
+    const int64_t token = s.q0 + row;
+#pragma unroll
+    for (int kk = 0; kk < KK; kk++) {
+        along_memory<BF16>(a.q, token * a.ldq + (int64_t)head * D, live, kk, lane, q[kk]);
+        q[kk].split();
+    }
+    f32x16 out[DB];
+#pragma unroll
+    for (int d = 0; d < DB; d++)
+#pragma unroll
+        for (int i = 0; i < 16; i++) out[d][i] = 0;
+    float m = -kInf, l = 0;  // the largest q.k, about; this lane's part of the sum
+    if (threadIdx.x == 0) odd_tile = -1;
+    const uint32_t along_lane = T::along_lane(lane) + part * 32 * T::kLineBytes, across_lane = T::across_lane(lane) + part * 32 * T::kLineBytes;
+#pragma unroll 1
+    for (int t0 = begin; t0 < end; t0 += BK) {
+        char *kt = lds + 2 * buffer * B::kTileBytes, *vt = kt + B::kTileBytes;
+        if (kBuffers == 1) {
+            __syncthreads();
+            fetch(t0, 0);
+        }
+        pk.arrive(kt);
+        pv.arrive(vt);
+        meet<DIRECT>();
+        if (kBuffers == 2 && t0 + BK < end) fetch(t0 + BK, buffer ^ 1);
+        if (t0 + BK > s.keys || (a.causal && t0 + BK - 1 > row0 + s.shift) || (a.window && t0 <= last_row + s.shift - a.window)) {
+            if (tile_not_finite<BF16, D, BK, kPartsThreads>(vt)) odd_tile = t0;
+            __syncthreads();
+        }
+        const uint32_t ka = tile::lds_address(kt) + along_lane, vx = tile::lds_address(vt) + across_lane;
+        buffer ^= kBuffers - 1;
+        const int k0 = t0 + 32 * part;  // this wave's 32 keys
+        if (k0 >= s.keys || wave_first >= s.rows || (a.causal && k0 > wave_last + s.shift) || (a.window && k0 + 31 <= wave_first + s.shift - a.window)) continue;
+        const bool masked = k0 + 32 > s.keys || (a.causal && k0 + 31 > wave_first + s.shift) || (a.window && k0 <= wave_last + s.shift - a.window);
+        const bool odd = masked && odd_tile == t0;
+        const Span span = keys_seen(a, s, row, k0, h);
+        f32x16 st;
+#pragma unroll
+        for (int i = 0; i < 16; i++) st[i] = 0;
+        in_turn<KK, BF16>([&](int i, Fragment<BF16>& f) { T::along(ka, 0, i, f); }, [&](int i, const Fragment<BF16>& f) { mma(st, f, q[i]); });
+        float top = -kInf;
+#pragma unroll
+        for (int i = 0; i < 16; i++) {
+            st[i] = masked && !span.has(0, i) ? -kInf : st[i];
+            top = max_of(top, st[i]);
+        }
+        const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(top), __float_as_uint(top), false, false);
+        top = max_of(__uint_as_float(r[0]), __uint_as_float(r[1]));
+        const float before = m;
+        const bool grown = (top - before) * a.scale_log2 > 8.f;  // (as above)
+        if (__any(grown)) {
+            m = grown ? top : before;
+            const float f = grown ? __builtin_amdgcn_exp2f((before - top) * a.scale_log2) : 1.f;
+            l *= f;
+#pragma unroll
+            for (int d = 0; d < DB; d++) out[d] *= f;
+        }
+        const float base = m == -kInf ? 0.f : m * a.scale_log2;
+        Fragment<BF16> pf[2];
+#pragma unroll
+        for (int n = 0; n < 2; n++) {
+            float p[8];
+#pragma unroll
+            for (int e = 0; e < 8; e++) {
+                p[e] = __builtin_amdgcn_exp2f(fmaf(st[8 * n + e], a.scale_log2, -base));
+                l += p[e];
+            }
+            operand_of(p, pf[n]);
+        }
+        auto read = [&](int i, Fragment<BF16>& f) { T::across(vx, 16 * (i / DB), 32 * (i % DB), f); };
+        if (!odd) {
+            in_turn<2 * DB, BF16>(read, [&](int i, const Fragment<BF16>& f) { mma(out[i % DB], f, pf[i / DB]); });
+            continue;
+        }
+#pragma unroll
+        for (int n = 0; n < 2; n++) {
+            bf16x8 seen;
+#pragma unroll
+            for (int e = 0; e < 8; e++) seen[e] = (__bf16)(span.has(0, 8 * n + e) ? 1.f : 0.f);
+#pragma unroll
+            for (int d = 0; d < DB; d++) {
+                Fragment<BF16> f;
+                read(DB * n + d, f);
+                mma_seen(out[d], f, pf[n], seen);
+                if (!BF16) __builtin_amdgcn_sched_barrier(0);
+            }
+        }
+    }
+    // all parts to one maximum
+    const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(l), __float_as_uint(l), false, false);
+    l = __uint_as_float(r[0]) + __uint_as_float(r[1]);
+    if (h == 0) stats[wave][lane] = make_float2(m, l);
+    __syncthreads();
+    float all = -kInf, sum = 0;
+#pragma unroll
+    for (int p = 0; p < B::kParts; p++) all = fmaxf(all, stats[p * B::kBlocks + block][lane & 31].x);
+    const float base = all == -kInf ? 0.f : all;
+#pragma unroll
+    for (int p = 0; p < B::kParts; p++) {
+        const float2 of_part = stats[p * B::kBlocks + block][lane & 31];
+        sum += of_part.y * __builtin_amdgcn_exp2f((of_part.x - base) * a.scale_log2);
+    }
+    const float f = __builtin_amdgcn_exp2f((m - base) * a.scale_log2);
+#pragma unroll
+    for (int d = 0; d < DB; d++) out[d] *= f;
+    if (!add_parts<DB, B::kParts, B::kBlocks>(out, lds, part, block, lane) || !live) return;
+    const float nan = __uint_as_float(0x7FC00000u);
+    const float by = s.bad ? nan : all == -kInf && sum == 0.f ? 0.f : 1.0f / sum;
+    const int64_t o = token * a.ldo + (int64_t)head * D;
+#pragma unroll
+    for (int d = 0; d < DB; d++)
+#pragma unroll
+        for (int j = 0; j < 4; j++)
+#pragma unroll
+            for (int e = 0; e < 4; e++) store1<BF16>(a.out, o + 32 * d + 8 * j + 4 * h + e, out[d][4 * j + e] * by);
+    if (a.lse && h == 0) a.lse[token * a.q_heads + head] = s.bad ? nan : all == -kInf ? -kInf : fmaf(all, a.scale, __builtin_amdgcn_logf(sum) * kLn2);
+}
+
 template <bool BF16, int D, bool DIRECT>
 hipError_t launch_shape(const PackedArgs& a, hipStream_t s) {
     typedef ForwardShape<BF16, D> F;
     const int64_t groups = tile_slots(a.Tq, F::kRows, a.n) * a.q_heads;
-    hipLaunchKernelGGL((attention_kernel<BF16, D, DIRECT>), dim3((unsigned)groups), dim3(F::kThreads), 0, s, a);
+    // Few: 1 prompt of 1000 tokens, 16 and 4 heads of 96 in fp32 (128 groups) 104 us so and 54 by
+    // parts, 1500 (192) 146 and 111, three of 500 (224) 59 and 61, 4096 (528) 419 and 608; heads
+    // of 128 in bf16, 200 tokens (32) 18 and 13, 611 and 54 of 6 and 3 (42) 25 and 19, 1000
+    // (128) 33 and 33, 1500 (192) 42 and 62.
+    if (groups < (BF16 ? 64 : 200)) hipLaunchKernelGGL((attention_few_kernel<BF16, D, DIRECT>), dim3((unsigned)(tile_slots(a.Tq, PartsShape<BF16, D>::kOwn, a.n) * a.q_heads)), dim3(kPartsThreads), 0, s, a);
+    else hipLaunchKernelGGL((attention_kernel<BF16, D, DIRECT>), dim3((unsigned)groups), dim3(F::kThreads), 0, s, a);
     return hipGetLastError();
 }
 template <bool BF16, int D>

@@ -136,7 +136,11 @@ CASES = [
     ([640], [1000], 3, 1, 128, True, 0, BF16, 5), ([900, 450], None, 2, 1, 128, True, 500, BF16, 3), ([1000], [300], 4, 2, 64, False, 0, BF16, 0),
     ([400], None, 4, 2, 192, True, 0, F32, 0), ([300, 100], None, 2, 1, 256, True, 0, F32, 3), ([520], None, 4, 1, 128, True, 200, F32, 0), ([600], None, 2, 1, 256, True, 0, BF16, 0),
     # workgroups enough for dK and dV by one each, in fp32
-    ([700, 333], None, 16, 8, 64, True, 0, F32, 0), ([600, 500], None, 16, 8, 96, False, 0, F32, 4)]
+    ([700, 333], None, 16, 8, 64, True, 0, F32, 0), ([600, 500], None, 16, 8, 96, False, 0, F32, 4),
+    # more rows than go by parts of the keys: bf16 from 64 tiles of 128 rows times heads on, fp32 from 200
+    ([130] * 5, None, 12, 4, 64, True, 0, BF16, 0), ([260, 40], [300, 90], 32, 8, 128, True, 90, BF16, 3), ([400, 20], None, 16, 2, 192, True, 0, BF16, 0),
+    ([333], None, 24, 4, 256, False, 0, BF16, 8), ([130] * 9, None, 12, 4, 64, True, 0, F32, 0), ([260, 40], [300, 90], 64, 8, 128, True, 90, F32, 3),
+    ([140] * 4, None, 26, 2, 192, True, 0, F32, 0), ([300], None, 80, 4, 256, True, 0, F32, 0)]
 
 
 @pytest.mark.parametrize("lq,lk,heads,Hkv,D,causal,window,dtype,gap", CASES)
@@ -162,15 +166,16 @@ def test_attention(ctx, lq, lk, heads, Hkv, D, causal, window, dtype, gap):
     assert torch.equal(alone, out[:n])
 
 
+@pytest.mark.parametrize("heads", [2, 100])  # few rows, and many
 @pytest.mark.parametrize("dtype", [BF16, F32])
-def test_scales_and_sharp_rows(ctx, dtype):
+def test_scales_and_sharp_rows(ctx, dtype, heads):
     """Scores far apart, all equal, and a scale of its own."""
     for factor, scale in ((40.0, 1.0), (0.0, 1.0), (1.0, 2.5), (1.0, 1e-20)):
-        q, k, v, oq, ok = _inputs(5, [150], [150], 2, 1, 64, dtype)
+        q, k, v, oq, ok = _inputs(5, [150], [150], heads, 1, 64, dtype)
         q = (q * factor).contiguous()
         out, lse = _forward(ctx, q, k, v, oq, ok, scale=scale)
         _check_forward(q, k, v, out, lse, [150], [150], scale)
-        dout = A.normal(A.gen(2), 150, 2, 64, dtype)
+        dout = A.normal(A.gen(2), 150, heads, 64, dtype)
         _check_backward(dout, q, k, v, out, lse, _backward(ctx, dout, q, k, v, out, lse, oq, ok, scale=scale), [150], [150], scale)
 
 
@@ -217,16 +222,17 @@ def test_packed_is_one_by_one(ctx):
             assert torch.equal(a[r], b)
 
 
+@pytest.mark.parametrize("heads", [2, 80])  # few rows, and many
 @pytest.mark.parametrize("dtype", [BF16, F32])
 @pytest.mark.parametrize("value", [math.nan, math.inf, -math.inf])
-def test_what_is_not_seen_adds_nothing(ctx, dtype, value):
+def test_what_is_not_seen_adds_nothing(ctx, dtype, value, heads):
     """Infinities and NaN in keys, values, queries and gradients: rows and keys that do
     not see them keep their bits, those that see them are NaN (in the value's channel)."""
     n, at, D, window = 150, 70, 64, 20
     for win in (0, window):
         kw = dict(window=win)
-        q, k, v, oq, ok = _inputs(8, [n, 40], [n, 40], 2, 1, D, dtype)
-        dout = A.normal(A.gen(1), n + 40, 2, D, dtype)
+        q, k, v, oq, ok = _inputs(8, [n, 40], [n, 40], heads, 1, D, dtype)
+        dout = A.normal(A.gen(1), n + 40, heads, D, dtype)
         out, lse = _forward(ctx, q, k, v, oq, ok, **kw)
         grads = _backward(ctx, dout, q, k, v, out, lse, oq, ok, **kw)
         row = torch.arange(n + 40, device="cuda")
@@ -255,17 +261,18 @@ def test_what_is_not_seen_adds_nothing(ctx, dtype, value):
             for a, b in zip(bad[1:], grads[1:]):
                 assert torch.equal(a[~seen], b[~seen])
             for a, b in zip(bad[:1], grads[:1]):
-                keep = torch.ones(n + 40, 2, dtype=torch.bool, device="cuda")
+                keep = torch.ones(n + 40, heads, dtype=torch.bool, device="cuda")
                 keep[at, 1] = False
                 assert torch.equal(a[keep], b[keep])
             assert not bad[1][seen][..., 5].isfinite().any() if which == "q" else not bad[2][seen][..., 5].isfinite().any()
 
 
-def test_offsets_that_cannot_be(ctx):
+@pytest.mark.parametrize("heads", [2, 20])  # few rows, and many
+def test_offsets_that_cannot_be(ctx, heads):
     """NaN for that sequence, error word, the others as ever, nothing outside."""
-    q, k, v, good, _ = _inputs(2, [40, 50, 60], [40, 50, 60], 2, 1, 64, BF16, tail=10)
+    q, k, v, good, _ = _inputs(2, [40, 50, 60], [40, 50, 60], heads, 1, 64, BF16, tail=10)
     out, lse = _forward(ctx, q, k, v, good, good)
-    dout = A.normal(A.gen(1), 160, 2, 64, BF16)
+    dout = A.normal(A.gen(1), 160, heads, 64, BF16)
     grads = _backward(ctx, dout, q, k, v, out, lse, good, good)
     assert moe.moe_check(ctx) == moe.MOE_OK
     for off, keep in (([0, 40, 90, 161], slice(0, 90)), ([-3, 40, 90, 150], slice(40, 150)), ([0, 40, 90, 2 ** 31 - 1], slice(0, 90))):
@@ -355,9 +362,10 @@ def test_prompt_then_decode(ctx):
     A.close(a, b.double(), torch.full_like(a, 1e-4, dtype=torch.float64))
 
 
-def test_tokens_far_apart(ctx):
+@pytest.mark.parametrize("heads", [2, 64])  # few rows, and many
+def test_tokens_far_apart(ctx, heads):
     """Tokens so far apart that a tile spans more than 2^32 bytes."""
-    q, k, v, oq, _ = _inputs(3, [70], [70], 2, 1, 64, BF16)
+    q, k, v, oq, _ = _inputs(3, [70], [70], heads, 1, 64, BF16)
     ld = (1 << 32) // 2 // 64 + 8
 
     def apart(t):
@@ -365,7 +373,7 @@ def test_tokens_far_apart(ctx):
         far.copy_(t)
         return far
     out, lse = _forward(ctx, q, k, v, oq, oq)
-    dout = A.normal(A.gen(4), 70, 2, 64, BF16)
+    dout = A.normal(A.gen(4), 70, heads, 64, BF16)
     grads = _backward(ctx, dout, q, k, v, out, lse, oq, oq)
     far = [apart(t) for t in (q, k, v)]
     o, s = _forward(ctx, *far, oq, oq)
