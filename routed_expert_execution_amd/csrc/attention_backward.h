@@ -18,7 +18,7 @@ namespace packed {
 
 // fp32, and bf16 heads of more than 128 channels, by PartsShape.  Two sequences of 611 and
 // 54 tokens, 6 and 3 heads of 96 in fp32: 65 us (one launch after the other, dK and dV
-// together: 123), ten steps one after the other, of whose 4 us the products take half.  fp32
+// together: 123), ten steps one after the other, of whose 4 us the products take 1.5.  fp32
 // heads of 192 and 256 channels spill.
 // What the others need of each row: L / ln 2 and delta = rowsum(dO O), by 16 or 32 lanes a
 // row.  Bound by bytes: 8532 rows of 16 heads of 128 in bf16 14 us.
@@ -338,9 +338,9 @@ __global__ __launch_bounds__(kPartsThreads) void attention_parts_kernel(PackedAr
 // (dK, dV).
 // DIRECT: tiles go straight from memory into LDS.
 // Four sequences of up to 4096 tokens, 16 query and 4 key heads of 128, causal: 511 us (dQ
-// after dK and dV in launches of their own 193 and 360, the matrix cores busy for 0.46 of
-// it; 3548 tokens 230 for 190, 665 tokens 72 for 50); what is left is the vector unit's
-// work, reads of LDS behind a step's barrier, and the eight products in place of five.
+// and dK, dV in launches of their own 193 and 360; 3548 tokens 230 for 190, 665 tokens 72
+// for 50), the matrix cores busy for 0.45 of it; what is left is the vector unit's work,
+// reads of LDS behind a step's barrier, and the eight products in place of five.
 constexpr int kAhead = 2;  // products between an operand's read and its use
 
 constexpr int kBesideThreads = 512;
