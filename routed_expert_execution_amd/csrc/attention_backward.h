@@ -836,7 +836,7 @@ inline dim3 grid_of(int64_t groups) {  // (threads of a grid's row: 32 bits)
 template <bool BF16, int D>
 void launch_rows(const PackedArgs& a, hipStream_t s) {
     const int64_t groups = ((int64_t)a.Tq * a.q_heads + 7) / 8;
-    hipLaunchKernelGGL((attention_rows_kernel<BF16, D>), dim3((unsigned)std::min<int64_t>(groups, 8192)), dim3(kRowsThreads), 0, s, a);
+    hipLaunchKernelGGL((attention_rows_kernel<BF16, D>), dim3((unsigned)std::min<int64_t>(std::max<int64_t>(groups, 1), 8192)), dim3(kRowsThreads), 0, s, a);
 }
 template <int D, bool DIRECT>
 void launch_beside(const PackedArgs& a, hipStream_t s) {

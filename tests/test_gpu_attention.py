@@ -291,6 +291,26 @@ def test_offsets_that_cannot_be(ctx, heads):
     assert moe.moe_check(ctx) == moe.MOE_EINVAL
 
 
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("D", [128, 256])
+def test_keys_without_queries(ctx, dtype, D):
+    """No queries at all, or no keys at all: gradients of zero, rows of zero."""
+    k, v = (A.normal(A.gen(6), 70, 2, D, dtype) for _ in range(2))
+    none, off, empty = torch.empty(0, 4, D, dtype=dtype, device="cuda"), A.ints([0, 30, 70]), A.ints([0, 0, 0])
+    dk, dv = torch.full_like(k, 7), torch.full_like(v, 7)
+    ws = torch.empty(256, dtype=torch.uint8, device="cuda")
+    moe.moe_attention(ctx, none, k, v, empty, none, offsets_k=off)
+    moe.moe_attention_backward(ctx, none, none, k, v, none, torch.empty(0, 4, device="cuda"), empty, dq=none, dk=dk, dv=dv, workspace=ws, offsets_k=off)
+    assert not dk.any() and not dv.any()
+    q, nothing = A.normal(A.gen(7), 70, 4, D, dtype), torch.empty(0, 2, D, dtype=dtype, device="cuda")
+    out, lse = _forward(ctx, q, nothing, nothing, off, empty)
+    assert not out[:70].any() and (lse[:70] == -math.inf).all()
+    dq = torch.full_like(q, 7)
+    ws = torch.empty(moe.moe_attention_workspace(ctx, q), dtype=torch.uint8, device="cuda")
+    moe.moe_attention_backward(ctx, q, q, nothing, nothing, out, lse, off, dq=dq, dk=nothing, dv=nothing, workspace=ws, offsets_k=empty)
+    assert not dq.any() and moe.moe_check(ctx) == moe.MOE_OK
+
+
 def test_a_tuning_step_captured(ctx):
     """Rotate, attend and back, captured once; each replay on new inputs and other lengths
     against the eager calls; and both on two streams at once."""
