@@ -281,7 +281,10 @@ __global__ __launch_bounds__(kThreads, cached_per_cu(W, BF16)) void cached_kerne
         for (int g = 0; g < G; g++) low[g] = 0;
 #pragma unroll 1
         for (; step < last_step; step += kWaves) {
-            bool fine = true;  // no value of the step is NaN
+            // no value of the step is NaN or infinite.  What a sequence holds is not infinite,
+            // but in place of a page before the tile's window page 0 is read, which nobody may
+            // have written
+            bool fine = true;
 #pragma unroll
             for (int x = 0; x < 4; x++)
 #pragma unroll
@@ -293,7 +296,7 @@ __global__ __launch_bounds__(kThreads, cached_per_cu(W, BF16)) void cached_kerne
                         pairs[wave][x][0][lane + 64 * n] = by;
                         const float rest = fmaf(x < 2 && !kCentred ? -16.f : 8.f, by, f16_bits_to_f32(w >> 16));
                         pairs[wave][x][1][lane + 64 * n] = rest;
-                        if (x >= 2) fine &= rest == rest;
+                        if (x >= 2) fine &= fabsf(rest) < kInf;  // (not so if either is infinite)
                     }
             __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
             __builtin_amdgcn_wave_barrier();

@@ -1,0 +1,58 @@
+"""GPU: attention where memory holds what no call has written, and where values are not finite."""
+import math
+
+import pytest
+
+from tests import harness as H
+
+pytestmark = pytest.mark.gpu
+
+torch = pytest.importorskip("torch")
+if not H.gpu_available():  # pragma: no cover
+    pytest.skip("no GPU", allow_module_level=True)
+
+from routed_expert_execution_amd import moe  # noqa: E402
+from tests import attention_cases as A  # noqa: E402
+from tests.attention_cases import BF16, F32  # noqa: E402
+
+
+@pytest.fixture(scope="module")
+def ctx():
+    return A.context()
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("new,lengths,page,D,group,window", [
+    ([1], [400], 16, 64, 32, 50), ([3, 1], [1000, 333], 16, 128, 64, 17), ([40], [700], 32, 96, 32, 100), ([1], [129], 64, 256, 128, 1), ([1], [5000], 16, 128, 128, 1000),
+    ([2, 1, 5], [77, 47, 300], 16, 192, 64, 30)])
+def test_unwritten_pages_and_a_window(ctx, new, lengths, page, D, group, window, dtype):
+    """Pages that no call has written hold fp16 infinities or NaN, page 0 among them; so do
+    those that lie before the windows, which the table no longer names."""
+    g, Hkv, heads = A.gen(31), 2, 4
+    table, total = A.page_table(g, lengths, page, spare=1)
+    table = torch.where(table >= 0, table + 1, table)  # page 0 is no sequence's
+    whole = moe.KvBatch(ctx, A.offsets(lengths), A.ints(lengths), table, tokens=sum(lengths))
+    x = [A.normal(g, sum(lengths), Hkv, D, F32) for _ in range(2)]
+    q = A.normal(g, sum(new), heads, D, dtype)
+    within = table.clone()
+    for s, (n, length) in enumerate(zip(new, lengths)):
+        within[s, :max(0, length - n - window + 1) // page] = -1
+    batch = moe.KvBatch(ctx, A.offsets(new), A.ints(lengths), within, tokens=sum(new), most_new=max(new))
+
+    def outcome(fill):
+        cache = moe.KvCache(ctx, total + 1, page, Hkv, D, group)
+        cache.data.view(torch.int16).fill_(fill)
+        moe.moe_kv_append(ctx, cache, whole, *x)
+        for s in range(len(lengths)):
+            for p in table[s][(within[s] < 0) & (table[s] >= 0)].tolist():
+                cache.data.view(cache.pages, -1)[p].view(torch.int16).fill_(fill)
+        out = torch.empty_like(q)
+        ws = torch.empty(moe.moe_attention_cached_workspace(ctx, cache, batch, heads), dtype=torch.uint8, device="cuda")
+        moe.moe_attention_cached(ctx, cache, batch, q, out, window=window, workspace=ws)
+        assert moe.moe_check(ctx) == moe.MOE_OK
+        return out
+
+    want = outcome(0)
+    assert want.isfinite().all()
+    for fill in (0x7C00, 0xFC00 - 0x10000, 0x7E00, -1):
+        assert torch.equal(outcome(fill), want), hex(fill & 0xFFFF)
