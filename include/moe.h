@@ -591,9 +591,12 @@ typedef struct moe_rotary {
  *                      highest stays, the lowest is divided by factor
  *   MOE_ROTARY_RAMP    those that turn at least `fast` times within `context` (the
  *                      trained length) stay, those that turn at most `slow` times are
- *                      divided by factor, between them by the pair's place between
- *                      the two (pairs' numbers, the ends rounded outwards); *scale
- *                      becomes 0.1 ln(factor) + 1, else 1
+ *                      divided by factor, those between by the pair's place between
+ *                      the two, t = (i - low) / (high - low) in 0 .. 1:
+ *                      f (1 - t) + f / factor t.  low and high are the pairs' numbers
+ *                      (real ones) that turn `fast` and `slow` times, rounded outwards,
+ *                      low at least 0, high at most rot - 1, which lies past the last
+ *                      pair; *scale becomes 0.1 ln(factor) + 1, else 1
  * freqs: host [rot / 2], scale: host [1].  base > 1, factor >= 1, 0 < slow < fast,
  * context >= 1 (the last three used by RAMP alone), else MOE_EINVAL. */
 enum { MOE_ROTARY_PLAIN = 0, MOE_ROTARY_LINEAR = 1, MOE_ROTARY_BASE = 2, MOE_ROTARY_RAMP = 3 };

@@ -87,8 +87,11 @@ moe_status moe_rotary_freqs(int32_t rot, double base, int32_t kind, double facto
             const double pi = 3.14159265358979323846;
             auto pair_of = [&](double n) { return rot * std::log(context / (2 * pi * n)) / (2 * std::log(base)); };
             low = std::fmax(std::floor(pair_of(fast)), 0);
-            high = std::fmin(std::ceil(pair_of(slow)), half - 1);
-            if (high <= low) high = low + 0.001;  // (all pairs on one side, or on both of one border)
+            high = std::fmin(std::ceil(pair_of(slow)), rot - 1);  // (may lie past the last pair)
+            if (high <= low) {  // all pairs on one side: none turns more than `slow` times, or all at least `fast`
+                if (low == 0) low = high - 1;
+                else high = low + 1;
+            }
             *scale = (float)(0.1 * std::log(factor) + 1);
             break;
         }
