@@ -700,12 +700,12 @@ typedef struct moe_attn {
  * [tokens_q, q_heads, head_dim], k, v: device [tokens_k, kv_heads, head_dim].
  * lse: device fp32 [tokens_q, q_heads] or NULL, the log of each row's sum of
  * exponentials, which the backward pass needs.  A query that sees no key gets zeros
- * and minus infinity.  Keys that a query does not see add nothing to its row, even
- * where their values are not finite; a value that is not finite makes the rows that
- * see it NaN in its channel.  Sums and softmax are fp32; the exponentials are
- * rounded to bf16 before the second product (bf16) or enter as three bf16 terms, as
- * every fp32 factor does (see moe_gated).  A sequence whose offsets cannot be gives
- * NaN. */
+ * and minus infinity; one that holds a NaN, or sees a key that does, gets NaN in both.
+ * Keys that a query does not see add nothing to its row, even where their values are
+ * not finite; a value that is not finite makes the rows that see it NaN in its channel.
+ * Sums and softmax are fp32; the exponentials are rounded to bf16 before the second
+ * product (bf16) or enter as three bf16 terms, as every fp32 factor does (see
+ * moe_gated).  A sequence whose offsets cannot be gives NaN. */
 moe_status moe_attention(moe_ctx* ctx, const moe_attn* attn, const void* q, int64_t ldq, const void* k, int64_t ldk,
                          const void* v, int64_t ldv, void* out, int64_t ldo, float* lse, moe_stream stream);
 

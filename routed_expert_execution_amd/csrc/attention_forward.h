@@ -288,8 +288,9 @@ __global__ __launch_bounds__(kForwardWaves * 64, BF16 && D <= 128 ? 2 : 1) void 
     const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(l), __float_as_uint(l), false, false);
     const float sum = __uint_as_float(r[0]) + __uint_as_float(r[1]);
     if (!live) return;
-    // a row that sees nothing: 0, and minus infinity
-    const float by = s.bad ? nan : m == -kInf && sum == 0.f ? 0.f : 1.0f / sum;
+    // a row that sees nothing: 0, and minus infinity (one whose scores are NaN leaves m so too, but not its sum)
+    const bool none = m == -kInf && sum == 0.f;
+    const float by = s.bad ? nan : none ? 0.f : 1.0f / sum;
     const int64_t token = s.q0 + row, o = token * a.ldo + (int64_t)head * D;
 #pragma unroll
     for (int d = 0; d < DB; d++)
@@ -297,7 +298,7 @@ __global__ __launch_bounds__(kForwardWaves * 64, BF16 && D <= 128 ? 2 : 1) void 
         for (int j = 0; j < 4; j++)
 #pragma unroll
             for (int e = 0; e < 4; e++) store1<BF16>(a.out, o + 32 * d + 8 * j + 4 * h + e, out[d][4 * j + e] * by);
-    if (a.lse && h == 0) a.lse[token * a.q_heads + head] = s.bad ? nan : m == -kInf ? -kInf : fmaf(m, a.scale, __builtin_amdgcn_logf(sum) * kLn2);
+    if (a.lse && h == 0) a.lse[token * a.q_heads + head] = s.bad ? nan : none ? -kInf : fmaf(m, a.scale, __builtin_amdgcn_logf(sum) * kLn2);
 }
 
 // The same for few rows, by PartsShape: 32 (or 64) rows a workgroup, its waves over parts of
@@ -449,7 +450,8 @@ __global__ __launch_bounds__(kPartsThreads) void attention_few_kernel(PackedArgs
     for (int d = 0; d < DB; d++) out[d] *= f;
     if (!add_parts<DB, B::kParts, B::kBlocks>(out, lds, part, block, lane) || !live) return;
     const float nan = __uint_as_float(0x7FC00000u);
-    const float by = s.bad ? nan : all == -kInf && sum == 0.f ? 0.f : 1.0f / sum;
+    const bool none = all == -kInf && sum == 0.f;  // (as above)
+    const float by = s.bad ? nan : none ? 0.f : 1.0f / sum;
     const int64_t o = token * a.ldo + (int64_t)head * D;
 #pragma unroll
     for (int d = 0; d < DB; d++)
@@ -457,7 +459,7 @@ __global__ __launch_bounds__(kPartsThreads) void attention_few_kernel(PackedArgs
         for (int j = 0; j < 4; j++)
 #pragma unroll
             for (int e = 0; e < 4; e++) store1<BF16>(a.out, o + 32 * d + 8 * j + 4 * h + e, out[d][4 * j + e] * by);
-    if (a.lse && h == 0) a.lse[token * a.q_heads + head] = s.bad ? nan : all == -kInf ? -kInf : fmaf(all, a.scale, __builtin_amdgcn_logf(sum) * kLn2);
+    if (a.lse && h == 0) a.lse[token * a.q_heads + head] = s.bad ? nan : none ? -kInf : fmaf(all, a.scale, __builtin_amdgcn_logf(sum) * kLn2);
 }
 
 template <bool BF16, int D, bool DIRECT>

@@ -56,3 +56,40 @@ def test_unwritten_pages_and_a_window(ctx, new, lengths, page, D, group, window,
     assert want.isfinite().all()
     for fill in (0x7C00, 0xFC00 - 0x10000, 0x7E00, -1):
         assert torch.equal(outcome(fill), want), hex(fill & 0xFFFF)
+
+
+def _forward(ctx, q, k, v, off, **kw):
+    out, lse = torch.empty_like(q), torch.empty(q.shape[:2], device="cuda")
+    moe.moe_attention(ctx, q, k, v, off, out, lse=lse, **kw)
+    return out, lse
+
+
+@pytest.mark.parametrize("heads", [2, 80])  # few rows, and many
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("window", [0, 20])
+def test_log_sums_of_rows_that_see_nan(ctx, dtype, heads, window):
+    """NaN, as the row itself: minus infinity is a row's that sees no key."""
+    lengths, D = [150, 40, 7], 64  # the last two fit into one tile
+    off, T = A.offsets(lengths), sum(lengths)
+    g = A.gen(8)
+    q, k, v = A.normal(g, T, heads, D, dtype), A.normal(g, T, 1, D, dtype), A.normal(g, T, 1, D, dtype)
+    out, lse = _forward(ctx, q, k, v, off, window=window)
+    assert lse.isfinite().all()
+    at = 0
+    for n in lengths:
+        key = at + n // 3
+        x = k.clone()
+        x[key, 0, 5] = math.nan
+        o, s = _forward(ctx, q, x, v, off, window=window)
+        row = torch.arange(T, device="cuda")
+        sees = (row >= key) & (row < at + n) & ((row < key + window) if window else True)
+        assert s[sees].isnan().all() and o[sees].isnan().all()
+        assert torch.equal(s[~sees], lse[~sees]) and torch.equal(o[~sees], out[~sees])
+        y = q.clone()
+        y[key, 1, 9] = math.nan
+        o, s = _forward(ctx, y, k, v, off, window=window)
+        keep = torch.ones(T, heads, dtype=torch.bool, device="cuda")
+        keep[key, 1] = False
+        assert s[key, 1].isnan() and o[key, 1].isnan().all()
+        assert torch.equal(s[keep], lse[keep]) and torch.equal(o[keep], out[keep])
+        at += n
