@@ -702,7 +702,8 @@ typedef struct moe_attn {
  * exponentials, which the backward pass needs.  A query that sees no key gets zeros
  * and minus infinity; one that holds a NaN, or sees a key that does, gets NaN in both.
  * Keys that a query does not see add nothing to its row, even where their values are
- * not finite; a value that is not finite makes the rows that see it NaN in its channel.
+ * not finite; a value that is not finite makes the rows that see it NaN in its channel
+ * (finite ones should stay below 2^98: they are summed times up to 2^8 before the division).
  * Sums and softmax are fp32; the exponentials are rounded to bf16 before the second
  * product (bf16) or enter as three bf16 terms, as every fp32 factor does (see
  * moe_gated).  A sequence whose offsets cannot be gives NaN. */
@@ -718,7 +719,9 @@ size_t moe_attention_workspace(int64_t tokens_q, int32_t q_heads);
  * those of k and v summed over the query heads of a key head, all three written (not
  * added to), every sum in fp32 and in one order.  P and dS are rounded to bf16 before
  * the second products (bf16).  Rows and keys that do not see each other add nothing
- * to each other's gradients, whatever they hold.  workspace: device, 256-byte
+ * to each other's gradients, whatever they hold; what is not finite makes those that it
+ * enters not finite.  dq, dk and dv may share memory neither with each other nor with an
+ * input, lse among them: all are read while they are written.  workspace: device, 256-byte
  * aligned, moe_attention_workspace() bytes, used until the call's work is done;
  * calls that may run at the same time need one each. */
 moe_status moe_attention_backward(moe_ctx* ctx, const moe_attn* attn, const void* dout, int64_t lddo, const void* q, int64_t ldq,

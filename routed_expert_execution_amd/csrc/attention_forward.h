@@ -297,7 +297,7 @@ __global__ __launch_bounds__(kForwardWaves * 64, BF16 && D <= 128 ? 2 : 1) void 
 #pragma unroll
         for (int j = 0; j < 4; j++)
 #pragma unroll
-            for (int e = 0; e < 4; e++) store1<BF16>(a.out, o + 32 * d + 8 * j + 4 * h + e, out[d][4 * j + e] * by);
+            for (int e = 0; e < 4; e++) store1<BF16>(a.out, o + 32 * d + 8 * j + 4 * h + e, nan_if_infinite(out[d][4 * j + e] * by));
     if (a.lse && h == 0) a.lse[token * a.q_heads + head] = s.bad ? nan : none ? -kInf : fmaf(m, a.scale, __builtin_amdgcn_logf(sum) * kLn2);
 }
 
@@ -458,7 +458,7 @@ __global__ __launch_bounds__(kPartsThreads) void attention_few_kernel(PackedArgs
 #pragma unroll
         for (int j = 0; j < 4; j++)
 #pragma unroll
-            for (int e = 0; e < 4; e++) store1<BF16>(a.out, o + 32 * d + 8 * j + 4 * h + e, out[d][4 * j + e] * by);
+            for (int e = 0; e < 4; e++) store1<BF16>(a.out, o + 32 * d + 8 * j + 4 * h + e, nan_if_infinite(out[d][4 * j + e] * by));
     if (a.lse && h == 0) a.lse[token * a.q_heads + head] = s.bad ? nan : none ? -kInf : fmaf(all, a.scale, __builtin_amdgcn_logf(sum) * kLn2);
 }
 

@@ -309,6 +309,10 @@ __device__ inline void mma_seen(f32x16& acc, const Fragment<false>& a, const Fra
     }
 }
 
+// A result that met an infinity: NaN, as a masked tile's values give it (mma_seen), and not
+// an infinity or NaN by where in the sequence the value lies.
+__device__ inline float nan_if_infinite(float v) { return fmaf(v, 0.f, v); }
+
 // A sequence's rows of queries and keys; what lies outside the tensors is cut off
 // and makes it bad.
 struct Sequence {

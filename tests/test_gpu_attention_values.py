@@ -93,3 +93,25 @@ def test_log_sums_of_rows_that_see_nan(ctx, dtype, heads, window):
         assert s[key, 1].isnan() and o[key, 1].isnan().all()
         assert torch.equal(s[keep], lse[keep]) and torch.equal(o[keep], out[keep])
         at += n
+
+
+@pytest.mark.parametrize("heads", [2, 80])  # few rows, and many
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("D", [64, 128, 192])
+@pytest.mark.parametrize("causal,window,at", [(False, 0, 100), (True, 0, 100), (True, 300, 200), (False, 0, 399), (True, 0, 399), (False, 0, 0)])
+def test_infinite_values(ctx, dtype, heads, D, causal, window, at):
+    """A value that is not finite makes the rows that see it NaN in its channel, wherever in
+    the sequence it lies: in a tile that all rows see whole, or in one that is masked."""
+    n = 400
+    off, g = A.ints([0, n]), A.gen(5)
+    q, k, v = A.normal(g, n, heads, D, dtype), A.normal(g, n, 1, D, dtype), A.normal(g, n, 1, D, dtype)
+    out, lse = _forward(ctx, q, k, v, off, causal=causal, window=window)
+    row = torch.arange(n, device="cuda")
+    sees = ((row >= at) | (not causal)) & ((row < at + window) if window else True)
+    others = torch.arange(D, device="cuda") != 5
+    for value in (math.inf, -math.inf, math.nan):
+        w = v.clone()
+        w[at, 0, 5] = value
+        o, s = _forward(ctx, q, k, w, off, causal=causal, window=window)
+        assert o[sees][..., 5].isnan().all()
+        assert torch.equal(s, lse) and torch.equal(o[~sees], out[~sees]) and torch.equal(o[..., others], out[..., others])
