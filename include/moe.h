@@ -616,7 +616,9 @@ moe_status moe_rotate(moe_ctx* ctx, const void* x, int32_t dtype, int64_t ldx, i
  * and `group` channels (32, 64 or 128, a divisor of head_dim):
  *   lowest = fp16(min x), step = fp16((max x - lowest) / 15),
  *   code = round((x - lowest) / step) in 0 .. 15,  value = lowest + step * code
- * (halves to the even code; step 0: code 0).  A group that holds a NaN, an infinity or a value
+ * (halves to the even code; a step of 0, or below it, where fp16's rounding takes the
+ * lowest past the highest value: code 0).  min, and max - lowest, reach fp16 by way of
+ * fp32; codes are those of the exact values, a rotated key's in 64 bits.  A group that holds a NaN, an infinity or a value
  * beyond 65504 in magnitude is kept as NaN.
  * data: device, 16-byte aligned, moe_kv_bytes() bytes; needs no clearing. */
 typedef struct moe_kv_cache {

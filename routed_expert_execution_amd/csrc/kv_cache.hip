@@ -24,8 +24,10 @@ template <typename F> __device__ inline float over_group(float v, int n, F f) {
 
 // Eight channels of a thread to codes.  Which of two values next to their border a step
 // or a code takes is decided in 64 bits, by the value and not by roundings on the way;
-// but only there, and 32 bits say where that is: the quotients are within 2^-21 of
-// theirs, relative, of 15 at most.
+// but only there, and 32 bits say where that is: x less the lowest value is taken in 64
+// bits (its own rounding to fp32 would be up to |x| 2^-24, many steps' parts where a group
+// lies far from zero for how far its values lie apart), so that the quotients are within
+// 2^-21 of theirs, relative, of 15 at most.
 // Returns eight codes, four bits each; *steps the word that stands for the group.
 __device__ inline uint32_t to_codes(const double (&x)[8], int group, uint32_t* steps) {
     const int n = group / 8;
@@ -66,7 +68,7 @@ __device__ inline uint32_t to_codes(const double (&x)[8], int group, uint32_t* s
     uint32_t codes = 0;
 #pragma unroll
     for (int i = 0; i < 8; i++) {
-        const float t = fminf(fmaxf((xf[i] - low) * inverse, 0.f), 15.f);
+        const float t = fminf(fmaxf((float)(x[i] - (double)low) * inverse, 0.f), 15.f);
         float q = rintf(t);
         const bool near = some && fabsf(fabsf(t - q) - 0.5f) < 1e-4f;
         if (__any(near)) {  // halves go to the even code

@@ -115,3 +115,31 @@ def test_infinite_values(ctx, dtype, heads, D, causal, window, at):
         o, s = _forward(ctx, q, k, w, off, causal=causal, window=window)
         assert o[sees][..., 5].isnan().all()
         assert torch.equal(s, lse) and torch.equal(o[~sees], out[~sees]) and torch.equal(o[..., others], out[..., others])
+
+
+@pytest.mark.parametrize("offset,spread,dtype", [(0.0, 1.0, F32), (100.0, 1.0, F32), (1000.0, 1.0, F32), (10000.0, 1.0, F32), (-10000.0, 6.0, F32), (30000.0, 20.0, F32), (1000.0, 30.0, BF16), (3000.0, 5.0, BF16)])
+def test_codes_of_far_keys(ctx, offset, spread, dtype):
+    """Rotated keys that lie far from zero for how far they lie apart: the codes are those
+    of the exact values."""
+    g, T, Hkv, D, group = A.gen(17), 1024, 8, 128, 32
+    want = (offset + spread * torch.rand(T, Hkv, D, generator=g, device="cuda", dtype=torch.float64))
+    positions, freqs = torch.arange(T, dtype=torch.int32, device="cuda") * 37, A.frequencies(D)
+    k = A.rotated(want, positions, freqs, False, inverse=True).to(dtype)
+    v = want.to(dtype)
+    table = torch.arange(T // 64, dtype=torch.int32, device="cuda").unsqueeze(0)
+    batch = moe.KvBatch(ctx, A.ints([0, T]), A.ints([T]), table, tokens=T)
+    cache = moe.KvCache(ctx, T // 64, 64, Hkv, D, group)
+    moe.moe_kv_append(ctx, cache, batch, k, v, rotary=moe.Rotary(ctx, freqs), positions=positions)
+    got = [torch.empty(T, Hkv, D, device="cuda") for _ in range(2)]
+    moe.moe_kv_read(ctx, cache, batch, *got)
+    for held, x in zip(got, (A.rotated(k, positions, freqs, False), v.double())):
+        x = x.unflatten(-1, (-1, group))
+        low = x.amin(-1, keepdim=True).float().half().double()
+        step = ((x.amax(-1, keepdim=True) - low) / 15).float().half().double()
+        place = torch.where(step > 0, (x - low) / step.clamp_min(1e-30), torch.zeros_like(x))
+        value = low + step * place.round().clamp(0, 15)
+        # the sum's rounding to fp32; next to a border (1e-9 of a step: cosines differ in their last bits) either code
+        border = (place - place.floor() - 0.5).abs() < 1e-9
+        tol = A.U * value.abs() + torch.where(border, step, torch.zeros_like(step))
+        off = (held.unflatten(-1, (-1, group)).double() - value).abs() > tol
+        assert not off.any(), f"{int(off.sum())} of {off.numel()} codes"
