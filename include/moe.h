@@ -618,8 +618,8 @@ moe_status moe_rotate(moe_ctx* ctx, const void* x, int32_t dtype, int64_t ldx, i
  *   code = round((x - lowest) / step) in 0 .. 15,  value = lowest + step * code
  * (halves to the even code; a step of 0, or below it, where fp16's rounding takes the
  * lowest past the highest value: code 0).  min, and max - lowest, reach fp16 by way of
- * fp32; codes are those of the exact values, a rotated key's in 64 bits.  A group that holds a NaN, an infinity or a value
- * beyond 65504 in magnitude is kept as NaN.
+ * fp32; codes are those of the exact values, a rotated key's in 64 bits.  A group that
+ * holds a NaN, an infinity or a value beyond 65504 in magnitude is kept as NaN.
  * data: device, 16-byte aligned, moe_kv_bytes() bytes; needs no clearing. */
 typedef struct moe_kv_cache {
     int64_t pages;

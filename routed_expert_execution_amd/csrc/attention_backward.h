@@ -2,6 +2,10 @@
 // exponentials L and the outputs O that the forward pass has kept:
 //   P = exp(scale Q K^T - L),  dV = P^T dO,  dP = dO V^T,  delta = rowsum(dO O),
 //   dS = P (dP - delta),  dQ = scale dS K,  dK = scale dS^T Q.
+// In bf16 P and dS are rounded to bf16 for the second products: the gradients are 0.0023 off,
+// their own rounding being 0.0017.  Two terms of both, in the steady loops, take 616 us for
+// 489 (four sequences of up to 4096 tokens, 16 and 4 heads of 128); who needs them whole
+// calls in fp32.
 // delta first, then one launch of workgroups with results of their own rows only, so that
 // sums have one order and nothing is added in memory: dQ over tiles of queries, dK and dV
 // over tiles of keys (with all query heads of the key head).  S and dP are computed in
@@ -19,9 +23,9 @@ namespace packed {
 // fp32, and bf16 heads of more than 128 channels, by PartsShape.  Two sequences of 611 and
 // 54 tokens, 6 and 3 heads of 96 in fp32: 65 us (one launch after the other, dK and dV
 // together: 123), ten steps one after the other, of whose 4 us the products take 1.5.  fp32
-// heads of 192 and 256 channels spill.
+// heads of 192 and 256 channels spill (361 and 882 registers), of 96 with ROLES 1 a few (42).
 // What the others need of each row: L / ln 2 and delta = rowsum(dO O), by 16 or 32 lanes a
-// row.  Bound by bytes: 8532 rows of 16 heads of 128 in bf16 14 us.
+// row.  Bound by bytes: 8532 rows of 16 heads of 128 in bf16 18 us.
 constexpr int kRowsThreads = 256;
 template <bool BF16, int D>
 __global__ __launch_bounds__(kRowsThreads) void attention_rows_kernel(PackedArgs a) {
@@ -336,7 +340,8 @@ __global__ __launch_bounds__(kPartsThreads) void attention_parts_kernel(PackedAr
 // exponentials, and the products with them follow, so that the matrix cores wait
 // neither for the vector unit nor for LDS.  A block is 32 keys (dQ) or 32 rows a wave
 // (dK, dV).
-// DIRECT: tiles go straight from memory into LDS.
+// DIRECT: tiles go straight from memory into LDS; 18 registers are spilled there at 128
+// channels, none in the steady loops (149 where lines go through registers).
 // Four sequences of up to 4096 tokens, 16 query and 4 key heads of 128, causal: 511 us (dQ
 // and dK, dV in launches of their own 193 and 360; 3548 tokens 230 for 190, 665 tokens 72
 // for 50), the matrix cores busy for 0.45 of it; what is left is the vector unit's work,

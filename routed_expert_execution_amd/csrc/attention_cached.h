@@ -161,10 +161,14 @@ template <int N> __device__ inline void terms_of(const float (&v)[8], bf16x8_t (
 // lowest) pairs scale the first product's result and the second one's P.  P times
 // the step is rounded to bf16 and multiplies code - 8, which lies about zero as the
 // values do; the rest, lowest + 8 steps, is added in fp32.  (With code itself the
-// result was 0.0031 off, its own rounding being 0.0016.)  Bound by the cache's bytes
-// where sequences are long: 64 of up to 16000 tokens, 64 query and 8 key heads of 128,
-// 128 us (3.8 TB/s); one of 130001 tokens, 32 and 8, 44 us (3.8 TB/s); by latency where
-// they are short: one of 777 tokens 7.5 us, the first read and one round.
+// result was 0.0031 off, its own rounding being 0.0016.)  P is rounded because two bf16
+// terms of it, which leave the result's own rounding alone (0.0022 -> 0.0017 for one of 777
+// tokens), take 140 us for 131 for the 64 sequences below and 57 for 52 for 130001 tokens;
+// who needs it whole calls in fp32.
+// Bound by the cache's bytes where sequences are long: 64 of up to 16000 tokens, 64 query
+// and 8 key heads of 128, 126 us (3.9 TB/s); one of 130001 tokens, 32 and 8, 47 us (3.5
+// TB/s); by latency where they are short: one of 777 tokens 7.5 us, the first read and one
+// round.
 template <int W, int JP, bool BF16>
 __global__ __launch_bounds__(kThreads, cached_per_cu(W, BF16)) void cached_kernel(CachedArgs a) {
     constexpr int N = BF16 ? 1 : 3;  // bf16 terms of a factor

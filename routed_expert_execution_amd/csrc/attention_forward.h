@@ -1,6 +1,9 @@
 // Attention over packed sequences, forward:
 //   S = scale Q K^T,  P = softmax of each row over the keys that it sees,  O = P V.
-// One pass over the keys with a running maximum and sum.
+// One pass over the keys with a running maximum and sum.  In bf16 P is rounded to bf16 for
+// the second product (S, the maximum, the sum and O are not): the result is 0.0021 off, its
+// own rounding being 0.0016.  Two bf16 terms of P in the steady loop take 752 us for 564
+// (8192 tokens of 32 and 8 heads of 128); who needs P whole calls in fp32.
 #pragma once
 
 #include <algorithm>
@@ -18,8 +21,10 @@ template <bool BF16, int D> struct ForwardShape {
     static constexpr int kTileBytes = kKeys * Tile<BF16, D>::kLineBytes;
 };
 
-// DIRECT: tiles go straight from memory into LDS (lines
-// whole 16-byte chunks in memory); else through registers.
+// DIRECT: tiles go straight from memory into LDS (lines whole 16-byte chunks in memory);
+// else through registers.  Two waves a SIMD, bf16 heads of up to 128 channels, spill 22
+// registers at 128 (41 through registers), none of them in the steady loop; fp32 heads of
+// 256 channels 114, inside it.
 template <bool BF16, int D, bool DIRECT>
 __global__ __launch_bounds__(kForwardWaves * 64, BF16 && D <= 128 ? 2 : 1) void attention_kernel(PackedArgs a) {
     typedef ForwardShape<BF16, D> F;
@@ -466,10 +471,14 @@ template <bool BF16, int D, bool DIRECT>
 hipError_t launch_shape(const PackedArgs& a, hipStream_t s) {
     typedef ForwardShape<BF16, D> F;
     const int64_t groups = tile_slots(a.Tq, F::kRows, a.n) * a.q_heads;
-    // Few: 1 prompt of 1000 tokens, 16 and 4 heads of 96 in fp32 (128 groups) 104 us so and 54 by
-    // parts, 1500 (192) 146 and 111, three of 500 (224) 59 and 61, 4096 (528) 419 and 608; heads
-    // of 128 in bf16, 200 tokens (32) 18 and 13, 611 and 54 of 6 and 3 (42) 25 and 19, 1000
-    // (128) 33 and 33, 1500 (192) 42 and 62.
+    // Few, by calls of one prompt of 16 and 4 heads, us so and by parts.  200 tokens (32
+    // groups), bf16, heads of 64 .. 256: 10 and 9, 12 and 10, 16 and 11, 18 and 15, 21 and 20;
+    // 500 (64): 14 and 11, 16 and 14, 22 and 15, 29 and 21, 34 and 28; 1000 (128): 20 and 18, 24
+    // and 28, 30 and 31, 44 and 43, 51 and 59; 1500 (192): 26 and 26 .. 65 and 116.  fp32, 1500:
+    // 109 and 77, 146 and 107, 179 and 125, 250 and 172, 453 and 357; 3000 (384): 220 and 243,
+    // 286 and 340, 350 and 395, 495 and 564, 998 and 1218.  (bf16 could go by parts up to about
+    // 100 groups.)  Rows alone decide: few of them over many keys are passed over by few
+    // workgroups (4 of 32 heads over 32768 keys 527 us).
     if (groups < (BF16 ? 64 : 200)) hipLaunchKernelGGL((attention_few_kernel<BF16, D, DIRECT>), dim3((unsigned)(tile_slots(a.Tq, PartsShape<BF16, D>::kOwn, a.n) * a.q_heads)), dim3(kPartsThreads), 0, s, a);
     else hipLaunchKernelGGL((attention_kernel<BF16, D, DIRECT>), dim3((unsigned)groups), dim3(F::kThreads), 0, s, a);
     return hipGetLastError();

@@ -35,7 +35,8 @@ __device__ inline int reg_line(int i, int h) { return 8 * (i >> 2) + 4 * h + (i 
 // A tile of R lines (tokens) of D channels in LDS: 16-byte chunks, lines padded to a
 // power of two of them; chunk c of line r lies at c ^ x(r), such that 16 lines read
 // at one chunk, and the 4 lines x 32 bytes that a transposing read takes, lie in
-// different banks.
+// different banks.  (Heads of 96 and 192 channels pay for the padding with a third more LDS
+// and loads: what goes straight into LDS fills the pad too.)
 template <bool BF16, int D>
 struct Tile {
     static constexpr int kPer = BF16 ? 8 : 4;  // elements a chunk

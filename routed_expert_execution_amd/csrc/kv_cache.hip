@@ -121,8 +121,9 @@ __device__ inline int first_token(int tokens) {
 // a wave finds each one's place; their angles once into LDS; then eight channels a
 // thread of keys, of values, and eight pairs of queries.  Bound by bytes in flight
 // (leaving out the codes' arithmetic, their stores or the cosines changes nothing):
-// five prompts, 32 query and 8 key heads of 128 in bf16, 85 us, 2.5 TB/s of all that is
-// read and written; 64 single tokens 6.5 us, the launch and one read after another.
+// five prompts, 32 query and 8 key heads of 128 in bf16, 86 us, 2.8 TB/s of the 242 MB
+// read and written (waves wait for 0.56 of their time and issue vector instructions for
+// 0.19); 64 single tokens 6.5 us, the launch and one read after another.
 template <bool BF16>
 __global__ __launch_bounds__(kThreads) void kv_append_kernel(KvAppendArgs a, int tokens) {
     __shared__ double2 turns[kTokens][128];
@@ -246,7 +247,7 @@ __global__ __launch_bounds__(kThreads) void kv_append_kernel(KvAppendArgs a, int
 }
 
 // The values kept for each packed token, eight channels a thread: the five prompts'
-// 20 us, the single tokens' 3 us.
+// 20 us (59 MB: 2.9 TB/s, a thread's eight bytes of values one by one), the single tokens' 4 us.
 template <bool BF16>
 __global__ __launch_bounds__(kThreads) void kv_read_kernel(KvReadArgs a, int tokens) {
     __shared__ TokenInfo infos[kTokens];

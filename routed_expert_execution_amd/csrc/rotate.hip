@@ -14,7 +14,8 @@ constexpr int kThreads = 256, kMaxTokens = 16;
 // Bound by bytes.  A workgroup takes a few tokens and turns each one's angles into
 // cosines and sines once, in LDS, for all heads; then eight pairs a thread, 16 bytes
 // a load.  Few tokens of many heads are shared out over gridDim.y workgroups.  8192
-// tokens of 32 heads of 128 in bf16, 32 pairs of each turned: 31 us, 4.3 TB/s; one token 3 us.
+// tokens of 32 heads of 128 in bf16, 32 pairs of each turned: 38 us, 3.5 TB/s (31 where the
+// last-level cache still holds half of it); one token 3 us.
 template <bool BF16>
 __global__ __launch_bounds__(kThreads) void rotate_kernel(RotateArgs a, int per_group) {
     extern __shared__ float2 turns[];  // [per_group][half]

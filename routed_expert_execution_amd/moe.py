@@ -950,7 +950,8 @@ def moe_attention(ctx: Context, q, k, v, offsets, out, *, lse=None, offsets_k=No
 
 
 def moe_attention_workspace(ctx: Context, q, k=None) -> int:
-    """Bytes of moe_attention_backward's workspace for q [tokens_q, q_heads, D]."""
+    """Bytes of moe_attention_backward's workspace for q [tokens_q, q_heads, D]; keys
+    take none of it, k may be left out."""
     n = int(_lib.moe_attention_workspace(q.shape[0], q.shape[1]))
     if n == 0:
         raise ValueError("bad sizes")
