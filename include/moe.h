@@ -648,7 +648,7 @@ typedef struct moe_kv_batch {
  * sequences; and if q is given, the queries [tokens, q_heads, head_dim] are rotated
  * into q_out (which may be q, with the same ld), as moe_rotate does (without a
  * rotary: copied).  A token whose place has no page, or whose sequence cannot be,
- * is left out (error word).  Two tokens of one call may not have the same place. */
+ * is left out (error word; its query is written as if it were not).  Two tokens of one call may not have the same place. */
 moe_status moe_kv_append(moe_ctx* ctx, const moe_kv_cache* cache, const moe_kv_batch* batch, const void* k, int64_t ldk,
                          const void* v, int64_t ldv, int32_t dtype, const moe_rotary* rotary, const int32_t* positions,
                          const void* q, int64_t ldq, int32_t q_heads, void* q_out, int64_t ldqo, moe_stream stream);
@@ -664,8 +664,8 @@ moe_status moe_kv_read(moe_ctx* ctx, const moe_kv_cache* cache, const moe_kv_bat
  * `window` of them:
  *   out = sum_j p_j v_j,  p = softmax_j(scale * q.k_j)
  * q, out: device [tokens, q_heads, head_dim] (dtype); q_heads is a multiple of the
- * cache's heads, the query heads of a key head lie side by side.  scale > 0, finite.
- * Sums and softmax are fp32; q and the cache's codes enter unrounded, p times the
+ * cache's heads, the query heads of a key head lie side by side.  scale > 0, below
+ * 2^127.  Sums and softmax are fp32; q and the cache's codes enter unrounded, p times the
  * step in bf16 (q bf16) or as three bf16 terms (q fp32).  Rows of a sequence that
  * cannot be (a length below its new tokens or above its pages, more than most_new of
  * them) and rows that see a place on a page outside the cache become NaN; other rows of
@@ -685,8 +685,8 @@ moe_status moe_attention_cached(moe_ctx* ctx, const moe_kv_cache* cache, const m
  * causal, query i of n sees keys 0 .. i + m - n of m (the last query sees all of
  * them), with window > 0 (causal only) the last `window` of these; else every
  * query sees every key of its sequence.  q_heads is a multiple of kv_heads (the
- * query heads of a key head lie side by side).  scale > 0, finite.  n up to 65536,
- * tokens up to 2^22. */
+ * query heads of a key head lie side by side).  scale > 0, below 2^127.  n up to
+ * 65536, tokens up to 2^22. */
 typedef struct moe_attn {
     const int32_t *offsets_q, *offsets_k; /* device [n + 1] */
     int32_t n;

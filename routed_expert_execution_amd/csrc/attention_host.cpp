@@ -198,6 +198,9 @@ moe_status moe_kv_read(moe_ctx* c, const moe_kv_cache* cache, const moe_kv_batch
     LAUNCH(moe::launch_kv_read(a, (hipStream_t)stream));
 }
 
+// The kernels' exponentials are powers of two: scale / ln 2 has to be finite as well.
+static float scale_log2_of(float scale) { return (float)((double)scale * 1.4426950408889634); }
+static bool scale_valid(float scale) { return scale > 0 && scale < 0x1p127f; }
 static bool query_heads_valid(int32_t q_heads, int32_t heads) { return q_heads >= 1 && q_heads <= kMaxHeads && q_heads % heads == 0; }
 
 size_t moe_attention_cached_workspace(const moe_kv_cache* m, const moe_kv_batch* b, int32_t q_heads) {
@@ -223,7 +226,7 @@ moe_status moe_attention_cached(moe_ctx* c, const moe_kv_cache* cache, const moe
     const int64_t T = batch->tokens, width = (int64_t)q_heads * g.D;
     if (moe_status st = tokens_check(c, fn, "q", q, dtype, T, width, ldq)) return st;
     if (moe_status st = tokens_check(c, fn, "out", out, dtype, T, width, ldo)) return st;
-    CHECK(std::isfinite(scale) && scale > 0, "%s: scale must be finite and positive", fn);
+    CHECK(scale_valid(scale), "%s: scale must be positive and below 2^127", fn);
     CHECK(window >= 0, "%s: negative window", fn);
     CHECK(workspace && aligned_to(workspace, 256), "%s: workspace must be 256-byte aligned", fn);
     const size_t need = moe_attention_cached_workspace(cache, batch, q_heads);
@@ -236,7 +239,7 @@ moe_status moe_attention_cached(moe_ctx* c, const moe_kv_cache* cache, const moe
     a.cache = moe::kv_view(g, cache->data);
     a.q = q; a.ldq = T > 1 ? ldq : width;
     a.per_head = q_heads / g.heads;
-    a.scale_log2 = (float)((double)scale * 1.4426950408889634);
+    a.scale_log2 = scale_log2_of(scale);
     a.window = (int)(window < (1 << 30) ? window : 0);  // (none reaches further back)
     a.out = out; a.ldo = T > 1 ? ldo : width;
     a.places = p.places; a.part_rows = p.part_rows;
@@ -260,7 +263,7 @@ static moe_status attn_check(moe_ctx* c, const char* fn, const moe_attn* t, moe:
     CHECK(moe::head_dim_valid(t->head_dim), "%s: head_dim=%d not 64, 96, 128, 192 or 256", fn, t->head_dim);
     CHECK(t->causal == 0 || t->causal == 1, "%s: causal must be 0 or 1", fn);
     CHECK(t->window >= 0 && (t->window == 0 || t->causal), "%s: a window is not negative, and needs causal", fn);
-    CHECK(std::isfinite(t->scale) && t->scale > 0, "%s: scale must be finite and positive", fn);
+    CHECK(scale_valid(t->scale), "%s: scale must be positive and below 2^127", fn);
     *a = moe::PackedArgs{};
     a->bf16 = t->dtype == MOE_BF16;
     a->D = t->head_dim; a->q_heads = t->q_heads; a->kv_heads = t->kv_heads; a->per_head = t->q_heads / t->kv_heads;
@@ -269,7 +272,7 @@ static moe_status attn_check(moe_ctx* c, const char* fn, const moe_attn* t, moe:
     a->causal = t->causal;
     a->window = (int)(t->window < (1 << 23) ? t->window : 0);  // (none reaches further back)
     a->scale = t->scale;
-    a->scale_log2 = (float)((double)t->scale * 1.4426950408889634);
+    a->scale_log2 = scale_log2_of(t->scale);
     // (a workgroup of 256 threads for each head of every 32 tokens at most, and one more a sequence: 2^32 threads)
     CHECK((t->tokens_q / 32 + t->n) * t->q_heads < ((int64_t)1 << 24) && (t->tokens_k / 32 + t->n) * t->kv_heads < ((int64_t)1 << 24),
           "%s: too many heads of too many tokens for one call", fn);
